@@ -59,7 +59,7 @@ typedef enum {
     SS_ERR_HIP = -4            /* a HIP runtime call or launch failed */
 } ss_status;
 
-typedef enum { SS_F32 = 0, SS_BF16 = 1 } ss_dtype;
+typedef enum { SS_F32 = 0, SS_BF16 = 1, SS_F16 = 2 /* where a call names it */ } ss_dtype;
 
 /* Host struct. Limits fixed for the handle's lifetime; workspace is sized from
  * them once, in ss_sampler_create. */
@@ -148,7 +148,8 @@ int64_t ss_sampler_workspace_bytes(const ss_sampler* s);
  * scan, row merge, residual tile sums, per-request finish), ss_tree_verify 5
  * (tree paths, tile scan, row merge and child tests, residual tile sums,
  * per-request finish), ss_lmhead_sample 2 (fused GEMM tiles, cross-tile
- * reduction) and ss_lmhead_sample_params 5 (as listed there).
+ * reduction), ss_lmhead_sample_params 5 (as listed there), ss_spec_verify_probs
+ * 2 (chunk sums, draw) and ss_lmhead_quant_logits 1.
  * Returns SS_ERR_INVALID_ARG for a null handle or n_events outside 0 .. 16.
  * Not meant for graph capture. */
 ss_status ss_sampler_set_launch_events(ss_sampler* s, void* const* events, int32_t n_events);
@@ -367,6 +368,199 @@ ss_status ss_sample_noalloc(const void* logits, ss_dtype dtype, int64_t row_stri
 ss_status ss_lmhead_sample_params(ss_sampler* s, const uint16_t* hidden, const uint16_t* weight,
                                   int32_t B, const ss_params* params, int32_t* out_tokens,
                                   int32_t* debug_path, void* stream);
+
+/* ss_spec_verify_probs -- verify a draft against probability rows that the
+ * caller holds, with uniforms that the caller drew (ss_spec_verify takes logits
+ * and draws its own).
+ *   target_probs  [B, G+1, target_stride] of dtype (SS_F32, SS_BF16 or SS_F16),
+ *                 element-aligned, target_stride >= V: the target's probabilities
+ *                 at the draft positions and behind the last one. Rows need not
+ *                 sum to 1: draws are relative to the row's sum. Entries are
+ *                 finite; a negative or NaN entry counts as 0 in a draw.
+ *   draft_probs   [B, G, draft_stride] of the same dtype, draft_stride >= V, or
+ *                 NULL for a greedy draft (q one-hot at each draft token).
+ *   draft_tokens  [B, G] int32; a token outside [0, V) is rejected. May be NULL
+ *                 when G = 0.
+ *   draft_len     [B] int32, or NULL: G for each. Request b drafts
+ *                 n_b = min(max(draft_len[b], 0), G) tokens; its later drafts,
+ *                 uniforms and rows are not read.
+ *   uniforms      [B, G+1] float32 in [0, 1): entry j < G for draft j's test,
+ *                 entry G for the final draw, whatever n_b is. For a value
+ *                 outside [0, 1) the tests below are made as written, and a draw
+ *                 that finds no entry takes the last one with mass.
+ *   B, G          0 .. max_batch, 0 .. max_draft.
+ *   out_tokens    [B, G+1] int32: accepted drafts, the final token, -1 padding.
+ *   out_num_accepted [B] int32 in [0, n_b].
+ *   seq           NULL, or the request sequences the emitted tokens are appended
+ *                 to, as ss_spec_verify_scatter does.
+ * Draft j is accepted iff u_j q_j(d_j) < p_j(d_j), all before it accepted. At
+ * the first rejected position r = max(0, p - q) (without draft rows: p with d_j
+ * removed), behind the last draft r = p; the final token is the lowest v whose
+ * running sum r(0) + ... + r(v) exceeds u_G times the whole sum. Where r has no
+ * mass p is drawn from, and where p has none the token is -1. Products and sums
+ * are binary64. Two kernels. Concurrent calls need handles of their own.
+ * Errors: SS_ERR_INVALID_ARG for a null handle, B or G out of range, another
+ * dtype, a null or misaligned pointer, a stride below V, or a seq that
+ * ss_spec_verify_scatter would refuse. */
+ss_status ss_spec_verify_probs(ss_sampler* s, const void* target_probs, ss_dtype dtype,
+                               int64_t target_stride, const void* draft_probs,
+                               int64_t draft_stride, const int32_t* draft_tokens,
+                               const int32_t* draft_len, const float* uniforms, int32_t B,
+                               int32_t G, int32_t* out_tokens, int32_t* out_num_accepted,
+                               const ss_sequences* seq, void* stream);
+
+/* ss_lmhead_quant_logits -- LM-head logits from 4-bit weights with group scales.
+ *   hidden        [B, K] bfloat16 bits (row-major), finite, 16-byte aligned.
+ *   qweight       [V, K/2] bytes, 16-byte aligned: weight (v, k) is the low
+ *                 nibble of byte k/2 for even k, the high one for odd k.
+ *   scales        [V, ceil(K / group)] of scale_dtype (SS_F16 or SS_BF16).
+ *   zeros         [V, ceil(ceil(K / group) / 2)] bytes of zero points, group g in
+ *                 the low nibble of byte g/2 for even g, else the high one; NULL:
+ *                 8 for every group.
+ *   group         32, 64 or 128 consecutive k; the last group may be shorter.
+ *   B             1 .. min(max_batch, 64); K = hidden_size of the handle.
+ *   out_logits    [B, out_stride] of out_dtype (SS_F32 or SS_BF16), out_stride
+ *                 >= V; entries behind V are left as they were.
+ * out[b, v] = sum over groups of scale (sum over k of (n - zero) hidden[b, k]).
+ * Nothing is rounded below binary32 before the output: products are exact, sums
+ * and scales binary32. A row depends on its own hidden states only, and the
+ * result is the same at every call. The logits are what ss_sample and
+ * ss_spec_verify read. One kernel.
+ * Errors: SS_ERR_INVALID_ARG for a null handle, a handle created with
+ * hidden_size 0, B out of range, a null pointer, another dtype, out_stride < V,
+ * or scales / out_logits not element-aligned; SS_ERR_UNSUPPORTED for another
+ * group or hidden / qweight not 16-byte aligned. */
+ss_status ss_lmhead_quant_logits(ss_sampler* s, const uint16_t* hidden, const uint8_t* qweight,
+                                 const uint16_t* scales, ss_dtype scale_dtype,
+                                 const uint8_t* zeros, int32_t group, int32_t B, void* out_logits,
+                                 ss_dtype out_dtype, int64_t out_stride, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Pages of a key/value cache around verification
+ *
+ * The target's forward pass over a draft writes one cache slot per drafted
+ * token; acceptance decides which of them stay. These calls keep the block
+ * tables on the device, so that no host round trip follows acceptance: reserve
+ * slots for a draft, run the model, verify, commit what was accepted.
+ *
+ * A cache is num_planes arrays of the same shape (a layer's keys, a layer's
+ * values, ...), each num_pages pages of page_size slots of heads pieces of
+ * piece_bytes. A page number names that page of every plane. Rows (requests)
+ * list their pages in a block table; ref[page] is the number of table entries
+ * that hold the page, 0 for a free page. The caller keeps the tables, counts
+ * and lengths in its own device arrays and starts with tables filled with -1
+ * and counts and lengths of 0. A negative or too large entry counts as no page.
+ *
+ * As for a sampler handle: calls only enqueue work, may be captured in a graph,
+ * and a cache handle (its workspace) serves one stream at a time. */
+typedef struct ss_cache ss_cache; /* opaque; owns its workspace, not the planes */
+
+typedef struct {
+    int32_t num_planes;  /* 1 .. 4096 */
+    int32_t num_pages;   /* 1 .. 4194304 */
+    int32_t page_size;   /* slots per page, 1 .. 65536 */
+    int32_t heads;       /* pieces per slot, >= 1; heads * piece_bytes <= 2^24 */
+    int32_t piece_bytes; /* >= 1; a page of one plane holds less than 2^31 bytes */
+    int64_t page_stride; /* bytes between pages, slots and heads: any order, as long */
+    int64_t slot_stride; /*   as no two pieces overlap; a dimension of one entry may */
+    int64_t head_stride; /*   have any stride */
+    int32_t max_batch;   /* rows of the block tables, 1 .. 65535 */
+    int32_t max_blocks;  /* entries of a row, >= 1; max_batch * max_blocks and
+                            max_blocks * page_size below 2^31 */
+    int32_t device;
+} ss_cache_config;
+
+/* Block tables (all pointers device, 4-byte aligned). */
+typedef struct {
+    int32_t* tables; /* [rows, stride]: row r's pages in order, -1 = none */
+    int64_t stride;  /* >= max_blocks */
+    int32_t rows;    /* 1 .. max_batch */
+    int32_t* ref;    /* [num_pages] */
+    int32_t* len;    /* [rows]: committed slots */
+} ss_block_tables;
+
+/* Creates a cache handle (the only call that allocates). planes: HOST array of
+ * num_planes device pointers, read during the call. Vectors of 16 bytes are
+ * copied where every plane, stride and piece is a multiple of 16, else of 4 or 1.
+ * Errors as ss_sampler_create. */
+ss_status ss_cache_create(const ss_cache_config* cfg, void* const* planes, ss_cache** out);
+
+/* Frees the workspace. The caller must ensure no enqueued call is pending. */
+void ss_cache_destroy(ss_cache* c);
+
+/* Bytes of device workspace the handle holds. */
+int64_t ss_cache_workspace_bytes(const ss_cache* c);
+
+/* ss_cache_reserve -- make slots [base_b, base_b + add_b) of rows 0 .. B-1 writable.
+ *   base    [B] int32, or NULL: t->len.   add  [B] int32 >= 0.
+ *   out_ok  NULL, or [B] int32: 1 served (add = 0 always is), 0 refused.
+ * Every table entry those slots lie on that holds no page, or one that others
+ * hold as well, gets a fresh page; of a shared page that holds slots before
+ * base_b those slots are copied along (all planes), and its count falls by one.
+ * Fresh pages are the lowest-numbered free ones, in row order, then table order;
+ * counts are those at the call's start, so rows that share a page and both
+ * reserve on it both leave it. Rows are served in order while their pages
+ * suffice: once one does not fit, later rows that need pages are refused too. A
+ * negative base or add, or slots behind max_blocks pages, is refused by itself.
+ * A refused row is left as it was. Two kernels. */
+ss_status ss_cache_reserve(ss_cache* c, const ss_block_tables* t, const int32_t* base,
+                           const int32_t* add, int32_t B, int32_t* out_ok, void* stream);
+
+/* ss_cache_fork -- rows dst[i] become copies of rows src[i] without copying: the
+ * pages that hold len[src] slots are shared, len[dst] = len[src], what dst held
+ * before is given back.
+ *   src, dst  [n] int32 rows, n <= rows.   out_ok  NULL, or [n] int32.
+ * A pair is refused (out_ok 0, nothing changed) if a row is out of range, or its
+ * dst is named by another pair's dst or by any pair's src. One kernel. */
+ss_status ss_cache_fork(ss_cache* c, const ss_block_tables* t, const int32_t* src,
+                        const int32_t* dst, int32_t n, int32_t* out_ok, void* stream);
+
+/* ss_cache_commit -- keep what verification accepted of rows 0 .. B-1.
+ *   base          [B] int32, or NULL: t->len. The forward pass wrote the last
+ *                 committed token (the root) to slot base_b and tree node n to
+ *                 slot base_b + n (linear drafts: draft j to base_b + 1 + j).
+ *   num_accepted  [B] int32, as ss_tree_verify / ss_spec_verify leave it.
+ *   nodes         [B, nodes_stride] int32, as ss_tree_verify's out_nodes: ascending
+ *                 nodes in 1 .. N-1, the first num_accepted read; or NULL: a
+ *                 linear draft, nothing moves (N and nodes_stride ignored).
+ *   N             1 .. 64, nodes_stride >= N.
+ *   release       nonzero: pages behind the new length are given back; else they
+ *                 stay for the next draft.
+ *   out_ok        NULL, or [B] int32.
+ * Slot base + nodes[i] moves to base + 1 + i on every plane, and len[b] becomes
+ * base + 1 + num_accepted. The pages written must be the row's own, as
+ * ss_cache_reserve leaves them. A row is refused (out_ok 0, left as it was) for
+ * a negative base, num_accepted outside 0 .. N-1, nodes out of range or not
+ * ascending, a slot without a page or behind max_blocks pages. One or two
+ * kernels. */
+ss_status ss_cache_commit(ss_cache* c, const ss_block_tables* t, const int32_t* base,
+                          const int32_t* nodes, int64_t nodes_stride, int32_t N,
+                          const int32_t* num_accepted, int32_t B, int32_t release,
+                          int32_t* out_ok, void* stream);
+
+/* ss_cache_truncate -- give back the pages behind new_len.
+ *   rows     [n] int32, or NULL: 0 .. n-1; rows out of range are skipped, a row
+ *            listed twice is truncated to the shorter length.
+ *   new_len  [n] int32, or NULL: 0 (the row ends); negative counts as 0.
+ * len[row] becomes min(len[row], new_len). One kernel. */
+ss_status ss_cache_truncate(ss_cache* c, const ss_block_tables* t, const int32_t* rows,
+                            const int32_t* new_len, int32_t n, void* stream);
+
+/* ss_cache_copy_pages -- copy whole pages, all planes, page src[i] of one cache to
+ * page dst[i] of another of the same shape and device (strides may differ), or
+ * of the same.
+ *   src, dst  [n] int32, n <= min(65535, the destination's num_pages).
+ *   out_ok    NULL, or [n] int32.
+ * A pair is refused (out_ok 0) if a page is out of range, its dst is another
+ * pair's dst, or, within one cache, any pair's src. Counts and tables are not
+ * touched. Uses dst_cache's workspace. Two kernels.
+ *
+ * Errors of the calls above, before any launch: SS_ERR_INVALID_ARG for a null
+ * handle, tables that are null, misaligned, too narrow or of too many rows, a
+ * count out of range or a null required pointer; SS_ERR_HIP if a launch fails.
+ * A count of 0 returns SS_OK. */
+ss_status ss_cache_copy_pages(ss_cache* src_cache, const int32_t* src, ss_cache* dst_cache,
+                              const int32_t* dst, int32_t n, int32_t* out_ok, void* stream);
 
 #ifdef __cplusplus
 }

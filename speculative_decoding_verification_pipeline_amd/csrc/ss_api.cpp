@@ -11,6 +11,7 @@
 #include <new>
 
 #include "ss_device.h"
+#include "ss_device_guard.h"
 #include "ss_internal.h"
 
 struct ss_sampler {
@@ -26,6 +27,7 @@ struct ss_sampler {
     ss::LmTileStat* lm_stats;
     int32_t* lm_unres;
     ss::LmCut* lm_cut;
+    double2* probs_part;  // [max_batch * n_wt]
     ss::LaunchEvents events;
     // defaults substituted for absent per-request parameters, [max_batch] each
     int32_t* def_zero_i;
@@ -285,6 +287,7 @@ ss_status ss_sampler_create(const ss_sampler_config* cfg, ss_sampler** out) {
         cfg->hidden_size > 0 ? take(64 * (int64_t)s->n_vtiles * (int64_t)sizeof(ss::LmTileStat)) : 0;
     const int64_t o_lmunres = cfg->hidden_size > 0 ? take(64 * 4) : 0;
     const int64_t o_lmcut = cfg->hidden_size > 0 ? take(64 * (int64_t)sizeof(ss::LmCut)) : 0;
+    const int64_t o_probs = take((int64_t)B * nw * (int64_t)sizeof(double2));
     const int64_t o_defaults = take(4 * (int64_t)B * 4);
     s->ws_bytes = off;
     if (hipMalloc(&s->ws_base, (size_t)off) != hipSuccess) {
@@ -312,6 +315,7 @@ ss_status ss_sampler_create(const ss_sampler_config* cfg, ss_sampler** out) {
     s->lm_stats = cfg->hidden_size > 0 ? reinterpret_cast<ss::LmTileStat*>(b + o_lmstat) : nullptr;
     s->lm_unres = cfg->hidden_size > 0 ? reinterpret_cast<int32_t*>(b + o_lmunres) : nullptr;
     s->lm_cut = cfg->hidden_size > 0 ? reinterpret_cast<ss::LmCut*>(b + o_lmcut) : nullptr;
+    s->probs_part = reinterpret_cast<double2*>(b + o_probs);
     {
         int32_t* d = reinterpret_cast<int32_t*>(b + o_defaults);
         s->def_zero_i = d;
@@ -542,6 +546,90 @@ ss_status ss_lmhead_sample(ss_sampler* s, const uint16_t* hidden, const uint16_t
     if (hipSetDevice(s->cfg.device) != hipSuccess) return SS_ERR_HIP;
     return ss::launch_lmhead(a, static_cast<hipStream_t>(stream), s->events) == hipSuccess ? SS_OK
                                                                                 : SS_ERR_HIP;
+}
+
+ss_status ss_spec_verify_probs(ss_sampler* s, const void* target_probs, ss_dtype dtype,
+                               int64_t target_stride, const void* draft_probs, int64_t draft_stride,
+                               const int32_t* draft_tokens, const int32_t* draft_len,
+                               const float* uniforms, int32_t B, int32_t G, int32_t* out_tokens,
+                               int32_t* out_num_accepted, const ss_sequences* seq, void* stream) {
+    if (!s || B < 0 || B > s->cfg.max_batch) return SS_ERR_INVALID_ARG;
+    if (G < 0 || G > s->cfg.max_draft) return SS_ERR_INVALID_ARG;
+    if (dtype != SS_F32 && dtype != SS_BF16 && dtype != SS_F16) return SS_ERR_INVALID_ARG;
+    if (B == 0) return SS_OK;
+    const int V = s->cfg.vocab_size;
+    const uintptr_t low = dtype == SS_F32 ? 3u : 1u;
+    if (!target_probs || (reinterpret_cast<uintptr_t>(target_probs) & low) || target_stride < V)
+        return SS_ERR_INVALID_ARG;
+    if (draft_probs && ((reinterpret_cast<uintptr_t>(draft_probs) & low) || draft_stride < V))
+        return SS_ERR_INVALID_ARG;
+    if ((G > 0 && !draft_tokens) || !uniforms || !out_tokens || !out_num_accepted)
+        return SS_ERR_INVALID_ARG;
+    if (seq && (!seq->tokens || !seq->len || seq->capacity < 0 || seq->stride < seq->capacity))
+        return SS_ERR_INVALID_ARG;
+    ss::ProbsArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.target = target_probs;
+    a.target_stride = target_stride;
+    a.draft = G > 0 ? draft_probs : nullptr;
+    a.draft_stride = draft_stride;
+    a.draft_tokens = draft_tokens;
+    a.draft_len = draft_len;
+    a.uniforms = uniforms;
+    a.B = B;
+    a.G = G;
+    a.V = V;
+    a.out_tokens = out_tokens;
+    a.out_num_accepted = out_num_accepted;
+    if (seq) {
+        a.seq_tokens = seq->tokens;
+        a.seq_stride = seq->stride;
+        a.seq_capacity = seq->capacity;
+        a.seq_len = seq->len;
+    }
+    a.part = s->probs_part;
+    a.n_chunks = (V + ss::WT - 1) / ss::WT;
+    ss::DeviceGuard guard(s->cfg.device);
+    if (!guard.ok) return SS_ERR_HIP;
+    return ss::launch_probs(a, dtype, static_cast<hipStream_t>(stream), s->events) == hipSuccess
+               ? SS_OK
+               : SS_ERR_HIP;
+}
+
+ss_status ss_lmhead_quant_logits(ss_sampler* s, const uint16_t* hidden, const uint8_t* qweight,
+                                 const uint16_t* scales, ss_dtype scale_dtype,
+                                 const uint8_t* zeros, int32_t group, int32_t B, void* out_logits,
+                                 ss_dtype out_dtype, int64_t out_stride, void* stream) {
+    if (!s || s->cfg.hidden_size <= 0) return SS_ERR_INVALID_ARG;
+    if (B < 1 || B > s->cfg.max_batch || B > 64) return SS_ERR_INVALID_ARG;
+    if (!hidden || !qweight || !scales || !out_logits) return SS_ERR_INVALID_ARG;
+    if (scale_dtype != SS_F16 && scale_dtype != SS_BF16) return SS_ERR_INVALID_ARG;
+    if (out_dtype != SS_F32 && out_dtype != SS_BF16) return SS_ERR_INVALID_ARG;
+    if (out_stride < s->cfg.vocab_size) return SS_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(scales) & 1u) ||
+        (reinterpret_cast<uintptr_t>(out_logits) & (out_dtype == SS_F32 ? 3u : 1u)))
+        return SS_ERR_INVALID_ARG;
+    if (group != 32 && group != 64 && group != 128) return SS_ERR_UNSUPPORTED;
+    if (!aligned16(hidden) || !aligned16(qweight)) return SS_ERR_UNSUPPORTED;
+    ss::QuantArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.hidden = hidden;
+    a.qweight = qweight;
+    a.scales = scales;
+    a.zeros = zeros;
+    a.scale_f16 = scale_dtype == SS_F16;
+    a.group = group;
+    a.B = B;
+    a.K = s->cfg.hidden_size;
+    a.V = s->cfg.vocab_size;
+    a.out = out_logits;
+    a.out_bf16 = out_dtype == SS_BF16;
+    a.out_stride = out_stride;
+    ss::DeviceGuard guard(s->cfg.device);
+    if (!guard.ok) return SS_ERR_HIP;
+    return ss::launch_quant(a, static_cast<hipStream_t>(stream), s->events) == hipSuccess
+               ? SS_OK
+               : SS_ERR_HIP;
 }
 
 ss_status ss_sample_noalloc(const void* logits, ss_dtype dtype, int64_t row_stride, int32_t B,

@@ -206,6 +206,132 @@ struct LmheadArgs {
     int32_t* dbg_path;       // [B] or null: 0 candidates, 1 whole row, 2 no filter or greedy
 };
 
+// Verification against probability rows with the caller's uniforms.
+struct ProbsArgs {
+    const void* target;        // [B * (G + 1)] rows
+    int64_t target_stride;
+    const void* draft;         // [B * G] rows, or null: one-hot drafts
+    int64_t draft_stride;
+    const int32_t* draft_tokens;
+    const int32_t* draft_len;  // [B] or null: G drafts each
+    const float* uniforms;     // [B, G + 1]
+    int B;
+    int G;
+    int V;
+    int32_t* out_tokens;
+    int32_t* out_num_accepted;
+    int32_t* seq_tokens;       // null: no append to the request sequences
+    int64_t seq_stride;
+    int32_t seq_capacity;
+    int32_t* seq_len;
+    double2* part;             // [B * n_chunks]: residual and target mass per 2048-entry chunk
+    int n_chunks;
+};
+
+// LM-head logits from 4-bit weights.
+struct QuantArgs {
+    const uint16_t* hidden;    // [B, K] bfloat16
+    const uint8_t* qweight;    // [V, K / 2]
+    const uint16_t* scales;    // [V, ceil(K / group)]
+    const uint8_t* zeros;      // [V, ceil(groups / 2)], or null: 8
+    int scale_f16;
+    int group;
+    int B;
+    int K;
+    int V;
+    void* out;
+    int out_bf16;
+    int64_t out_stride;
+};
+
+// ---------------------------------------------------------------------------
+// page cache
+
+constexpr int CACHE_REF_CHUNK = 4096;   // page counts listed by one workgroup
+constexpr int CACHE_MAX_CHUNKS = 1024;
+constexpr int CACHE_MAX_PAGES = CACHE_REF_CHUNK * CACHE_MAX_CHUNKS;
+
+struct CacheTables {
+    int32_t* tables;  // [rows, stride]
+    int64_t stride;
+    int32_t rows;
+    int32_t* ref;     // [num_pages]
+    int32_t* len;     // [rows]
+};
+
+// How slots of one cache are copied to slots of another (or the same): strides
+// in bytes, a piece of one head is `units` vectors of `vec` bytes.
+struct CacheCopy {
+    const char* const* src_planes;  // device array
+    char* const* dst_planes;
+    int64_t src_page, src_slot, src_head;
+    int64_t dst_page, dst_slot, dst_head;
+    int heads;
+    int units;
+    int vec;
+    int joined;  // consecutive slots of a head follow each other on both sides
+};
+
+struct CacheWork {
+    int32_t* free_ids;  // [chunks * CACHE_REF_CHUNK]: free pages, ascending within a chunk
+    int32_t* free_cnt;  // [chunks]
+    int32_t* need;      // [max_batch]: fresh pages a request needs, -1 refused
+    int32_t* carry;     // [max_batch]: shared page whose first slots move along, or -1
+    int32_t* mark;      // [max_batch * max_blocks]
+    int32_t* pair_ok;   // [num_pages]
+};
+
+struct CacheReserve {
+    CacheTables t;
+    CacheWork ws;
+    const int32_t* base;
+    const int32_t* add;
+    int B;
+    int32_t* out_ok;
+    int num_pages, num_planes, page_size, max_blocks, n_chunks;
+};
+
+struct CacheTruncate {
+    CacheTables t;
+    const int32_t* rows;     // null: 0 .. n - 1
+    const int32_t* new_len;  // null: 0
+    int n;
+    int num_pages, page_size, max_blocks;
+};
+
+struct CacheFork {
+    CacheTables t;
+    const int32_t* src;
+    const int32_t* dst;
+    int n;
+    int32_t* out_ok;
+    int num_pages, page_size, max_blocks;
+};
+
+struct CacheCommit {
+    CacheTables t;
+    const int32_t* base;
+    const int32_t* num_accepted;
+    const int32_t* nodes;    // null: a linear draft, nothing moves
+    int64_t nodes_stride;
+    int N;
+    int B;
+    int release;
+    int32_t* out_ok;
+    int num_pages, num_planes, page_size, max_blocks;
+};
+
+struct CachePages {
+    const int32_t* src;
+    const int32_t* dst;
+    int n;
+    int same;
+    int src_pages, dst_pages;
+    int num_planes, page_size;
+    int32_t* pair_ok;
+    int32_t* out_ok;
+};
+
 // Optional timing events of a call (see ss_sampler_set_launch_events): launch
 // k is bracketed by ev[2k] (its start) and ev[2k + 1] (its end), recorded by
 // the dispatch itself.
@@ -231,6 +357,13 @@ hipError_t launch_spec(const SpecArgs& a, ss_dtype dt, hipStream_t st, const Lau
 hipError_t launch_tree(const TreeArgs& a, ss_dtype dt, hipStream_t st, const LaunchEvents& le);
 hipError_t launch_lmhead(const LmheadArgs& a, hipStream_t st, const LaunchEvents& le);
 hipError_t launch_lmhead_params(const LmheadArgs& a, hipStream_t st, const LaunchEvents& le);
+hipError_t launch_probs(const ProbsArgs& a, ss_dtype dt, hipStream_t st, const LaunchEvents& le);
+hipError_t launch_quant(const QuantArgs& a, hipStream_t st, const LaunchEvents& le);
+hipError_t launch_cache_reserve(const CacheReserve& a, const CacheCopy& g, hipStream_t st);
+hipError_t launch_cache_truncate(const CacheTruncate& a, hipStream_t st);
+hipError_t launch_cache_fork(const CacheFork& a, hipStream_t st);
+hipError_t launch_cache_commit(const CacheCommit& a, const CacheCopy& g, hipStream_t st);
+hipError_t launch_cache_copy(const CachePages& a, const CacheCopy& g, hipStream_t st);
 // the row kernels of ss_lmhead_sample_params (in the row-kernel source)
 void launch_lm_merge(const LmheadArgs& a, hipStream_t st, const LaunchEvents& le, int k);
 void launch_lm_slow(const LmheadArgs& a, hipStream_t st, const LaunchEvents& le, int k);

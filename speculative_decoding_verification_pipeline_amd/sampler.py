@@ -23,11 +23,15 @@ SS_ERR_OUT_OF_MEMORY = -3
 SS_ERR_HIP = -4
 SS_F32 = 0
 SS_BF16 = 1
+SS_F16 = 2
 
 EXPORTED = ("ss_sampler_create", "ss_sampler_destroy", "ss_status_string",
             "ss_sampler_workspace_bytes", "ss_sampler_set_launch_events", "ss_sample",
             "ss_spec_verify", "ss_spec_verify_scatter", "ss_tree_verify", "ss_lmhead_sample",
-            "ss_lmhead_sample_params", "ss_sample_noalloc")
+            "ss_lmhead_sample_params", "ss_sample_noalloc", "ss_spec_verify_probs",
+            "ss_lmhead_quant_logits", "ss_cache_create", "ss_cache_destroy",
+            "ss_cache_workspace_bytes", "ss_cache_reserve", "ss_cache_fork", "ss_cache_commit",
+            "ss_cache_truncate", "ss_cache_copy_pages")
 NOALLOC_MAX_BATCH = 64
 NOALLOC_MAX_ENTRIES = 1 << 23
 
@@ -60,6 +64,20 @@ class CDebug(ctypes.Structure):
 class CSequences(ctypes.Structure):
     _fields_ = [("tokens", ctypes.c_void_p), ("stride", ctypes.c_int64),
                 ("capacity", ctypes.c_int32), ("len", ctypes.c_void_p)]
+
+
+class CacheConfig(ctypes.Structure):
+    _fields_ = [("num_planes", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("piece_bytes", ctypes.c_int32), ("page_stride", ctypes.c_int64),
+                ("slot_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("max_batch", ctypes.c_int32), ("max_blocks", ctypes.c_int32),
+                ("device", ctypes.c_int32)]
+
+
+class CBlockTables(ctypes.Structure):
+    _fields_ = [("tables", ctypes.c_void_p), ("stride", ctypes.c_int64),
+                ("rows", ctypes.c_int32), ("ref", ctypes.c_void_p), ("len", ctypes.c_void_p)]
 
 
 class SamplerError(RuntimeError):
@@ -110,6 +128,29 @@ def load_library(path=None):
     lib.ss_lmhead_sample_params.restype = i32
     lib.ss_sample_noalloc.argtypes = [vp, i32, i64, i32, i32, ctypes.POINTER(CParams), vp, vp]
     lib.ss_sample_noalloc.restype = i32
+    lib.ss_spec_verify_probs.argtypes = [vp, vp, i32, i64, vp, i64, vp, vp, vp, i32, i32, vp, vp,
+                                         ctypes.POINTER(CSequences), vp]
+    lib.ss_spec_verify_probs.restype = i32
+    lib.ss_lmhead_quant_logits.argtypes = [vp, vp, vp, vp, i32, vp, i32, i32, vp, i32, i64, vp]
+    lib.ss_lmhead_quant_logits.restype = i32
+    tables = ctypes.POINTER(CBlockTables)
+    lib.ss_cache_create.argtypes = [ctypes.POINTER(CacheConfig), ctypes.POINTER(vp),
+                                    ctypes.POINTER(vp)]
+    lib.ss_cache_create.restype = i32
+    lib.ss_cache_destroy.argtypes = [vp]
+    lib.ss_cache_destroy.restype = None
+    lib.ss_cache_workspace_bytes.argtypes = [vp]
+    lib.ss_cache_workspace_bytes.restype = i64
+    lib.ss_cache_reserve.argtypes = [vp, tables, vp, vp, i32, vp, vp]
+    lib.ss_cache_reserve.restype = i32
+    lib.ss_cache_fork.argtypes = [vp, tables, vp, vp, i32, vp, vp]
+    lib.ss_cache_fork.restype = i32
+    lib.ss_cache_commit.argtypes = [vp, tables, vp, vp, i64, i32, vp, i32, i32, vp, vp]
+    lib.ss_cache_commit.restype = i32
+    lib.ss_cache_truncate.argtypes = [vp, tables, vp, vp, i32, vp]
+    lib.ss_cache_truncate.restype = i32
+    lib.ss_cache_copy_pages.argtypes = [vp, vp, vp, vp, i32, vp, vp]
+    lib.ss_cache_copy_pages.restype = i32
     _lib = lib
     return lib
 
@@ -125,6 +166,12 @@ def _ptr(t):
 
 def _stream(stream):
     s = stream if stream is not None else torch.cuda.current_stream()
+    return ctypes.c_void_p(s.cuda_stream)
+
+
+def _stream_on(stream, device):
+    """The given stream, or the current one of a device that need not be current."""
+    s = stream if stream is not None else torch.cuda.current_stream(device)
     return ctypes.c_void_p(s.cuda_stream)
 
 
@@ -153,6 +200,26 @@ def _check_rows(t, name, n, dtypes, device):
     _check_dev(t, name, dtypes, device)
     _require(t.dim() == 2 and t.shape[0] >= n, f"{name} must be 2-D with >= {n} rows")
     _require(t.shape[1] <= 1 or t.stride(1) == 1, f"{name} must have unit stride along its last dim")
+
+
+_PROB_DTYPES = {torch.float32: SS_F32, torch.bfloat16: SS_BF16, torch.float16: SS_F16}
+
+
+def _check_block(t, name, shape, dtype, device):
+    """A contiguous array of exactly this shape."""
+    _check_dev(t, name, (dtype,), device)
+    _require(tuple(t.shape) == shape and t.is_contiguous(),
+             f"{name} must be a contiguous {list(shape)} array of {dtype}")
+
+
+def _row_stride(t, name):
+    """The one stride between the rows of a [B, R, V] array (row b * R + r)."""
+    B, R, V = t.shape
+    _require(V <= 1 or t.stride(2) == 1, f"{name} must have unit stride along V")
+    stride = t.stride(1) if R > 1 else t.stride(0) if B > 1 else V
+    _require((B <= 1 or R == 0 or t.stride(0) == R * stride) and stride >= V,
+             f"{name} rows must be evenly spaced and must not overlap")
+    return int(stride)
 
 
 @dataclass
@@ -483,6 +550,92 @@ class Sampler:
                                        int(seed) & 0xFFFFFFFFFFFFFFFF, _ptr(out),
                                        _ptr(debug_logits), _stream(stream))
         _check("ss_lmhead_sample", st)
+        return out
+
+
+    def spec_verify_probs(self, target_probs, draft_probs, draft_tokens, uniforms, draft_len=None,
+                          out_tokens=None, out_num_accepted=None, stream=None, seq_tokens=None,
+                          seq_len=None):
+        """Verify drafts against probability rows target_probs [B, G+1, V] (float32,
+        bfloat16 or float16) with the caller's uniforms [B, G+1] float32 in
+        [0, 1). draft_probs [B, G, V] of the same dtype, or None for greedy
+        drafts; draft_len [B] int32: drafts of each request (None: G).
+        seq_tokens / seq_len as in spec_verify. Returns (tokens [B, G+1],
+        num_accepted [B])."""
+        dev = self.device
+        _check_dev(target_probs, "target_probs", tuple(_PROB_DTYPES), dev)
+        _require(target_probs.dim() == 3 and target_probs.shape[1] >= 1,
+                 "target_probs must be [B, G+1, V]")
+        B, G1, V = target_probs.shape
+        G = G1 - 1
+        _require(V == self.vocab_size, f"target_probs have {V} columns, the sampler {self.vocab_size}")
+        tstride = _row_stride(target_probs, "target_probs")
+        dstride = 0
+        if draft_probs is not None:
+            _check_dev(draft_probs, "draft_probs", (target_probs.dtype,), dev)
+            _require(tuple(draft_probs.shape) == (B, G, V), "draft_probs must be [B, G, V]")
+            dstride = _row_stride(draft_probs, "draft_probs")
+        _check_block(draft_tokens, "draft_tokens", (B, G), torch.int32, dev)
+        _check_block(uniforms, "uniforms", (B, G1), torch.float32, dev)
+        _check_vec(draft_len, "draft_len", B, torch.int32, dev)
+        if out_tokens is None:
+            out_tokens = torch.empty(B, G1, dtype=torch.int32, device=target_probs.device)
+        else:
+            _check_block(out_tokens, "out_tokens", (B, G1), torch.int32, dev)
+        if out_num_accepted is None:
+            out_num_accepted = torch.empty(B, dtype=torch.int32, device=target_probs.device)
+        else:
+            _check_vec(out_num_accepted, "out_num_accepted", B, torch.int32, dev)
+        seq = None
+        if seq_tokens is not None or seq_len is not None:
+            _require(seq_tokens is not None and seq_len is not None,
+                     "seq_tokens and seq_len go together")
+            _check_rows(seq_tokens, "seq_tokens", B, (torch.int32,), dev)
+            _check_vec(seq_len, "seq_len", B, torch.int32, dev)
+            _require(B <= 1 or seq_tokens.stride(0) >= seq_tokens.shape[1],
+                     "seq_tokens rows must not overlap")
+            seq = CSequences(_ptr(seq_tokens), int(seq_tokens.stride(0)) if B > 1 else
+                             int(seq_tokens.shape[1]), int(seq_tokens.shape[1]), _ptr(seq_len))
+        st = self.lib.ss_spec_verify_probs(
+            self.handle, _ptr(target_probs), _PROB_DTYPES[target_probs.dtype], tstride,
+            _ptr(draft_probs), dstride, _ptr(draft_tokens), _ptr(draft_len), _ptr(uniforms), B, G,
+            _ptr(out_tokens), _ptr(out_num_accepted),
+            ctypes.byref(seq) if seq is not None else None, _stream_on(stream, dev))
+        _check("ss_spec_verify_probs", st)
+        return out_tokens, out_num_accepted
+
+    def lmhead_quant_logits(self, hidden, qweight, scales, group, zeros=None, out=None,
+                            out_dtype=torch.float32, stream=None):
+        """LM-head logits [B, V] of hidden [B, K] bfloat16 and 4-bit weights: qweight
+        [V, K/2] uint8 (even k in the low nibble), scales [V, ceil(K/group)]
+        float16 or bfloat16, zeros [V, ceil(groups/2)] uint8 nibbles (None: 8).
+        out: [B, V] float32 or bfloat16 with unit column stride, else one of
+        out_dtype is made."""
+        dev, V, K = self.device, self.vocab_size, self.hidden_size
+        _check_dev(hidden, "hidden", (torch.bfloat16, torch.int16), dev)
+        _require(hidden.dim() == 2 and hidden.is_contiguous(), "hidden must be a contiguous [B, K] array")
+        B = hidden.shape[0]
+        _require(hidden.shape[1] == K, f"hidden has K = {hidden.shape[1]}, the sampler {K}")
+        _require(isinstance(group, int) and group in (32, 64, 128), "group must be 32, 64 or 128")
+        groups = -(-K // group)
+        _check_block(qweight, "qweight", (V, K // 2), torch.uint8, dev)
+        _check_dev(scales, "scales", (torch.float16, torch.bfloat16), dev)
+        _check_block(scales, "scales", (V, groups), scales.dtype, dev)
+        if zeros is not None:
+            _check_block(zeros, "zeros", (V, (groups + 1) // 2), torch.uint8, dev)
+        if out is None:
+            _require(out_dtype in (torch.float32, torch.bfloat16),
+                     "out_dtype must be float32 or bfloat16")
+            out = torch.empty(B, V, dtype=out_dtype, device=hidden.device)
+        else:
+            _check_rows(out, "out", B, (torch.float32, torch.bfloat16), dev)
+            _require(tuple(out.shape) == (B, V) and (B <= 1 or out.stride(0) >= V),
+                     "out must be [B, V] with rows that do not overlap")
+        st = self.lib.ss_lmhead_quant_logits(
+            self.handle, _ptr(hidden), _ptr(qweight), _ptr(scales),
+            SS_F16 if scales.dtype == torch.float16 else SS_BF16, _ptr(zeros), group, B, _ptr(out),
+            self._dtype(out), int(out.stride(0)) if B > 1 else V, _stream_on(stream, dev))
+        _check("ss_lmhead_quant_logits", st)
         return out
 
 

@@ -1,0 +1,354 @@
+"""The page cache against its definition on host lists (oracle.cache): tables,
+counts, lengths, verdicts and every byte of the planes are equal after each call."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache as OC
+from speculative_decoding_verification_pipeline_amd import sampler as SM
+from speculative_decoding_verification_pipeline_amd.cache import BlockTables, PageCache
+from tests.gpu_support import device, log
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(v):
+    return torch.tensor(np.asarray(v), dtype=torch.int32, device=device())
+
+
+class Pair:
+    """A cache on the device and its oracle, run side by side."""
+
+    def __init__(self, planes, P, ps, heads, dim, rows, M, dtype=torch.int16, layout="nhd",
+                 separate=False, pad=0, seed=0):
+        g = torch.Generator().manual_seed(seed)
+        info = torch.iinfo(dtype)
+        x = torch.randint(info.min, info.max + 1, (planes, P, ps, heads, dim), generator=g, dtype=dtype)
+        d = x.to(device())
+        if layout == "hnd":  # heads outside the slots
+            d = d.transpose(2, 3).contiguous().transpose(2, 3)
+        elif layout == "padded":
+            big = torch.zeros(planes, P, ps, heads, dim + pad, dtype=dtype, device=device())
+            big[..., :dim] = d
+            d = big[..., :dim]
+        elif layout == "heads first":  # [heads, page, slot, dim] within a plane
+            d = d.permute(0, 3, 1, 2, 4).contiguous().permute(0, 2, 3, 1, 4)
+        self.d = [d[i].clone(memory_format=torch.preserve_format) for i in range(planes)] \
+            if separate else d
+        self.cache = PageCache(self.d, rows, M)
+        self.bt = self.cache.new_tables()
+        self.o = OC.Pages(x.numpy().copy(), rows, M)
+        self.rng = np.random.default_rng(seed)
+
+    def pool(self):
+        p = torch.stack(list(self.d)) if isinstance(self.d, list) else self.d
+        return p.cpu().numpy()
+
+    def same(self, what, got=None, want=None):
+        if want is not None:
+            assert got.cpu().tolist() == want, what
+        assert self.bt.tables.cpu().tolist() == self.o.tables, what
+        assert self.bt.ref.cpu().tolist() == self.o.ref, what
+        assert self.bt.lens.cpu().tolist() == self.o.lens, what
+        assert np.array_equal(self.pool(), self.o.pool), what
+        assert self.o.consistent(), what
+
+    def reserve(self, add, base=None):
+        got = self.cache.reserve(self.bt, i32(add), lens=None if base is None else i32(base))
+        self.same(("reserve", add, base), got, self.o.reserve(add, base))
+
+    def fork(self, src, dst):
+        got = self.cache.fork(self.bt, i32(src), i32(dst))
+        self.same(("fork", src, dst), got, self.o.fork(src, dst))
+
+    def commit(self, acc, nodes=None, base=None, release=True):
+        got = self.cache.commit(self.bt, i32(acc), nodes=None if nodes is None else i32(nodes),
+                                base=None if base is None else i32(base), release=release)
+        self.same(("commit", acc, nodes, base, release), got,
+                  self.o.commit(acc, nodes, base, release))
+
+    def truncate(self, new_len=None, rows=None):
+        self.cache.truncate(self.bt, new_len=None if new_len is None else i32(new_len),
+                            rows=None if rows is None else i32(rows))
+        self.o.truncate(new_len, rows)
+        self.same(("truncate", new_len, rows))
+
+    def copy(self, src, dst):
+        got = self.cache.copy_pages(i32(src), i32(dst))
+        self.same(("copy", src, dst), got, self.o.copy_pages(src, dst))
+
+    def tree(self, B, N):
+        """Accepted paths: ascending nodes behind the root, -1 padded."""
+        acc = self.rng.integers(0, N, B)
+        nodes = np.full((B, N), -1, np.int64)
+        for b in range(B):
+            nodes[b, :acc[b]] = np.sort(self.rng.permutation(np.arange(1, N))[:acc[b]])
+        return acc.tolist(), nodes.tolist()
+
+    def step(self, B, N, release=True):
+        """Reserve for a tree of N nodes, write their slots, commit what is accepted."""
+        base = list(self.o.lens[:B])
+        self.reserve([N] * B)
+        ok = [base[b] + N <= self.o.M * self.o.ps and
+              all(self.o.held(self.o.tables[b][i]) for i in
+                  range(base[b] // self.o.ps, self.o.pages_of(base[b] + N))) for b in range(B)]
+        for b in range(B):  # the forward pass
+            for n in range(N if ok[b] else 0):
+                page, slot = self.o.tables[b][(base[b] + n) // self.o.ps], (base[b] + n) % self.o.ps
+                v = self.rng.integers(-100, 100, self.o.pool[:, 0, 0].shape).astype(self.o.pool.dtype)
+                self.o.pool[:, page, slot] = v
+                for i in range(v.shape[0]):
+                    self.d[i][page, slot] = torch.from_numpy(v[i]).to(device())
+        acc, nodes = self.tree(B, N)
+        self.commit(acc, nodes, release=release)
+
+
+GEOMETRIES = [
+    # planes, pages, page size, heads, dim, dtype, layout, separate, pad
+    (2, 40, 4, 2, 8, torch.int16, "nhd", False, 0),      # 16-byte pieces
+    (3, 40, 1, 1, 16, torch.int16, "nhd", True, 0),      # one slot per page, planes apart
+    (2, 30, 5, 3, 6, torch.int16, "hnd", False, 0),      # 12-byte pieces, heads outside
+    (4, 25, 16, 2, 33, torch.int8, "nhd", False, 0),     # odd bytes
+    (2, 40, 8, 4, 16, torch.int16, "hnd", True, 0),
+    (2, 40, 7, 3, 8, torch.int16, "padded", False, 8),   # gaps between pieces
+    (2, 40, 6, 3, 8, torch.int16, "heads first", False, 0),
+    (1, 30, 64, 1, 128, torch.int16, "nhd", False, 0),
+]
+
+
+@pytest.mark.parametrize("geo", range(len(GEOMETRIES)))
+def test_random_runs_match_the_oracle(geo):
+    planes, P, ps, heads, dim, dtype, layout, separate, pad = GEOMETRIES[geo]
+    rows, M = 6, 9
+    c = Pair(planes, P, ps, heads, dim, rows, M, dtype, layout, separate, pad, seed=geo)
+    r = c.rng
+    for turn in range(14):
+        log(f"cache: geometry {geo} turn {turn}")
+        c.step(rows, int(r.integers(1, 7)), release=bool(r.integers(0, 2)))
+        kind = r.integers(0, 4)
+        if kind == 0:
+            src = int(r.integers(0, rows))
+            dst = [x for x in r.permutation(rows)[:3].tolist() if x != src]
+            c.fork([src] * len(dst), dst)
+        elif kind == 1:
+            n = int(r.integers(1, rows + 1))
+            c.truncate(rows=r.permutation(rows)[:n].tolist(),
+                       new_len=r.integers(-1, M * ps, n).tolist())
+        elif kind == 2:
+            c.reserve(r.integers(0, 3 * ps, rows).tolist())
+        else:
+            perm = r.permutation(P)[:6].tolist()
+            c.copy(perm[:3], perm[3:])
+    c.truncate()
+    assert not any(c.o.ref)
+
+
+def test_many_pages_and_rows():
+    """Free pages in several chunks of counts, rows in several workgroups."""
+    rows, M, P = 300, 40, 9001
+    c = Pair(1, P, 2, 1, 8, rows, M, seed=3)
+    log("cache: many pages")
+    add = c.rng.integers(0, 2 * M + 1, rows)
+    c.reserve(add.tolist())
+    c.commit((add - 1).tolist())  # rows that reserved nothing (-1 accepted) are refused
+    c.truncate(rows=c.rng.permutation(rows)[:200].tolist())
+    c.fork([0] * 50 + list(range(1, 20)), list(range(100, 150)) + list(range(200, 219)))
+    c.reserve(c.rng.integers(0, 2 * M + 20, rows).tolist())
+    c.reserve([2 * M] * rows, base=[0] * rows)  # runs out
+
+
+def test_out_of_pages_in_row_order():
+    c = Pair(1, 5, 2, 1, 8, 4, 6)
+    c.reserve([4, 8, 2, 0])      # 2 of 5, then 4 do not fit, then 1 is behind it
+    c.reserve([4, 6, 2, 0])      # row 0 has its pages; 3 fit exactly; none left
+    c.reserve([13, -1, 0, 0])    # behind max_blocks; negative
+    c.reserve([1, 1, 1, 1], base=[-1, 12, 2147483647, 0])
+    c.reserve([2147483647] * 4, base=[2147483647, 0, 1, 5])
+
+
+def test_copy_on_write():
+    c = Pair(2, 20, 4, 2, 8, 5, 6)
+    c.reserve([7, 0, 0, 0, 0])
+    c.commit([6], nodes=None)
+    c.fork([0, 0, 0], [1, 2, 3])
+    c.reserve([1, 0, 1, 3])      # rows 0, 2, 3 leave the shared last page, row 1 keeps it
+    c.reserve([1, 1, 1, 1])      # nothing is shared there any more
+    c.truncate(new_len=[4, 4, 4, 4])
+    c.reserve([4, 4, 0, 0])      # at a page's border: nothing to carry
+    c.fork([0], [4])
+    c.reserve([0, 0, 0, 0, 8], base=[0, 0, 0, 0, 2])  # a rollback into shared pages
+
+
+def test_commit_refusals_and_identity():
+    c = Pair(2, 30, 3, 1, 8, 8, 6)
+    c.reserve([10] * 8)
+    nodes = [[1, 2, 3, -1, -1], [2, 2, -1, -1, -1], [0, 1, -1, -1, -1], [1, 5, -1, -1, -1],
+             [3, 2, -1, -1, -1], [-5, 1, -1, -1, -1], [4, -1, -1, -1, -1], [2, 4, -1, -1, -1]]
+    c.commit([3, 2, 2, 2, 2, 2, 5, 2], nodes)      # row 6: more accepted than nodes; 3: node 5 of 5
+    c.commit([-1, 0, 4, 17, 18, 1, 1, 1], base=[0, 17, 17, 0, 0, -1, 0, 2])
+    c.commit([2] * 8, [[2, 4, 0]] * 8)             # node 4 of 3
+    c.commit([1] * 8, [[2, 0, 0]] * 8, base=[16] * 8)  # a slot behind the table
+
+
+def test_commit_of_the_widest_tree():
+    """64 nodes: moves in several batches, each row's slots read before they are overwritten."""
+    c = Pair(2, 60, 16, 2, 8, 3, 8)
+    for seed in range(3):
+        c.truncate()
+        c.step(3, 64)
+
+
+def test_pages_named_twice_or_out_of_range():
+    c = Pair(2, 12, 2, 1, 8, 8, 4)
+    c.reserve([5, 3, 1, 0])
+    c.commit([4, 2, 0, 0], release=False)
+    c.fork([0, 0, 1, 8, -1, 1, 0], [1, 3, 3, 2, 2, 8, 5])
+    c.fork([2, 2, 2], [2, 0, 1])
+    c.copy([0, 1, 2, 3, 99, -1, 5], [1, 6, 6, 7, 8, 9, 12])
+    c.copy([0], [0])
+    c.truncate(rows=[0, 0, 9, -1], new_len=[3, 1, 0, 0])
+    c.truncate(rows=[1, 1])
+
+
+def test_foreign_entries_of_a_table_are_no_pages():
+    """Entries outside [0, num_pages) are never followed."""
+    c = Pair(1, 10, 2, 1, 8, 3, 4)
+    bad = [[77, -9, 1 << 30, -1], [0, 10, -1, -1], [-(1 << 31), -1, -1, -1]]
+    c.bt.tables.copy_(i32(bad))
+    c.o.tables = [list(t) for t in bad]
+    c.bt.ref[0] = 1
+    c.o.ref[0] = 1
+    c.bt.lens.copy_(i32([6, 3, 0]))
+    c.o.lens = [6, 3, 0]
+    c.commit([1, 1, 0], [[3, -1, -1, -1]] * 3, base=[0, 0, 0])  # rows without pages are refused
+    c.fork([1], [2])
+    c.reserve([2, 2, 2])
+    c.truncate()
+
+
+def test_copy_between_caches():
+    """Another cache of the same shape, its pages laid out otherwise."""
+    a = Pair(3, 9, 4, 2, 8, 2, 2, layout="nhd", seed=1)
+    b = Pair(3, 20, 4, 2, 8, 2, 2, layout="hnd", seed=2)
+    src, dst = [3, 8, 3, 0, 9, 1], [19, 0, 4, 3, 5, 20]  # a source twice, page 9 / 20 out of range
+    ok = b.cache.copy_pages(i32(src), i32(dst), src_cache=a.cache)
+    assert ok.cpu().tolist() == [1, 1, 1, 1, 0, 0]
+    want = b.o.pool.copy()
+    for s, d in zip(src[:4], dst[:4]):
+        want[:, d] = a.o.pool[:, s]
+    assert np.array_equal(b.pool(), want) and np.array_equal(a.pool(), a.o.pool)
+    other = PageCache(torch.zeros(3, 9, 4, 2, 9, dtype=torch.int16, device=device()), 2, 2)
+    with pytest.raises(SM.SamplerError):
+        b.cache.copy_pages(i32([0]), i32([0]), src_cache=other)
+
+
+def test_more_pairs_than_a_workgroup():
+    c = Pair(1, 3000, 1, 1, 8, 1, 1)
+    perm = c.rng.permutation(3000)
+    src, dst = perm[:1400].tolist(), perm[1400:2800].tolist()
+    dst[1399] = dst[0]
+    c.copy(src, dst)
+
+
+def test_captured_step_replays():
+    """Reserve, commit and a fork in one graph; eager work between the replays."""
+    c = Pair(2, 64, 4, 2, 8, 4, 8)
+    add, acc = i32([5] * 4), i32([0] * 4)
+    nodes = i32([[-1] * 5] * 4)
+    src, dst = i32([0]), i32([3])
+    ok = [torch.zeros(4, dtype=torch.int32, device=device()) for _ in range(3)]
+
+    def step():
+        c.cache.reserve(c.bt, add, ok=ok[0])
+        c.cache.commit(c.bt, acc, nodes=nodes, ok=ok[1])
+        c.cache.fork(c.bt, src, dst, ok=ok[2])
+
+    c.reserve([2] * 4)
+    c.commit([0] * 4, [[-1] * 5] * 4)
+    c.fork([0], [3])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for turn in range(5):
+        a, n = c.tree(4, 5)
+        acc.copy_(i32(a))
+        nodes.copy_(i32(n))
+        torch.cuda.synchronize()
+        graph.replay()
+        want = c.o.reserve([5] * 4), c.o.commit(a, n), c.o.fork([0], [3])
+        torch.cuda.synchronize()
+        for g, w in zip(ok, want):
+            assert g.cpu().tolist()[:len(w)] == w
+        c.same(("replay", turn))
+        c.truncate(new_len=[1, 2, 3, 4])
+
+
+def test_other_stream():
+    c = Pair(2, 32, 4, 2, 8, 4, 6)
+    st = torch.cuda.Stream()
+    add, acc = i32([9] * 4), i32([3] * 4)
+    nodes = i32([[2, 4, 8, -1, -1, -1, -1, -1, -1]] * 4)
+    st.wait_stream(torch.cuda.current_stream())
+    ok = c.cache.reserve(c.bt, add, stream=st)
+    ok2 = c.cache.commit(c.bt, acc, nodes=nodes, stream=st)
+    st.synchronize()
+    assert c.o.reserve([9] * 4) == ok.cpu().tolist()
+    c.same("other stream", ok2, c.o.commit([3] * 4, nodes.cpu().tolist()))
+
+
+def test_refusals():
+    d = device()
+    pool = torch.zeros(2, 8, 4, 2, 8, dtype=torch.int16, device=d)
+    for planes, mb, bl in ((pool[:, :, :, :, ::2], 2, 2), ([pool[0], pool[1, :4]], 2, 2),
+                           ([pool[0], pool[1].float()], 2, 2), (pool[0], 2, 2), (pool[:, :0], 2, 2)):
+        with pytest.raises(ValueError):
+            PageCache(planes, mb, bl)
+    for planes, mb, bl in ((pool, 0, 2), (pool, 2, 0), (pool[:, :, :1].expand(2, 8, 4, 2, 8), 2, 2)):
+        with pytest.raises(SM.SamplerError):
+            PageCache(planes, mb, bl)
+    c = PageCache(pool, 4, 5)
+    t = c.new_tables()
+    v = torch.zeros(4, dtype=torch.int32, device=d)
+    five = torch.zeros(5, dtype=torch.int32, device=d)
+    for bt in (BlockTables(t.tables.long(), t.ref, t.lens), BlockTables(t.tables[:, :4], t.ref, t.lens),
+               BlockTables(t.tables, t.ref[:7], t.lens), BlockTables(t.tables, t.ref, t.lens[:3]),
+               BlockTables(t.tables.t(), t.ref, t.lens), BlockTables(t.tables.cpu(), t.ref, t.lens),
+               BlockTables(torch.zeros(5, 5, dtype=torch.int32, device=d), t.ref, five),
+               BlockTables(t.tables[:1].expand(4, 5), t.ref, t.lens)):
+        with pytest.raises(ValueError):
+            c.reserve(bt, v)
+    for bad in (five, v.long(), v[None], v[::2], v.cpu()):
+        for call in (lambda: c.reserve(t, bad), lambda: c.fork(t, bad, bad),
+                     lambda: c.commit(t, bad), lambda: c.truncate(t, new_len=bad)):
+            with pytest.raises(ValueError):
+                call()
+    for call in (lambda: c.reserve(t, v, lens=v[:3]), lambda: c.fork(t, v, v[:3]),
+                 lambda: c.commit(t, v, nodes=torch.zeros(4, 65, dtype=torch.int32, device=d)),
+                 lambda: c.commit(t, v, nodes=torch.zeros(3, 5, dtype=torch.int32, device=d)),
+                 lambda: c.commit(t, v, base=v.float()), lambda: c.copy_pages(v, v[:3]),
+                 lambda: c.truncate(t, new_len=v, rows=v[:3]), lambda: c.reserve(t, v, ok=v[:3])):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(SM.SamplerError):
+        c.copy_pages(torch.zeros(9, dtype=torch.int32, device=d), torch.zeros(9, dtype=torch.int32, device=d))
+    ct = SM.CBlockTables(t.tables.data_ptr(), 4, 4, t.ref.data_ptr(), t.lens.data_ptr())
+    lib, p = c.lib, SM._ptr
+    bad = SM.SS_ERR_INVALID_ARG
+    assert lib.ss_cache_reserve(c.handle, ctypes.byref(ct), None, p(v), 4, None, None) == bad
+    ct.stride, ct.rows = 5, 0
+    assert lib.ss_cache_truncate(c.handle, ctypes.byref(ct), None, None, 0, None) == bad
+    ct.rows, ct.ref = 4, t.ref.data_ptr() + 2
+    assert lib.ss_cache_fork(c.handle, ctypes.byref(ct), p(v), p(v), 1, None, None) == bad
+    ct.ref = t.ref.data_ptr()
+    r = ctypes.byref(ct)
+    assert lib.ss_cache_reserve(c.handle, r, None, None, 4, None, None) == bad
+    assert lib.ss_cache_reserve(c.handle, r, None, p(v), 5, None, None) == bad
+    assert lib.ss_cache_fork(c.handle, r, None, p(v), 1, None, None) == bad
+    assert lib.ss_cache_commit(c.handle, r, None, p(t.tables), 5, 0, p(v), 4, 1, None, None) == bad
+    assert lib.ss_cache_commit(c.handle, r, None, p(t.tables), 4, 5, p(v), 4, 1, None, None) == bad
+    assert lib.ss_cache_commit(c.handle, r, None, None, 0, 0, None, 4, 1, None, None) == bad
+    assert lib.ss_cache_truncate(c.handle, r, None, None, -1, None) == bad
+    assert lib.ss_cache_reserve(c.handle, r, None, None, 0, None, None) == SM.SS_OK
+    assert t.tables.cpu().eq(-1).all() and not t.ref.any()
