@@ -13,8 +13,8 @@ from dataclasses import dataclass
 
 import torch
 
-from .sampler import (CacheConfig, CBlockTables, _check, _check_block, _check_dev, _check_rows,
-                      _check_vec, _ptr, _require, _stream_on, load_library)
+from .sampler import (SS_OK, CacheConfig, CBlockTables, _check, _check_array, _check_block,
+                      _check_dev, _check_rows, _require, _stream_on, load_library)
 
 
 @dataclass
@@ -79,25 +79,39 @@ class PageCache:
                            torch.zeros(rows, dtype=torch.int32, device=dev))
 
     def _tables(self, t):
-        dev = self.device
-        _check_rows(t.tables, "tables", 1, (torch.int32,), dev)
-        rows, cols = t.tables.shape
-        _require(rows <= self.max_batch and cols >= self.max_blocks,
-                 f"tables must be [1 .. {self.max_batch}, >= {self.max_blocks}]")
-        _require(rows <= 1 or t.tables.stride(0) >= self.max_blocks, "tables rows must not overlap")
-        _check_vec(t.ref, "ref", self.num_pages, torch.int32, dev)
-        _check_vec(t.lens, "lens", rows, torch.int32, dev)
-        stride = t.tables.stride(0) if rows > 1 else cols
-        return CBlockTables(t.tables.data_ptr(), stride, rows, t.ref.data_ptr(), t.lens.data_ptr())
+        """The tables as the ABI takes them, checked by what costs least; the
+        messages are formed on failure only."""
+        dev, tab = self.device, t.tables
+        if not (isinstance(tab, torch.Tensor) and tab.dtype is torch.int32 and
+                tab.get_device() == dev and tab.dim() == 2 and tab.is_contiguous() and
+                0 < tab.shape[0] <= self.max_batch and tab.shape[1] >= self.max_blocks):
+            _check_rows(tab, "tables", 1, (torch.int32,), dev)
+            _require(tab.shape[0] <= self.max_batch and tab.shape[1] >= self.max_blocks,
+                     f"tables must be [1 .. {self.max_batch}, >= {self.max_blocks}]")
+            _require(tab.shape[0] <= 1 or tab.stride(0) >= self.max_blocks,
+                     "tables rows must not overlap")
+        rows, cols = tab.shape
+        return CBlockTables(tab.data_ptr(), tab.stride(0) if rows > 1 else cols, rows,
+                            _check_array(t.ref, "ref", self.num_pages, dev),
+                            _check_array(t.lens, "lens", rows, dev))
+
+    def _count(self, v, name, most):
+        """Entries of a contiguous 1-D int32 array of at most `most`, and its address."""
+        if not (isinstance(v, torch.Tensor) and v.dtype is torch.int32 and
+                v.get_device() == self.device and v.dim() == 1 and v.is_contiguous() and
+                v.shape[0] <= most):
+            _check_dev(v, name, (torch.int32,), self.device)
+            raise ValueError(f"{name} must be a contiguous 1-D array of at most {most} entries")
+        return v.shape[0], v.data_ptr()
 
     def _ok(self, ok, n):
         if ok is None:
             return torch.empty(n, dtype=torch.int32, device=self.planes[0].device)
-        _check_vec(ok, "ok", n, torch.int32, self.device)
+        _check_array(ok, "ok", n, self.device)
         return ok
 
     def _vec(self, v, name, n):
-        _check_block(v, name, (n,), torch.int32, self.device)
+        return _check_block(v, name, (n,), torch.int32, self.device)
 
     def reserve(self, tables: BlockTables, add, lens=None, ok=None, stream=None):
         """Make slots [lens, lens + add) of rows 0 .. B-1 writable (add [B] int32;
@@ -105,30 +119,26 @@ class PageCache:
         shared ones (copy on write). Returns ok [B] int32 (0: not enough pages,
         row unchanged)."""
         ct = self._tables(tables)
-        _check_dev(add, "add", (torch.int32,), self.device)
-        _require(add.dim() == 1 and add.shape[0] <= ct.rows, "add must be [B] with B <= rows")
-        B = add.shape[0]
-        self._vec(add, "add", B)
-        _check_vec(lens, "lens", B, torch.int32, self.device)
+        B, add_ptr = self._count(add, "add", ct.rows)
+        base = _check_array(lens, "lens", B, self.device)
         ok = self._ok(ok, B)
-        _check("ss_cache_reserve", self.lib.ss_cache_reserve(
-            self.handle, ctypes.byref(ct), _ptr(lens), _ptr(add), B, _ptr(ok),
-            _stream_on(stream, self.device)))
+        st = self.lib.ss_cache_reserve(self.handle, ctypes.byref(ct), base, add_ptr, B,
+                                       ok.data_ptr(), _stream_on(stream, self.device))
+        if st != SS_OK:
+            _check("ss_cache_reserve", st)
         return ok
 
     def fork(self, tables: BlockTables, src, dst, ok=None, stream=None):
         """Rows dst become copies of rows src (int32 [n]) that share their pages;
         what dst held is given back. Returns ok [n] int32."""
         ct = self._tables(tables)
-        _check_dev(src, "src", (torch.int32,), self.device)
-        _require(src.dim() == 1 and src.shape[0] <= ct.rows, "src must be [n] with n <= rows")
-        n = src.shape[0]
-        self._vec(src, "src", n)
-        self._vec(dst, "dst", n)
+        n, src_ptr = self._count(src, "src", ct.rows)
+        dst_ptr = self._vec(dst, "dst", n)
         ok = self._ok(ok, n)
-        _check("ss_cache_fork", self.lib.ss_cache_fork(
-            self.handle, ctypes.byref(ct), _ptr(src), _ptr(dst), n, _ptr(ok),
-            _stream_on(stream, self.device)))
+        st = self.lib.ss_cache_fork(self.handle, ctypes.byref(ct), src_ptr, dst_ptr, n,
+                                    ok.data_ptr(), _stream_on(stream, self.device))
+        if st != SS_OK:
+            _check("ss_cache_fork", st)
         return ok
 
     def commit(self, tables: BlockTables, num_accepted, nodes=None, base=None, release=True,
@@ -139,53 +149,49 @@ class PageCache:
         tables.lens becomes base + 1 + num_accepted; release: pages behind it are
         given back. Returns ok [B] int32."""
         ct = self._tables(tables)
-        _check_dev(num_accepted, "num_accepted", (torch.int32,), self.device)
-        _require(num_accepted.dim() == 1 and num_accepted.shape[0] <= ct.rows,
-                 "num_accepted must be [B] with B <= rows")
-        B = num_accepted.shape[0]
-        self._vec(num_accepted, "num_accepted", B)
-        _check_vec(base, "base", B, torch.int32, self.device)
-        stride = N = 0
+        B, acc = self._count(num_accepted, "num_accepted", ct.rows)
+        base = _check_array(base, "base", B, self.device)
+        at, stride, N = None, 0, 0
         if nodes is not None:
             _check_rows(nodes, "nodes", B, (torch.int32,), self.device)
             N = nodes.shape[1]
-            _require(1 <= N <= 64, "nodes must be [B, N] with N in 1 .. 64")
             stride = nodes.stride(0) if B > 1 else N
-            _require(stride >= N, "nodes rows must not overlap")
+            if not 1 <= N <= 64 or stride < N:
+                raise ValueError("nodes must be [B, N] with N in 1 .. 64 and rows that do not overlap")
+            at = nodes.data_ptr()
         ok = self._ok(ok, B)
-        _check("ss_cache_commit", self.lib.ss_cache_commit(
-            self.handle, ctypes.byref(ct), _ptr(base), _ptr(nodes), stride, N, _ptr(num_accepted),
-            B, int(bool(release)), _ptr(ok), _stream_on(stream, self.device)))
+        st = self.lib.ss_cache_commit(self.handle, ctypes.byref(ct), base, at, stride, N, acc, B,
+                                      1 if release else 0, ok.data_ptr(),
+                                      _stream_on(stream, self.device))
+        if st != SS_OK:
+            _check("ss_cache_commit", st)
         return ok
 
     def truncate(self, tables: BlockTables, new_len=None, rows=None, stream=None):
         """Give back the pages of rows (None: 0, 1, ...) behind new_len [n] int32
         (None: all their pages: the requests end)."""
         ct = self._tables(tables)
-        n = ct.rows
-        for name, v in (("rows", rows), ("new_len", new_len)):
-            if v is not None:
-                _check_dev(v, name, (torch.int32,), self.device)
-                _require(v.dim() == 1 and v.shape[0] <= ct.rows, f"{name} must be [n] with n <= rows")
-                n = v.shape[0]
-        for name, v in (("rows", rows), ("new_len", new_len)):
-            if v is not None:
-                self._vec(v, name, n)
-        _check("ss_cache_truncate", self.lib.ss_cache_truncate(
-            self.handle, ctypes.byref(ct), _ptr(rows), _ptr(new_len), n,
-            _stream_on(stream, self.device)))
+        n, at, keep = ct.rows, None, None
+        if rows is not None:
+            n, at = self._count(rows, "rows", ct.rows)
+            if new_len is not None:
+                keep = self._vec(new_len, "new_len", n)
+        elif new_len is not None:
+            n, keep = self._count(new_len, "new_len", ct.rows)
+        st = self.lib.ss_cache_truncate(self.handle, ctypes.byref(ct), at, keep, n,
+                                        _stream_on(stream, self.device))
+        if st != SS_OK:
+            _check("ss_cache_truncate", st)
 
     def copy_pages(self, src, dst, src_cache: PageCache | None = None, ok=None, stream=None):
         """Copy pages src (int32 [n]) of src_cache (None: this cache) to pages dst of
         this cache, all planes. Returns ok [n] int32."""
         other = self if src_cache is None else src_cache
-        _check_dev(src, "src", (torch.int32,), self.device)
-        _require(src.dim() == 1, "src must be [n]")
-        n = src.shape[0]
-        self._vec(src, "src", n)
-        self._vec(dst, "dst", n)
+        n, src_ptr = self._count(src, "src", 65535)
+        dst_ptr = self._vec(dst, "dst", n)
         ok = self._ok(ok, n)
-        _check("ss_cache_copy_pages", self.lib.ss_cache_copy_pages(
-            other.handle, _ptr(src), self.handle, _ptr(dst), n, _ptr(ok),
-            _stream_on(stream, self.device)))
+        st = self.lib.ss_cache_copy_pages(other.handle, src_ptr, self.handle, dst_ptr, n,
+                                          ok.data_ptr(), _stream_on(stream, self.device))
+        if st != SS_OK:
+            _check("ss_cache_copy_pages", st)
         return ok

@@ -3,29 +3,38 @@
 //   y[b, v] = sum_g s[v, g] ( sum_{k in g} (n[v, k] - z[v, g]) x[b, k] )
 //
 // What bounds it: the weight stream (V K / 2 bytes) while the rows are few, and
-// beside it the vector ALU that widens nibbles for the matrix cores.
+// beside it, at 64 rows, the vector ALU that widens nibbles, the matrix cores
+// and the LDS reads of x.
 //
-//  * Widening costs one operation per weight: a nibble shifted into the top of
-//    a bfloat16 mantissa under the exponent of 16 is the number 16 + n exactly,
-//    two at a time (nibbles j and j + 4 of a word share the mask), and no
-//    product is rounded: the matrix cores multiply by 16 + n, and the group's
-//    accumulators start from -(16 + z) sum_k x[b, k] instead of 0. Scales are
-//    applied to the finished group in binary32. (Widening to s (n - z) would
-//    round every weight to 8 bits.)
-//  * v_mfma_f32_16x16x32_bf16, W as the A operand: a wave owns RT tiles of 16
-//    vocabulary rows and NT tiles of 16 batch rows; widened weights are used NT
-//    times. Weights go from memory straight to the registers of the one wave
-//    that uses them: a lane loads 16 bytes (32 weights) of its row at a time,
-//    one chunk ahead.
+//  * Widening costs two operations for two weights: byte j of a word times
+//    2^3 + 2^15 puts its nibbles on the top mantissa bits of two bfloat16, and
+//    under the exponent of 16 they read 16 + n, exactly. (Widening to s (n - z)
+//    would round every weight to 8 bits.) The matrix cores sum (16 + n) x; the
+//    scaled group is added in binary32, and
+//      - sum_g s (16 + z) (sum_{k in g} x)
+//    is a product over groups of its own, four groups per binary32 MFMA. Its sums
+//    of x come from MFMAs against ones, each batch tile's made by one wave and
+//    shared through LDS.
+//  * v_mfma_f32_16x16x32_bf16 with x as the A operand (batch rows) and W as B
+//    (vocabulary rows as columns): a lane's accumulators then belong to the
+//    vocabulary row whose weights it widens, so the scale is one value per lane
+//    and row tile, straight from memory.
+//  * Operands go from memory to LDS by global_load_lds_dwordx4, S - 1 stages of
+//    128 k ahead, so the stream stays in flight without registers. Each stage is
+//    an LDS object of its own: the compiler then orders a read against the
+//    copies into its own stage only, which the explicit wait has seen land. A
+//    wave copies the weights it uses and its share of x. What lies behind K is
+//    copied as zeros of x, so no block is special.
 //  * Any assignment of k to MFMA slots is right as long as both operands share
-//    it. A lane's four words serve four MFMAs; for groups of 128 as they are,
-//    for groups of 64 and 32 after exchanging words between the lanes that hold
-//    the same row (permlane swaps), so that no MFMA crosses a group.
-//  * x is staged in LDS once per workgroup and chunk, in the order in which the
-//    MFMAs read it (each operand read is 1 KB of consecutive LDS), with the
-//    sums over each group.
-//  * 8 waves: RW row blocks by KW splits of K. The splits are added in a fixed
-//    order through LDS.
+//    it. A lane's 16 bytes are 32 weights of one row, its four words serve four
+//    MFMAs: for groups of 128 as they are, for groups of 64 and 32 after
+//    exchanging words between the lanes that hold the same row (permlane
+//    swaps), so that no MFMA crosses a group.
+//  * Four waves: RW row blocks of RT tiles by KW ranges of K, whose sums are
+//    added in a fixed order through LDS.
+#include <type_traits>
+#include <utility>
+
 #include "ss_device.h"
 #include "ss_internal.h"
 
@@ -34,36 +43,32 @@ namespace ss {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef float floatx4u __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint16_t u16x4u __attribute__((ext_vector_type(4), aligned(2)));
 
-constexpr int LQ_NT = 512;
-constexpr int LQ_WAVES = LQ_NT / WAVE;
-constexpr int LQ_KB = 128;      // k per block: one 16-byte load per lane and row tile
-constexpr int LQ_STEP = 4;      // blocks per wave and chunk
+constexpr int LQ_KB = 128;   // k per block: 16 bytes of weights per lane and row tile
 
-// Half-word masks and the exponent of 16 in bfloat16.
-constexpr uint32_t LQ_MASK = 0x00780078u;
-constexpr uint32_t LQ_BASE = 0x41804180u;
+#define LQ_LDS(x) ((__attribute__((address_space(3))) void*)(x))
 
-// Word of eight nibbles -> eight bfloat16 16 + n, in the order 0 4 1 5 2 6 3 7.
-__device__ __forceinline__ bf16x8 lq_widen(uint32_t w) {
-    u32x4 r;
-    r[0] = ((w << 3) & LQ_MASK) | LQ_BASE;
-    r[1] = ((w >> 1) & LQ_MASK) | LQ_BASE;
-    r[2] = ((w >> 5) & LQ_MASK) | LQ_BASE;
-    r[3] = ((w >> 9) & LQ_MASK) | LQ_BASE;
-    return __builtin_bit_cast(bf16x8, r);
-}
+// s_waitcnt with vmcnt n, lgkmcnt 0, expcnt free (gfx9 encoding).
+constexpr int lq_wait(int n) { return (n & 15) | (n >> 4 & 3) << 14 | 0x0070; }
 
-// The same order for eight consecutive bfloat16 of x.
-__device__ __forceinline__ u32x4 lq_order(u32x4 x) {
-    u32x4 r;
-    r[0] = (x[0] & 0xFFFFu) | (x[2] << 16);
-    r[1] = (x[0] >> 16) | (x[2] & 0xFFFF0000u);
-    r[2] = (x[1] & 0xFFFFu) | (x[3] << 16);
-    r[3] = (x[1] >> 16) | (x[3] & 0xFFFF0000u);
-    return r;
-}
+// Word of eight nibbles -> eight bfloat16 16 + n, in order. mask and exponent come
+// in vector registers: one v_and_or_b32 takes them, literals would take two
+// operations.
+struct LqWiden {
+    uint32_t mask, exponent;
+    __device__ __forceinline__ LqWiden() {
+        asm("v_mov_b32 %0, 0x780078" : "=v"(mask));
+        asm("v_mov_b32 %0, 0x41804180" : "=v"(exponent));
+    }
+    __device__ __forceinline__ bf16x8 operator()(uint32_t w) const {
+        u32x4 r;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            r[j] = (__umul24(w >> 8 * j & 0xFFu, 0x8008u) & mask) | exponent;
+        return __builtin_bit_cast(bf16x8, r);
+    }
+};
 
 __device__ __forceinline__ void lq_swap32(uint32_t& a, uint32_t& b) {
     const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
@@ -79,7 +84,7 @@ __device__ __forceinline__ void lq_swap16(uint32_t& a, uint32_t& b) {
 // Exchanges words between the lanes l, l ^ 16, l ^ 32, l ^ 48 (one row) so that
 // MFMA i multiplies words of one group only.
 template <int GROUP>
-__device__ __forceinline__ void lq_regroup(u32x4& w) {
+__device__ __forceinline__ u32x4 lq_regroup(u32x4 w) {
     uint32_t a = w[0], b = w[1], c = w[2], d = w[3];
     if (GROUP <= 64) {
         lq_swap32(a, c);
@@ -89,64 +94,228 @@ __device__ __forceinline__ void lq_regroup(u32x4& w) {
         lq_swap16(a, b);
         lq_swap16(c, d);
     }
-    w[0] = a;
-    w[1] = b;
-    w[2] = c;
-    w[3] = d;
+    return u32x4{a, b, c, d};
 }
 
-// Where the unit e (eight k) of a block lies after lq_regroup: MFMA * 4 + lane quarter.
-template <int GROUP>
-__device__ __forceinline__ int lq_slot(int e) {
-    if (GROUP == 32) return e;                                  // MFMA e / 4, quarter e % 4
-    if (GROUP == 64) {
-        const int t = (e & 7) >> 1;                             // 16 k each: quarters 0 2 1 3
-        return ((e >> 3) * 2 + (e & 1)) * 4 + ((t & 1) << 1 | t >> 1);
+// A stage holds BPS blocks of 128 k. A copy moves rows of 64 BPS bytes, 16 / BPS
+// of them, consecutive lanes a row: memory requests are formed over consecutive
+// lanes. With BPS = 2 a row of weights is a whole 128-byte line, read once and
+// not kept (non-temporal); with BPS = 1 its halves come a stage apart, and the
+// line has to stay in L2 meanwhile. In LDS row r's 16-byte unit j lies at
+// 64 BPS r + 16 (j ^ swizzle(r)): sixteen lanes that read one unit of sixteen
+// rows touch every bank once.
+//
+// x of one 16-row tile and stage is four such tiles of 32 BPS k. MFMA i, quarter
+// q of the wave reads the unit that lq_regroup gives it: unit 4 q + i of the
+// block (128); 8 (i / 2) + i % 2 + 2 q', q' the bits of q reversed (64); 4 i + q
+// (32). The lane's part of that is its offset, the step's part is added, or, in
+// the bits the swizzle uses, goes in by xor.
+template <int BPS>
+__device__ __forceinline__ uint32_t lq_unit(int r, int j) {
+    return r * 64 * BPS + ((j ^ (BPS == 2 ? r >> 1 : r >> 2)) << 4);
+}
+template <int GROUP, int BPS>
+__device__ __forceinline__ uint32_t lq_lane_offset(int lane) {
+    const int q = lane >> 4, r = lane & 15;
+    if (GROUP == 32) return lq_unit<BPS>(r, q);
+    if (BPS == 2) {
+        if (GROUP == 64) return lq_unit<BPS>(r, (q & 1) * 4 + (q >> 1) * 2);
+        return (q >> 1) * 2048 + lq_unit<BPS>(r, (q & 1) * 4);
     }
-    return (e & 3) * 4 + (e >> 2);                              // MFMA e % 4, quarter e / 4
+    if (GROUP == 64) return (q & 1) * 1024 + lq_unit<BPS>(r, q & 2);
+    return q * 1024 + lq_unit<BPS>(r, 0);
+}
+template <int GROUP, int BPS>
+constexpr int lq_step_offset(int i) {
+    return GROUP == 128 ? 0 : GROUP == 64 || BPS == 2 ? (i >> 1) * 2048 : i * 1024;
+}
+template <int GROUP, int BPS>
+constexpr int lq_step_xor(int i) {
+    return GROUP == 128 ? i << 4 : GROUP == 64 ? (i & 1) << 4 : BPS == 2 ? (i & 1) << 6 : 0;
 }
 
-__device__ __forceinline__ float lq_scale(uint16_t bits, int f16) {
+__device__ __forceinline__ u32x4 lq_at(const uint8_t* p) { return *reinterpret_cast<const u32x4*>(p); }
+
+__device__ __forceinline__ floatx4 lq_mfma(bf16x8 x, bf16x8 w, floatx4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w, c, 0, 0, 0);
+}
+
+// The scales (16 bits each) and zero points (4 bits each) of four consecutive
+// groups of one vocabulary row; groups behind the last one have scale 0.
+struct LqRaw {
+    uint64_t s;
+    uint32_t z;
+};
+
+__device__ __forceinline__ LqRaw lq_load(const QuantArgs& a, int v, int g0, int n_groups) {
+    const uint16_t* s = a.scales + (int64_t)v * n_groups + g0;
+    LqRaw r;
+    r.s = 0;
+    if (g0 + 4 <= n_groups) {
+        r.s = __builtin_bit_cast(uint64_t, *reinterpret_cast<const u16x4u*>(s));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (g0 + i < n_groups) r.s |= (uint64_t)s[i] << 16 * i;
+    }
+    r.z = 0x8888u;
+    if (a.zeros) {
+        const uint8_t* z = a.zeros + (int64_t)v * ((n_groups + 1) / 2) + g0 / 2;
+        r.z = g0 < n_groups ? z[0] : 0u;
+        if (g0 + 2 < n_groups) r.z |= (uint32_t)z[1] << 8;
+    }
+    return r;
+}
+
+__device__ __forceinline__ float lq_scale(uint16_t bits, bool f16) {
     return f16 ? (float)__builtin_bit_cast(_Float16, bits) : __uint_as_float((uint32_t)bits << 16);
 }
 
-template <int GROUP, int NT, int RT, int KW>
-__global__ __launch_bounds__(LQ_NT) void k_lmhead_quant(QuantArgs a) {
-    constexpr int RW = LQ_WAVES / KW;
+// The binary32 scales of four groups, and - s (16 + z) of the group that this
+// lane's quarter contributes to the product of the sums.
+struct LqScales {
+    float s[4];
+    float c;
+};
+
+__device__ __forceinline__ LqScales lq_convert(const LqRaw& r, bool f16, int quarter) {
+    LqScales o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o.s[i] = lq_scale((uint16_t)(r.s >> 16 * i), f16);
+    const float s = quarter & 2 ? (quarter & 1 ? o.s[3] : o.s[2]) : (quarter & 1 ? o.s[1] : o.s[0]);
+    o.c = -s * (16.f + (float)(r.z >> 4 * quarter & 15u));
+    return o;
+}
+
+template <class F, int... I>
+__device__ __forceinline__ void lq_each(F& f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+
+__device__ const u32x4 lq_zero = {0u, 0u, 0u, 0u};
+
+template <int GROUP, int NT, int RT, int KW, int WAVES, int BPS, int S>
+__global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
+    static_assert(S >= 2 && S <= 4, "stages");
+    constexpr int RW = WAVES / KW;
     constexpr int ROWS = RW * RT * 16;           // vocabulary rows per workgroup
-    constexpr int CB = LQ_STEP * KW;             // blocks per chunk
     constexpr int GPB = LQ_KB / GROUP;           // groups per block
-    constexpr int MPG = 4 / GPB;                 // MFMAs per group
-    __shared__ __attribute__((aligned(16))) u32x4 s_x[CB * 4 * NT * WAVE];
-    __shared__ float s_sum[CB * GPB * NT * 16];
-    __shared__ __attribute__((aligned(16))) float s_scale[CB * GPB * ROWS];
-    __shared__ __attribute__((aligned(16))) float s_zero[CB * GPB * ROWS];
+    constexpr int PER = 4 / GPB;                 // MFMAs per group
+    constexpr int GPS = GPB * BPS;               // groups per stage
+    constexpr int SET = GPS < 4 ? 4 / GPS : 1;   // stages per set of four groups
+    constexpr int SPS = GPS > 4 ? GPS / 4 : 1;   // sets per stage
+    constexpr int XT = 4096 * BPS;               // bytes of a tile of x, of a tile of weights
+    constexpr int WT_ = 1024 * BPS;
+    constexpr int XB = KW * NT * XT;             // bytes of x, of weights per stage
+    constexpr int WB = WAVES * RT * WT_;
+    constexpr int XC = NT * KW * 4 * BPS / WAVES;  // copies of x per wave and stage
+    constexpr int COPIES = RT * BPS + XC;
+    __shared__ __attribute__((aligned(1024))) uint8_t b0[XB + WB];
+    __shared__ __attribute__((aligned(1024))) uint8_t b1[XB + WB];
+    __shared__ __attribute__((aligned(1024))) uint8_t b2[S > 2 ? XB + WB : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t b3[S > 3 ? XB + WB : 16];
+    __shared__ float s_sum[2 * SPS][KW][4][NT * 16];  // sums of x over a set's groups
     const int tid = threadIdx.x;
     const int lane = tid & (WAVE - 1);
-    const int wave = tid / WAVE;
+    const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
     const int rw = wave % RW, kw = wave / RW;
     const int r16 = lane & 15, quarter = lane >> 4;
     const int K = a.K, V = a.V;
     const int row0 = blockIdx.x * ROWS + rw * RT * 16;
-    const int nb = (K + LQ_KB - 1) / LQ_KB;
     const int n_groups = (K + GROUP - 1) / GROUP;
+    // stages of a range: whole sets where there are several ranges
+    const int all = (K + LQ_KB * BPS - 1) / (LQ_KB * BPS);
+    const int stages = KW == 1 ? all : ((all + KW - 1) / KW + SET - 1) / SET * SET;
+    const int first_stage = kw * stages;
+    // Each workgroup starts at a set of its own, so that the rows that are read
+    // at the same time are read at different places: rows a power of two apart
+    // would otherwise meet in the same memory channels. A last, partial set
+    // stays last.
+    const int whole_sets = (KW == 1 ? all : stages) / SET;
+    const int turn = (int)((blockIdx.x * 2654435761u >> 8) % (unsigned)max(whole_sets, 1));
+    auto place = [&](int j) {
+        int set = j / SET;
+        if (set < whole_sets) {
+            set += turn;
+            set = set >= whole_sets ? set - whole_sets : set;
+        }
+        return set * SET + j % SET;
+    };
+    // Each wave takes the tiles of x in an order of its own: the first is the one
+    // whose sums it makes.
+    auto tile_of = [&](int n) { return (n + rw) % NT; };
+    const bool f16 = a.scale_f16 != 0;
+    const LqWiden widen;
+    const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
 
-    const uint8_t* wrow[RT];
+    // This lane's place in a copy, as an offset from an address that is the same
+    // for the wave: a stage's copies then cost the vector ALU nothing.
+    constexpr int LPR = 4 * BPS, RPC = 16 / BPS;  // lanes per row, rows per copy
+    auto unit_of = [&](int row) { return (lane % LPR) ^ (BPS == 2 ? row >> 1 : row >> 2); };
+    const uint8_t* wbase[RT];
+    uint32_t woff[RT][BPS];
 #pragma unroll
-    for (int t = 0; t < RT; ++t)
-        wrow[t] = a.qweight + (int64_t)min(row0 + t * 16 + r16, V - 1) * (K / 2) + quarter * 16;
-    // block j of this wave's share of the chunk that starts at block c0
-    auto load_w = [&](int c0, u32x4 w[RT][LQ_STEP]) {
+    for (int t = 0; t < RT; ++t) {
+        const int first = min(row0 + t * 16, V - 1);
+        wbase[t] = a.qweight + (int64_t)first * (K / 2);
 #pragma unroll
-        for (int t = 0; t < RT; ++t)
+        for (int c = 0; c < BPS; ++c) {
+            const int row = c * RPC + lane / LPR;
+            woff[t][c] = (uint32_t)(min(row0 + t * 16 + row, V - 1) - first) * (K / 2) + unit_of(row) * 16;
+        }
+    }
+    // x: copy u of the stage is rows (u % BPS) RPC .. of segment (u / BPS) % 4 of
+    // tile u / (4 BPS) % NT of range u / (4 BPS NT); a wave's XC copies follow
+    // each other and stay within one tile.
+    static_assert(XC * WAVES == NT * KW * 4 * BPS && 4 * BPS % XC == 0, "copies of x");
+    const int xu = wave * XC;
+    const int xtile = xu / (4 * BPS) % NT, xrange = xu / (4 * BPS * NT);
+    const uint8_t* xbase = reinterpret_cast<const uint8_t*>(a.hidden);
+    uint32_t xoff[BPS];
 #pragma unroll
-            for (int j = 0; j < LQ_STEP; ++j) {
-                const int kb = c0 + kw * LQ_STEP + j;
-                u32x4 v = {0u, 0u, 0u, 0u};
-                if (kb * LQ_KB + quarter * 32 < K)
-                    v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wrow[t] + kb * (LQ_KB / 2)));
-                w[t][j] = v;
+    for (int c = 0; c < BPS; ++c) {
+        const int row = c * RPC + lane / LPR;
+        xoff[c] = (uint32_t)min(xtile * 16 + row, a.B - 1) * (uint32_t)K * 2 + unit_of(row) * 16;
+    }
+    // Copies of a stage: always COPIES of them, from addresses kept in bounds.
+    auto copy = [&](uint8_t* buf, int j) {
+        uint8_t* ws = buf + XB + wave * RT * WT_;
+        const int at = place(j);
+        const int kb = (first_stage + at) * BPS;
+        if ((kb + BPS) * LQ_KB <= K) {
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int c = 0; c < BPS; ++c)
+                    __builtin_amdgcn_global_load_lds(
+                        (const void*)(wbase[t] + (int64_t)kb * (LQ_KB / 2) + woff[t][c]),
+                        LQ_LDS(ws + t * WT_ + c * 1024), 16, 0, BPS == 2 ? 2 : 0);
+        } else {
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int c = 0; c < BPS; ++c) {
+                    const int64_t k = (int64_t)kb * (LQ_KB / 2) + unit_of(c * RPC + lane / LPR) * 16;
+                    const int64_t back = k > K / 2 - 16 ? k - (K / 2 - 16) : 0;
+                    __builtin_amdgcn_global_load_lds(
+                        (const void*)(wbase[t] + (int64_t)kb * (LQ_KB / 2) + woff[t][c] - back),
+                        LQ_LDS(ws + t * WT_ + c * 1024), 16, 0, 0);
+                }
+        }
+        const int k0 = (xrange * stages + at) * BPS * LQ_KB;
+        uint8_t* xs = buf + xu * 1024;
+#pragma unroll
+        for (int i = 0; i < XC; ++i) {
+            const int u = xu % (4 * BPS) + i;
+            const int c = XC % BPS == 0 ? i % BPS : u % BPS;  // known ahead where a wave has several
+            const uint32_t off = BPS == 2 && c ? xoff[BPS - 1] : xoff[0];
+            const uint8_t* src = xbase + ((int64_t)k0 + u / BPS * 32 * BPS) * 2 + off;
+            if (k0 + BPS * LQ_KB > K) {
+                const int k = k0 + u / BPS * 32 * BPS + unit_of(c * RPC + lane / LPR) * 8;
+                if (k >= K) src = reinterpret_cast<const uint8_t*>(&lq_zero);
             }
+            __builtin_amdgcn_global_load_lds((const void*)src, LQ_LDS(xs + i * 1024), 16, 0, 0);
+        }
     };
 
     floatx4 out[RT][NT];
@@ -154,107 +323,138 @@ __global__ __launch_bounds__(LQ_NT) void k_lmhead_quant(QuantArgs a) {
     for (int t = 0; t < RT; ++t)
 #pragma unroll
         for (int n = 0; n < NT; ++n) out[t][n] = floatx4{0.f, 0.f, 0.f, 0.f};
+    for (int i = tid; i < 2 * SPS * KW * 4 * NT * 16; i += WAVES * WAVE) (&s_sum[0][0][0][0])[i] = 0.f;
 
-    u32x4 w[RT][LQ_STEP];
-    load_w(0, w);
-    for (int c0 = 0; c0 < nb; c0 += CB) {
-        __syncthreads();
-        // x: a thread takes 32 k of one batch row (a wave: 16 rows, one block)
-        for (int i = wave; i < CB * NT; i += LQ_WAVES) {
-            const int kb = i / NT, nt = i % NT;
-            const int b = nt * 16 + r16;
-            const int k0 = (c0 + kb) * LQ_KB + quarter * 32;
-            u32x4 v[4];
-            const bool on = b < a.B && k0 < K;
+    LqRaw raw[SPS][RT], next[SPS][RT];
+    LqScales sc[RT];
+    float c_now[SPS][RT], c_before[SPS][RT];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                v[e] = on ? *reinterpret_cast<const u32x4*>(a.hidden + (int64_t)b * K + k0 + e * 8)
-                          : u32x4{0u, 0u, 0u, 0u};
-            float s = 0.f;
+    for (int h = 0; h < SPS; ++h)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+        for (int t = 0; t < RT; ++t) c_now[h][t] = 0.f;
+    auto load_scales = [&](int j) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    s += __uint_as_float(v[e][q] << 16) + __uint_as_float(v[e][q] & 0xFFFF0000u);
-                const int slot = lq_slot<GROUP>(quarter * 4 + e);
-                s_x[((kb * 4 + (slot >> 2)) * NT + nt) * WAVE + (slot & 3) * 16 + r16] = lq_order(v[e]);
-            }
-            if (GROUP >= 64) s += __shfl_xor(s, 16);
-            if (GROUP >= 128) s += __shfl_xor(s, 32);
-            if ((quarter & (GROUP / 32 - 1)) == 0)
-                s_sum[((kb * GPB + quarter / (GROUP / 32)) * NT + nt) * 16 + r16] = s;
+        for (int h = 0; h < SPS; ++h)
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+                next[h][t] = lq_load(a, min(row0 + t * 16 + r16, V - 1),
+                                     (first_stage + place(j)) * GPS + h * 4, n_groups);
+    };
+    // - s (16 + z) times the sums of x, of the sets before the one that begins at stage j
+    auto add_sums = [&](int j, const float (&c)[SPS][RT]) {
+#pragma unroll
+        for (int h = 0; h < SPS; ++h) {
+            const int slot = (SPS == 2 ? (j + 1) % 2 * 2 : (j / SET + 1) % 2) + h;
+            float x[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) x[n] = s_sum[slot][kw][quarter][tile_of(n) * 16 + r16];
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    out[t][n] = __builtin_amdgcn_mfma_f32_16x16x4f32(x[n], c[h][t], out[t][n], 0, 0, 0);
         }
-        // scales and zero points of the workgroup's rows, the chunk's groups
-        for (int i = tid; i < ROWS * CB * GPB; i += LQ_NT) {
-            const int g = i % (CB * GPB), r = i / (CB * GPB);
-            const int gg = c0 * GPB + g;
-            const int v = min((int)blockIdx.x * ROWS + r, V - 1);
-            float s = 0.f, z = 8.f;
-            if (gg < n_groups) {
-                s = lq_scale(a.scales[(int64_t)v * n_groups + gg], a.scale_f16);
-                if (a.zeros)
-                    z = (float)(a.zeros[(int64_t)v * ((n_groups + 1) / 2) + (gg >> 1)] >> (gg & 1) * 4 & 15);
+    };
+
+    // block h of a stage; g0: its first group's place in its set, slot: the set's sums
+    auto block = [&](const uint8_t* buf, int slot, auto hc, auto gc) {
+        constexpr int h = decltype(hc)::value, g0 = decltype(gc)::value;
+        const uint32_t xs = kw * NT * XT + h * 4096 + lq_lane_offset<GROUP, BPS>(lane);
+        const uint32_t ws = XB + wave * RT * WT_ + (lq_unit<BPS>(r16, quarter) ^ (h << 6));
+        u32x4 w[RT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) w[t] = lq_at(buf + ws + t * WT_);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) w[t] = lq_regroup<GROUP>(w[t]);
+        const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
+        floatx4 acc[RT][NT], sum = zero;
+        // x of the next MFMA step is read while this one's is multiplied
+        bf16x8 now[NT], then[NT];
+        auto read_x = [&](int i, bf16x8 (&x)[NT]) {
+            const uint8_t* at = buf + (xs ^ lq_step_xor<GROUP, BPS>(i)) + lq_step_offset<GROUP, BPS>(i);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) x[n] = __builtin_bit_cast(bf16x8, lq_at(at + tile_of(n) * XT));
+        };
+        read_x(0, then);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) now[n] = then[n];
+            if (i < 3) read_x(i + 1, then);
+            __builtin_amdgcn_sched_barrier(0);
+            const bool first = i % PER == 0;
+            sum = lq_mfma(ones, now[0], first ? zero : sum);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                const bf16x8 wv = widen(w[t][i]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) acc[t][n] = lq_mfma(now[n], wv, first ? zero : acc[t][n]);
             }
-            s_scale[g * ROWS + r] = s;
-            s_zero[g * ROWS + r] = -(16.f + z);
-        }
-        __syncthreads();
-        u32x4 next[RT][LQ_STEP];
-        load_w(c0 + CB, next);
-#pragma unroll
-        for (int j = 0; j < LQ_STEP; ++j) {
-            const int kb = kw * LQ_STEP + j;
-#pragma unroll
-            for (int t = 0; t < RT; ++t) lq_regroup<GROUP>(w[t][j]);
-#pragma unroll
-            for (int g = 0; g < GPB; ++g) {
-                floatx4 acc[RT][NT], sc[RT];
-                float sum[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) sum[n] = s_sum[((kb * GPB + g) * NT + n) * 16 + r16];
-#pragma unroll
-                for (int t = 0; t < RT; ++t) {
-                    const int at = (kb * GPB + g) * ROWS + (rw * RT + t) * 16 + quarter * 4;
-                    const floatx4 z = *reinterpret_cast<const floatx4*>(&s_zero[at]);
-                    sc[t] = *reinterpret_cast<const floatx4*>(&s_scale[at]);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) acc[t][n][q] = z[q] * sum[n];
-                }
-#pragma unroll
-                for (int m = 0; m < MPG; ++m) {
-                    const int i = g * MPG + m;
-                    bf16x8 x[NT];
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        x[n] = __builtin_bit_cast(bf16x8, s_x[((kb * 4 + i) * NT + n) * WAVE + lane]);
-#pragma unroll
-                    for (int t = 0; t < RT; ++t) {
-                        const bf16x8 wv = lq_widen(w[t][j][i]);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            acc[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, x[n], acc[t][n], 0, 0, 0);
-                    }
-                }
+            if (i % PER == PER - 1) {
+                const int g = g0 + i / PER;
 #pragma unroll
                 for (int t = 0; t < RT; ++t)
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            out[t][n][q] = __builtin_fmaf(sc[t][q], acc[t][n][q], out[t][n][q]);
+                            out[t][n][q] = __builtin_fmaf(sc[t].s[g], acc[t][n][q], out[t][n][q]);
+                // every row of the product with ones is the sum of batch row r16
+                if (rw < NT && quarter == 0) s_sum[slot][kw][g][tile_of(0) * 16 + r16] = sum[0];
             }
         }
-#pragma unroll
-        for (int t = 0; t < RT; ++t)
-#pragma unroll
-            for (int j = 0; j < LQ_STEP; ++j) w[t][j] = next[t][j];
-    }
+    };
 
-    if (KW > 1) {  // the splits of K, added in order
-        floatx4* s_red = reinterpret_cast<floatx4*>(s_x);
-        static_assert(KW == 1 || (KW - 1) * RW * RT <= CB * 4, "the splits' sums fit the x stage");
+    load_scales(0);
+    copy(b0, 0);
+    if (S > 2 && 1 < stages) copy(b1, 1);
+    if (S > 3 && 2 < stages) copy(b2, 2);
+    constexpr int U = S == 3 ? 3 * SET : S > SET ? S : SET;  // a multiple of both
+    for (int j0 = 0; j0 < stages; j0 += U) {
+        auto stage = [&](auto uc) {
+            constexpr int u = decltype(uc)::value;
+            const int j = j0 + u;
+            if (j >= stages) return;
+            // this stage has landed for every wave, and the one before has been read
+            if (j + S - 1 <= stages) __builtin_amdgcn_s_waitcnt(lq_wait((S - 2) * COPIES));
+            else __builtin_amdgcn_s_waitcnt(lq_wait(0));
+            __builtin_amdgcn_s_barrier();
+            uint8_t* const bufs[4] = {b0, b1, b2, b3};
+            if (u % SET == 0) {
+#pragma unroll
+                for (int h = 0; h < SPS; ++h)
+#pragma unroll
+                    for (int t = 0; t < RT; ++t) {
+                        raw[h][t] = next[h][t];
+                        c_before[h][t] = c_now[h][t];
+                    }
+                if (j + SET < stages) load_scales(j + SET);
+            }
+            if (j + S - 1 < stages) copy(bufs[(u + S - 1) % S], j + S - 1);
+            const int slot = SPS == 2 ? j % 2 * 2 : j / SET % 2;
+            auto one = [&](auto hc) {
+                constexpr int h = decltype(hc)::value;
+                constexpr int g = (u % SET * GPS + h * GPB) % 4;  // place of its first group
+                if constexpr (g == 0) {
+#pragma unroll
+                    for (int t = 0; t < RT; ++t) {
+                        sc[t] = lq_convert(raw[h % SPS][t], f16, quarter);
+                        c_now[h % SPS][t] = sc[t].c;
+                    }
+                }
+                block(bufs[u % S], slot + h % SPS, hc, std::integral_constant<int, g>{});
+            };
+            lq_each(one, std::make_integer_sequence<int, BPS>{});
+            if (u % SET == 0 && j > 0) add_sums(j, c_before);
+        };
+        lq_each(stage, std::make_integer_sequence<int, U>{});
+    }
+    __syncthreads();
+    add_sums((stages + SET - 1) / SET * SET, c_now);
+
+    if constexpr (KW > 1) {  // the ranges of K, added in order
+        static_assert((KW - 1) * RW * RT * NT * 1024 <= XB + WB, "the ranges' sums fit a stage");
+        floatx4* s_red = reinterpret_cast<floatx4*>(b0);
         __syncthreads();
         if (kw > 0) {
 #pragma unroll
@@ -273,43 +473,45 @@ __global__ __launch_bounds__(LQ_NT) void k_lmhead_quant(QuantArgs a) {
                 for (int n = 0; n < NT; ++n)
                     out[t][n] += s_red[((((k - 1) * RW + rw) * RT + t) * NT + n) * WAVE + lane];
     }
-    // a lane holds four consecutive vocabulary entries of one batch row
+    // a lane holds four batch rows of one vocabulary entry
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int b = n * 16 + r16;
-        if (b >= a.B) continue;
+    for (int t = 0; t < RT; ++t) {
+        const int v = row0 + t * 16 + r16;
+        if (v >= V) continue;
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            const int v = row0 + t * 16 + quarter * 4;
-            if (v >= V) continue;
-            const int64_t at = (int64_t)b * a.out_stride + v;
-            if (a.out_bf16) {
-                __bf16* o = static_cast<__bf16*>(a.out) + at;
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (v + q < V) o[q] = (__bf16)out[t][n][q];  // rounded once, to nearest even
-            } else {
-                float* o = static_cast<float*>(a.out) + at;
-                if (v + 4 <= V) *reinterpret_cast<floatx4u*>(o) = out[t][n];
-                else
-                    for (int q = 0; q < 4; ++q)
-                        if (v + q < V) o[q] = out[t][n][q];
+            for (int q = 0; q < 4; ++q) {
+                const int b = tile_of(n) * 16 + quarter * 4 + q;
+                if (b >= a.B) continue;
+                const int64_t at = (int64_t)b * a.out_stride + v;
+                if (a.out_bf16) static_cast<__bf16*>(a.out)[at] = (__bf16)out[t][n][q];  // rounded once
+                else static_cast<float*>(a.out)[at] = out[t][n][q];
             }
-        }
     }
 }
 
-template <int GROUP, int NT, int RT, int KW>
+template <int GROUP, int NT, int RT, int KW, int WAVES, int BPS, int S>
 static void launch_quant_t(const QuantArgs& a, hipStream_t st, const LaunchEvents& le) {
-    constexpr int rows = LQ_WAVES / KW * RT * 16;
-    launch_k(le, 0, k_lmhead_quant<GROUP, NT, RT, KW>, dim3((a.V + rows - 1) / rows), dim3(LQ_NT), st, a);
+    constexpr int rows = WAVES / KW * RT * 16;
+    launch_k(le, 0, k_lmhead_quant<GROUP, NT, RT, KW, WAVES, BPS, S>, dim3((a.V + rows - 1) / rows),
+             dim3(WAVES * WAVE), st, a);
 }
 
 template <int GROUP>
 static void launch_quant_g(const QuantArgs& a, hipStream_t st, const LaunchEvents& le) {
-    if (a.B <= 16) launch_quant_t<GROUP, 1, 2, 2>(a, st, le);
-    else if (a.B <= 32) launch_quant_t<GROUP, 2, 2, 2>(a, st, le);
-    else launch_quant_t<GROUP, 4, 2, 1>(a, st, le);
+    if (a.B <= 16) {
+        // 64 rows a workgroup; where those are fewer than two a CU, twice the
+        // waves, half of K each
+        if (a.V <= 32768) launch_quant_t<GROUP, 1, 1, 2, 8, 2, 2>(a, st, le);
+        else launch_quant_t<GROUP, 1, 1, 1, 4, 2, 2>(a, st, le);
+    } else if (a.B <= 32) {
+        launch_quant_t<GROUP, 2, 2, 1, 8, 2, 2>(a, st, le);
+    } else if (a.V <= 65536) {
+        launch_quant_t<GROUP, 4, 2, 1, 4, 1, 2>(a, st, le);
+    } else {
+        launch_quant_t<GROUP, 4, 2, 1, 8, 1, 3>(a, st, le);
+    }
 }
 
 hipError_t launch_quant(const QuantArgs& a, hipStream_t st, const LaunchEvents& le) {

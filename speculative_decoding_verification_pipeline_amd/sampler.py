@@ -171,8 +171,7 @@ def _stream(stream):
 
 def _stream_on(stream, device):
     """The given stream, or the current one of a device that need not be current."""
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return ctypes.c_void_p(s.cuda_stream)
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
 
 
 def _require(cond, msg):
@@ -206,20 +205,45 @@ _PROB_DTYPES = {torch.float32: SS_F32, torch.bfloat16: SS_BF16, torch.float16: S
 
 
 def _check_block(t, name, shape, dtype, device):
-    """A contiguous array of exactly this shape."""
-    _check_dev(t, name, (dtype,), device)
-    _require(tuple(t.shape) == shape and t.is_contiguous(),
-             f"{name} must be a contiguous {list(shape)} array of {dtype}")
+    """A contiguous array of exactly this shape; returns its address. A call that
+    takes microseconds is checked by what costs least, the message formed on
+    failure only."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and
+            t.get_device() == device and t.is_contiguous()):
+        _check_dev(t, name, (dtype,), device)
+        raise ValueError(f"{name} must be a contiguous {list(shape)} array of {dtype}")
+    return t.data_ptr()
+
+
+def _check_array(t, name, n, device, dtype=torch.int32):
+    """A 1-D array of at least n entries with unit stride; returns its address
+    (None for None)."""
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and
+            t.dim() == 1 and t.shape[0] >= n and t.is_contiguous()):
+        _check_vec(t, name, n, dtype, device)  # a longer strided array of one entry passes
+    return t.data_ptr()
+
+
+def _check_rank3(t, name, shape, dtype, device):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and
+            t.shape == shape):
+        _check_dev(t, name, (dtype,), device)
+        raise ValueError(f"{name} must be {list(shape)}")
 
 
 def _row_stride(t, name):
     """The one stride between the rows of a [B, R, V] array (row b * R + r)."""
     B, R, V = t.shape
-    _require(V <= 1 or t.stride(2) == 1, f"{name} must have unit stride along V")
+    if t.is_contiguous():
+        return V
+    if V > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} must have unit stride along V")
     stride = t.stride(1) if R > 1 else t.stride(0) if B > 1 else V
-    _require((B <= 1 or R == 0 or t.stride(0) == R * stride) and stride >= V,
-             f"{name} rows must be evenly spaced and must not overlap")
-    return int(stride)
+    if not ((B <= 1 or R == 0 or t.stride(0) == R * stride) and stride >= V):
+        raise ValueError(f"{name} rows must be evenly spaced and must not overlap")
+    return stride
 
 
 @dataclass
@@ -563,29 +587,33 @@ class Sampler:
         seq_tokens / seq_len as in spec_verify. Returns (tokens [B, G+1],
         num_accepted [B])."""
         dev = self.device
-        _check_dev(target_probs, "target_probs", tuple(_PROB_DTYPES), dev)
-        _require(target_probs.dim() == 3 and target_probs.shape[1] >= 1,
-                 "target_probs must be [B, G+1, V]")
+        dtype = getattr(target_probs, "dtype", None)
+        code = _PROB_DTYPES.get(dtype)
+        if code is None or target_probs.get_device() != dev:
+            _check_dev(target_probs, "target_probs", tuple(_PROB_DTYPES), dev)
+        if target_probs.dim() != 3 or target_probs.shape[1] < 1:
+            raise ValueError("target_probs must be [B, G+1, V]")
         B, G1, V = target_probs.shape
         G = G1 - 1
-        _require(V == self.vocab_size, f"target_probs have {V} columns, the sampler {self.vocab_size}")
+        if V != self.vocab_size:
+            raise ValueError(f"target_probs have {V} columns, the sampler {self.vocab_size}")
         tstride = _row_stride(target_probs, "target_probs")
-        dstride = 0
+        dptr, dstride = None, 0
         if draft_probs is not None:
-            _check_dev(draft_probs, "draft_probs", (target_probs.dtype,), dev)
-            _require(tuple(draft_probs.shape) == (B, G, V), "draft_probs must be [B, G, V]")
+            _check_rank3(draft_probs, "draft_probs", (B, G, V), dtype, dev)
             dstride = _row_stride(draft_probs, "draft_probs")
-        _check_block(draft_tokens, "draft_tokens", (B, G), torch.int32, dev)
-        _check_block(uniforms, "uniforms", (B, G1), torch.float32, dev)
-        _check_vec(draft_len, "draft_len", B, torch.int32, dev)
+            dptr = draft_probs.data_ptr()
+        tokens = _check_block(draft_tokens, "draft_tokens", (B, G), torch.int32, dev)
+        u = _check_block(uniforms, "uniforms", (B, G1), torch.float32, dev)
+        n = _check_array(draft_len, "draft_len", B, dev)
         if out_tokens is None:
-            out_tokens = torch.empty(B, G1, dtype=torch.int32, device=target_probs.device)
+            out_tokens = torch.empty((B, G1), dtype=torch.int32, device=target_probs.device)
         else:
             _check_block(out_tokens, "out_tokens", (B, G1), torch.int32, dev)
         if out_num_accepted is None:
             out_num_accepted = torch.empty(B, dtype=torch.int32, device=target_probs.device)
         else:
-            _check_vec(out_num_accepted, "out_num_accepted", B, torch.int32, dev)
+            _check_array(out_num_accepted, "out_num_accepted", B, dev)
         seq = None
         if seq_tokens is not None or seq_len is not None:
             _require(seq_tokens is not None and seq_len is not None,
@@ -597,11 +625,11 @@ class Sampler:
             seq = CSequences(_ptr(seq_tokens), int(seq_tokens.stride(0)) if B > 1 else
                              int(seq_tokens.shape[1]), int(seq_tokens.shape[1]), _ptr(seq_len))
         st = self.lib.ss_spec_verify_probs(
-            self.handle, _ptr(target_probs), _PROB_DTYPES[target_probs.dtype], tstride,
-            _ptr(draft_probs), dstride, _ptr(draft_tokens), _ptr(draft_len), _ptr(uniforms), B, G,
-            _ptr(out_tokens), _ptr(out_num_accepted),
+            self.handle, target_probs.data_ptr(), code, tstride, dptr, dstride, tokens, n, u, B, G,
+            out_tokens.data_ptr(), out_num_accepted.data_ptr(),
             ctypes.byref(seq) if seq is not None else None, _stream_on(stream, dev))
-        _check("ss_spec_verify_probs", st)
+        if st != SS_OK:
+            _check("ss_spec_verify_probs", st)
         return out_tokens, out_num_accepted
 
     def lmhead_quant_logits(self, hidden, qweight, scales, group, zeros=None, out=None,
@@ -612,30 +640,39 @@ class Sampler:
         out: [B, V] float32 or bfloat16 with unit column stride, else one of
         out_dtype is made."""
         dev, V, K = self.device, self.vocab_size, self.hidden_size
-        _check_dev(hidden, "hidden", (torch.bfloat16, torch.int16), dev)
-        _require(hidden.dim() == 2 and hidden.is_contiguous(), "hidden must be a contiguous [B, K] array")
+        if not (isinstance(hidden, torch.Tensor) and hidden.dtype is torch.bfloat16 and
+                hidden.get_device() == dev):
+            _check_dev(hidden, "hidden", (torch.bfloat16, torch.int16), dev)
+        if hidden.dim() != 2 or not hidden.is_contiguous():
+            raise ValueError("hidden must be a contiguous [B, K] array")
         B = hidden.shape[0]
-        _require(hidden.shape[1] == K, f"hidden has K = {hidden.shape[1]}, the sampler {K}")
-        _require(isinstance(group, int) and group in (32, 64, 128), "group must be 32, 64 or 128")
+        if hidden.shape[1] != K:
+            raise ValueError(f"hidden has K = {hidden.shape[1]}, the sampler {K}")
+        if group not in (32, 64, 128):
+            raise ValueError("group must be 32, 64 or 128")
         groups = -(-K // group)
-        _check_block(qweight, "qweight", (V, K // 2), torch.uint8, dev)
-        _check_dev(scales, "scales", (torch.float16, torch.bfloat16), dev)
-        _check_block(scales, "scales", (V, groups), scales.dtype, dev)
+        q = _check_block(qweight, "qweight", (V, K // 2), torch.uint8, dev)
+        half = getattr(scales, "dtype", None) is torch.float16
+        s = _check_block(scales, "scales", (V, groups), torch.float16 if half else torch.bfloat16, dev)
+        z = None
         if zeros is not None:
-            _check_block(zeros, "zeros", (V, (groups + 1) // 2), torch.uint8, dev)
+            z = _check_block(zeros, "zeros", (V, (groups + 1) // 2), torch.uint8, dev)
         if out is None:
-            _require(out_dtype in (torch.float32, torch.bfloat16),
-                     "out_dtype must be float32 or bfloat16")
-            out = torch.empty(B, V, dtype=out_dtype, device=hidden.device)
+            if out_dtype is not torch.float32 and out_dtype is not torch.bfloat16:
+                raise ValueError("out_dtype must be float32 or bfloat16")
+            out = torch.empty((B, V), dtype=out_dtype, device=hidden.device)
+            stride = V
         else:
             _check_rows(out, "out", B, (torch.float32, torch.bfloat16), dev)
-            _require(tuple(out.shape) == (B, V) and (B <= 1 or out.stride(0) >= V),
-                     "out must be [B, V] with rows that do not overlap")
+            stride = out.stride(0) if B > 1 else V
+            if out.shape != (B, V) or stride < V:
+                raise ValueError("out must be [B, V] with rows that do not overlap")
         st = self.lib.ss_lmhead_quant_logits(
-            self.handle, _ptr(hidden), _ptr(qweight), _ptr(scales),
-            SS_F16 if scales.dtype == torch.float16 else SS_BF16, _ptr(zeros), group, B, _ptr(out),
-            self._dtype(out), int(out.stride(0)) if B > 1 else V, _stream_on(stream, dev))
-        _check("ss_lmhead_quant_logits", st)
+            self.handle, hidden.data_ptr(), q, s, SS_F16 if half else SS_BF16, z, group, B,
+            out.data_ptr(), SS_BF16 if out.dtype is torch.bfloat16 else SS_F32, stride,
+            _stream_on(stream, dev))
+        if st != SS_OK:
+            _check("ss_lmhead_quant_logits", st)
         return out
 
 
