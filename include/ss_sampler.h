@@ -149,7 +149,7 @@ int64_t ss_sampler_workspace_bytes(const ss_sampler* s);
  * (tree paths, tile scan, row merge and child tests, residual tile sums,
  * per-request finish), ss_lmhead_sample 2 (fused GEMM tiles, cross-tile
  * reduction), ss_lmhead_sample_params 5 (as listed there), ss_spec_verify_probs
- * 2 (chunk sums, draw) and ss_lmhead_quant_logits 1.
+ * and ss_lmhead_quant_logits 1.
  * Returns SS_ERR_INVALID_ARG for a null handle or n_events outside 0 .. 16.
  * Not meant for graph capture. */
 ss_status ss_sampler_set_launch_events(ss_sampler* s, void* const* events, int32_t n_events);
@@ -376,7 +376,8 @@ ss_status ss_lmhead_sample_params(ss_sampler* s, const uint16_t* hidden, const u
  *                 element-aligned, target_stride >= V: the target's probabilities
  *                 at the draft positions and behind the last one. Rows need not
  *                 sum to 1: draws are relative to the row's sum. Entries are
- *                 finite; a negative or NaN entry counts as 0 in a draw.
+ *                 finite and not negative; in a draw a negative or NaN target
+ *                 entry has no mass, and neither has one whose draft entry is NaN.
  *   draft_probs   [B, G, draft_stride] of the same dtype, draft_stride >= V, or
  *                 NULL for a greedy draft (q one-hot at each draft token).
  *   draft_tokens  [B, G] int32; a token outside [0, V) is rejected. May be NULL
@@ -398,7 +399,9 @@ ss_status ss_lmhead_sample_params(ss_sampler* s, const uint16_t* hidden, const u
  * removed), behind the last draft r = p; the final token is the lowest v whose
  * running sum r(0) + ... + r(v) exceeds u_G times the whole sum. Where r has no
  * mass p is drawn from, and where p has none the token is -1. Products and sums
- * are binary64. Two kernels. Concurrent calls need handles of their own.
+ * are binary64. One kernel; it counts in the handle's workspace, so calls that
+ * overlap in time need handles of their own (graphs captured from one handle are
+ * replayed one after the other).
  * Errors: SS_ERR_INVALID_ARG for a null handle, B or G out of range, another
  * dtype, a null or misaligned pointer, a stride below V, or a seq that
  * ss_spec_verify_scatter would refuse. */
@@ -531,8 +534,7 @@ ss_status ss_cache_fork(ss_cache* c, const ss_block_tables* t, const int32_t* sr
  * base + 1 + num_accepted. The pages written must be the row's own, as
  * ss_cache_reserve leaves them. A row is refused (out_ok 0, left as it was) for
  * a negative base, num_accepted outside 0 .. N-1, nodes out of range or not
- * ascending, a slot without a page or behind max_blocks pages. One or two
- * kernels. */
+ * ascending, a slot without a page or behind max_blocks pages. One kernel. */
 ss_status ss_cache_commit(ss_cache* c, const ss_block_tables* t, const int32_t* base,
                           const int32_t* nodes, int64_t nodes_stride, int32_t N,
                           const int32_t* num_accepted, int32_t B, int32_t release,
@@ -553,7 +555,8 @@ ss_status ss_cache_truncate(ss_cache* c, const ss_block_tables* t, const int32_t
  *   out_ok    NULL, or [n] int32.
  * A pair is refused (out_ok 0) if a page is out of range, its dst is another
  * pair's dst, or, within one cache, any pair's src. Counts and tables are not
- * touched. Uses dst_cache's workspace. Two kernels.
+ * touched. The planes of two caches must not overlap. Uses dst_cache's workspace.
+ * One kernel (two for more than 1024 pairs).
  *
  * Errors of the calls above, before any launch: SS_ERR_INVALID_ARG for a null
  * handle, tables that are null, misaligned, too narrow or of too many rows, a

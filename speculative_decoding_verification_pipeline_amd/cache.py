@@ -58,6 +58,7 @@ class PageCache:
         self.num_pages, self.page_size = p.shape[0], p.shape[1]
         self.max_batch, self.max_blocks = max_batch, max_blocks
         self.device = p.device.index
+        self._place = p.device
 
     def close(self):
         if getattr(self, "handle", None):
@@ -106,7 +107,7 @@ class PageCache:
 
     def _ok(self, ok, n):
         if ok is None:
-            return torch.empty(n, dtype=torch.int32, device=self.planes[0].device)
+            return torch.empty(n, dtype=torch.int32, device=self._place)
         _check_array(ok, "ok", n, self.device)
         return ok
 
@@ -153,7 +154,10 @@ class PageCache:
         base = _check_array(base, "base", B, self.device)
         at, stride, N = None, 0, 0
         if nodes is not None:
-            _check_rows(nodes, "nodes", B, (torch.int32,), self.device)
+            if not (isinstance(nodes, torch.Tensor) and nodes.dtype is torch.int32 and
+                    nodes.get_device() == self.device and nodes.dim() == 2 and
+                    nodes.shape[0] >= B and nodes.is_contiguous()):
+                _check_rows(nodes, "nodes", B, (torch.int32,), self.device)
             N = nodes.shape[1]
             stride = nodes.stride(0) if B > 1 else N
             if not 1 <= N <= 64 or stride < N:

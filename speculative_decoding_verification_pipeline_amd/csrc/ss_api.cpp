@@ -27,7 +27,8 @@ struct ss_sampler {
     ss::LmTileStat* lm_stats;
     int32_t* lm_unres;
     ss::LmCut* lm_cut;
-    double2* probs_part;  // [max_batch * n_wt]
+    double* probs_part;      // [max_batch * n_wt]
+    int32_t* probs_arrived;  // [max_batch * PROBS_COUNTER]: 0 between calls
     ss::LaunchEvents events;
     // defaults substituted for absent per-request parameters, [max_batch] each
     int32_t* def_zero_i;
@@ -287,8 +288,9 @@ ss_status ss_sampler_create(const ss_sampler_config* cfg, ss_sampler** out) {
         cfg->hidden_size > 0 ? take(64 * (int64_t)s->n_vtiles * (int64_t)sizeof(ss::LmTileStat)) : 0;
     const int64_t o_lmunres = cfg->hidden_size > 0 ? take(64 * 4) : 0;
     const int64_t o_lmcut = cfg->hidden_size > 0 ? take(64 * (int64_t)sizeof(ss::LmCut)) : 0;
-    const int64_t o_probs = take((int64_t)B * nw * (int64_t)sizeof(double2));
-    const int64_t o_defaults = take(4 * (int64_t)B * 4);
+    const int64_t o_probs = take((int64_t)B * nw * (int64_t)sizeof(double));
+    // counters of 0, filled together with the defaults
+    const int64_t o_defaults = take((4 + ss::PROBS_COUNTER) * (int64_t)B * 4);
     s->ws_bytes = off;
     if (hipMalloc(&s->ws_base, (size_t)off) != hipSuccess) {
         (void)hipGetLastError();
@@ -315,14 +317,15 @@ ss_status ss_sampler_create(const ss_sampler_config* cfg, ss_sampler** out) {
     s->lm_stats = cfg->hidden_size > 0 ? reinterpret_cast<ss::LmTileStat*>(b + o_lmstat) : nullptr;
     s->lm_unres = cfg->hidden_size > 0 ? reinterpret_cast<int32_t*>(b + o_lmunres) : nullptr;
     s->lm_cut = cfg->hidden_size > 0 ? reinterpret_cast<ss::LmCut*>(b + o_lmcut) : nullptr;
-    s->probs_part = reinterpret_cast<double2*>(b + o_probs);
+    s->probs_part = reinterpret_cast<double*>(b + o_probs);
     {
         int32_t* d = reinterpret_cast<int32_t*>(b + o_defaults);
         s->def_zero_i = d;
         s->def_zero_f = reinterpret_cast<float*>(d + B);
         s->def_one_f = reinterpret_cast<float*>(d + 2 * B);
         s->def_iota = d + 3 * B;
-        int32_t* h = new (std::nothrow) int32_t[4 * (size_t)B];
+        s->probs_arrived = d + 4 * B;
+        int32_t* h = new (std::nothrow) int32_t[(4 + ss::PROBS_COUNTER) * (size_t)B]();
         if (!h) {
             (void)hipFree(s->ws_base);
             delete s;
@@ -335,7 +338,7 @@ ss_status ss_sampler_create(const ss_sampler_config* cfg, ss_sampler** out) {
             std::memcpy(&h[2 * B + i], &one, 4);
             h[3 * B + i] = i;
         }
-        const bool ok = hipMemcpy(d, h, 4 * (size_t)B * 4, hipMemcpyHostToDevice) == hipSuccess;
+        const bool ok = hipMemcpy(d, h, (4 + ss::PROBS_COUNTER) * (size_t)B * 4, hipMemcpyHostToDevice) == hipSuccess;
         delete[] h;
         if (!ok) {
             (void)hipFree(s->ws_base);
@@ -589,6 +592,7 @@ ss_status ss_spec_verify_probs(ss_sampler* s, const void* target_probs, ss_dtype
     }
     a.part = s->probs_part;
     a.n_chunks = (V + ss::WT - 1) / ss::WT;
+    a.arrived = s->probs_arrived;
     ss::DeviceGuard guard(s->cfg.device);
     if (!guard.ok) return SS_ERR_HIP;
     return ss::launch_probs(a, dtype, static_cast<hipStream_t>(stream), s->events) == hipSuccess

@@ -9,8 +9,8 @@
 // Nothing here depends on the order in which workgroups run: counts change by
 // integer atomics only, a free page is named by its rank among the free pages
 // in ascending order, and every launch reads either what no workgroup of that
-// launch writes or entries that it alone owns. The kernel boundary is the only
-// synchronisation.
+// launch writes or entries that it alone owns; a commit's table is written by the
+// workgroup that finds, at its row's counter, that the others have read it.
 //
 // What bounds it: the copying is bound by HBM (each byte read once and written
 // once, 16 bytes per lane and as many loads in flight as rows are moved); the
@@ -28,6 +28,9 @@ constexpr int CA_WAVES = CA_NT / WAVE;
 constexpr int CA_REF_EPT = CACHE_REF_CHUNK / CA_NT;  // counts per thread of a free-page chunk
 constexpr int CA_UNROLL = 8;
 static_assert(CA_REF_EPT == 16, "four vector loads of counts per thread");
+constexpr int CACHE_COMPARED = 1024;  // pairs that every copying workgroup compares itself
+
+typedef int int4u __attribute__((ext_vector_type(4), aligned(4)));
 
 template <int VEC>
 struct CacheVec;
@@ -93,9 +96,17 @@ __global__ __launch_bounds__(CA_NT) void k_cache_plan(CacheReserve a) {
         __shared__ RedT<CA_NT> red;
         const int p0 = blockIdx.x * CACHE_REF_CHUNK + tid * CA_REF_EPT;
         int free_mask = 0;
+        if (p0 + CA_REF_EPT <= a.num_pages) {
+            int4u v[CA_REF_EPT / 4];
 #pragma unroll
-        for (int i = 0; i < CA_REF_EPT; ++i)
-            if (p0 + i < a.num_pages && a.t.ref[p0 + i] == 0) free_mask |= 1 << i;
+            for (int i = 0; i < CA_REF_EPT / 4; ++i) v[i] = reinterpret_cast<const int4u*>(a.t.ref + p0)[i];
+#pragma unroll
+            for (int i = 0; i < CA_REF_EPT; ++i)
+                if (v[i / 4][i % 4] == 0) free_mask |= 1 << i;
+        } else {
+            for (int i = 0; i < CA_REF_EPT; ++i)
+                if (p0 + i < a.num_pages && a.t.ref[p0 + i] == 0) free_mask |= 1 << i;
+        }
         int total;
         int at = block_excl_scan_i<CA_NT>(__popc(free_mask), red, total);
         int32_t* out = a.ws.free_ids + (int64_t)blockIdx.x * CACHE_REF_CHUNK;
@@ -273,18 +284,22 @@ struct CommitRow {
 __device__ __forceinline__ CommitRow commit_row(const CacheCommit& a, const CacheCopy& g, int b) {
     const int lane = threadIdx.x & (WAVE - 1);
     CommitRow r;
+    // what does not depend on anything is loaded together
     r.acc = a.num_accepted[b];
+    const int64_t base = a.base[b];
+    int node = 0, prev = 0;
+    if (a.nodes && lane < a.N) {
+        const int32_t* nodes = a.nodes + (int64_t)b * a.nodes_stride;
+        node = nodes[lane];
+        prev = lane ? nodes[lane - 1] : 0;
+    }
     r.src = r.dst = 0;
     r.moves = false;
-    const int64_t base = a.base[b];
     const int64_t room = (int64_t)a.max_blocks * a.page_size;
     r.ok = base >= 0 && r.acc >= 0 && base + 1 + r.acc <= room && (!a.nodes || r.acc < a.N);
     if (!r.ok || !a.nodes) return r;
-    const int32_t* nodes = a.nodes + (int64_t)b * a.nodes_stride;
     bool bad = false;
     if (lane < r.acc) {
-        const int node = nodes[lane];
-        const int prev = lane ? nodes[lane - 1] : 0;
         bad = node <= prev || node >= a.N || base + node >= room;
         if (!bad && node != lane + 1) {
             const int64_t s = base + node, d = base + 1 + lane;
@@ -300,47 +315,56 @@ __device__ __forceinline__ CommitRow commit_row(const CacheCommit& a, const Cach
     return r;
 }
 
-// Grid (units / 256, B): a lane owns one vector of one head of one plane and
-// moves it for every accepted node in order, eight loads at a time: a slot
-// written here is read by no later node (their sources lie further back).
+// Grid (units / 256, B); without nodes (1, B). A lane owns one vector of one head
+// of one plane and moves it for every accepted node in order, eight loads at a
+// time: a slot written here is read by no later node (their sources lie further
+// back). The workgroup that is the last of its row to have read the table and the
+// length (which may be the base) writes them: the new length, and the pages
+// behind it given back. It reads nothing that the others write.
 template <int VEC>
-__global__ __launch_bounds__(CA_NT) void k_cache_move(CacheCommit a, CacheCopy g) {
+__global__ __launch_bounds__(CA_NT) void k_cache_commit(CacheCommit a, CacheCopy g) {
     typedef typename CacheVec<VEC>::type V;
+    __shared__ int s_settles;
     const int b = blockIdx.y;
-    const CommitRow r = commit_row(a, g, b);
-    if (!r.ok) return;
-    const unsigned long long moves = __ballot(r.moves);
-    if (!moves) return;
     const unsigned per_plane = (unsigned)g.heads * g.units;
     const unsigned u = blockIdx.x * CA_NT + threadIdx.x;
     const unsigned plane = u / per_plane;
     const bool on = plane < (unsigned)a.num_planes;
-    const unsigned w = u - plane * per_plane;
-    const unsigned h = w / g.units;
-    char* p = on ? g.dst_planes[plane] + h * g.dst_head + (int64_t)(w - h * g.units) * VEC : nullptr;
-    for (int i0 = __builtin_ctzll(moves); i0 < r.acc; i0 += CA_UNROLL) {
-        V v[CA_UNROLL];
+    char* p = on ? g.dst_planes[plane] : nullptr;
+    const CommitRow r = commit_row(a, g, b);
+    // every wave has its loads: their values have decided r
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        int32_t* arrived = a.arrived + b * CACHE_COUNTER;
+        s_settles = __hip_atomic_fetch_add(arrived, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                    (int)gridDim.x - 1;
+        if (s_settles) __hip_atomic_store(arrived, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    const unsigned long long moves = r.ok ? __ballot(r.moves) : 0;
+    if (moves) {
+        const unsigned w = u - plane * per_plane;
+        const unsigned h = w / g.units;
+        if (on) p += h * g.dst_head + (int64_t)(w - h * g.units) * VEC;
+        for (int i0 = __builtin_ctzll(moves); i0 < r.acc; i0 += CA_UNROLL) {
+            V v[CA_UNROLL];
 #pragma unroll
-        for (int k = 0; k < CA_UNROLL; ++k) {
-            const int64_t s = __shfl(r.src, i0 + k);
-            if (on && i0 + k < r.acc) v[k] = *reinterpret_cast<const V*>(p + s);
-        }
+            for (int k = 0; k < CA_UNROLL; ++k) {
+                const int64_t s = __shfl(r.src, i0 + k);
+                if (on && i0 + k < r.acc) v[k] = *reinterpret_cast<const V*>(p + s);
+            }
 #pragma unroll
-        for (int k = 0; k < CA_UNROLL; ++k) {
-            const int64_t d = __shfl(r.dst, i0 + k);
-            if (on && i0 + k < r.acc) *reinterpret_cast<V*>(p + d) = v[k];
+            for (int k = 0; k < CA_UNROLL; ++k) {
+                const int64_t d = __shfl(r.dst, i0 + k);
+                if (on && i0 + k < r.acc) *reinterpret_cast<V*>(p + d) = v[k];
+            }
         }
     }
-}
-
-// The new lengths, and the pages behind them given back.
-__global__ __launch_bounds__(CA_NT) void k_cache_settle(CacheCommit a, CacheCopy g) {
-    const int b = blockIdx.x;
-    const CommitRow r = commit_row(a, g, b);
-    const int len = r.ok ? a.base[b] + 1 + r.acc : 0;
-    __syncthreads();  // every wave has read the table and the length it may share with base
+    __syncthreads();
+    if (!s_settles) return;
     if (threadIdx.x == 0 && a.out_ok) a.out_ok[b] = r.ok ? 1 : 0;
     if (!r.ok) return;
+    const int len = a.base[b] + 1 + r.acc;
+    __syncthreads();  // the length may be the base that is read above
     if (threadIdx.x == 0) a.t.len[b] = len;
     if (a.release)
         release_from(a.t, a.num_pages, a.max_blocks, b,
@@ -350,28 +374,34 @@ __global__ __launch_bounds__(CA_NT) void k_cache_settle(CacheCommit a, CacheCopy
 // ---------------------------------------------------------------------------
 // copy: page src[i] of one cache to page dst[i] of another or the same
 
-// One wave per pair: out of range, a destination named twice, or (within one
-// cache) one that is also a source is refused.
+// Whether pair i is refused: out of range, a destination named twice, or (within
+// one cache) one that is also a source. first, step: the pairs this lane compares.
+__device__ __forceinline__ bool pair_bad(const CachePages& a, int i, int first, int step) {
+    const int src = a.src[i], dst = a.dst[i];
+    bool bad = !page_ok(src, a.src_pages) || !page_ok(dst, a.dst_pages);
+    for (int k = first; k < a.n; k += step)
+        if ((a.same && a.src[k] == dst) || (k != i && a.dst[k] == dst)) bad = true;
+    return bad;
+}
+
+// One wave per pair, for calls of many pairs.
 __global__ __launch_bounds__(CA_NT) void k_cache_pairs(CachePages a) {
     const int i = blockIdx.x * CA_WAVES + threadIdx.x / WAVE;
     const int lane = threadIdx.x & (WAVE - 1);
     if (i >= a.n) return;
-    const int src = a.src[i], dst = a.dst[i];
-    bool bad = !page_ok(src, a.src_pages) || !page_ok(dst, a.dst_pages);
-    for (int k = lane; k < a.n; k += WAVE)
-        if ((a.same && a.src[k] == dst) || (k != i && a.dst[k] == dst)) bad = true;
-    const bool ok = __ballot(bad) == 0;
-    if (lane == 0) {
-        a.pair_ok[i] = ok ? 1 : 0;
-        if (a.out_ok) a.out_ok[i] = ok ? 1 : 0;
-    }
+    const bool ok = __ballot(pair_bad(a, i, lane, WAVE)) == 0;
+    if (lane == 0) a.pair_ok[i] = ok ? 1 : 0;
 }
 
-template <int VEC>
+// Grid (planes, pairs). Few pairs are compared by every workgroup that copies:
+// one launch instead of two.
+template <int VEC, bool COMPARE>
 __global__ __launch_bounds__(CA_NT) void k_cache_copy(CachePages a, CacheCopy g) {
     const int i = blockIdx.y;
-    if (!a.pair_ok[i]) return;
     const int plane = blockIdx.x;
+    const bool ok = COMPARE ? !__syncthreads_or(pair_bad(a, i, threadIdx.x, CA_NT)) : a.pair_ok[i] != 0;
+    if (plane == 0 && threadIdx.x == 0 && a.out_ok) a.out_ok[i] = ok ? 1 : 0;
+    if (!ok) return;
     copy_slots<VEC>(g, g.src_planes[plane] + a.src[i] * g.src_page,
                     g.dst_planes[plane] + a.dst[i] * g.dst_page, a.page_size);
 }
@@ -399,23 +429,29 @@ hipError_t launch_cache_fork(const CacheFork& a, hipStream_t st) {
 }
 
 hipError_t launch_cache_commit(const CacheCommit& a, const CacheCopy& g, hipStream_t st) {
-    if (a.nodes) {
-        const int64_t units = (int64_t)a.num_planes * g.heads * g.units;
-        const dim3 grid((unsigned)((units + CA_NT - 1) / CA_NT), a.B);
-        if (g.vec == 16) hipLaunchKernelGGL(k_cache_move<16>, grid, dim3(CA_NT), 0, st, a, g);
-        else if (g.vec == 4) hipLaunchKernelGGL(k_cache_move<4>, grid, dim3(CA_NT), 0, st, a, g);
-        else hipLaunchKernelGGL(k_cache_move<1>, grid, dim3(CA_NT), 0, st, a, g);
-    }
-    hipLaunchKernelGGL(k_cache_settle, dim3(a.B), dim3(CA_NT), 0, st, a, g);
+    const int64_t units = a.nodes ? (int64_t)a.num_planes * g.heads * g.units : 1;
+    const dim3 grid((unsigned)((units + CA_NT - 1) / CA_NT), a.B);
+    if (g.vec == 16) hipLaunchKernelGGL(k_cache_commit<16>, grid, dim3(CA_NT), 0, st, a, g);
+    else if (g.vec == 4) hipLaunchKernelGGL(k_cache_commit<4>, grid, dim3(CA_NT), 0, st, a, g);
+    else hipLaunchKernelGGL(k_cache_commit<1>, grid, dim3(CA_NT), 0, st, a, g);
     return hipGetLastError();
 }
 
-hipError_t launch_cache_copy(const CachePages& a, const CacheCopy& g, hipStream_t st) {
-    hipLaunchKernelGGL(k_cache_pairs, dim3((a.n + CA_WAVES - 1) / CA_WAVES), dim3(CA_NT), 0, st, a);
+template <int VEC>
+static void launch_cache_copy_v(const CachePages& a, const CacheCopy& g, hipStream_t st) {
     const dim3 grid(a.num_planes, a.n);
-    if (g.vec == 16) hipLaunchKernelGGL(k_cache_copy<16>, grid, dim3(CA_NT), 0, st, a, g);
-    else if (g.vec == 4) hipLaunchKernelGGL(k_cache_copy<4>, grid, dim3(CA_NT), 0, st, a, g);
-    else hipLaunchKernelGGL(k_cache_copy<1>, grid, dim3(CA_NT), 0, st, a, g);
+    if (a.n <= CACHE_COMPARED) {
+        hipLaunchKernelGGL((k_cache_copy<VEC, true>), grid, dim3(CA_NT), 0, st, a, g);
+    } else {
+        hipLaunchKernelGGL(k_cache_pairs, dim3((a.n + CA_WAVES - 1) / CA_WAVES), dim3(CA_NT), 0, st, a);
+        hipLaunchKernelGGL((k_cache_copy<VEC, false>), grid, dim3(CA_NT), 0, st, a, g);
+    }
+}
+
+hipError_t launch_cache_copy(const CachePages& a, const CacheCopy& g, hipStream_t st) {
+    if (g.vec == 16) launch_cache_copy_v<16>(a, g, st);
+    else if (g.vec == 4) launch_cache_copy_v<4>(a, g, st);
+    else launch_cache_copy_v<1>(a, g, st);
     return hipGetLastError();
 }
 

@@ -141,6 +141,7 @@ ss_status ss_cache_create(const ss_cache_config* cfg, void* const* planes, ss_ca
     const int64_t o_carry = take((int64_t)cfg->max_batch * 4);
     const int64_t o_mark = take((int64_t)cfg->max_batch * cfg->max_blocks * 4);
     const int64_t o_pair = take((int64_t)cfg->num_pages * 4);
+    const int64_t o_arrived = take((int64_t)cfg->max_batch * ss::CACHE_COUNTER * 4);
     c->ws_bytes = off;
     if (hipMalloc(&c->ws_base, (size_t)off) != hipSuccess) {
         (void)hipGetLastError();
@@ -155,8 +156,12 @@ ss_status ss_cache_create(const ss_cache_config* cfg, void* const* planes, ss_ca
     c->ws.carry = reinterpret_cast<int32_t*>(b + o_carry);
     c->ws.mark = reinterpret_cast<int32_t*>(b + o_mark);
     c->ws.pair_ok = reinterpret_cast<int32_t*>(b + o_pair);
+    c->ws.arrived = reinterpret_cast<int32_t*>(b + o_arrived);
+    // the null stream's copy and clear are done before create returns
     if (hipMemcpy(c->planes, planes, (size_t)cfg->num_planes * sizeof(char*),
-                  hipMemcpyHostToDevice) != hipSuccess) {
+                  hipMemcpyHostToDevice) != hipSuccess ||
+        hipMemset(c->ws.arrived, 0, (size_t)cfg->max_batch * ss::CACHE_COUNTER * 4) != hipSuccess ||
+        hipStreamSynchronize(nullptr) != hipSuccess) {
         (void)hipFree(c->ws_base);
         delete c;
         return SS_ERR_HIP;
@@ -244,6 +249,7 @@ ss_status ss_cache_commit(ss_cache* c, const ss_block_tables* t, const int32_t* 
     a.N = N;
     a.B = B;
     a.release = release != 0;
+    a.arrived = c->ws.arrived;
     a.out_ok = out_ok;
     a.num_pages = c->cfg.num_pages;
     a.num_planes = c->cfg.num_planes;

@@ -206,7 +206,9 @@ struct LmheadArgs {
     int32_t* dbg_path;       // [B] or null: 0 candidates, 1 whole row, 2 no filter or greedy
 };
 
-// Verification against probability rows with the caller's uniforms.
+// Verification against probability rows with the caller's uniforms. Counters
+// stand this many integers apart: in one line they would be counted one by one.
+constexpr int PROBS_COUNTER = 64;
 struct ProbsArgs {
     const void* target;        // [B * (G + 1)] rows
     int64_t target_stride;
@@ -224,8 +226,10 @@ struct ProbsArgs {
     int64_t seq_stride;
     int32_t seq_capacity;
     int32_t* seq_len;
-    double2* part;             // [B * n_chunks]: residual and target mass per 2048-entry chunk
+    double* part;              // [B * n_chunks]: residual mass per 2048-entry chunk
     int n_chunks;
+    int32_t* arrived;          // [B * PROBS_COUNTER]: workgroups of each request that have left their sums; 0
+                               //      between calls
 };
 
 // LM-head logits from 4-bit weights.
@@ -249,6 +253,8 @@ struct QuantArgs {
 
 constexpr int CACHE_REF_CHUNK = 4096;   // page counts listed by one workgroup
 constexpr int CACHE_MAX_CHUNKS = 1024;
+constexpr int CACHE_COUNTER = 64;       // integers between counters: in one line they would be
+                                        //   counted one by one
 constexpr int CACHE_MAX_PAGES = CACHE_REF_CHUNK * CACHE_MAX_CHUNKS;
 
 struct CacheTables {
@@ -279,6 +285,8 @@ struct CacheWork {
     int32_t* carry;     // [max_batch]: shared page whose first slots move along, or -1
     int32_t* mark;      // [max_batch * max_blocks]
     int32_t* pair_ok;   // [num_pages]
+    int32_t* arrived;   // [max_batch * CACHE_COUNTER]: workgroups of each row that have read its
+                        //   table; 0 between calls
 };
 
 struct CacheReserve {
@@ -317,6 +325,7 @@ struct CacheCommit {
     int N;
     int B;
     int release;
+    int32_t* arrived;
     int32_t* out_ok;
     int num_pages, num_planes, page_size, max_blocks;
 };

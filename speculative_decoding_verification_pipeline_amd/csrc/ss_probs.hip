@@ -2,7 +2,8 @@
 //
 //   accept draft j     iff  u_j q_j(d_j) < p_j(d_j)            (j = 0, 1, ... until one fails)
 //   r(v) = max(0, p(v) - q(v))   at the first rejected position,
-//          max(0, p(v))          at the position behind the last draft
+//          max(0, p(v))          at the position behind the last draft, and where
+//                                the first has no mass
 //   token = the lowest v with  r(0) + ... + r(v)  >  u_G (r(0) + ... + r(V-1))
 //
 // Products, differences and sums are binary64: u q of two binary32 values is
@@ -10,10 +11,13 @@
 //
 // What bounds it: the one row (two with draft rows) that a request draws from;
 // every other row costs a gather per draft. One workgroup per request would
-// read a row at one CU's rate, so a row is cut into chunks of 2048 entries, one
-// workgroup each, that first repeat the (few) accept tests to learn which row
-// it is. A second launch scans the chunks' sums, finds the chunk the draw lies
-// in and searches it. The kernel boundary is the only synchronisation.
+// read a row at one CU's rate, so a row is cut into chunks of 2048 entries,
+// PER of them a workgroup, that first repeats the (few) accept tests to learn
+// which row it is. The chunks' sums go to the workspace; the workgroup that
+// arrives last at its request's counter has them all, finds the chunk the draw
+// lies in and searches it, and sets the counter back to 0. (As two launches the
+// draw waited for the slowest request and cost 3 us more on the host.)
+// Which workgroup draws is open, what it computes is not: it sums in order.
 #include <limits.h>
 
 #include "ss_device.h"
@@ -42,7 +46,7 @@ struct Raw8<float> {
         a = *reinterpret_cast<const v4*>(p);
         b = *reinterpret_cast<const v4*>(p + 4);
     }
-    __device__ __forceinline__ double at(int i) const { return (double)(i < 4 ? a[i] : b[i - 4]); }
+    __device__ __forceinline__ float at(int i) const { return i < 4 ? a[i] : b[i - 4]; }
 };
 struct Bf16 {
     uint16_t bits;
@@ -52,23 +56,19 @@ struct Raw8<Bf16> {
     typedef uint16_t v8 __attribute__((ext_vector_type(8), aligned(2)));
     v8 a;
     __device__ __forceinline__ void load(const Bf16* p) { a = *reinterpret_cast<const v8*>(p); }
-    __device__ __forceinline__ double at(int i) const {
-        return (double)__uint_as_float((uint32_t)a[i] << 16);
-    }
+    __device__ __forceinline__ float at(int i) const { return __uint_as_float((uint32_t)a[i] << 16); }
 };
 template <>
 struct Raw8<_Float16> {
     typedef _Float16 v8 __attribute__((ext_vector_type(8), aligned(2)));
     v8 a;
     __device__ __forceinline__ void load(const _Float16* p) { a = *reinterpret_cast<const v8*>(p); }
-    __device__ __forceinline__ double at(int i) const { return (double)(float)a[i]; }
+    __device__ __forceinline__ float at(int i) const { return (float)a[i]; }
 };
 
-__device__ __forceinline__ double to_f64(float x) { return (double)x; }
-__device__ __forceinline__ double to_f64(Bf16 x) {
-    return (double)__uint_as_float((uint32_t)x.bits << 16);
-}
-__device__ __forceinline__ double to_f64(_Float16 x) { return (double)(float)x; }
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(Bf16 x) { return __uint_as_float((uint32_t)x.bits << 16); }
+__device__ __forceinline__ float to_f32(_Float16 x) { return (float)x; }
 
 // The rows a request draws from.
 template <class T>
@@ -97,8 +97,8 @@ __device__ __forceinline__ ProbsRow<T> probs_row(const ProbsArgs& a, int b) {
         d = a.draft_tokens[(int64_t)b * a.G + lane];
         if (d >= 0 && d < a.V) {
             const double u = (double)a.uniforms[(int64_t)b * (a.G + 1) + lane];
-            const double p = to_f64(target[lane * a.target_stride + d]);
-            const double q = draft ? to_f64(draft[lane * a.draft_stride + d]) : 1.0;
+            const double p = to_f32(target[lane * a.target_stride + d]);
+            const double q = draft ? to_f32(draft[lane * a.draft_stride + d]) : 1.0;
             ok = u * q < p;
         }
     }
@@ -112,29 +112,35 @@ __device__ __forceinline__ ProbsRow<T> probs_row(const ProbsArgs& a, int b) {
     return r;
 }
 
-// Residual (x) and target mass (p) of the thread's entries v0 .. v0 + 7.
-// fmax takes a NaN entry for 0, and a negative one as well.
+// The thread's entries v0 .. v0 + 7, where all of them lie in the row.
 template <class T>
-__device__ __forceinline__ void probs_entries(const ProbsRow<T>& r, int v0, int V, double x[PV_EPT],
-                                              double p[PV_EPT]) {
+__device__ __forceinline__ void probs_load(const ProbsRow<T>& r, int v0, int V, Raw8<T>& rp, Raw8<T>& rq) {
     if (v0 + PV_EPT <= V) {
-        Raw8<T> rp, rq;
         rp.load(r.p + v0);
         if (r.q) rq.load(r.q + v0);
+    }
+}
+
+// Their residual; those of a row's end are loaded here. max(0, p - q) is formed
+// as p - min(p, q): the comparison in binary32 is exact, and binary64, a quarter
+// of its rate, only subtracts. A negative or NaN p counts as 0, and a NaN q
+// leaves nothing.
+__device__ __forceinline__ double residual(float p, float q) {
+    const float a = fmaxf(p, 0.0f);
+    return (double)a - (double)fminf(a, q);
+}
+template <class T>
+__device__ __forceinline__ void probs_entries(const ProbsRow<T>& r, int v0, int V, const Raw8<T>& rp,
+                                              const Raw8<T>& rq, double x[PV_EPT]) {
+    if (v0 + PV_EPT <= V) {
 #pragma unroll
-        for (int i = 0; i < PV_EPT; ++i) {
-            p[i] = fmax(rp.at(i), 0.0);
-            x[i] = r.q ? fmax(rp.at(i) - rq.at(i), 0.0) : p[i];
-        }
+        for (int i = 0; i < PV_EPT; ++i)
+            x[i] = r.q ? residual(rp.at(i), rq.at(i)) : (double)fmaxf(rp.at(i), 0.0f);
     } else {
 #pragma unroll
         for (int i = 0; i < PV_EPT; ++i) {
-            p[i] = x[i] = 0.0;
-            if (v0 + i < V) {
-                const double pv = to_f64(r.p[v0 + i]);
-                p[i] = fmax(pv, 0.0);
-                x[i] = r.q ? fmax(pv - to_f64(r.q[v0 + i]), 0.0) : p[i];
-            }
+            x[i] = 0.0;
+            if (v0 + i < V) x[i] = residual(to_f32(r.p[v0 + i]), r.q ? to_f32(r.q[v0 + i]) : 0.0f);
         }
     }
     if (r.hot >= 0) {
@@ -144,56 +150,93 @@ __device__ __forceinline__ void probs_entries(const ProbsRow<T>& r, int v0, int 
     }
 }
 
-template <class T>
-__global__ __launch_bounds__(PV_NT) void k_probs_mass(ProbsArgs a) {
-    __shared__ double2 s_part[PV_WAVES];
-    const int b = blockIdx.y;
-    const int wave = threadIdx.x / WAVE;
-    const ProbsRow<T> r = probs_row<T>(a, b);
-    double x[PV_EPT], p[PV_EPT];
-    probs_entries(r, blockIdx.x * PV_CHUNK + threadIdx.x * PV_EPT, a.V, x, p);
-    double sx = 0.0, sp = 0.0;
-#pragma unroll
-    for (int i = 0; i < PV_EPT; ++i) {
-        sx += x[i];
-        sp += p[i];
-    }
-    sx = wave_sum_d(sx);
-    sp = wave_sum_d(sp);
-    if ((threadIdx.x & (WAVE - 1)) == 0) s_part[wave] = make_double2(sx, sp);
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        double2 t = s_part[0];
-#pragma unroll
-        for (int w = 1; w < PV_WAVES; ++w) {
-            t.x += s_part[w].x;
-            t.y += s_part[w].y;
-        }
-        a.part[(int64_t)b * a.n_chunks + blockIdx.x] = t;
-    }
+// Sums cross from the workgroups that made them to the one that draws, on another
+// XCD and behind another L2. They are stored and loaded at agent scope, past the
+// caches that are not shared, and a wait for the stores stands before the count:
+// a release would order the same, and write back the whole L2 for it, 20 us with
+// a thousand workgroups.
+__device__ __forceinline__ void put_sum(double* p, double v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ double get_sum(const double* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-template <class T>
-__global__ __launch_bounds__(PV_NT) void k_probs_draw(ProbsArgs a) {
+template <class T, int PER>
+__global__ __launch_bounds__(PV_NT) void k_probs(ProbsArgs a) {
+    __shared__ double s_part[PER][PV_WAVES];
+    __shared__ double s_chunk[MAX_WT];
     __shared__ double s_wave[PV_WAVES];
     __shared__ int s_first[PV_WAVES], s_last[PV_WAVES];
-    const int b = blockIdx.x;
+    __shared__ int s_draws;
+    const int b = blockIdx.y;
     const int tid = threadIdx.x;
     const int lane = tid & (WAVE - 1);
     const int wave = tid / WAVE;
-    const ProbsRow<T> r = probs_row<T>(a, b);
+    ProbsRow<T> r = probs_row<T>(a, b);
+    double* part = a.part + (int64_t)b * a.n_chunks;
+    {
+        Raw8<T> rp[PER], rq[PER];  // every chunk's loads in flight together
+        const int c0 = blockIdx.x * PER;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) probs_load(r, (c0 + k) * PV_CHUNK + tid * PV_EPT, a.V, rp[k], rq[k]);
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            double x[PV_EPT];
+            probs_entries(r, (c0 + k) * PV_CHUNK + tid * PV_EPT, a.V, rp[k], rq[k], x);
+            double sum = 0.0;
+#pragma unroll
+            for (int i = 0; i < PV_EPT; ++i) sum += x[i];
+            sum = wave_sum_d(sum);
+            if (lane == 0) s_part[k][wave] = sum;
+        }
+    }
+    __syncthreads();
+    if (wave == 0) {  // lane k: chunk k of this workgroup
+        const int c = blockIdx.x * PER + lane;
+        if (lane < PER && c < a.n_chunks) {
+            double t = s_part[lane][0];
+#pragma unroll
+            for (int w = 1; w < PV_WAVES; ++w) t += s_part[lane][w];
+            put_sum(part + c, t);
+        }
+        // the wave's sums have reached the agent's point of coherence before its count does
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        if (lane == 0) {
+            int32_t* arrived = a.arrived + b * PROBS_COUNTER;
+            const int before = __hip_atomic_fetch_add(arrived, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            s_draws = before == (int)gridDim.x - 1;
+            if (s_draws) __hip_atomic_store(arrived, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+    }
+    __syncthreads();
+    if (!s_draws) return;
     // the chunk of the draw, found by every wave: two chunks per lane (V <= 262144: 128 chunks)
-    const double2* part = a.part + (int64_t)b * a.n_chunks;
-    double2 c0 = make_double2(0.0, 0.0), c1 = c0;
-    if (2 * lane < a.n_chunks) c0 = part[2 * lane];
-    if (2 * lane + 1 < a.n_chunks) c1 = part[2 * lane + 1];
-    double incl = wave_incl_scan_d(c0.x + c1.x);
+    double m0 = 2 * lane < a.n_chunks ? get_sum(part + 2 * lane) : 0.0;
+    double m1 = 2 * lane + 1 < a.n_chunks ? get_sum(part + 2 * lane + 1) : 0.0;
+    double incl = wave_incl_scan_d(m0 + m1);
     double total = __shfl(incl, WAVE - 1);
-    const bool whole = !(total > 0.0);  // p <= q everywhere: draw from p itself
-    double m0 = c0.x, m1 = c1.x;
-    if (whole) {
-        m0 = c0.y;
-        m1 = c1.y;
+    if (!(total > 0.0) && (r.q || r.hot >= 0)) {
+        // p <= q everywhere (rounded rows, or one that p alone fills): the draw is
+        // from p itself, whose sums this workgroup makes, a chunk a wave
+        r.q = nullptr;
+        r.hot = -1;
+        for (int c = wave; c < a.n_chunks; c += PV_WAVES) {
+            double sum = 0.0;
+            for (int i = lane * PV_EPT; i < PV_CHUNK; i += WAVE * PV_EPT) {
+                Raw8<T> rp, rq;
+                double x[PV_EPT];
+                probs_load(r, c * PV_CHUNK + i, a.V, rp, rq);
+                probs_entries(r, c * PV_CHUNK + i, a.V, rp, rq, x);
+#pragma unroll
+                for (int k = 0; k < PV_EPT; ++k) sum += x[k];
+            }
+            sum = wave_sum_d(sum);
+            if (lane == 0) s_chunk[c] = sum;
+        }
+        __syncthreads();
+        m0 = 2 * lane < a.n_chunks ? s_chunk[2 * lane] : 0.0;
+        m1 = 2 * lane + 1 < a.n_chunks ? s_chunk[2 * lane + 1] : 0.0;
         incl = wave_incl_scan_d(m0 + m1);
         total = __shfl(incl, WAVE - 1);
     }
@@ -217,15 +260,14 @@ __global__ __launch_bounds__(PV_NT) void k_probs_draw(ProbsArgs a) {
             chunk = 2 * l + (__shfl(m1, l) > 0.0 ? 1 : 0);
             base = 0.0;
         }
-        double x[PV_EPT], p[PV_EPT];
+        double x[PV_EPT];
         const int v0 = chunk * PV_CHUNK + tid * PV_EPT;
-        probs_entries(r, v0, a.V, x, p);
+        Raw8<T> rp, rq;
+        probs_load(r, v0, a.V, rp, rq);
+        probs_entries(r, v0, a.V, rp, rq, x);
         double own = 0.0;
 #pragma unroll
-        for (int i = 0; i < PV_EPT; ++i) {
-            if (whole) x[i] = p[i];
-            own += x[i];
-        }
+        for (int i = 0; i < PV_EPT; ++i) own += x[i];
         const double scan = wave_incl_scan_d(own);
         if (lane == WAVE - 1) s_wave[wave] = scan;
         __syncthreads();
@@ -277,10 +319,18 @@ __global__ __launch_bounds__(PV_NT) void k_probs_draw(ProbsArgs a) {
     }
 }
 
+template <class T, int PER>
+static void launch_probs_p(const ProbsArgs& a, hipStream_t st, const LaunchEvents& le) {
+    launch_k(le, 0, k_probs<T, PER>, dim3((a.n_chunks + PER - 1) / PER, a.B), dim3(PV_NT), st, a);
+}
+
 template <class T>
 static void launch_probs_t(const ProbsArgs& a, hipStream_t st, const LaunchEvents& le) {
-    launch_k(le, 0, k_probs_mass<T>, dim3(a.n_chunks, a.B), dim3(PV_NT), st, a);
-    launch_k(le, 1, k_probs_draw<T>, dim3(a.B), dim3(PV_NT), st, a);
+    // A chunk a workgroup while all of them are resident at once: [1, 4, 32000] f32
+    // 5.4 us (two chunks: 5.8), [48, 5, 50257] 7.4 (7.6). Beyond, two: [32, 4, 128256]
+    // f32 9.6 us (one: 10.6, four: 10.1), [64, 7, 152064] bf16 12.5 (17.5, 12.8).
+    if ((int64_t)a.n_chunks * a.B <= 1536) launch_probs_p<T, 1>(a, st, le);
+    else launch_probs_p<T, 2>(a, st, le);
 }
 
 hipError_t launch_probs(const ProbsArgs& a, ss_dtype dt, hipStream_t st, const LaunchEvents& le) {

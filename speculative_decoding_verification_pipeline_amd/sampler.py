@@ -169,9 +169,14 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+# torch's current stream as an address, without the Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream_on(stream, device):
     """The given stream, or the current one of a device that need not be current."""
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    return _raw_stream(device) if stream is None else stream.cuda_stream
 
 
 def _require(cond, msg):
@@ -607,11 +612,11 @@ class Sampler:
         u = _check_block(uniforms, "uniforms", (B, G1), torch.float32, dev)
         n = _check_array(draft_len, "draft_len", B, dev)
         if out_tokens is None:
-            out_tokens = torch.empty((B, G1), dtype=torch.int32, device=target_probs.device)
+            out_tokens = uniforms.new_empty((B, G1), dtype=torch.int32)
         else:
             _check_block(out_tokens, "out_tokens", (B, G1), torch.int32, dev)
         if out_num_accepted is None:
-            out_num_accepted = torch.empty(B, dtype=torch.int32, device=target_probs.device)
+            out_num_accepted = uniforms.new_empty(B, dtype=torch.int32)
         else:
             _check_array(out_num_accepted, "out_num_accepted", B, dev)
         seq = None
