@@ -393,12 +393,13 @@ __global__ __launch_bounds__(CA_NT) void k_cache_pairs(CachePages a) {
     if (lane == 0) a.pair_ok[i] = ok ? 1 : 0;
 }
 
-// Grid (planes, pairs). Few pairs are compared by every workgroup that copies:
+// Grid (pairs, planes): a plane's pages side by side, 95 -> 93 us for 100 pages of
+// 2 MB. Few pairs are compared by every workgroup that copies:
 // one launch instead of two.
 template <int VEC, bool COMPARE>
 __global__ __launch_bounds__(CA_NT) void k_cache_copy(CachePages a, CacheCopy g) {
-    const int i = blockIdx.y;
-    const int plane = blockIdx.x;
+    const int i = blockIdx.x;
+    const int plane = blockIdx.y;
     const bool ok = COMPARE ? !__syncthreads_or(pair_bad(a, i, threadIdx.x, CA_NT)) : a.pair_ok[i] != 0;
     if (plane == 0 && threadIdx.x == 0 && a.out_ok) a.out_ok[i] = ok ? 1 : 0;
     if (!ok) return;
@@ -439,7 +440,7 @@ hipError_t launch_cache_commit(const CacheCommit& a, const CacheCopy& g, hipStre
 
 template <int VEC>
 static void launch_cache_copy_v(const CachePages& a, const CacheCopy& g, hipStream_t st) {
-    const dim3 grid(a.num_planes, a.n);
+    const dim3 grid(a.n, a.num_planes);
     if (a.n <= CACHE_COMPARED) {
         hipLaunchKernelGGL((k_cache_copy<VEC, true>), grid, dim3(CA_NT), 0, st, a, g);
     } else {
