@@ -134,14 +134,16 @@ ss_status ss_cache_create(const ss_cache_config* cfg, void* const* planes, ss_ca
         off = align_up(off + bytes);
         return o;
     };
+    // the plane pointers and the counters of 0, filled by one copy
     const int64_t o_planes = take((int64_t)cfg->num_planes * sizeof(char*));
+    const int64_t o_arrived = take((int64_t)cfg->max_batch * ss::CACHE_COUNTER * 4);
+    const int64_t filled = off;
     const int64_t o_ids = take((int64_t)c->n_chunks * ss::CACHE_REF_CHUNK * 4);
     const int64_t o_cnt = take((int64_t)c->n_chunks * 4);
     const int64_t o_need = take((int64_t)cfg->max_batch * 4);
     const int64_t o_carry = take((int64_t)cfg->max_batch * 4);
     const int64_t o_mark = take((int64_t)cfg->max_batch * cfg->max_blocks * 4);
     const int64_t o_pair = take((int64_t)cfg->num_pages * 4);
-    const int64_t o_arrived = take((int64_t)cfg->max_batch * ss::CACHE_COUNTER * 4);
     c->ws_bytes = off;
     if (hipMalloc(&c->ws_base, (size_t)off) != hipSuccess) {
         (void)hipGetLastError();
@@ -157,11 +159,16 @@ ss_status ss_cache_create(const ss_cache_config* cfg, void* const* planes, ss_ca
     c->ws.mark = reinterpret_cast<int32_t*>(b + o_mark);
     c->ws.pair_ok = reinterpret_cast<int32_t*>(b + o_pair);
     c->ws.arrived = reinterpret_cast<int32_t*>(b + o_arrived);
-    // the null stream's copy and clear are done before create returns
-    if (hipMemcpy(c->planes, planes, (size_t)cfg->num_planes * sizeof(char*),
-                  hipMemcpyHostToDevice) != hipSuccess ||
-        hipMemset(c->ws.arrived, 0, (size_t)cfg->max_batch * ss::CACHE_COUNTER * 4) != hipSuccess ||
-        hipStreamSynchronize(nullptr) != hipSuccess) {
+    char* h = new (std::nothrow) char[(size_t)filled]();
+    if (!h) {
+        (void)hipFree(c->ws_base);
+        delete c;
+        return SS_ERR_OUT_OF_MEMORY;
+    }
+    std::memcpy(h + o_planes, planes, (size_t)cfg->num_planes * sizeof(char*));
+    const bool ok = hipMemcpy(b, h, (size_t)filled, hipMemcpyHostToDevice) == hipSuccess;
+    delete[] h;
+    if (!ok) {
         (void)hipFree(c->ws_base);
         delete c;
         return SS_ERR_HIP;

@@ -43,7 +43,7 @@ namespace ss {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint16_t u16x4u __attribute__((ext_vector_type(4), aligned(2)));
+
 
 constexpr int LQ_KB = 128;   // k per block: 16 bytes of weights per lane and row tile
 
@@ -140,51 +140,23 @@ __device__ __forceinline__ floatx4 lq_mfma(bf16x8 x, bf16x8 w, floatx4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w, c, 0, 0, 0);
 }
 
-// The scales (16 bits each) and zero points (4 bits each) of four consecutive
-// groups of one vocabulary row; groups behind the last one have scale 0.
+// Scale and zero point of one group of one vocabulary row, as loaded: those of
+// groups behind the last one are 0.
 struct LqRaw {
-    uint64_t s;
-    uint32_t z;
+    uint32_t s, z;
 };
 
-__device__ __forceinline__ LqRaw lq_load(const QuantArgs& a, int v, int g0, int n_groups) {
-    const uint16_t* s = a.scales + (int64_t)v * n_groups + g0;
-    LqRaw r;
-    r.s = 0;
-    if (g0 + 4 <= n_groups) {
-        r.s = __builtin_bit_cast(uint64_t, *reinterpret_cast<const u16x4u*>(s));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (g0 + i < n_groups) r.s |= (uint64_t)s[i] << 16 * i;
-    }
-    r.z = 0x8888u;
-    if (a.zeros) {
-        const uint8_t* z = a.zeros + (int64_t)v * ((n_groups + 1) / 2) + g0 / 2;
-        r.z = g0 < n_groups ? z[0] : 0u;
-        if (g0 + 2 < n_groups) r.z |= (uint32_t)z[1] << 8;
+__device__ __forceinline__ LqRaw lq_load(const QuantArgs& a, int v, int g, int n_groups) {
+    LqRaw r = {0u, 8u};
+    if (g < n_groups) {
+        r.s = a.scales[(int64_t)v * n_groups + g];
+        if (a.zeros) r.z = a.zeros[(int64_t)v * ((n_groups + 1) / 2) + (g >> 1)] >> (g & 1) * 4 & 15;
     }
     return r;
 }
 
-__device__ __forceinline__ float lq_scale(uint16_t bits, bool f16) {
-    return f16 ? (float)__builtin_bit_cast(_Float16, bits) : __uint_as_float((uint32_t)bits << 16);
-}
-
-// The binary32 scales of four groups, and - s (16 + z) of the group that this
-// lane's quarter contributes to the product of the sums.
-struct LqScales {
-    float s[4];
-    float c;
-};
-
-__device__ __forceinline__ LqScales lq_convert(const LqRaw& r, bool f16, int quarter) {
-    LqScales o;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o.s[i] = lq_scale((uint16_t)(r.s >> 16 * i), f16);
-    const float s = quarter & 2 ? (quarter & 1 ? o.s[3] : o.s[2]) : (quarter & 1 ? o.s[1] : o.s[0]);
-    o.c = -s * (16.f + (float)(r.z >> 4 * quarter & 15u));
-    return o;
+__device__ __forceinline__ float lq_scale(uint32_t bits, bool f16) {
+    return f16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)bits) : __uint_as_float(bits << 16);
 }
 
 template <class F, int... I>
@@ -215,6 +187,7 @@ __global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
     __shared__ __attribute__((aligned(1024))) uint8_t b2[S > 2 ? XB + WB : 16];
     __shared__ __attribute__((aligned(1024))) uint8_t b3[S > 3 ? XB + WB : 16];
     __shared__ float s_sum[2 * SPS][KW][4][NT * 16];  // sums of x over a set's groups
+    __shared__ float s_scale[WAVES][SPS][4][RT * 16];
     const int tid = threadIdx.x;
     const int lane = tid & (WAVE - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
@@ -325,8 +298,10 @@ __global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
         for (int n = 0; n < NT; ++n) out[t][n] = floatx4{0.f, 0.f, 0.f, 0.f};
     for (int i = tid; i < 2 * SPS * KW * 4 * NT * 16; i += WAVES * WAVE) (&s_sum[0][0][0][0])[i] = 0.f;
 
-    LqRaw raw[SPS][RT], next[SPS][RT];
-    LqScales sc[RT];
+    // A lane loads scale and zero point of the one group of a set that its quarter
+    // contributes to the product of the sums, a set ahead; the wave's lanes share
+    // the scales through LDS.
+    LqRaw next[SPS][RT];
     float c_now[SPS][RT], c_before[SPS][RT];
 #pragma unroll
     for (int h = 0; h < SPS; ++h)
@@ -338,7 +313,7 @@ __global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
 #pragma unroll
             for (int t = 0; t < RT; ++t)
                 next[h][t] = lq_load(a, min(row0 + t * 16 + r16, V - 1),
-                                     (first_stage + place(j)) * GPS + h * 4, n_groups);
+                                     (first_stage + place(j)) * GPS + h * 4 + quarter, n_groups);
     };
     // - s (16 + z) times the sums of x, of the sets before the one that begins at stage j
     auto add_sums = [&](int j, const float (&c)[SPS][RT]) {
@@ -393,12 +368,14 @@ __global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
             if (i % PER == PER - 1) {
                 const int g = g0 + i / PER;
 #pragma unroll
-                for (int t = 0; t < RT; ++t)
+                for (int t = 0; t < RT; ++t) {
+                    const float scale = s_scale[wave][h % SPS][g][t * 16 + r16];
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            out[t][n][q] = __builtin_fmaf(sc[t].s[g], acc[t][n][q], out[t][n][q]);
+                            out[t][n][q] = __builtin_fmaf(scale, acc[t][n][q], out[t][n][q]);
+                }
                 // every row of the product with ones is the sum of batch row r16
                 if (rw < NT && quarter == 0) s_sum[slot][kw][g][tile_of(0) * 16 + r16] = sum[0];
             }
@@ -425,8 +402,10 @@ __global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
                 for (int h = 0; h < SPS; ++h)
 #pragma unroll
                     for (int t = 0; t < RT; ++t) {
-                        raw[h][t] = next[h][t];
                         c_before[h][t] = c_now[h][t];
+                        const float scale = lq_scale(next[h][t].s, f16);
+                        c_now[h][t] = -scale * (16.f + (float)next[h][t].z);
+                        s_scale[wave][h][quarter][t * 16 + r16] = scale;
                     }
                 if (j + SET < stages) load_scales(j + SET);
             }
@@ -435,13 +414,6 @@ __global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
             auto one = [&](auto hc) {
                 constexpr int h = decltype(hc)::value;
                 constexpr int g = (u % SET * GPS + h * GPB) % 4;  // place of its first group
-                if constexpr (g == 0) {
-#pragma unroll
-                    for (int t = 0; t < RT; ++t) {
-                        sc[t] = lq_convert(raw[h % SPS][t], f16, quarter);
-                        c_now[h % SPS][t] = sc[t].c;
-                    }
-                }
                 block(bufs[u % S], slot + h % SPS, hc, std::integral_constant<int, g>{});
             };
             lq_each(one, std::make_integer_sequence<int, BPS>{});
@@ -498,19 +470,169 @@ static void launch_quant_t(const QuantArgs& a, hipStream_t st, const LaunchEvent
              dim3(WAVES * WAVE), st, a);
 }
 
+// ---------------------------------------------------------------------------
+// one batch row: no matrix cores
+//
+// For a single token the weight stream is all there is: a wave reads QR_R whole
+// rows side by side, 2048 k of each at a time, 32 consecutive k a lane, and dots
+// its widened weights with x (v_dot2_f32_bf16: exact products, binary32 sums). x
+// lies in LDS, swizzled as above, with the sum over every 32 k; waves meet at no
+// barrier after it is there. A lane's 32 k are of one group, so scale and zero
+// point are one value, and only the finished rows cross lanes.
+
+constexpr int QR_NT = 256;
+constexpr int QR_R = 4;        // rows per wave
+constexpr int QR_K = WAVE * 32;
+constexpr int QR_ROWS = QR_NT / WAVE * QR_R;
+constexpr int QR_MOST_K = 24576;  // x and its sums stay within 64 KB of LDS
+
+template <int GROUP>
+__global__ __launch_bounds__(QR_NT) void k_quant_rows(QuantArgs a) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    extern __shared__ __attribute__((aligned(16))) uint8_t s_x[];  // [K] bfloat16, then sums
+    const int K = a.K, V = a.V;
+    float* s_sum = reinterpret_cast<float*>(s_x + (size_t)K * 2);  // [K / 32]
+    const int tid = threadIdx.x;
+    const int lane = tid & (WAVE - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
+    const int n_groups = (K + GROUP - 1) / GROUP;
+    const int zero_pitch = (n_groups + 1) / 2;
+    const int chunks = (K + QR_K - 1) / QR_K;
+    const bool f16 = a.scale_f16 != 0;
+    const int first = (blockIdx.x * (QR_NT / WAVE) + wave) * QR_R;
+
+    struct Load {
+        u32x4 w;
+        uint32_t s, z;
+    };
+    auto load = [&](int c, Load (&l)[QR_R]) {
+        const int k = c * QR_K + lane * 32;
+        const bool on = k < K;
+        const int g = k / GROUP;
+#pragma unroll
+        for (int r = 0; r < QR_R; ++r) {
+            const int64_t row = min(first + r, V - 1);
+            l[r].w = u32x4{0u, 0u, 0u, 0u};
+            l[r].s = 0u;
+            l[r].z = 0x88u;  // both nibbles: which one is chosen where it is used
+            if (on) {
+                l[r].w = __builtin_nontemporal_load(
+                    reinterpret_cast<const u32x4*>(a.qweight + row * (K / 2) + (k >> 1)));
+                l[r].s = a.scales[row * n_groups + g];
+                if (a.zeros) l[r].z = a.zeros[row * zero_pitch + (g >> 1)];
+            }
+        }
+    };
+    Load now[QR_R], then[QR_R];
+    load(0, then);
+
+    // x: 16-byte unit u to the 64 bytes of the lane that uses it
+    for (int u = tid; u < K / 8; u += QR_NT) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(a.hidden + u * 8);
+        *reinterpret_cast<u32x4*>(s_x + (u >> 2) * 64 + (((u & 3) ^ (u >> 4 & 3)) << 4)) = v;
+        float s = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            s += __uint_as_float(v[q] << 16) + __uint_as_float(v[q] & 0xFFFF0000u);
+        // K is a multiple of 64: the four units of 32 k lie in four lanes of one quad
+        s += __uint_as_float(dpp_mov<DPP_QUAD_X1>(__float_as_uint(s)));
+        s += __uint_as_float(dpp_mov<DPP_QUAD_X2>(__float_as_uint(s)));
+        if ((u & 3) == 0) s_sum[u >> 2] = s;
+    }
+    __syncthreads();
+
+    const LqWiden widen;
+    float acc[QR_R];
+#pragma unroll
+    for (int r = 0; r < QR_R; ++r) acc[r] = 0.f;
+    for (int c = 0; c < chunks; ++c) {
+#pragma unroll
+        for (int r = 0; r < QR_R; ++r) now[r] = then[r];
+        const int k = c * QR_K + lane * 32;
+        if (c + 1 < chunks) load(c + 1, then);
+        const int at = k < K ? k : 0;  // lanes behind K have scale 0
+        u32x4 x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = lq_at(s_x + at * 2 + ((u ^ (at >> 7 & 3)) << 4));
+        const float sum = s_sum[at >> 5];
+        const int nibble = (k / GROUP & 1) * 4;
+#pragma unroll
+        for (int r = 0; r < QR_R; ++r) {
+            float dot = 0.f;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const u32x4 w = __builtin_bit_cast(u32x4, widen(now[r].w[u]));
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t wq = w[q], xq = x[u][q];
+                    dot = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, wq),
+                                                          __builtin_bit_cast(bf16x2, xq), dot, false);
+                }
+            }
+            const float z = -16.f - (float)(now[r].z >> nibble & 15u);
+            acc[r] = __builtin_fmaf(lq_scale(now[r].s, f16), __builtin_fmaf(z, sum, dot), acc[r]);
+        }
+    }
+    float mine = 0.f;  // lane r: row r
+#pragma unroll
+    for (int r = 0; r < QR_R; ++r) {
+        const float sum = wave_allreduce32(acc[r], [](float x, float y) { return x + y; });
+        if (lane == r) mine = sum;
+    }
+    const int v = first + lane;
+    if (lane < QR_R && v < V) {
+        if (a.out_bf16) static_cast<__bf16*>(a.out)[v] = (__bf16)mine;  // rounded once
+        else static_cast<float*>(a.out)[v] = mine;
+    }
+}
+
+template <int GROUP>
+static void launch_rows_t(const QuantArgs& a, hipStream_t st, const LaunchEvents& le) {
+    const size_t lds = (size_t)a.K * 2 + (size_t)(a.K / 32) * 4;
+    const dim3 grid((a.V + QR_ROWS - 1) / QR_ROWS);
+    if (le.start(0))
+        hipExtLaunchKernelGGL((k_quant_rows<GROUP>), grid, dim3(QR_NT), lds, st, le.start(0),
+                              le.stop(0), 0, a);
+    else
+        hipLaunchKernelGGL((k_quant_rows<GROUP>), grid, dim3(QR_NT), lds, st, a);
+}
+
 template <int GROUP>
 static void launch_quant_g(const QuantArgs& a, hipStream_t st, const LaunchEvents& le) {
+    // One row: whole rows by v_dot2, where at least four fifths of the lanes have k
+    // to read: V = 128256, K = 4096, groups of 32: 59 us (matrix cores: 105), K = 8192,
+    // groups of 128: 111 (127), V = 32000, K = 2048: 10.2 (14.1); K = 4160, of three
+    // chunks the last nearly empty: 40 (36).
+    const int chunks = (a.K + QR_K - 1) / QR_K;
+    if (a.B == 1 && (int64_t)a.K * 5 >= (int64_t)chunks * QR_K * 4 && a.K <= QR_MOST_K) {
+        launch_rows_t<GROUP>(a, st, le);
+        return;
+    }
+    // Fewer, larger workgroups share a stage of x and widen a weight for more batch
+    // rows; where they are fewer than the CUs, smaller ones, with K in two ranges
+    // where those are still few.
     if (a.B <= 16) {
-        // 64 rows a workgroup; where those are fewer than two a CU, twice the
-        // waves, half of K each
+        // V = 20000, K = 4096: 17.0 us (one range: 21), V = 50257: 44.8 (40.0)
         if (a.V <= 32768) launch_quant_t<GROUP, 1, 1, 2, 8, 2, 2>(a, st, le);
         else launch_quant_t<GROUP, 1, 1, 1, 4, 2, 2>(a, st, le);
     } else if (a.B <= 32) {
-        launch_quant_t<GROUP, 2, 2, 1, 8, 2, 2>(a, st, le);
-    } else if (a.V <= 65536) {
-        launch_quant_t<GROUP, 4, 2, 1, 4, 1, 2>(a, st, le);
-    } else {
-        launch_quant_t<GROUP, 4, 2, 1, 8, 1, 3>(a, st, le);
+        // V = 32000, K = 2048: 16.8 us (one range: 22.9), V = 50257, K = 4160: 57.7 (46.5)
+        if (a.V <= 32768) launch_quant_t<GROUP, 2, 1, 2, 8, 1, 2>(a, st, le);
+        else launch_quant_t<GROUP, 2, 2, 1, 4, 2, 2>(a, st, le);
+    } else if (a.V <= 12288) {
+        // V = 8000, K = 4096: 19.8 us (one range: 27.2)
+        launch_quant_t<GROUP, 4, 1, 2, 8, 1, 2>(a, st, le);
+    } else if (a.V <= 32768 || GROUP == 32) {
+        // V = 32000, K = 2048: 25.3 us (two row tiles a wave: 28.7). Groups of 32 end
+        // with every MFMA: with two row tiles their accumulators do not fit.
+        launch_quant_t<GROUP, 4, 1, 1, 4, 1, 2>(a, st, le);
+    } else if constexpr (GROUP >= 64) {
+        // V = 50257, K = 4160: 63 us (256 rows: 64); V = 128256: 256 rows a workgroup,
+        // K = 8192, groups of 128: 250 us (128 rows: 268), by whole lines (half lines: 269);
+        // K = 4096, groups of 64: 154 by half lines (220)
+        if (a.V <= 65536) launch_quant_t<GROUP, 4, 2, 1, 4, 1, 2>(a, st, le);
+        else if constexpr (GROUP == 128) launch_quant_t<GROUP, 4, 2, 1, 8, 2, 2>(a, st, le);
+        else launch_quant_t<GROUP, 4, 2, 1, 8, 1, 3>(a, st, le);
     }
 }
 

@@ -57,6 +57,27 @@ def call(sampler, x, q, s, z, group, **kw):
     (20, 33000, 256, 128, True, "f16", "f32"),
     (40, 70001, 192, 64, False, "f16", "f32"),
     (5, 130001, 128, 32, False, "f16", "f32"),
+    # every choice of tiles, at sizes on both sides of its rule
+    (64, 12288, 448, 64, True, "f16", "f32"),
+    (36, 12289, 448, 128, True, "f16", "f32"),
+    (40, 32768, 192, 32, True, "bf16", "f32"),
+    (33, 40001, 256, 32, True, "f16", "f32"),
+    (50, 40001, 192, 64, True, "f16", "f32"),
+    (64, 65537, 320, 128, True, "f16", "f32"),
+    (35, 65600, 576, 64, True, "f16", "bf16"),
+    (17, 32768, 448, 64, False, "f16", "f32"),
+    (31, 32769, 704, 32, True, "bf16", "f32"),
+    (16, 32769, 1088, 64, True, "f16", "f32"),
+    (2, 32767, 704, 128, True, "f16", "f32"),
+    # one row: whole rows where the lanes are used, else the tiles
+    (1, 301, 2048, 64, False, "f16", "f32"),
+    (1, 18, 4096, 128, True, "bf16", "bf16"),
+    (1, 5, 1664, 32, True, "f16", "f32"),
+    (1, 37, 1600, 32, True, "f16", "f32"),
+    (1, 33, 24576, 128, True, "f16", "f32"),
+    (1, 3, 24640, 64, True, "f16", "f32"),
+    (1, 1, 3776, 128, True, "f16", "f32"),
+    (64, 16, 24640, 128, True, "f16", "f32"),
 ])
 def test_matches_the_oracle(B, V, K, group, zeros, scale, out):
     log(f"quant: B={B} V={V} K={K} group={group} zeros={zeros} {scale} {out}")
