@@ -426,13 +426,13 @@ ss_status ss_spec_verify_probs(ss_sampler* s, const void* target_probs, ss_dtype
  *                 >= V; entries behind V are left as they were.
  * out[b, v] = sum over groups of scale (sum over k of (n - zero) hidden[b, k]).
  * Nothing is rounded below binary32 before the output: products are exact, sums
- * and scales binary32. A row depends on its own hidden states only, and the
- * result is the same at every call. The logits are what ss_sample and
- * ss_spec_verify read. One kernel.
+ * and scales binary32. A row depends on its own hidden states only, and calls of
+ * one shape give the same bits (B chooses the tiles, so another B may round
+ * differently). The logits are what ss_sample and ss_spec_verify read. One kernel.
  * Errors: SS_ERR_INVALID_ARG for a null handle, a handle created with
  * hidden_size 0, B out of range, a null pointer, another dtype, out_stride < V,
  * or scales / out_logits not element-aligned; SS_ERR_UNSUPPORTED for another
- * group or hidden / qweight not 16-byte aligned. */
+ * group, K above 2^24, or hidden / qweight not 16-byte aligned. */
 ss_status ss_lmhead_quant_logits(ss_sampler* s, const uint16_t* hidden, const uint8_t* qweight,
                                  const uint16_t* scales, ss_dtype scale_dtype,
                                  const uint8_t* zeros, int32_t group, int32_t B, void* out_logits,
@@ -455,7 +455,10 @@ ss_status ss_lmhead_quant_logits(ss_sampler* s, const uint16_t* hidden, const ui
  * and counts and lengths of 0. A negative or too large entry counts as no page.
  *
  * As for a sampler handle: calls only enqueue work, may be captured in a graph,
- * and a cache handle (its workspace) serves one stream at a time. */
+ * and calls on one handle must not overlap in time (its workspace, counters
+ * among it, serves one call after the other; graphs captured from one handle are
+ * replayed one after the other). Outputs must not overlap inputs, but for base,
+ * which may be t->len. */
 typedef struct ss_cache ss_cache; /* opaque; owns its workspace, not the planes */
 
 typedef struct {
@@ -463,7 +466,8 @@ typedef struct {
     int32_t num_pages;   /* 1 .. 4194304 */
     int32_t page_size;   /* slots per page, 1 .. 65536 */
     int32_t heads;       /* pieces per slot, >= 1; heads * piece_bytes <= 2^24 */
-    int32_t piece_bytes; /* >= 1; a page of one plane holds less than 2^31 bytes */
+    int32_t piece_bytes; /* >= 1; a page of one plane and a slot of all planes hold
+                            less than 2^31 bytes each */
     int64_t page_stride; /* bytes between pages, slots and heads: any order, as long */
     int64_t slot_stride; /*   as no two pieces overlap; a dimension of one entry may */
     int64_t head_stride; /*   have any stride */
@@ -496,7 +500,7 @@ int64_t ss_cache_workspace_bytes(const ss_cache* c);
 
 /* ss_cache_reserve -- make slots [base_b, base_b + add_b) of rows 0 .. B-1 writable.
  *   base    [B] int32, or NULL: t->len.   add  [B] int32 >= 0.
- *   out_ok  NULL, or [B] int32: 1 served (add = 0 always is), 0 refused.
+ *   out_ok  NULL, or [B] int32: 1 served (add = 0 at base >= 0 always is), 0 refused.
  * Every table entry those slots lie on that holds no page, or one that others
  * hold as well, gets a fresh page; of a shared page that holds slots before
  * base_b those slots are copied along (all planes), and its count falls by one.

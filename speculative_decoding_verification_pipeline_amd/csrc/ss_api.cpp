@@ -614,6 +614,7 @@ ss_status ss_lmhead_quant_logits(ss_sampler* s, const uint16_t* hidden, const ui
         (reinterpret_cast<uintptr_t>(out_logits) & (out_dtype == SS_F32 ? 3u : 1u)))
         return SS_ERR_INVALID_ARG;
     if (group != 32 && group != 64 && group != 128) return SS_ERR_UNSUPPORTED;
+    if (s->cfg.hidden_size > (1 << 24)) return SS_ERR_UNSUPPORTED;  // 32-bit offsets within a tile
     if (!aligned16(hidden) || !aligned16(qweight)) return SS_ERR_UNSUPPORTED;
     ss::QuantArgs a;
     std::memset(&a, 0, sizeof(a));

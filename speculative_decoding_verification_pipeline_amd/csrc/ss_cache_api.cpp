@@ -35,6 +35,7 @@ bool bad_config(const ss_cache_config* c) {
     if ((int64_t)c->max_batch * c->max_blocks > INT32_MAX) return true;
     if ((int64_t)c->max_blocks * c->page_size > INT32_MAX) return true;  // lengths are 32 bits
     if ((int64_t)c->heads * c->piece_bytes > (1 << 24)) return true;
+    if ((int64_t)c->num_planes * c->heads * c->piece_bytes > INT32_MAX) return true;
     if ((int64_t)c->page_size * c->heads * c->piece_bytes > INT32_MAX) return true;
     // Every piece of a plane has bytes of its own: the strides, sorted, each
     // span what lies within them.

@@ -46,6 +46,8 @@ GOOD = dict(num_planes=2, num_pages=8, page_size=4, heads=2, piece_bytes=16, pag
     {"head_stride": 15}, {"slot_stride": 31}, {"page_stride": 127}, {"page_stride": 32},
     {"max_batch": 65535, "max_blocks": 65535}, {"page_size": 4096, "max_blocks": 1 << 20},
     {"page_stride": 1 << 60},
+    {"num_planes": 4096, "heads": 1024, "piece_bytes": 1024, "page_size": 1, "num_pages": 1,
+     "head_stride": 1024},
 ])
 def test_cache_create_rejects_bad_shapes_before_touching_hip(lib, change):
     cfg = SM.CacheConfig(**{**GOOD, **change})

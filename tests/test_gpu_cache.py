@@ -298,6 +298,54 @@ def test_other_stream():
     c.same("other stream", ok2, c.o.commit([3] * 4, nodes.cpu().tolist()))
 
 
+def test_pages_beyond_32_bit_offsets():
+    """A plane of more than 2^32 bytes: its last pages copied, shared, moved."""
+    P, ps = 70000, 16
+    pool = torch.zeros(1, P, ps, 1, 4096, dtype=torch.int8, device=device())
+    for page in (P - 3, P - 2, P - 1):
+        pool[0, page] = torch.randint(-99, 99, (ps, 1, 4096), device=device(), dtype=torch.int8)
+    cache = PageCache(pool, 2, 2)
+    bt = cache.new_tables()
+    before = pool[0, P - 3:].clone()
+    cache.copy_pages(i32([P - 1, P - 2]), i32([5, P - 4]))
+    assert torch.equal(pool[0, 5], before[2]) and torch.equal(pool[0, P - 4], before[1])
+    bt.tables.copy_(i32([[P - 3, P - 2], [-1, -1]]))
+    bt.ref.fill_(1)
+    bt.ref[7] = 0
+    bt.lens[0] = 10
+    cache.fork(bt, i32([0]), i32([1]))
+    assert cache.reserve(bt, i32([0, 3])).cpu().tolist() == [1, 1]
+    assert bt.tables.cpu().tolist() == [[P - 3, P - 2], [7, -1]]
+    assert torch.equal(pool[0, 7, :10], before[0, :10]) and not pool[0, 7, 10:].any()
+    assert cache.commit(bt, i32([1]), nodes=i32([[8, -1, -1, -1, -1, -1, -1, -1, -1]]),
+                        base=i32([14])).cpu().tolist() == [1]  # slot 22 to slot 15
+    assert torch.equal(pool[0, P - 3, 15], before[1, 6])
+    cache.close()
+
+
+def test_two_caches_on_two_streams():
+    """Steps that overlap in time, each on its own cache."""
+    caches = [Pair(2, 32, 4, 2, 8, 4, 6, seed=k) for k in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    add, acc, nodes = i32([9] * 4), i32([3, 1, 0, 2]), i32([[2, 4, 8, -1, -1, -1, -1, -1, -1]] * 4)
+    src, dst, keep = i32([0]), i32([2]), i32([5, 9, 6, 0])
+    torch.cuda.synchronize()
+    for turn in range(3):
+        for c, st in zip(caches, streams):
+            c.cache.reserve(c.bt, add, stream=st)
+            c.cache.commit(c.bt, acc, nodes=nodes, stream=st)
+            c.cache.fork(c.bt, src, dst, stream=st)
+            c.cache.truncate(c.bt, new_len=keep, stream=st)
+    torch.cuda.synchronize()
+    for c in caches:
+        for turn in range(3):
+            c.o.reserve([9] * 4)
+            c.o.commit([3, 1, 0, 2], nodes.cpu().tolist())
+            c.o.fork([0], [2])
+            c.o.truncate([5, 9, 6, 0])
+        c.same("two streams")
+
+
 def test_refusals():
     d = device()
     pool = torch.zeros(2, 8, 4, 2, 8, dtype=torch.int16, device=d)

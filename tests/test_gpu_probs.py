@@ -211,6 +211,44 @@ def test_other_stream_and_partial_batch():
     s.close()
 
 
+def test_two_handles_on_two_streams():
+    """Calls that overlap in time, each with its own handle."""
+    B, G, V = 24, 3, 50000
+    sets = [make(B, G, V, torch.float32, True, True, 60 + k) for k in range(2)]
+    handles = [SM.Sampler(B, V, max_draft=G, device=0) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for turn in range(5):
+        for k in range(2):
+            got[k].append(handles[k].spec_verify_probs(*sets[k][:4], draft_len=sets[k][4],
+                                                       stream=streams[k]))
+    torch.cuda.synchronize()
+    for k in range(2):
+        want = expect(*sets[k])
+        for out, acc in got[k]:
+            assert np.array_equal(out.cpu().numpy(), want[0])
+            assert np.array_equal(acc.cpu().numpy(), want[1])
+        handles[k].close()
+
+
+def test_rows_beyond_32_bit_offsets():
+    """Rows more than 2^31 entries apart from the first."""
+    B, G, V, W = 2, 2, 3000, 450_000_000
+    near = make(B, G, V, torch.bfloat16, True, False, 11)
+
+    def spread(x):
+        R = x.shape[1]
+        flat = torch.zeros((B * R - 1) * W + V, dtype=x.dtype, device=device())
+        far = flat.as_strided((B, R, V), (R * W, W, 1))
+        far.copy_(x)
+        return far
+
+    want = expect(*near)
+    got = run(spread(near[0]), spread(near[1]), *near[2:])
+    assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+
+
 def test_refusals():
     B, G, V = 2, 3, 64
     s = SM.Sampler(B, V, max_draft=G, device=0)

@@ -168,6 +168,24 @@ def test_captured_calls_replay():
     s.close()
 
 
+def test_weights_beyond_32_bit_offsets():
+    """The last vocabulary rows of a weight of more than 2^32 bytes."""
+    V, K, group = 131200, 65536, 128
+    for B in (2, 40):
+        log(f"quant: {V * K // 2} bytes of weights, B={B}")
+        g = torch.Generator(device=device()).manual_seed(B)
+        x = torch.randn(B, K, generator=g, device=device()).bfloat16()
+        q = torch.randint(0, 256, (V, K // 2), generator=g, device=device(), dtype=torch.uint8)
+        sc = (0.01 * torch.rand(V, K // group, generator=g, device=device())).half()
+        z = torch.randint(0, 256, (V, K // group // 2), generator=g, device=device(), dtype=torch.uint8)
+        s = SM.Sampler(B, V, hidden_size=K, device=0)
+        got = s.lmhead_quant_logits(x, q, sc, group, zeros=z)
+        for rows in (slice(0, 3), slice(V - 21, V)):
+            want, bound = expect(x.cpu(), q[rows].cpu(), sc[rows].cpu(), z[rows].cpu(), group)
+            assert np.all(np.abs(got[:, rows].double().cpu().numpy() - want) <= bound)
+        s.close()
+
+
 def test_refusals():
     B, V, K = 4, 100, 128
     x, q, sc, z = make(B, V, K, 32, True, torch.float16)
