@@ -102,8 +102,11 @@ __device__ __forceinline__ u32x4 lq_regroup(u32x4 w) {
 // lanes. With BPS = 2 a row of weights is a whole 128-byte line, read once and
 // not kept (non-temporal); with BPS = 1 its halves come a stage apart, and the
 // line has to stay in L2 meanwhile. In LDS row r's 16-byte unit j lies at
-// 64 BPS r + 16 (j ^ swizzle(r)): sixteen lanes that read one unit of sixteen
-// rows touch every bank once.
+// 64 BPS r + 16 (j ^ swizzle(r)). A read of 16 bytes a lane is served sixteen lanes
+// at a time, and not sixteen in a row: rows 0 .. 3 and 12 .. 15 of one quarter
+// with rows 4 .. 11 of the next. The swizzle spreads those over all banks, whatever
+// unit each of the two quarters reads (bits 0 and 1 of r / 4 are b and c: c, b ^ c
+// from the top; by r / 2 alone a seventh of the time went into conflicts).
 //
 // x of one 16-row tile and stage is four such tiles of 32 BPS k. MFMA i, quarter
 // q of the wave reads the unit that lq_regroup gives it: unit 4 q + i of the
@@ -111,8 +114,13 @@ __device__ __forceinline__ u32x4 lq_regroup(u32x4 w) {
 // (32). The lane's part of that is its offset, the step's part is added, or, in
 // the bits the swizzle uses, goes in by xor.
 template <int BPS>
+__device__ __forceinline__ int lq_swizzle(int r) {
+    const int c = r >> 3 & 1, bc = (r >> 2 & 1) ^ c;
+    return BPS == 2 ? c << 2 | bc << 1 | (r >> 1 & 1) : bc << 1 | c;
+}
+template <int BPS>
 __device__ __forceinline__ uint32_t lq_unit(int r, int j) {
-    return r * 64 * BPS + ((j ^ (BPS == 2 ? r >> 1 : r >> 2)) << 4);
+    return r * 64 * BPS + ((j ^ lq_swizzle<BPS>(r)) << 4);
 }
 template <int GROUP, int BPS>
 __device__ __forceinline__ uint32_t lq_lane_offset(int lane) {
@@ -224,7 +232,7 @@ __global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
     // This lane's place in a copy, as an offset from an address that is the same
     // for the wave: a stage's copies then cost the vector ALU nothing.
     constexpr int LPR = 4 * BPS, RPC = 16 / BPS;  // lanes per row, rows per copy
-    auto unit_of = [&](int row) { return (lane % LPR) ^ (BPS == 2 ? row >> 1 : row >> 2); };
+    auto unit_of = [&](int row) { return (lane % LPR) ^ lq_swizzle<BPS>(row); };
     const uint8_t* wbase[RT];
     uint32_t woff[RT][BPS];
 #pragma unroll
