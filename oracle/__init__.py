@@ -13,6 +13,9 @@ philox    Counter-based Philox4x32-10 generator, written from its published
 pipeline  Per-request logit processing and sampling: penalties, logit bias,
           grammar mask, temperature, top-k, top-p, min-p, inverse-CDF draw.
 spec      Speculative verification by rejection sampling of draft tokens.
+probs     Verification of drafts against probability rows with given uniforms.
+quant     LM-head logits from 4-bit weights with group scales.
+cache     Pages of a key/value cache: reserve, fork, commit, truncate, copy.
 lmhead    LM-head projection followed by Gumbel-max sampling over vocabulary
           tiles with a cross-tile argmax.
 

@@ -211,6 +211,27 @@ def test_other_stream_and_partial_batch():
     s.close()
 
 
+def test_launch_events_bracket_the_kernel():
+    B, G, V = 2, 1, 4000
+    s = SM.Sampler(B, V, max_draft=G, hidden_size=64, device=0)
+    ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    for e in ev:
+        e.record()
+    torch.cuda.synchronize()
+    s.set_launch_events(ev)
+    args = make(B, G, V, torch.float32, True, False, 2)
+    s.spec_verify_probs(*args[:4])
+    torch.cuda.synchronize()
+    assert 0 < ev[0].elapsed_time(ev[1]) < 100
+    x = torch.ones(1, 64, dtype=torch.bfloat16, device=device())
+    s.lmhead_quant_logits(x, torch.zeros(V, 32, dtype=torch.uint8, device=device()),
+                          torch.ones(V, 1, dtype=torch.float16, device=device()), 64)
+    torch.cuda.synchronize()
+    assert 0 < ev[0].elapsed_time(ev[1]) < 100
+    s.set_launch_events(None)
+    s.close()
+
+
 def test_two_handles_on_two_streams():
     """Calls that overlap in time, each with its own handle."""
     B, G, V = 24, 3, 50000
