@@ -537,8 +537,10 @@ ss_status ss_cache_fork(ss_cache* c, const ss_block_tables* t, const int32_t* sr
  * Slot base + nodes[i] moves to base + 1 + i on every plane, and len[b] becomes
  * base + 1 + num_accepted. The pages written must be the row's own, as
  * ss_cache_reserve leaves them. A row is refused (out_ok 0, left as it was) for
- * a negative base, num_accepted outside 0 .. N-1, nodes out of range or not
- * ascending, a slot without a page or behind max_blocks pages. One kernel. */
+ * a negative base, num_accepted outside 0 .. N-1 (linear drafts: negative), nodes
+ * out of range or not ascending, and where a slot of base .. base + num_accepted
+ * or one that moves has no page or lies behind max_blocks pages, so that a row
+ * whose reserve was refused does not grow. One kernel. */
 ss_status ss_cache_commit(ss_cache* c, const ss_block_tables* t, const int32_t* base,
                           const int32_t* nodes, int64_t nodes_stride, int32_t N,
                           const int32_t* num_accepted, int32_t B, int32_t release,

@@ -77,6 +77,8 @@ class Pages:
         ok = []
         for b, n in enumerate(acc):
             good = base[b] >= 0 and n >= 0 and base[b] + 1 + n <= room
+            good = good and all(self.held(self.tables[b][i])
+                                for i in range(base[b] // self.ps, self.pages_of(base[b] + 1 + n)))
             moves = []
             if good and nodes is not None:
                 N = len(nodes[b])

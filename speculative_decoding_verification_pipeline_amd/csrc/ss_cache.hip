@@ -126,8 +126,8 @@ __global__ __launch_bounds__(CA_NT) void k_cache_plan(CacheReserve a) {
     if (base < 0 || add < 0 || (add > 0 && base + add > (int64_t)a.max_blocks * a.page_size)) {
         need = -1;  // refused
     } else if (add > 0) {
-        const int lo = (int)(base / a.page_size);
-        const int hi = (int)((base + add + a.page_size - 1) / a.page_size);
+        const int lo = (int)((unsigned)base / (unsigned)a.page_size);
+        const int hi = (int)((unsigned)(base + add + a.page_size - 1) / (unsigned)a.page_size);
         for (int i0 = lo; i0 < hi; i0 += WAVE) {
             const int i = i0 + lane;
             bool take = false;
@@ -143,7 +143,7 @@ __global__ __launch_bounds__(CA_NT) void k_cache_plan(CacheReserve a) {
             if (i < hi)
                 mark[i] = take ? need + __popcll(m & ((1ull << lane) - 1)) : -1;
             need += __popcll(m);
-            if (i0 == lo && base % a.page_size) carry = __shfl(shared ? page : -1, 0);
+            if (i0 == lo && (unsigned)base % (unsigned)a.page_size) carry = __shfl(shared ? page : -1, 0);
         }
     }
     if (lane == 0) {
@@ -195,13 +195,15 @@ __global__ __launch_bounds__(CA_NT) void k_cache_take(CacheReserve a, CacheCopy 
         const int plane = blockIdx.x - 1;
         char* p = g.dst_planes[plane];
         copy_slots<VEC>(g, p + carry * g.src_page, p + fresh(before) * g.dst_page,
-                        (int)((int64_t)a.base[b] % a.page_size));
+                        (int)((unsigned)a.base[b] % (unsigned)a.page_size));
         return;
     }
     if (tid == 0 && a.out_ok) a.out_ok[b] = ok ? 1 : 0;
     if (!ok || need == 0) return;
-    const int lo = a.base[b] / a.page_size;
-    const int hi = (int)(((int64_t)a.base[b] + a.add[b] + a.page_size - 1) / a.page_size);
+    // not negative, and base + add < 2^31: so k_cache_plan has left it
+    const unsigned base = a.base[b], page_size = a.page_size;
+    const int lo = (int)(base / page_size);
+    const int hi = (int)((base + a.add[b] + page_size - 1) / page_size);
     int32_t* tab = a.t.tables + (int64_t)b * a.t.stride;
     const int32_t* mark = a.ws.mark + (int64_t)b * a.max_blocks;
     for (int i = lo + tid; i < hi; i += CA_NT) {
@@ -233,8 +235,8 @@ __global__ __launch_bounds__(CA_NT) void k_cache_truncate(CacheTruncate a) {
     const int row = a.rows ? a.rows[i] : i;
     if ((unsigned)row >= (unsigned)a.t.rows) return;
     const int keep = a.new_len ? max(a.new_len[i], 0) : 0;
-    const int64_t first = ((int64_t)keep + a.page_size - 1) / a.page_size;
-    if (first < a.max_blocks) release_from(a.t, a.num_pages, a.max_blocks, row, (int)first);
+    const unsigned first = ((unsigned)keep + a.page_size - 1) / (unsigned)a.page_size;
+    if (first < (unsigned)a.max_blocks) release_from(a.t, a.num_pages, a.max_blocks, row, (int)first);
     if (threadIdx.x == 0) atomicMin(&a.t.len[row], keep);
 }
 
@@ -253,12 +255,12 @@ __global__ __launch_bounds__(CA_NT) void k_cache_fork(CacheFork a) {
     if (tid == 0 && a.out_ok) a.out_ok[i] = bad ? 0 : 1;
     if (bad) return;
     const int len = a.t.len[src];
-    const int64_t held = len > 0 ? ((int64_t)len + a.page_size - 1) / a.page_size : 0;
+    const unsigned held = len > 0 ? ((unsigned)len + a.page_size - 1) / (unsigned)a.page_size : 0;
     const int32_t* from = a.t.tables + (int64_t)src * a.t.stride;
     int32_t* to = a.t.tables + (int64_t)dst * a.t.stride;
     for (int k = tid; k < a.max_blocks; k += CA_NT) {
         const int old = to[k];
-        int page = k < held ? from[k] : -1;
+        int page = (unsigned)k < held ? from[k] : -1;
         if (!page_ok(page, a.num_pages)) page = -1;
         if (page >= 0) atomicAdd(&a.t.ref[page], 1);
         if (page_ok(old, a.num_pages)) atomicSub(&a.t.ref[old], 1);
@@ -273,7 +275,9 @@ __global__ __launch_bounds__(CA_NT) void k_cache_fork(CacheFork a) {
 // Whether request b's step can be committed, for every wave of a workgroup:
 // node indices ascend from at least 1 and stay below N (so a row moves towards
 // the front only, and no row is overwritten before it is read), and every slot
-// involved lies on a page the table names. Lane i gets row i's offsets.
+// that is kept or moved lies on a page the table names: a row whose reserve was
+// refused does not grow over pages it never got. Lane i gets row i's offsets.
+// Slots stay below 2^31, so they are divided as 32-bit numbers.
 struct CommitRow {
     bool ok;
     int acc;
@@ -297,17 +301,22 @@ __device__ __forceinline__ CommitRow commit_row(const CacheCommit& a, const Cach
     r.moves = false;
     const int64_t room = (int64_t)a.max_blocks * a.page_size;
     r.ok = base >= 0 && r.acc >= 0 && base + 1 + r.acc <= room && (!a.nodes || r.acc < a.N);
-    if (!r.ok || !a.nodes) return r;
+    if (!r.ok) return r;
+    const int32_t* tab = a.t.tables + (int64_t)b * a.t.stride;
+    const unsigned page_size = a.page_size;
+    const unsigned last = ((unsigned)base + r.acc) / page_size;
     bool bad = false;
-    if (lane < r.acc) {
-        bad = node <= prev || node >= a.N || base + node >= room;
-        if (!bad && node != lane + 1) {
-            const int64_t s = base + node, d = base + 1 + lane;
-            const int32_t* tab = a.t.tables + (int64_t)b * a.t.stride;
-            const int sp = tab[s / a.page_size], dp = tab[d / a.page_size];
-            bad = !page_ok(sp, a.num_pages) || !page_ok(dp, a.num_pages);
-            r.src = sp * g.src_page + (s % a.page_size) * g.src_slot;
-            r.dst = dp * g.dst_page + (d % a.page_size) * g.dst_slot;
+    for (unsigned i = (unsigned)base / page_size + lane; i <= last; i += WAVE)
+        bad |= !page_ok(tab[i], a.num_pages);
+    if (a.nodes && lane < r.acc) {
+        if (node <= prev || node >= a.N || base + node >= room) {
+            bad = true;
+        } else if (node != lane + 1) {
+            const unsigned s = (unsigned)base + node, d = (unsigned)base + 1 + lane;
+            const int sp = tab[s / page_size], dp = tab[d / page_size];
+            bad |= !page_ok(sp, a.num_pages) || !page_ok(dp, a.num_pages);
+            r.src = sp * g.src_page + (s % page_size) * g.src_slot;
+            r.dst = dp * g.dst_page + (d % page_size) * g.dst_slot;
             r.moves = true;
         }
     }
@@ -332,7 +341,8 @@ __global__ __launch_bounds__(CA_NT) void k_cache_commit(CacheCommit a, CacheCopy
     const bool on = plane < (unsigned)a.num_planes;
     char* p = on ? g.dst_planes[plane] : nullptr;
     const CommitRow r = commit_row(a, g, b);
-    // every wave has its loads: their values have decided r
+    // every wave has its loads before the workgroup is counted
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (threadIdx.x == 0) {
         int32_t* arrived = a.arrived + b * CACHE_COUNTER;
@@ -368,7 +378,7 @@ __global__ __launch_bounds__(CA_NT) void k_cache_commit(CacheCommit a, CacheCopy
     if (threadIdx.x == 0) a.t.len[b] = len;
     if (a.release)
         release_from(a.t, a.num_pages, a.max_blocks, b,
-                     (int)(((int64_t)len + a.page_size - 1) / a.page_size));
+                     (int)(((unsigned)len + a.page_size - 1) / (unsigned)a.page_size));
 }
 
 // ---------------------------------------------------------------------------

@@ -192,6 +192,21 @@ def test_commit_refusals_and_identity():
     c.commit([1] * 8, [[2, 0, 0]] * 8, base=[16] * 8)  # a slot behind the table
 
 
+@pytest.mark.parametrize("linear", [True, False])
+def test_a_refused_reserve_does_not_grow(linear):
+    """What a step keeps has to lie on pages: a row that got none is left as it was."""
+    c = Pair(2, 7, 2, 1, 8, 4, 300)
+    c.reserve([5, 9, 3, 2])      # rows 1 .. 3 do not fit any more
+    nodes = None if linear else [[1, 2, 3, -1]] * 4
+    c.commit([3, 3, 2, 0], nodes)
+    assert c.o.lens == [4, 0, 0, 0]
+    c.reserve([2, 0, 0, 0])
+    c.commit([2, 0, 0, 0], None if linear else [[1, 2, 3, -1]] * 4)  # the last slot's page is missing
+    assert c.o.lens == [4, 0, 0, 0]
+    c.commit([590, 598, 0, 0])   # many pages, most of them missing
+    assert c.o.lens == [4, 0, 0, 0]
+
+
 def test_commit_of_the_widest_tree():
     """64 nodes: moves in several batches, each row's slots read before they are overwritten."""
     c = Pair(2, 60, 16, 2, 8, 3, 8)

@@ -84,7 +84,7 @@ def test_pages_refusals():
     assert c.reserve([4, 4, 2]) == [1, 0, 0]        # one free page left, row 1 needs two
     assert c.reserve([4, -1, 2]) == [1, 0, 1] and c.consistent()
     assert c.fork([0, 0, 1], [1, 2, 0]) == [0, 1, 0]  # rows 0 and 1 are sources as well
-    assert c.commit([0, 5, 9]) == [1, 1, 0]
+    assert c.commit([0, 5, 9]) == [1, 0, 0]         # row 1 holds no pages; row 2's 9 lie behind them
     assert c.commit([1], nodes=[[2, -1, 0]], base=[6]) == [0]
     assert c.commit([2], nodes=[[2, 2, 0]], base=[0]) == [0]
     assert c.copy_pages([0, 1, 2, 9], [1, 2, 2, 0]) == [0, 0, 0, 0]
