@@ -487,7 +487,8 @@ typedef struct {
 } ss_block_tables;
 
 /* Creates a cache handle (the only call that allocates). planes: HOST array of
- * num_planes device pointers, read during the call. Vectors of 16 bytes are
+ * num_planes device pointers, read during the call; planes must not share bytes
+ * (one named twice is SS_ERR_INVALID_ARG). Vectors of 16 bytes are
  * copied where every plane, stride and piece is a multiple of 16, else of 4 or 1.
  * Errors as ss_sampler_create. */
 ss_status ss_cache_create(const ss_cache_config* cfg, void* const* planes, ss_cache** out);

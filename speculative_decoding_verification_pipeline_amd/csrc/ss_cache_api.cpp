@@ -119,6 +119,9 @@ ss_status ss_cache_create(const ss_cache_config* cfg, void* const* planes, ss_ca
     for (int i = 0; i < cfg->num_planes; ++i) {
         if (!planes[i]) return SS_ERR_INVALID_ARG;
         low |= (uint64_t)reinterpret_cast<uintptr_t>(planes[i]);
+        // a plane named twice would be moved twice, by workgroups that do not wait
+        for (int j = 0; j < i; ++j)
+            if (planes[j] == planes[i]) return SS_ERR_INVALID_ARG;
     }
     int ndev = 0;
     if (hipGetDeviceCount(&ndev) != hipSuccess || cfg->device >= ndev) return SS_ERR_HIP;

@@ -51,7 +51,7 @@ GOOD = dict(num_planes=2, num_pages=8, page_size=4, heads=2, piece_bytes=16, pag
 ])
 def test_cache_create_rejects_bad_shapes_before_touching_hip(lib, change):
     cfg = SM.CacheConfig(**{**GOOD, **change})
-    planes = (ctypes.c_void_p * 4097)(*[64] * 4097)
+    planes = (ctypes.c_void_p * 4097)(*range(64, 64 * 4098, 64))
     h = ctypes.c_void_p()
     assert lib.ss_cache_create(ctypes.byref(cfg), planes, ctypes.byref(h)) == SM.SS_ERR_INVALID_ARG
     assert not h.value
@@ -64,6 +64,15 @@ def test_cache_create_rejects_null_pointers(lib):
     for c, p, o in ((None, planes, ctypes.byref(h)), (ctypes.byref(cfg), None, ctypes.byref(h)),
                     (ctypes.byref(cfg), planes, None), (ctypes.byref(cfg), planes, ctypes.byref(h))):
         assert lib.ss_cache_create(c, p, o) == SM.SS_ERR_INVALID_ARG
+
+
+def test_cache_create_rejects_a_plane_named_twice(lib):
+    cfg = SM.CacheConfig(**{**GOOD, "num_planes": 3})
+    h = ctypes.c_void_p()
+    for at in ([4096, 8192, 4096], [64, 64, 128]):
+        planes = (ctypes.c_void_p * 3)(*at)
+        assert lib.ss_cache_create(ctypes.byref(cfg), planes, ctypes.byref(h)) == SM.SS_ERR_INVALID_ARG
+        assert not h.value
 
 
 def test_page_cache_takes_device_planes_only(lib):
