@@ -404,7 +404,7 @@ ss_status ss_lmhead_sample_params(ss_sampler* s, const uint16_t* hidden, const u
  * replayed one after the other).
  * Errors: SS_ERR_INVALID_ARG for a null handle, B or G out of range, another
  * dtype, a null or misaligned pointer, a stride below V, or a seq that
- * ss_spec_verify_scatter would refuse. */
+ * ss_spec_verify_scatter would refuse; SS_ERR_UNSUPPORTED for B above 65535. */
 ss_status ss_spec_verify_probs(ss_sampler* s, const void* target_probs, ss_dtype dtype,
                                int64_t target_stride, const void* draft_probs,
                                int64_t draft_stride, const int32_t* draft_tokens,

@@ -560,6 +560,7 @@ ss_status ss_spec_verify_probs(ss_sampler* s, const void* target_probs, ss_dtype
     if (G < 0 || G > s->cfg.max_draft) return SS_ERR_INVALID_ARG;
     if (dtype != SS_F32 && dtype != SS_BF16 && dtype != SS_F16) return SS_ERR_INVALID_ARG;
     if (B == 0) return SS_OK;
+    if (B > 65535) return SS_ERR_UNSUPPORTED;  // the grid's second dimension
     const int V = s->cfg.vocab_size;
     const uintptr_t low = dtype == SS_F32 ? 3u : 1u;
     if (!target_probs || (reinterpret_cast<uintptr_t>(target_probs) & low) || target_stride < V)

@@ -313,3 +313,21 @@ def test_refusals():
     assert np.array_equal(s.spec_verify_probs(**good)[0].cpu().numpy(),
                           expect(target, draft, tokens, u, n)[0])
     s.close()
+
+
+def test_the_most_requests():
+    """65535 requests are verified in one call, more are refused."""
+    B, V = 65536, 5
+    s = SM.Sampler(B, V, max_draft=0, device=device().index or 0)
+    p = torch.rand(B, 1, V, generator=torch.Generator().manual_seed(3)).to(device())
+    u = torch.rand(B, 1, generator=torch.Generator().manual_seed(4)).to(device())
+    none = torch.empty(B, 0, dtype=torch.int32, device=device())
+    log("probs: 65535 requests")
+    got, acc = s.spec_verify_probs(p[:-1], None, none[:-1], u[:-1])
+    cum = p[:-1, 0].double().cumsum(1)
+    assert torch.equal(got, (cum <= u[:-1].double() * cum[:, -1:]).sum(1, keepdim=True).int())
+    assert not acc.any()
+    with pytest.raises(SM.SamplerError) as e:
+        s.spec_verify_probs(p, None, none, u)
+    assert e.value.status == SM.SS_ERR_UNSUPPORTED
+    s.close()
