@@ -18,9 +18,9 @@
 //  * v_mfma_f32_16x16x32_bf16 with x as the A operand (batch rows) and W as B
 //    (vocabulary rows as columns): a lane's accumulators then belong to the
 //    vocabulary row whose weights it widens, so the scale is one value per lane
-//    and row tile, straight from memory.
+//    and row tile.
 //  * Operands go from memory to LDS by global_load_lds_dwordx4, S - 1 stages of
-//    128 k ahead, so the stream stays in flight without registers. Each stage is
+//    128 BPS k ahead, so the stream stays in flight without registers. Each stage is
 //    an LDS object of its own: the compiler then orders a read against the
 //    copies into its own stage only, which the explicit wait has seen land. A
 //    wave copies the weights it uses and its share of x. What lies behind K is
@@ -30,7 +30,7 @@
 //    MFMAs: for groups of 128 as they are, for groups of 64 and 32 after
 //    exchanging words between the lanes that hold the same row (permlane
 //    swaps), so that no MFMA crosses a group.
-//  * Four waves: RW row blocks of RT tiles by KW ranges of K, whose sums are
+//  * WAVES waves: RW row blocks of RT tiles by KW ranges of K, whose sums are
 //    added in a fixed order through LDS.
 #include <type_traits>
 #include <utility>
@@ -43,7 +43,6 @@ namespace ss {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
 
 constexpr int LQ_KB = 128;   // k per block: 16 bytes of weights per lane and row tile
 
@@ -401,9 +400,14 @@ __global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
             const int j = j0 + u;
             if (j >= stages) return;
             // this stage has landed for every wave, and the one before has been read
+            asm volatile("" ::: "memory");
             if (j + S - 1 <= stages) __builtin_amdgcn_s_waitcnt(lq_wait((S - 2) * COPIES));
             else __builtin_amdgcn_s_waitcnt(lq_wait(0));
+            // the builtins say nothing about memory: no access may cross them (1% at
+            // B = 64, V = 128256, K = 8192)
+            asm volatile("" ::: "memory");
             __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
             uint8_t* const bufs[4] = {b0, b1, b2, b3};
             if (u % SET == 0) {
 #pragma unroll
