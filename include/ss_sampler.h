@@ -428,7 +428,8 @@ ss_status ss_spec_verify_probs(ss_sampler* s, const void* target_probs, ss_dtype
  * Nothing is rounded below binary32 before the output: products are exact, sums
  * and scales binary32. A row depends on its own hidden states only, and calls of
  * one shape give the same bits (B chooses the tiles, so another B may round
- * differently). The logits are what ss_sample and ss_spec_verify read. One kernel.
+ * differently). The logits are what ss_sample and ss_spec_verify read. One kernel;
+ * it counts in the handle's workspace, as ss_spec_verify_probs does.
  * Errors: SS_ERR_INVALID_ARG for a null handle, a handle created with
  * hidden_size 0, B out of range, a null pointer, another dtype, out_stride < V,
  * or scales / out_logits not element-aligned; SS_ERR_UNSUPPORTED for another

@@ -29,6 +29,8 @@ struct ss_sampler {
     ss::LmCut* lm_cut;
     double* probs_part;      // [max_batch * n_wt]
     int32_t* probs_arrived;  // [max_batch * PROBS_COUNTER]: 0 between calls
+    uint64_t* quant_part;    // [QUANT_CUS * QUANT_PART_BYTES]
+    int32_t* quant_arrived;  // [QUANT_CUS * QUANT_COUNTER]: 0 between calls
     ss::LaunchEvents events;
     // defaults substituted for absent per-request parameters, [max_batch] each
     int32_t* def_zero_i;
@@ -289,8 +291,11 @@ ss_status ss_sampler_create(const ss_sampler_config* cfg, ss_sampler** out) {
     const int64_t o_lmunres = cfg->hidden_size > 0 ? take(64 * 4) : 0;
     const int64_t o_lmcut = cfg->hidden_size > 0 ? take(64 * (int64_t)sizeof(ss::LmCut)) : 0;
     const int64_t o_probs = take((int64_t)B * nw * (int64_t)sizeof(double));
+    const int64_t o_quant = cfg->hidden_size > 0 ? take(ss::QUANT_CUS * ss::QUANT_PART_BYTES) : 0;
     // counters of 0, filled together with the defaults
-    const int64_t o_defaults = take((4 + ss::PROBS_COUNTER) * (int64_t)B * 4);
+    const size_t n_quant = cfg->hidden_size > 0 ? ss::QUANT_CUS * ss::QUANT_COUNTER : 0;
+    const size_t n_filled = (4 + ss::PROBS_COUNTER) * (size_t)B + n_quant;
+    const int64_t o_defaults = take((int64_t)n_filled * 4);
     s->ws_bytes = off;
     if (hipMalloc(&s->ws_base, (size_t)off) != hipSuccess) {
         (void)hipGetLastError();
@@ -324,8 +329,10 @@ ss_status ss_sampler_create(const ss_sampler_config* cfg, ss_sampler** out) {
         s->def_zero_f = reinterpret_cast<float*>(d + B);
         s->def_one_f = reinterpret_cast<float*>(d + 2 * B);
         s->def_iota = d + 3 * B;
-        s->probs_arrived = d + 4 * B;
-        int32_t* h = new (std::nothrow) int32_t[(4 + ss::PROBS_COUNTER) * (size_t)B]();
+        s->probs_arrived = d + 4 * (size_t)B;
+        s->quant_part = cfg->hidden_size > 0 ? reinterpret_cast<uint64_t*>(b + o_quant) : nullptr;
+        s->quant_arrived = s->probs_arrived + ss::PROBS_COUNTER * (size_t)B;
+        int32_t* h = new (std::nothrow) int32_t[n_filled]();
         if (!h) {
             (void)hipFree(s->ws_base);
             delete s;
@@ -338,7 +345,7 @@ ss_status ss_sampler_create(const ss_sampler_config* cfg, ss_sampler** out) {
             std::memcpy(&h[2 * B + i], &one, 4);
             h[3 * B + i] = i;
         }
-        const bool ok = hipMemcpy(d, h, (4 + ss::PROBS_COUNTER) * (size_t)B * 4, hipMemcpyHostToDevice) == hipSuccess;
+        const bool ok = hipMemcpy(d, h, n_filled * 4, hipMemcpyHostToDevice) == hipSuccess;
         delete[] h;
         if (!ok) {
             (void)hipFree(s->ws_base);
@@ -631,6 +638,8 @@ ss_status ss_lmhead_quant_logits(ss_sampler* s, const uint16_t* hidden, const ui
     a.out = out_logits;
     a.out_bf16 = out_dtype == SS_BF16;
     a.out_stride = out_stride;
+    a.part = s->quant_part;
+    a.arrived = s->quant_arrived;
     ss::DeviceGuard guard(s->cfg.device);
     if (!guard.ok) return SS_ERR_HIP;
     return ss::launch_quant(a, static_cast<hipStream_t>(stream), s->events) == hipSuccess

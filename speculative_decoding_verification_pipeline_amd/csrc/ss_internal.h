@@ -246,6 +246,18 @@ struct QuantArgs {
     void* out;
     int out_bf16;
     int64_t out_stride;
+    // row blocks whose K is cut in parts, behind the whole ones (set by the launch)
+    int whole_blocks, split_blocks, split, split_stages;
+    uint64_t* part;            // [QUANT_CUS * QUANT_PART_BYTES]: the parts' sums
+    int32_t* arrived;          // [QUANT_CUS * QUANT_COUNTER]: parts of each row block that have left
+                               //   their sums; 0 between calls
+};
+constexpr int QUANT_CUS = 256;
+constexpr int QUANT_COUNTER = 64;  // integers between counters
+constexpr int QUANT_SPLIT = 8;     // parts of a row block at most; of all, one a CU
+constexpr int64_t QUANT_PART_BYTES = 64 << 10;  // one part's sums at most
+struct QuantSplit {
+    int whole_blocks, split_blocks, split, sets;
 };
 
 // ---------------------------------------------------------------------------

@@ -30,6 +30,8 @@
 //    MFMAs: for groups of 128 as they are, for groups of 64 and 32 after
 //    exchanging words between the lanes that hold the same row (permlane
 //    swaps), so that no MFMA crosses a group.
+//  * The row blocks left over beyond a multiple of the CUs are cut along K between
+//    workgroups; the one that arrives last adds the parts, in order.
 //  * WAVES waves: RW row blocks of RT tiles by KW ranges of K, whose sums are
 //    added in a fixed order through LDS.
 #include <type_traits>
@@ -98,8 +100,8 @@ __device__ __forceinline__ u32x4 lq_regroup(u32x4 w) {
 
 // A stage holds BPS blocks of 128 k. A copy moves rows of 64 BPS bytes, 16 / BPS
 // of them, consecutive lanes a row: memory requests are formed over consecutive
-// lanes. With BPS = 2 a row of weights is a whole 128-byte line, read once and
-// not kept (non-temporal); with BPS = 1 its halves come a stage apart, and the
+// lanes. With BPS = 2 a row of weights is a whole 128-byte line (K a multiple of
+// 256), read once and not kept (non-temporal); with BPS = 1 its halves come a stage apart, and the
 // line has to stay in L2 meanwhile. In LDS row r's 16-byte unit j lies at
 // 64 BPS r + 16 (j ^ swizzle(r)). A read of 16 bytes a lane is served sixteen lanes
 // at a time, and not sixteen in a row: rows 0 .. 3 and 12 .. 15 of one quarter
@@ -171,6 +173,10 @@ __device__ __forceinline__ void lq_each(F& f, std::integer_sequence<int, I...>) 
     (f(std::integral_constant<int, I>{}), ...);
 }
 
+__device__ __forceinline__ uint64_t lq_pair(float lo, float hi) {
+    return (uint64_t)__float_as_uint(hi) << 32 | __float_as_uint(lo);
+}
+
 __device__ const u32x4 lq_zero = {0u, 0u, 0u, 0u};
 
 template <int GROUP, int NT, int RT, int KW, int WAVES, int BPS, int S>
@@ -201,17 +207,22 @@ __global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
     const int rw = wave % RW, kw = wave / RW;
     const int r16 = lane & 15, quarter = lane >> 4;
     const int K = a.K, V = a.V;
-    const int row0 = blockIdx.x * ROWS + rw * RT * 16;
+    // the first workgroups take a part of K of one of the last row blocks each
+    const bool part = KW == 1 && (int)blockIdx.x < a.split_blocks * a.split;
+    const int row_block = part ? a.whole_blocks + blockIdx.x / a.split : blockIdx.x - a.split_blocks * a.split;
+    const int row0 = row_block * ROWS + rw * RT * 16;
     const int n_groups = (K + GROUP - 1) / GROUP;
     // stages of a range: whole sets where there are several ranges
     const int all = (K + LQ_KB * BPS - 1) / (LQ_KB * BPS);
-    const int stages = KW == 1 ? all : ((all + KW - 1) / KW + SET - 1) / SET * SET;
-    const int first_stage = kw * stages;
+    const int start = part ? blockIdx.x % a.split * a.split_stages : 0;
+    const int stages = KW > 1 ? ((all + KW - 1) / KW + SET - 1) / SET * SET
+                       : part ? min(a.split_stages, all - start) : all;
+    const int first_stage = KW > 1 ? kw * stages : start;
     // Each workgroup starts at a set of its own, so that the rows that are read
     // at the same time are read at different places: rows a power of two apart
     // would otherwise meet in the same memory channels. A last, partial set
     // stays last.
-    const int whole_sets = (KW == 1 ? all : stages) / SET;
+    const int whole_sets = stages / SET;
     const int turn = (int)((blockIdx.x * 2654435761u >> 8) % (unsigned)max(whole_sets, 1));
     auto place = [&](int j) {
         int set = j / SET;
@@ -251,6 +262,8 @@ __global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
     const int xu = wave * XC;
     const int xtile = xu / (4 * BPS) % NT, xrange = xu / (4 * BPS * NT);
     const uint8_t* xbase = reinterpret_cast<const uint8_t*>(a.hidden);
+    // lines that hold parts of two copies are kept for the second (K = 4160: 41.7 -> 39.2 us)
+    const bool whole_lines = BPS == 2 && K % 256 == 0;
     uint32_t xoff[BPS];
 #pragma unroll
     for (int c = 0; c < BPS; ++c) {
@@ -266,10 +279,11 @@ __global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
 #pragma unroll
             for (int t = 0; t < RT; ++t)
 #pragma unroll
-                for (int c = 0; c < BPS; ++c)
-                    __builtin_amdgcn_global_load_lds(
-                        (const void*)(wbase[t] + (int64_t)kb * (LQ_KB / 2) + woff[t][c]),
-                        LQ_LDS(ws + t * WT_ + c * 1024), 16, 0, BPS == 2 ? 2 : 0);
+                for (int c = 0; c < BPS; ++c) {
+                    const void* src = wbase[t] + (int64_t)kb * (LQ_KB / 2) + woff[t][c];
+                    if (whole_lines) __builtin_amdgcn_global_load_lds(src, LQ_LDS(ws + t * WT_ + c * 1024), 16, 0, 2);
+                    else __builtin_amdgcn_global_load_lds(src, LQ_LDS(ws + t * WT_ + c * 1024), 16, 0, 0);
+                }
         } else {
 #pragma unroll
             for (int t = 0; t < RT; ++t)
@@ -282,7 +296,7 @@ __global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
                         LQ_LDS(ws + t * WT_ + c * 1024), 16, 0, 0);
                 }
         }
-        const int k0 = (xrange * stages + at) * BPS * LQ_KB;
+        const int k0 = (KW > 1 ? xrange * stages + at : first_stage + at) * BPS * LQ_KB;
         uint8_t* xs = buf + xu * 1024;
 #pragma unroll
         for (int i = 0; i < XC; ++i) {
@@ -457,6 +471,50 @@ __global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
                 for (int n = 0; n < NT; ++n)
                     out[t][n] += s_red[((((k - 1) * RW + rw) * RT + t) * NT + n) * WAVE + lane];
     }
+    if constexpr (KW == 1) {
+        if (part) {  // the parts of K, added in order by the workgroup that is last to leave its own
+            __shared__ int s_last;
+            constexpr int SUMS = WAVES * RT * NT * 2 * WAVE;  // pairs of sums per workgroup
+            const int mine = wave * RT * NT * 2 * WAVE + lane;
+            uint64_t* to = a.part + (int64_t)blockIdx.x * SUMS + mine;
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        __hip_atomic_store(to + ((t * NT + n) * 2 + h) * WAVE,
+                                           lq_pair(out[t][n][2 * h], out[t][n][2 * h + 1]),
+                                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+            if (tid == 0) {
+                int32_t* arrived = a.arrived + (row_block - a.whole_blocks) * QUANT_COUNTER;
+                s_last = __hip_atomic_fetch_add(arrived, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                         a.split - 1;
+                if (s_last) __hip_atomic_store(arrived, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+            __syncthreads();
+            if (!s_last) return;
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) out[t][n] = floatx4{0.f, 0.f, 0.f, 0.f};
+            const uint64_t* from = a.part + (int64_t)(blockIdx.x - blockIdx.x % a.split) * SUMS + mine;
+            for (int p = 0; p < a.split; ++p, from += SUMS)
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint64_t v = __hip_atomic_load(from + ((t * NT + n) * 2 + h) * WAVE,
+                                                                 __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                            out[t][n][2 * h] += __uint_as_float((uint32_t)v);
+                            out[t][n][2 * h + 1] += __uint_as_float((uint32_t)(v >> 32));
+                        }
+        }
+    }
     // a lane holds four batch rows of one vocabulary entry
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
@@ -475,11 +533,46 @@ __global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
     }
 }
 
+// Where a few row blocks are left over beyond a multiple of the CUs, most CUs would
+// wait for those that have one more. These blocks are cut along K, in as many parts
+// as there are CUs for them: B = 64, V = 70000, K = 8192, groups of 128: 190 -> 128 us,
+// B = 20, V = 67000, K = 4096: 61 -> 50, B = 13, V = 50257, K = 4160: 39 -> 37. Where
+// fewer than all whole blocks are resident, late ones fill the gaps by themselves
+// (B = 24, V = 100000: 73, cut 74.5), and with more parts than CUs their sums cost more
+// than they gain (B = 32, V = 50257, 411 parts: 59, uncut 47).
+static QuantSplit quant_split(int blocks, int resident, int sets) {
+    QuantSplit s = {blocks, 0, 1, 0};
+    const int over = blocks % QUANT_CUS;
+    const int rounds = blocks / QUANT_CUS;
+    if (over == 0 || rounds < 1 || (resident > 1 && rounds > resident)) return s;
+    for (int f = 2; f <= QUANT_SPLIT && f <= sets && f * over <= QUANT_CUS; ++f) {
+        const int per = (sets + f - 1) / f;
+        if ((sets + per - 1) / per == f)  // else a part would be empty
+            s = {blocks - over, over, f, per};
+    }
+    return s;
+}
+
 template <int GROUP, int NT, int RT, int KW, int WAVES, int BPS, int S>
 static void launch_quant_t(const QuantArgs& a, hipStream_t st, const LaunchEvents& le) {
     constexpr int rows = WAVES / KW * RT * 16;
-    launch_k(le, 0, k_lmhead_quant<GROUP, NT, RT, KW, WAVES, BPS, S>, dim3((a.V + rows - 1) / rows),
-             dim3(WAVES * WAVE), st, a);
+    const int blocks = (a.V + rows - 1) / rows;
+    QuantArgs b = a;
+    b.whole_blocks = blocks;
+    b.split = 1;
+    if constexpr (KW == 1) {
+        constexpr int GPS = LQ_KB / GROUP * BPS, SET = GPS < 4 ? 4 / GPS : 1;
+        const int all = (a.K + LQ_KB * BPS - 1) / (LQ_KB * BPS);
+        constexpr int LDS = S * BPS * (NT * 4096 + WAVES * RT * 1024);
+        static_assert(WAVES * RT * NT * WAVE * 16 <= QUANT_PART_BYTES, "a part's sums fit the workspace");
+        const QuantSplit s = quant_split(blocks, 160 * 1024 / LDS, (all + SET - 1) / SET);
+        b.whole_blocks = s.whole_blocks;
+        b.split_blocks = s.split_blocks;
+        b.split = s.split;
+        b.split_stages = s.sets * SET;
+    }
+    launch_k(le, 0, k_lmhead_quant<GROUP, NT, RT, KW, WAVES, BPS, S>,
+             dim3(b.whole_blocks + b.split_blocks * b.split), dim3(WAVES * WAVE), st, b);
 }
 
 // ---------------------------------------------------------------------------
@@ -624,27 +717,28 @@ static void launch_quant_g(const QuantArgs& a, hipStream_t st, const LaunchEvent
     // rows; where they are fewer than the CUs, smaller ones, with K in two ranges
     // where those are still few.
     if (a.B <= 16) {
-        // V = 20000, K = 4096: 17.0 us (one range: 21), V = 50257: 44.8 (40.0)
+        // V = 20000, K = 4096: 17.0 us (one range: 19.1), V = 50257, K = 4160: 44.8 (36.8)
         if (a.V <= 32768) launch_quant_t<GROUP, 1, 1, 2, 8, 2, 2>(a, st, le);
         else launch_quant_t<GROUP, 1, 1, 1, 4, 2, 2>(a, st, le);
     } else if (a.B <= 32) {
-        // V = 32000, K = 2048: 16.8 us (one range: 22.9), V = 50257, K = 4160: 57.7 (46.5)
+        // V = 32000, K = 2048: 16.8 us (one range: 22.9), V = 50257, K = 4160: 57.7 (45.1;
+        // two row tiles a wave: 46.2), V = 128256, K = 4096: two row tiles 98 (one: 112)
         if (a.V <= 32768) launch_quant_t<GROUP, 2, 1, 2, 8, 1, 2>(a, st, le);
+        else if (a.V <= 53248) launch_quant_t<GROUP, 2, 1, 1, 4, 2, 2>(a, st, le);
         else launch_quant_t<GROUP, 2, 2, 1, 4, 2, 2>(a, st, le);
     } else if (a.V <= 12288) {
         // V = 8000, K = 4096: 19.8 us (one range: 27.2)
         launch_quant_t<GROUP, 4, 1, 2, 8, 1, 2>(a, st, le);
     } else if (a.V <= 32768 || GROUP == 32) {
-        // V = 32000, K = 2048: 25.3 us (two row tiles a wave: 28.7). Groups of 32 end
+        // V = 32000, K = 2048: 26.5 us (two row tiles a wave: 28.8). Groups of 32 end
         // with every MFMA: with two row tiles their accumulators do not fit.
         launch_quant_t<GROUP, 4, 1, 1, 4, 1, 2>(a, st, le);
     } else if constexpr (GROUP >= 64) {
-        // V = 50257, K = 4160: 63 us (256 rows: 64); V = 128256: 256 rows a workgroup,
-        // K = 8192, groups of 128: 250 us (128 rows: 268), by whole lines (half lines: 269);
-        // K = 4096, groups of 64: 154 by half lines (220)
-        if (a.V <= 65536) launch_quant_t<GROUP, 4, 2, 1, 4, 1, 2>(a, st, le);
+        // V = 66000, K = 4096: 70 us (256 rows a workgroup: 74); groups of 128, by whole
+        // lines: V = 128256: 114 (128 rows: 121), V = 200000: 176 (191); groups of 64 by
+        // half lines, 128 rows: V = 128256: 140 (256 rows: 154, by whole lines 246)
+        if (GROUP == 64 || a.V <= 65536) launch_quant_t<GROUP, 4, 2, 1, 4, 1, 2>(a, st, le);
         else if constexpr (GROUP == 128) launch_quant_t<GROUP, 4, 2, 1, 8, 2, 2>(a, st, le);
-        else launch_quant_t<GROUP, 4, 2, 1, 8, 1, 3>(a, st, le);
     }
 }
 

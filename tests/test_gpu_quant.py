@@ -96,6 +96,53 @@ def test_matches_the_oracle(B, V, K, group, zeros, scale, out):
     s.close()
 
 
+@pytest.mark.parametrize("B,V,K,group", [
+    (13, 32800, 1088, 128),   # one block left over, the last part shorter
+    (8, 40000, 2048, 32),     # nearly half a round left over
+    (16, 33500, 1600, 64),    # as many parts as stages
+    (24, 32900, 1024, 128),
+    (20, 67000, 768, 64),
+    (64, 33500, 1024, 128),
+    (64, 17000, 1024, 64),
+    (33, 50000, 1088, 32),
+    (50, 70000, 1280, 128),
+    (33, 131100, 768, 128),   # behind two whole rounds
+    (9, 32769, 128, 128),     # a single set: not cut
+])
+def test_left_over_row_blocks(B, V, K, group):
+    """Row blocks behind a multiple of the CUs are cut along K between workgroups:
+    eager, again, and in a graph that is replayed with other hidden states."""
+    log(f"quant: left over, B={B} V={V} K={K} group={group}")
+    x, q, sc, z = make(B, V, K, group, True, torch.float16, V + K)
+    s = SM.Sampler(B, V, hidden_size=K, device=0)
+    d = device()
+    xd, qd, sd, zd = x.to(d), q.to(d), sc.to(d), z.to(d)
+    out = torch.empty(B, V, device=d)
+
+    def go(o=None):
+        return s.lmhead_quant_logits(xd, qd, sd, group, zeros=zd, out=o)
+
+    want, bound = expect(x, q, sc, z, group)
+    go(out)
+    got = out.double().cpu().numpy()
+    assert np.all(np.abs(got - want) <= bound)
+    assert np.linalg.norm(got - want) <= 1e-5 * np.linalg.norm(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go(out)
+    for turn in range(4):
+        if turn:
+            xd.copy_(make(B, 1, K, group, False, torch.float16, turn)[0])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, go())
+    xd.copy_(x)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert np.array_equal(out.double().cpu().numpy(), got)
+    s.close()
+
+
 @pytest.mark.parametrize("group", [32, 64, 128])
 def test_every_weight_has_its_place(group):
     """One nonzero x per row: the logit is that weight times its scale, exactly
