@@ -14,7 +14,7 @@ from dataclasses import dataclass
 import torch
 
 from .sampler import (SS_OK, CacheConfig, CBlockTables, _check, _check_array, _check_block,
-                      _check_dev, _check_rows, _require, _stream_on, load_library)
+                      _check_dev, _check_rows, _empty_rows, _require, _stream_on, load_library)
 
 
 @dataclass
@@ -58,7 +58,6 @@ class PageCache:
         self.num_pages, self.page_size = p.shape[0], p.shape[1]
         self.max_batch, self.max_blocks = max_batch, max_blocks
         self.device = p.device.index
-        self._place = p.device
 
     def close(self):
         if getattr(self, "handle", None):
@@ -83,15 +82,16 @@ class PageCache:
         """The tables as the ABI takes them, checked by what costs least; the
         messages are formed on failure only."""
         dev, tab = self.device, t.tables
-        if not (isinstance(tab, torch.Tensor) and tab.dtype is torch.int32 and
-                tab.get_device() == dev and tab.dim() == 2 and tab.is_contiguous() and
-                0 < tab.shape[0] <= self.max_batch and tab.shape[1] >= self.max_blocks):
+        shape = getattr(tab, "shape", ())
+        if not (len(shape) == 2 and isinstance(tab, torch.Tensor) and tab.dtype is torch.int32 and
+                tab.get_device() == dev and tab.is_contiguous() and
+                0 < shape[0] <= self.max_batch and shape[1] >= self.max_blocks):
             _check_rows(tab, "tables", 1, (torch.int32,), dev)
             _require(tab.shape[0] <= self.max_batch and tab.shape[1] >= self.max_blocks,
                      f"tables must be [1 .. {self.max_batch}, >= {self.max_blocks}]")
             _require(tab.shape[0] <= 1 or tab.stride(0) >= self.max_blocks,
                      "tables rows must not overlap")
-        rows, cols = tab.shape
+        rows, cols = shape
         return CBlockTables(tab.data_ptr(), tab.stride(0) if rows > 1 else cols, rows,
                             _check_array(t.ref, "ref", self.num_pages, dev),
                             _check_array(t.lens, "lens", rows, dev))
@@ -105,9 +105,9 @@ class PageCache:
             raise ValueError(f"{name} must be a contiguous 1-D array of at most {most} entries")
         return v.shape[0], v.data_ptr()
 
-    def _ok(self, ok, n):
+    def _ok(self, ok, n, like):
         if ok is None:
-            return torch.empty(n, dtype=torch.int32, device=self._place)
+            return _empty_rows(n, None, like)
         _check_array(ok, "ok", n, self.device)
         return ok
 
@@ -122,7 +122,7 @@ class PageCache:
         ct = self._tables(tables)
         B, add_ptr = self._count(add, "add", ct.rows)
         base = _check_array(lens, "lens", B, self.device)
-        ok = self._ok(ok, B)
+        ok = self._ok(ok, B, add)
         st = self.lib.ss_cache_reserve(self.handle, ctypes.byref(ct), base, add_ptr, B,
                                        ok.data_ptr(), _stream_on(stream, self.device))
         if st != SS_OK:
@@ -135,7 +135,7 @@ class PageCache:
         ct = self._tables(tables)
         n, src_ptr = self._count(src, "src", ct.rows)
         dst_ptr = self._vec(dst, "dst", n)
-        ok = self._ok(ok, n)
+        ok = self._ok(ok, n, src)
         st = self.lib.ss_cache_fork(self.handle, ctypes.byref(ct), src_ptr, dst_ptr, n,
                                     ok.data_ptr(), _stream_on(stream, self.device))
         if st != SS_OK:
@@ -163,7 +163,7 @@ class PageCache:
             if not 1 <= N <= 64 or stride < N:
                 raise ValueError("nodes must be [B, N] with N in 1 .. 64 and rows that do not overlap")
             at = nodes.data_ptr()
-        ok = self._ok(ok, B)
+        ok = self._ok(ok, B, num_accepted)
         st = self.lib.ss_cache_commit(self.handle, ctypes.byref(ct), base, at, stride, N, acc, B,
                                       1 if release else 0, ok.data_ptr(),
                                       _stream_on(stream, self.device))
@@ -193,7 +193,7 @@ class PageCache:
         other = self if src_cache is None else src_cache
         n, src_ptr = self._count(src, "src", 65535)
         dst_ptr = self._vec(dst, "dst", n)
-        ok = self._ok(ok, n)
+        ok = self._ok(ok, n, src)
         st = self.lib.ss_cache_copy_pages(other.handle, src_ptr, self.handle, dst_ptr, n,
                                           ok.data_ptr(), _stream_on(stream, self.device))
         if st != SS_OK:
