@@ -186,14 +186,14 @@ _empty_strided = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", N
 _current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
-def _empty_rows(n, m, like):
-    """An uninitialised [n, m] int32 array (m None: [n]) on the device of `like`."""
+def _empty_rows(n, m, like, dtype=torch.int32):
+    """An uninitialised [n, m] array (m None: [n]) on the device of `like`."""
     if _empty_strided is not None and _current_device is not None and \
             _current_device() == like.get_device():
         if m is None:
-            return _empty_strided((n,), (1,), torch.int32)
-        return _empty_strided((n, m), (m, 1), torch.int32)
-    return like.new_empty(n if m is None else (n, m), dtype=torch.int32)
+            return _empty_strided((n,), (1,), dtype)
+        return _empty_strided((n, m), (m, 1), dtype)
+    return like.new_empty(n if m is None else (n, m), dtype=dtype)
 
 
 def _require(cond, msg):
@@ -666,11 +666,12 @@ class Sampler:
         if not (isinstance(hidden, torch.Tensor) and hidden.dtype is torch.bfloat16 and
                 hidden.get_device() == dev):
             _check_dev(hidden, "hidden", (torch.bfloat16, torch.int16), dev)
-        if hidden.dim() != 2 or not hidden.is_contiguous():
+        shape = hidden.shape
+        if len(shape) != 2 or not hidden.is_contiguous():
             raise ValueError("hidden must be a contiguous [B, K] array")
-        B = hidden.shape[0]
-        if hidden.shape[1] != K:
-            raise ValueError(f"hidden has K = {hidden.shape[1]}, the sampler {K}")
+        B = shape[0]
+        if shape[1] != K:
+            raise ValueError(f"hidden has K = {shape[1]}, the sampler {K}")
         if group not in (32, 64, 128):
             raise ValueError("group must be 32, 64 or 128")
         groups = -(-K // group)
@@ -683,7 +684,7 @@ class Sampler:
         if out is None:
             if out_dtype is not torch.float32 and out_dtype is not torch.bfloat16:
                 raise ValueError("out_dtype must be float32 or bfloat16")
-            out = torch.empty((B, V), dtype=out_dtype, device=hidden.device)
+            out = _empty_rows(B, V, hidden, out_dtype)
             stride = V
         else:
             _check_rows(out, "out", B, (torch.float32, torch.bfloat16), dev)
