@@ -30,8 +30,9 @@
 //    MFMAs: for groups of 128 as they are, for groups of 64 and 32 after
 //    exchanging words between the lanes that hold the same row (permlane
 //    swaps), so that no MFMA crosses a group.
-//  * The row blocks left over beyond a multiple of the CUs are cut along K between
-//    workgroups; the one that arrives last adds the parts, in order.
+//  * The row blocks left over beyond a multiple of the CUs, or all where they are
+//    few, are cut along K between workgroups; the one that arrives last adds the
+//    parts, in order.
 //  * WAVES waves: RW row blocks of RT tiles by KW ranges of K, whose sums are
 //    added in a fixed order through LDS.
 #include <type_traits>
@@ -208,16 +209,16 @@ __global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
     const int r16 = lane & 15, quarter = lane >> 4;
     const int K = a.K, V = a.V;
     // the first workgroups take a part of K of one of the last row blocks each
-    const bool part = KW == 1 && (int)blockIdx.x < a.split_blocks * a.split;
+    const bool part = (int)blockIdx.x < a.split_blocks * a.split;
     const int row_block = part ? a.whole_blocks + blockIdx.x / a.split : blockIdx.x - a.split_blocks * a.split;
     const int row0 = row_block * ROWS + rw * RT * 16;
     const int n_groups = (K + GROUP - 1) / GROUP;
     // stages of a range: whole sets where there are several ranges
     const int all = (K + LQ_KB * BPS - 1) / (LQ_KB * BPS);
     const int start = part ? blockIdx.x % a.split * a.split_stages : 0;
-    const int stages = KW > 1 ? ((all + KW - 1) / KW + SET - 1) / SET * SET
-                       : part ? min(a.split_stages, all - start) : all;
-    const int first_stage = KW > 1 ? kw * stages : start;
+    const int own = part ? a.split_stages : all;
+    const int stages = KW > 1 ? ((own + KW - 1) / KW + SET - 1) / SET * SET : min(own, all - start);
+    const int first_stage = start + kw * stages;
     // Each workgroup starts at a set of its own, so that the rows that are read
     // at the same time are read at different places: rows a power of two apart
     // would otherwise meet in the same memory channels. A last, partial set
@@ -296,7 +297,7 @@ __global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
                         LQ_LDS(ws + t * WT_ + c * 1024), 16, 0, 0);
                 }
         }
-        const int k0 = (KW > 1 ? xrange * stages + at : first_stage + at) * BPS * LQ_KB;
+        const int k0 = (start + xrange * stages + at) * BPS * LQ_KB;
         uint8_t* xs = buf + xu * 1024;
 #pragma unroll
         for (int i = 0; i < XC; ++i) {
@@ -462,20 +463,22 @@ __global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
                     s_red[((((kw - 1) * RW + rw) * RT + t) * NT + n) * WAVE + lane] = out[t][n];
         }
         __syncthreads();
-        if (kw > 0) return;
+        if (kw == 0) {
 #pragma unroll
-        for (int k = 1; k < KW; ++k)
+            for (int k = 1; k < KW; ++k)
 #pragma unroll
-            for (int t = 0; t < RT; ++t)
+                for (int t = 0; t < RT; ++t)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    out[t][n] += s_red[((((k - 1) * RW + rw) * RT + t) * NT + n) * WAVE + lane];
+                    for (int n = 0; n < NT; ++n)
+                        out[t][n] += s_red[((((k - 1) * RW + rw) * RT + t) * NT + n) * WAVE + lane];
+        }
     }
-    if constexpr (KW == 1) {
-        if (part) {  // the parts of K, added in order by the workgroup that is last to leave its own
-            __shared__ int s_last;
-            constexpr int SUMS = WAVES * RT * NT * 2 * WAVE;  // pairs of sums per workgroup
-            const int mine = wave * RT * NT * 2 * WAVE + lane;
+    const bool holds = KW == 1 || kw == 0;  // the workgroup's sums
+    if (part) {  // the parts of K, added in order by the workgroup that is last to leave its own
+        __shared__ int s_last;
+        constexpr int SUMS = RW * RT * NT * 2 * WAVE;  // pairs of sums per workgroup
+        const int mine = rw * RT * NT * 2 * WAVE + lane;
+        if (holds) {
             uint64_t* to = a.part + (int64_t)blockIdx.x * SUMS + mine;
 #pragma unroll
             for (int t = 0; t < RT; ++t)
@@ -486,16 +489,18 @@ __global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
                         __hip_atomic_store(to + ((t * NT + n) * 2 + h) * WAVE,
                                            lq_pair(out[t][n][2 * h], out[t][n][2 * h + 1]),
                                            __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            __syncthreads();
-            if (tid == 0) {
-                int32_t* arrived = a.arrived + (row_block - a.whole_blocks) * QUANT_COUNTER;
-                s_last = __hip_atomic_fetch_add(arrived, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-                         a.split - 1;
-                if (s_last) __hip_atomic_store(arrived, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            }
-            __syncthreads();
-            if (!s_last) return;
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (tid == 0) {
+            int32_t* arrived = a.arrived + (row_block - a.whole_blocks) * QUANT_COUNTER;
+            s_last = __hip_atomic_fetch_add(arrived, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                     a.split - 1;
+            if (s_last) __hip_atomic_store(arrived, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        __syncthreads();
+        if (!s_last) return;
+        if (holds) {
 #pragma unroll
             for (int t = 0; t < RT; ++t)
 #pragma unroll
@@ -515,6 +520,7 @@ __global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
                         }
         }
     }
+    if (!holds) return;
     // a lane holds four batch rows of one vocabulary entry
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
@@ -533,18 +539,19 @@ __global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
     }
 }
 
-// Where a few row blocks are left over beyond a multiple of the CUs, most CUs would
-// wait for those that have one more. These blocks are cut along K, in as many parts
-// as there are CUs for them: B = 64, V = 70000, K = 8192, groups of 128: 190 -> 128 us,
-// B = 20, V = 67000, K = 4096: 61 -> 50, B = 13, V = 50257, K = 4160: 39 -> 37. Where
-// fewer than all whole blocks are resident, late ones fill the gaps by themselves
-// (B = 24, V = 100000: 73, cut 74.5), and with more parts than CUs their sums cost more
-// than they gain (B = 32, V = 50257, 411 parts: 59, uncut 47).
+// Where row blocks are left over beyond a multiple of the CUs, other CUs would wait for
+// those that have one more. These blocks are cut along K, in as many parts as there
+// are CUs for them. B = 8, V = 3000, K = 8192: 21.1 -> 10.3 us, B = 64: 35.8 -> 15.8;
+// B = 64, V = 70000, K = 8192, groups of 128: 190 -> 128, B = 20, V = 67000, K = 4096:
+// 61 -> 50, B = 13, V = 50257, K = 4160: 39 -> 37. Where not all whole blocks are
+// resident, late ones fill the gaps by themselves (B = 24, V = 100000: 73, cut 74.5),
+// unless there is one a CU. With more parts than CUs their sums cost more than they
+// gain (B = 64, V = 11000, K = 4096, 516 parts: 31, uncut 22).
 static QuantSplit quant_split(int blocks, int resident, int sets) {
     QuantSplit s = {blocks, 0, 1, 0};
     const int over = blocks % QUANT_CUS;
     const int rounds = blocks / QUANT_CUS;
-    if (over == 0 || rounds < 1 || (resident > 1 && rounds > resident)) return s;
+    if (over == 0 || (resident > 1 && rounds > resident)) return s;
     for (int f = 2; f <= QUANT_SPLIT && f <= sets && f * over <= QUANT_CUS; ++f) {
         const int per = (sets + f - 1) / f;
         if ((sets + per - 1) / per == f)  // else a part would be empty
@@ -558,19 +565,15 @@ static void launch_quant_t(const QuantArgs& a, hipStream_t st, const LaunchEvent
     constexpr int rows = WAVES / KW * RT * 16;
     const int blocks = (a.V + rows - 1) / rows;
     QuantArgs b = a;
-    b.whole_blocks = blocks;
-    b.split = 1;
-    if constexpr (KW == 1) {
-        constexpr int GPS = LQ_KB / GROUP * BPS, SET = GPS < 4 ? 4 / GPS : 1;
-        const int all = (a.K + LQ_KB * BPS - 1) / (LQ_KB * BPS);
-        constexpr int LDS = S * BPS * (NT * 4096 + WAVES * RT * 1024);
-        static_assert(WAVES * RT * NT * WAVE * 16 <= QUANT_PART_BYTES, "a part's sums fit the workspace");
-        const QuantSplit s = quant_split(blocks, 160 * 1024 / LDS, (all + SET - 1) / SET);
-        b.whole_blocks = s.whole_blocks;
-        b.split_blocks = s.split_blocks;
-        b.split = s.split;
-        b.split_stages = s.sets * SET;
-    }
+    constexpr int GPS = LQ_KB / GROUP * BPS, SET = (GPS < 4 ? 4 / GPS : 1) * KW;
+    constexpr int LDS = S * BPS * (KW * NT * 4096 + WAVES * RT * 1024);
+    static_assert(WAVES / KW * RT * NT * WAVE * 16 <= QUANT_PART_BYTES, "a part's sums fit the workspace");
+    const int all = (a.K + LQ_KB * BPS - 1) / (LQ_KB * BPS);
+    const QuantSplit s = quant_split(blocks, 160 * 1024 / LDS, (all + SET - 1) / SET);
+    b.whole_blocks = s.whole_blocks;
+    b.split_blocks = s.split_blocks;
+    b.split = s.split;
+    b.split_stages = s.sets * SET;
     launch_k(le, 0, k_lmhead_quant<GROUP, NT, RT, KW, WAVES, BPS, S>,
              dim3(b.whole_blocks + b.split_blocks * b.split), dim3(WAVES * WAVE), st, b);
 }
@@ -714,8 +717,8 @@ static void launch_quant_g(const QuantArgs& a, hipStream_t st, const LaunchEvent
         return;
     }
     // Fewer, larger workgroups share a stage of x and widen a weight for more batch
-    // rows; where they are fewer than the CUs, smaller ones, with K in two ranges
-    // where those are still few.
+    // rows; where they are few, smaller ones, with K in two ranges where those are few
+    // as well.
     if (a.B <= 16) {
         // V = 20000, K = 4096: 17.0 us (one range: 19.1), V = 50257, K = 4160: 44.8 (36.8)
         if (a.V <= 32768) launch_quant_t<GROUP, 1, 1, 2, 8, 2, 2>(a, st, le);
@@ -726,8 +729,8 @@ static void launch_quant_g(const QuantArgs& a, hipStream_t st, const LaunchEvent
         if (a.V <= 32768) launch_quant_t<GROUP, 2, 1, 2, 8, 1, 2>(a, st, le);
         else if (a.V <= 53248) launch_quant_t<GROUP, 2, 1, 1, 4, 2, 2>(a, st, le);
         else launch_quant_t<GROUP, 2, 2, 1, 4, 2, 2>(a, st, le);
-    } else if (a.V <= 12288) {
-        // V = 8000, K = 4096: 19.8 us (one range: 27.2)
+    } else if (a.V <= 16384) {
+        // V = 16000, K = 4096: 23.2 us (one range: 31.7), V = 24000, K = 2048: 23.1 (21.1)
         launch_quant_t<GROUP, 4, 1, 2, 8, 1, 2>(a, st, le);
     } else if (a.V <= 32768 || GROUP == 32) {
         // V = 32000, K = 2048: 26.5 us (two row tiles a wave: 28.8). Groups of 32 end

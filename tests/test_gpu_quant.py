@@ -108,10 +108,21 @@ def test_matches_the_oracle(B, V, K, group, zeros, scale, out):
     (50, 70000, 1280, 128),
     (33, 131100, 768, 128),   # behind two whole rounds
     (9, 32769, 128, 128),     # a single set: not cut
+    # all row blocks cut, with K in two ranges inside each part
+    (2, 1, 8192, 128),
+    (16, 1000, 8192, 128),
+    (3, 3001, 2112, 32),
+    (24, 2999, 4160, 64),
+    (40, 8192, 2048, 128),
+    (64, 70, 24640, 32),
+    (64, 1003, 3136, 64),
+    (10, 20000, 2048, 64),    # one round and some blocks cut
+    (64, 16384, 1024, 128),
+    (1, 300, 4160, 128),      # one row that the tiles take
 ])
 def test_left_over_row_blocks(B, V, K, group):
-    """Row blocks behind a multiple of the CUs are cut along K between workgroups:
-    eager, again, and in a graph that is replayed with other hidden states."""
+    """Row blocks behind a multiple of the CUs, or all of few, are cut along K between
+    workgroups: eager, again, and in a graph replayed with other hidden states."""
     log(f"quant: left over, B={B} V={V} K={K} group={group}")
     x, q, sc, z = make(B, V, K, group, True, torch.float16, V + K)
     s = SM.Sampler(B, V, hidden_size=K, device=0)
