@@ -418,8 +418,7 @@ __global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
             asm volatile("" ::: "memory");
             if (j + S - 1 <= stages) __builtin_amdgcn_s_waitcnt(lq_wait((S - 2) * COPIES));
             else __builtin_amdgcn_s_waitcnt(lq_wait(0));
-            // the builtins say nothing about memory: no access may cross them (1% at
-            // B = 64, V = 128256, K = 8192)
+            // the builtins say nothing about memory: no access may cross them
             asm volatile("" ::: "memory");
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
