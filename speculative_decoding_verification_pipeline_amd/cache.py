@@ -148,7 +148,8 @@ class PageCache:
         tables.lens): the root and num_accepted [B] drafts; with nodes [B, N] (as
         tree_verify returns them) the accepted nodes' slots are moved together.
         tables.lens becomes base + 1 + num_accepted; release: pages behind it are
-        given back. Returns ok [B] int32."""
+        given back. Returns ok [B] int32 (0: row unchanged, as where its reserve
+        was refused)."""
         ct = self._tables(tables)
         B, acc = self._count(num_accepted, "num_accepted", ct.rows)
         base = _check_array(base, "base", B, self.device)
