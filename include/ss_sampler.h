@@ -459,7 +459,7 @@ ss_status ss_lmhead_quant_logits(ss_sampler* s, const uint16_t* hidden, const ui
  * and calls on one handle must not overlap in time (its workspace, counters
  * among it, serves one call after the other; graphs captured from one handle are
  * replayed one after the other). Outputs must not overlap inputs, but for base,
- * which may be t->len. */
+ * which may be t->len, and reserved, which may be out_ok. */
 typedef struct ss_cache ss_cache; /* opaque; owns its workspace, not the planes */
 
 typedef struct {
@@ -537,16 +537,28 @@ ss_status ss_cache_fork(ss_cache* c, const ss_block_tables* t, const int32_t* sr
  *                 stay for the next draft.
  *   out_ok        NULL, or [B] int32.
  * Slot base + nodes[i] moves to base + 1 + i on every plane, and len[b] becomes
- * base + 1 + num_accepted. The pages written must be the row's own, as
- * ss_cache_reserve leaves them. A row is refused (out_ok 0, left as it was) for
+ * base + 1 + num_accepted. A row is refused (out_ok 0, left as it was) for
  * a negative base, num_accepted outside 0 .. N-1 (linear drafts: negative), nodes
  * out of range or not ascending, and where a slot of base .. base + num_accepted
- * or one that moves has no page or lies behind max_blocks pages, so that a row
- * whose reserve was refused does not grow. One kernel. */
+ * or one that moves has no page, lies behind max_blocks pages or on a page whose
+ * count is above 1: others hold it, so reserve has not made it writable. Counts are
+ * those at the call's start, whatever pages other rows give back in it. A row whose
+ * reserve was refused may still have room on a last page of its own: only the
+ * verdict tells (ss_cache_commit_reserved). One kernel. */
 ss_status ss_cache_commit(ss_cache* c, const ss_block_tables* t, const int32_t* base,
                           const int32_t* nodes, int64_t nodes_stride, int32_t N,
                           const int32_t* num_accepted, int32_t B, int32_t release,
                           int32_t* out_ok, void* stream);
+
+/* ss_cache_commit_reserved -- ss_cache_commit that also refuses the rows that
+ * ss_cache_reserve refused.
+ *   reserved      NULL, or [B] int32, reserve's out_ok: rows with 0 there are
+ *                 refused. Slots of a refused reserve must not be written by the
+ *                 forward pass either: they may lie on pages of other rows. */
+ss_status ss_cache_commit_reserved(ss_cache* c, const ss_block_tables* t, const int32_t* base,
+                                   const int32_t* nodes, int64_t nodes_stride, int32_t N,
+                                   const int32_t* num_accepted, int32_t B, int32_t release,
+                                   const int32_t* reserved, int32_t* out_ok, void* stream);
 
 /* ss_cache_truncate -- give back the pages behind new_len.
  *   rows     [n] int32, or NULL: 0 .. n-1; rows out of range are skipped, a row

@@ -71,13 +71,19 @@ class Pages:
                 self.lens[d] = lens[s]
         return ok
 
-    def commit(self, acc, nodes=None, base=None, release=True):
+    def commit(self, acc, nodes=None, base=None, release=True, reserved=None):
         base = list(self.lens if base is None else base)
+        before = list(self.ref)
         room = self.M * self.ps
         ok = []
+
+        def own(page):
+            return self.held(page) and before[page] <= 1
+
         for b, n in enumerate(acc):
             good = base[b] >= 0 and n >= 0 and base[b] + 1 + n <= room
-            good = good and all(self.held(self.tables[b][i])
+            good = good and (reserved is None or reserved[b] != 0)
+            good = good and all(own(self.tables[b][i])
                                 for i in range(base[b] // self.ps, self.pages_of(base[b] + 1 + n)))
             moves = []
             if good and nodes is not None:
@@ -91,7 +97,7 @@ class Pages:
                     if good and node != i + 1:
                         s, d = base[b] + node, base[b] + 1 + i
                         sp, dp = self.tables[b][s // self.ps], self.tables[b][d // self.ps]
-                        good = self.held(sp) and self.held(dp)
+                        good = own(sp) and own(dp)
                         moves.append((sp, s % self.ps, dp, d % self.ps))
             ok.append(int(good))
             if not good:

@@ -143,16 +143,19 @@ class PageCache:
         return ok
 
     def commit(self, tables: BlockTables, num_accepted, nodes=None, base=None, release=True,
-               ok=None, stream=None):
+               ok=None, stream=None, reserved=None):
         """Keep what was accepted of a draft written behind base (None:
         tables.lens): the root and num_accepted [B] drafts; with nodes [B, N] (as
         tree_verify returns them) the accepted nodes' slots are moved together.
         tables.lens becomes base + 1 + num_accepted; release: pages behind it are
-        given back. Returns ok [B] int32 (0: row unchanged, as where its reserve
-        was refused)."""
+        given back. reserved [B] int32: what reserve returned for this draft; rows
+        with 0 there are refused. Rows whose slots lie on no page, or on one that
+        others hold as well, are refused in any case. Returns ok [B] int32 (0: row
+        unchanged)."""
         ct = self._tables(tables)
         B, acc = self._count(num_accepted, "num_accepted", ct.rows)
         base = _check_array(base, "base", B, self.device)
+        reserved = _check_array(reserved, "reserved", B, self.device)
         at, stride, N = None, 0, 0
         if nodes is not None:
             if not (isinstance(nodes, torch.Tensor) and nodes.dtype is torch.int32 and
@@ -165,11 +168,11 @@ class PageCache:
                 raise ValueError("nodes must be [B, N] with N in 1 .. 64 and rows that do not overlap")
             at = nodes.data_ptr()
         ok = self._ok(ok, B, num_accepted)
-        st = self.lib.ss_cache_commit(self.handle, ctypes.byref(ct), base, at, stride, N, acc, B,
-                                      1 if release else 0, ok.data_ptr(),
-                                      _stream_on(stream, self.device))
+        st = self.lib.ss_cache_commit_reserved(self.handle, ctypes.byref(ct), base, at, stride, N,
+                                               acc, B, 1 if release else 0, reserved,
+                                               ok.data_ptr(), _stream_on(stream, self.device))
         if st != SS_OK:
-            _check("ss_cache_commit", st)
+            _check("ss_cache_commit_reserved", st)
         return ok
 
     def truncate(self, tables: BlockTables, new_len=None, rows=None, stream=None):

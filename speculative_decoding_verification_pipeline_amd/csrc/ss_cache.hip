@@ -10,7 +10,9 @@
 // integer atomics only, a free page is named by its rank among the free pages
 // in ascending order, and every launch reads either what no workgroup of that
 // launch writes or entries that it alone owns; a commit's table is written by the
-// workgroup that finds, at its row's counter, that the others have read it.
+// workgroup that finds, at its row's counter, that the others have read it, and
+// counts of pages that others hold as well are lowered by the one that finds, at
+// the call's counter, that every row is settled.
 //
 // What bounds it: the copying is bound by HBM (each byte read once and written
 // once, 16 bytes per lane and as many loads in flight as rows are moved); the
@@ -217,16 +219,18 @@ __global__ __launch_bounds__(CA_NT) void k_cache_take(CacheReserve a, CacheCopy 
 }
 
 // ---------------------------------------------------------------------------
-// release: the entries from `first` on leave the table of one row
+// release: the entries from `first` on leave the table of one row, drop gives
+// each page back
 
+template <class Drop>
 __device__ __forceinline__ void release_from(const CacheTables& t, int num_pages, int max_blocks,
-                                             int row, int first) {
+                                             int row, int first, Drop drop) {
     int32_t* tab = t.tables + (int64_t)row * t.stride;
     for (int i = first + threadIdx.x; i < max_blocks; i += CA_NT) {
         // a row listed twice is released once: only one exchange sees the page
         if (tab[i] == -1) continue;
         const int page = atomicExch(&tab[i], -1);
-        if (page_ok(page, num_pages)) atomicSub(&t.ref[page], 1);
+        if (page_ok(page, num_pages)) drop(page);
     }
 }
 
@@ -236,7 +240,9 @@ __global__ __launch_bounds__(CA_NT) void k_cache_truncate(CacheTruncate a) {
     if ((unsigned)row >= (unsigned)a.t.rows) return;
     const int keep = a.new_len ? max(a.new_len[i], 0) : 0;
     const unsigned first = ((unsigned)keep + a.page_size - 1) / (unsigned)a.page_size;
-    if (first < (unsigned)a.max_blocks) release_from(a.t, a.num_pages, a.max_blocks, row, (int)first);
+    if (first < (unsigned)a.max_blocks)
+        release_from(a.t, a.num_pages, a.max_blocks, row, (int)first,
+                     [&](int page) { atomicSub(&a.t.ref[page], 1); });
     if (threadIdx.x == 0) atomicMin(&a.t.len[row], keep);
 }
 
@@ -272,17 +278,22 @@ __global__ __launch_bounds__(CA_NT) void k_cache_fork(CacheFork a) {
 // ---------------------------------------------------------------------------
 // commit
 
-// Whether request b's step can be committed, for every wave of a workgroup:
-// node indices ascend from at least 1 and stay below N (so a row moves towards
-// the front only, and no row is overwritten before it is read), and every slot
-// that is kept or moved lies on a page the table names: a row whose reserve was
-// refused does not grow over pages it never got. Lane i gets row i's offsets.
+// Whether request b's step can be committed, for every wave of a workgroup: the
+// reserve's verdict, where the caller passes it, is not 0; node indices ascend from
+// at least 1 and stay below N (so a row moves towards the front only, and no row is
+// overwritten before it is read); and every slot that is kept or moved lies on a
+// page that the table names and no other entry holds: a row whose reserve was
+// refused neither grows over pages it never got nor writes to ones it shares.
+// Lane i gets row i's offsets and the counts of the pages that it looked up, which
+// the caller compares, so that loads of data go out beside those of the counts.
 // Slots stay below 2^31, so they are divided as 32-bit numbers.
 struct CommitRow {
-    bool ok;
+    bool ok;           // but for the counts
     int acc;
+    int len;           // base + 1 + acc
     int64_t src, dst;  // page * src_page + slot * src_slot of lane i's move
     bool moves;
+    int kept, moved;   // counts: of the kept slots' pages, of the page moved from
 };
 
 __device__ __forceinline__ CommitRow commit_row(const CacheCommit& a, const CacheCopy& g, int b) {
@@ -291,6 +302,7 @@ __device__ __forceinline__ CommitRow commit_row(const CacheCommit& a, const Cach
     // what does not depend on anything is loaded together
     r.acc = a.num_accepted[b];
     const int64_t base = a.base[b];
+    const int reserved = a.reserved ? a.reserved[b] : 1;
     int node = 0, prev = 0;
     if (a.nodes && lane < a.N) {
         const int32_t* nodes = a.nodes + (int64_t)b * a.nodes_stride;
@@ -299,26 +311,45 @@ __device__ __forceinline__ CommitRow commit_row(const CacheCommit& a, const Cach
     }
     r.src = r.dst = 0;
     r.moves = false;
+    r.len = r.kept = r.moved = 0;
     const int64_t room = (int64_t)a.max_blocks * a.page_size;
-    r.ok = base >= 0 && r.acc >= 0 && base + 1 + r.acc <= room && (!a.nodes || r.acc < a.N);
+    r.ok = base >= 0 && r.acc >= 0 && base + 1 + r.acc <= room && (!a.nodes || r.acc < a.N) &&
+           reserved != 0;
     if (!r.ok) return r;
+    r.len = (int)base + 1 + r.acc;
     const int32_t* tab = a.t.tables + (int64_t)b * a.t.stride;
     const unsigned page_size = a.page_size;
+    const unsigned first = (unsigned)base / page_size + lane;
     const unsigned last = ((unsigned)base + r.acc) / page_size;
+    int kept = -1, sp = -1, dp = -1;
     bool bad = false;
-    for (unsigned i = (unsigned)base / page_size + lane; i <= last; i += WAVE)
-        bad |= !page_ok(tab[i], a.num_pages);
+    if (first <= last) {
+        kept = tab[first];
+        bad = !page_ok(kept, a.num_pages);
+    }
     if (a.nodes && lane < r.acc) {
         if (node <= prev || node >= a.N || base + node >= room) {
             bad = true;
         } else if (node != lane + 1) {
             const unsigned s = (unsigned)base + node, d = (unsigned)base + 1 + lane;
-            const int sp = tab[s / page_size], dp = tab[d / page_size];
-            bad |= !page_ok(sp, a.num_pages) || !page_ok(dp, a.num_pages);
-            r.src = sp * g.src_page + (s % page_size) * g.src_slot;
-            r.dst = dp * g.dst_page + (d % page_size) * g.dst_slot;
-            r.moves = true;
+            sp = tab[s / page_size];
+            dp = tab[d / page_size];
+            if (!page_ok(sp, a.num_pages) || !page_ok(dp, a.num_pages)) {
+                bad = true;
+            } else {
+                r.src = sp * g.src_page + (s % page_size) * g.src_slot;
+                r.dst = dp * g.dst_page + (d % page_size) * g.dst_slot;
+                r.moves = true;
+            }
         }
+    }
+    if (first <= last && !bad) r.kept = a.t.ref[kept];
+    if (r.moves) r.moved = a.t.ref[sp];
+    for (unsigned i = first + WAVE; i <= last; i += WAVE) {  // more pages than lanes
+        const int page = tab[i];
+        const bool held = page_ok(page, a.num_pages);
+        bad |= !held;
+        if (held) r.kept = max(r.kept, a.t.ref[page]);
     }
     r.ok = __ballot(bad) == 0;
     return r;
@@ -327,58 +358,99 @@ __device__ __forceinline__ CommitRow commit_row(const CacheCommit& a, const Cach
 // Grid (units / 256, B); without nodes (1, B). A lane owns one vector of one head
 // of one plane and moves it for every accepted node in order, eight loads at a
 // time: a slot written here is read by no later node (their sources lie further
-// back). The workgroup that is the last of its row to have read the table and the
-// length (which may be the base) writes them: the new length, and the pages
-// behind it given back. It reads nothing that the others write.
+// back). The first eight go out before the counts have come (their addresses are
+// good whatever the verdict), nothing is stored before. The workgroup that is the
+// last of its row to have read the table and the length (which may be the base)
+// writes them: the new length, and the pages behind it given back. It reads
+// nothing that the others write.
+//
+// Counts of pages that others hold as well stay as they were until every row's
+// workgroups have compared them: their releases are listed, and the workgroup that
+// settles its row last of all takes the list off the counts. (A page that nobody
+// else holds is given back at once: no other row looks at it.)
 template <int VEC>
 __global__ __launch_bounds__(CA_NT) void k_cache_commit(CacheCommit a, CacheCopy g) {
     typedef typename CacheVec<VEC>::type V;
-    __shared__ int s_settles;
+    __shared__ int s_settles, s_last;
     const int b = blockIdx.y;
+    const int tid = threadIdx.x;
     const unsigned per_plane = (unsigned)g.heads * g.units;
-    const unsigned u = blockIdx.x * CA_NT + threadIdx.x;
+    const unsigned u = blockIdx.x * CA_NT + tid;
     const unsigned plane = u / per_plane;
     const bool on = plane < (unsigned)a.num_planes;
     char* p = on ? g.dst_planes[plane] : nullptr;
-    const CommitRow r = commit_row(a, g, b);
-    // every wave has its loads before the workgroup is counted
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        int32_t* arrived = a.arrived + b * CACHE_COUNTER;
-        s_settles = __hip_atomic_fetch_add(arrived, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-                    (int)gridDim.x - 1;
-        if (s_settles) __hip_atomic_store(arrived, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
+    CommitRow r = commit_row(a, g, b);
     const unsigned long long moves = r.ok ? __ballot(r.moves) : 0;
+    int i0 = moves ? __builtin_ctzll(moves) : r.acc;
+    V v[CA_UNROLL];
+    auto load = [&] {
+#pragma unroll
+        for (int k = 0; k < CA_UNROLL; ++k) {
+            const int64_t s = __shfl(r.src, i0 + k);
+            if (on && i0 + k < r.acc) v[k] = *reinterpret_cast<const V*>(p + s);
+        }
+    };
     if (moves) {
         const unsigned w = u - plane * per_plane;
         const unsigned h = w / g.units;
         if (on) p += h * g.dst_head + (int64_t)(w - h * g.units) * VEC;
-        for (int i0 = __builtin_ctzll(moves); i0 < r.acc; i0 += CA_UNROLL) {
-            V v[CA_UNROLL];
-#pragma unroll
-            for (int k = 0; k < CA_UNROLL; ++k) {
-                const int64_t s = __shfl(r.src, i0 + k);
-                if (on && i0 + k < r.acc) v[k] = *reinterpret_cast<const V*>(p + s);
-            }
+        load();
+    }
+    r.ok = r.ok && __ballot(max(r.kept, r.moved) > 1) == 0;
+    // every wave has its loads before the workgroup is counted
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    int32_t* arrived = a.arrived + b * CACHE_COUNTER;
+    int before = 0;
+    if (tid == 0) before = __hip_atomic_fetch_add(arrived, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (moves && r.ok) {
+        for (;;) {
 #pragma unroll
             for (int k = 0; k < CA_UNROLL; ++k) {
                 const int64_t d = __shfl(r.dst, i0 + k);
                 if (on && i0 + k < r.acc) *reinterpret_cast<V*>(p + d) = v[k];
             }
+            i0 += CA_UNROLL;
+            if (i0 >= r.acc) break;
+            load();
         }
+    }
+    if (tid == 0) {
+        s_settles = before == (int)gridDim.x - 1;
+        if (s_settles) __hip_atomic_store(arrived, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     __syncthreads();
     if (!s_settles) return;
-    if (threadIdx.x == 0 && a.out_ok) a.out_ok[b] = r.ok ? 1 : 0;
-    if (!r.ok) return;
-    const int len = a.base[b] + 1 + r.acc;
-    __syncthreads();  // the length may be the base that is read above
-    if (threadIdx.x == 0) a.t.len[b] = len;
-    if (a.release)
+    if (tid == 0 && a.out_ok) a.out_ok[b] = r.ok ? 1 : 0;
+    if (tid == 0 && r.ok) a.t.len[b] = r.len;
+    if (!a.release) return;
+    if (r.ok)
         release_from(a.t, a.num_pages, a.max_blocks, b,
-                     (int)(((unsigned)len + a.page_size - 1) / (unsigned)a.page_size));
+                     (int)(((unsigned)r.len + a.page_size - 1) / (unsigned)a.page_size), [&](int page) {
+                         if (a.t.ref[page] > 1) {
+                             const int at = __hip_atomic_fetch_add(a.n_left, 1, __ATOMIC_RELAXED,
+                                                                   __HIP_MEMORY_SCOPE_AGENT);
+                             __hip_atomic_store(a.left + at, page, __ATOMIC_RELAXED,
+                                                __HIP_MEMORY_SCOPE_AGENT);
+                         } else {
+                             atomicSub(&a.t.ref[page], 1);
+                         }
+                     });
+    // the row's entries have reached the agent's point of coherence before its count does
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (tid == 0)
+        s_last = __hip_atomic_fetch_add(a.settled, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == a.B - 1;
+    __syncthreads();
+    if (!s_last) return;
+    const int n = __hip_atomic_load(a.n_left, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int i = tid; i < n; i += CA_NT)
+        atomicSub(&a.t.ref[__hip_atomic_load(a.left + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)], 1);
+    __syncthreads();
+    if (tid == 0) {
+        __hip_atomic_store(a.n_left, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(a.settled, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
 }
 
 // ---------------------------------------------------------------------------

@@ -140,7 +140,7 @@ ss_status ss_cache_create(const ss_cache_config* cfg, void* const* planes, ss_ca
     };
     // the plane pointers and the counters of 0, filled by one copy
     const int64_t o_planes = take((int64_t)cfg->num_planes * sizeof(char*));
-    const int64_t o_arrived = take((int64_t)cfg->max_batch * ss::CACHE_COUNTER * 4);
+    const int64_t o_arrived = take(((int64_t)cfg->max_batch + 2) * ss::CACHE_COUNTER * 4);
     const int64_t filled = off;
     const int64_t o_ids = take((int64_t)c->n_chunks * ss::CACHE_REF_CHUNK * 4);
     const int64_t o_cnt = take((int64_t)c->n_chunks * 4);
@@ -163,6 +163,8 @@ ss_status ss_cache_create(const ss_cache_config* cfg, void* const* planes, ss_ca
     c->ws.mark = reinterpret_cast<int32_t*>(b + o_mark);
     c->ws.pair_ok = reinterpret_cast<int32_t*>(b + o_pair);
     c->ws.arrived = reinterpret_cast<int32_t*>(b + o_arrived);
+    c->ws.settled = c->ws.arrived + (int64_t)cfg->max_batch * ss::CACHE_COUNTER;
+    c->ws.n_left = c->ws.settled + ss::CACHE_COUNTER;
     char* h = new (std::nothrow) char[(size_t)filled]();
     if (!h) {
         (void)hipFree(c->ws_base);
@@ -244,6 +246,14 @@ ss_status ss_cache_commit(ss_cache* c, const ss_block_tables* t, const int32_t* 
                           const int32_t* nodes, int64_t nodes_stride, int32_t N,
                           const int32_t* num_accepted, int32_t B, int32_t release,
                           int32_t* out_ok, void* stream) {
+    return ss_cache_commit_reserved(c, t, base, nodes, nodes_stride, N, num_accepted, B, release,
+                                    nullptr, out_ok, stream);
+}
+
+ss_status ss_cache_commit_reserved(ss_cache* c, const ss_block_tables* t, const int32_t* base,
+                                   const int32_t* nodes, int64_t nodes_stride, int32_t N,
+                                   const int32_t* num_accepted, int32_t B, int32_t release,
+                                   const int32_t* reserved, int32_t* out_ok, void* stream) {
     ss_status st = check_tables(c, t);
     if (st != SS_OK) return st;
     if (B < 0 || B > t->rows) return SS_ERR_INVALID_ARG;
@@ -260,7 +270,11 @@ ss_status ss_cache_commit(ss_cache* c, const ss_block_tables* t, const int32_t* 
     a.N = N;
     a.B = B;
     a.release = release != 0;
+    a.reserved = reserved;
     a.arrived = c->ws.arrived;
+    a.settled = c->ws.settled;
+    a.n_left = c->ws.n_left;
+    a.left = c->ws.mark;
     a.out_ok = out_ok;
     a.num_pages = c->cfg.num_pages;
     a.num_planes = c->cfg.num_planes;

@@ -295,10 +295,12 @@ struct CacheWork {
     int32_t* free_cnt;  // [chunks]
     int32_t* need;      // [max_batch]: fresh pages a request needs, -1 refused
     int32_t* carry;     // [max_batch]: shared page whose first slots move along, or -1
-    int32_t* mark;      // [max_batch * max_blocks]
+    int32_t* mark;      // [max_batch * max_blocks]; in a commit: pages that rows left and others hold
     int32_t* pair_ok;   // [num_pages]
     int32_t* arrived;   // [max_batch * CACHE_COUNTER]: workgroups of each row that have read its
                         //   table; 0 between calls
+    int32_t* settled;   // rows of a commit that are settled; 0 between calls
+    int32_t* n_left;    // entries of the list in mark; 0 between calls
 };
 
 struct CacheReserve {
@@ -337,7 +339,11 @@ struct CacheCommit {
     int N;
     int B;
     int release;
+    const int32_t* reserved;  // [B] or null: the reserve's verdicts
     int32_t* arrived;
+    int32_t* settled;
+    int32_t* n_left;
+    int32_t* left;
     int32_t* out_ok;
     int num_pages, num_planes, page_size, max_blocks;
 };

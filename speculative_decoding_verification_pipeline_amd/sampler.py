@@ -31,7 +31,7 @@ EXPORTED = ("ss_sampler_create", "ss_sampler_destroy", "ss_status_string",
             "ss_lmhead_sample_params", "ss_sample_noalloc", "ss_spec_verify_probs",
             "ss_lmhead_quant_logits", "ss_cache_create", "ss_cache_destroy",
             "ss_cache_workspace_bytes", "ss_cache_reserve", "ss_cache_fork", "ss_cache_commit",
-            "ss_cache_truncate", "ss_cache_copy_pages")
+            "ss_cache_commit_reserved", "ss_cache_truncate", "ss_cache_copy_pages")
 NOALLOC_MAX_BATCH = 64
 NOALLOC_MAX_ENTRIES = 1 << 23
 
@@ -147,6 +147,8 @@ def load_library(path=None):
     lib.ss_cache_fork.restype = i32
     lib.ss_cache_commit.argtypes = [vp, tables, vp, vp, i64, i32, vp, i32, i32, vp, vp]
     lib.ss_cache_commit.restype = i32
+    lib.ss_cache_commit_reserved.argtypes = [vp, tables, vp, vp, i64, i32, vp, i32, i32, vp, vp, vp]
+    lib.ss_cache_commit_reserved.restype = i32
     lib.ss_cache_truncate.argtypes = [vp, tables, vp, vp, i32, vp]
     lib.ss_cache_truncate.restype = i32
     lib.ss_cache_copy_pages.argtypes = [vp, vp, vp, vp, i32, vp, vp]

@@ -92,3 +92,10 @@ def test_row_stride():
                 x.transpose(0, 1)):
         with pytest.raises(ValueError):
             SM._row_stride(bad, "x")
+
+
+def test_commit_with_verdicts_rejects_a_null_handle(lib):
+    t = SM.CBlockTables()
+    assert lib.ss_cache_commit_reserved(None, ctypes.byref(t), None, None, 0, 0, None, 1, 1, None, None,
+                                        None) == SM.SS_ERR_INVALID_ARG
+    assert "ss_cache_commit_reserved" in SM.EXPORTED

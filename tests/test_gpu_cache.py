@@ -415,3 +415,94 @@ def test_refusals():
     assert lib.ss_cache_truncate(c.handle, r, None, None, -1, None) == bad
     assert lib.ss_cache_reserve(c.handle, r, None, None, 0, None, None) == SM.SS_OK
     assert t.tables.cpu().eq(-1).all() and not t.ref.any()
+
+
+@pytest.mark.parametrize("planes", [2, 48])  # one workgroup a row, several
+def test_commit_refuses_what_a_reserve_refused(planes):
+    """Rows that share the page they would write, and rows whose reserve's verdict is 0."""
+    c = Pair(planes, 2, 4, 4, 16, 2, 2)
+    nodes = i32([[2, -1, -1]] * 2)
+
+    def commit(acc, tree, reserved):
+        got = c.cache.commit(c.bt, i32(acc), nodes=nodes if tree else None, reserved=reserved)
+        want = c.o.commit(acc, nodes.tolist() if tree else None,
+                          reserved=None if reserved is None else reserved.tolist())
+        c.same(("commit", acc, tree, reserved), got, want)
+        return want
+
+    c.reserve([5, 0])
+    c.commit([4, -1])
+    c.fork([0], [1])
+    ok = c.cache.reserve(c.bt, i32([3, 3]))
+    c.same("reserve", ok, c.o.reserve([3, 3]))
+    assert ok.tolist() == [0, 0]
+    for reserved in (None, ok):
+        for tree in (True, False):
+            assert commit([1, 1] if tree else [0, 0], tree, reserved) == [0, 0]
+    c.truncate(rows=[1])
+    c.reserve([8, 0])
+    assert commit([0, -1], False, i32([0, 1])) == [0, 0]  # its last page has room: the verdict tells
+    verdict = i32([1, 1])                                 # served and answered in one array
+    got = c.cache.commit(c.bt, i32([1, -1]), nodes=nodes, reserved=verdict, ok=verdict)
+    assert got is verdict
+    c.same("in place", got, c.o.commit([1, -1], nodes.tolist(), reserved=[1, 1]))
+    assert c.o.lens == [7, 0]
+    with pytest.raises(ValueError):
+        c.cache.commit(c.bt, i32([1, 0]), reserved=i32([1]))
+
+
+def test_commit_reads_counts_as_they_were():
+    """Rows that leave shared pages do not make them another's own in the same call:
+    64 rows leave pages that a 65th holds, in an order that is open."""
+    rows, ps, held = 65, 2, 7
+    c = Pair(3, held + 200, ps, 2, 8, rows, held)
+    for turn in range(4):
+        c.truncate()
+        stays = [0, 64, 31, 7][turn]
+        others = [b for b in range(rows) if b != stays]
+        add = [0] * rows
+        add[stays] = held * ps - 1
+        c.reserve(add)
+        c.commit([add[b] - 1 for b in range(rows)])
+        c.fork([stays] * len(others), others)
+        base = [0] * rows
+        base[stays] = held * ps - 1
+        c.reserve([0 if b == stays else 1 for b in range(rows)], base=base)
+        nodes = [[-1] * 3] * rows
+        c.commit([0] * rows, nodes if turn % 2 else None, base=base)
+        assert c.o.lens == [held * ps - 1 if b == stays else 1 for b in range(rows)]
+        assert max(c.o.ref) == 1
+        c.commit([0] * rows, base=base)   # now they are its own
+        assert c.o.lens[stays] == held * ps
+
+
+def test_captured_commit_with_verdicts():
+    """Reserve's verdicts go to commit within a graph; pages run out in some replays."""
+    c = Pair(2, 10, 4, 2, 8, 4, 8)
+    add, acc, nodes = i32([5] * 4), i32([0] * 4), i32([[-1] * 5] * 4)
+    ok = [torch.zeros(4, dtype=torch.int32, device=device()) for _ in range(2)]
+
+    def step():
+        c.cache.reserve(c.bt, add, ok=ok[0])
+        c.cache.commit(c.bt, acc, nodes=nodes, reserved=ok[0], ok=ok[1])
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    seen = []
+    for turn in range(6):
+        c.truncate(new_len=[9, 2, 3, 14] if turn % 3 else [0, 0, 0, 0])
+        c.fork([0], [1])
+        a, n = c.tree(4, 5)
+        acc.copy_(i32(a))
+        nodes.copy_(i32(n))
+        torch.cuda.synchronize()
+        graph.replay()
+        r = c.o.reserve([5] * 4)
+        want = r, c.o.commit(a, n, reserved=r)
+        torch.cuda.synchronize()
+        for g, w in zip(ok, want):
+            assert g.cpu().tolist() == w
+        c.same(("replay", turn))
+        seen += r
+    assert 0 in seen and 1 in seen

@@ -88,3 +88,43 @@ def test_pages_refusals():
     assert c.commit([1], nodes=[[2, -1, 0]], base=[6]) == [0]
     assert c.commit([2], nodes=[[2, 2, 0]], base=[0]) == [0]
     assert c.copy_pages([0, 1, 2, 9], [1, 2, 2, 0]) == [0, 0, 0, 0]
+
+
+def test_commit_refuses_what_a_reserve_refused():
+    """Rows that share the page they would write, and rows whose reserve's verdict is 0."""
+    c = OC.Pages(np.arange(2 * 2 * 4, dtype=np.float64).reshape(2, 2, 4, 1, 1), rows=2, max_blocks=2)
+    assert c.reserve([5, 0]) == [1, 1]
+    assert c.commit([4, -1]) == [1, 0] and c.lens == [5, 0]
+    assert c.fork([0], [1]) == [1] and c.ref == [2, 2]
+    before = c.pool.copy()
+    ok = c.reserve([3, 3])                          # a copy each of the last page: none is free
+    assert ok == [0, 0]
+    nodes = [[2, -1, -1]] * 2
+    for reserved in (None, ok):                     # slot 7 to slot 6 of one page, for both
+        assert c.commit([1, 1], nodes, reserved=reserved) == [0, 0]
+        assert c.commit([0, 0], reserved=reserved) == [0, 0]
+    assert c.lens == [5, 5] and np.array_equal(c.pool, before) and c.consistent()
+    c.truncate(rows=[1])
+    assert c.reserve([8, 0]) == [0, 1]              # 13 slots on 2 pages: behind the table
+    assert c.commit([0, -1], reserved=[0, 1]) == [0, 0] and c.lens == [5, 0]
+    assert c.commit([1, -1], nodes, reserved=[1, 1]) == [1, 0] and c.lens == [7, 0]
+    assert np.array_equal(c.pool[:, 1, 2], before[:, 1, 3])
+
+
+def test_commit_reads_counts_as_they_were():
+    """A row that leaves a shared page does not make it another's own in the same call."""
+    for rows in ([0, 1], [1, 0]):
+        stays, leaves = rows
+        c = OC.Pages(np.zeros((1, 3, 4, 1, 1)), rows=2, max_blocks=2)
+        add, base = [0, 0], [0, 0]
+        add[stays] = 5
+        assert c.reserve(add) == [1, 1]
+        c.lens[stays] = base[stays] = 5
+        assert c.fork([stays], [leaves]) == [1] and c.ref == [2, 2, 0]
+        add[stays], add[leaves] = 0, 1
+        assert c.reserve(add, base=base) == [1, 1] and c.ref == [1, 2, 1]
+        want = [0, 0]
+        want[leaves] = 1
+        assert c.commit([0, 0], base=base) == want
+        assert c.ref == [1, 1, 1] and c.lens[stays] == 5 and c.lens[leaves] == 1 and c.consistent()
+        assert c.commit([0, 0], base=base) == [1, 1]
