@@ -105,9 +105,9 @@ class PageCache:
             raise ValueError(f"{name} must be a contiguous 1-D array of at most {most} entries")
         return v.shape[0], v.data_ptr()
 
-    def _ok(self, ok, n, like):
+    def _ok(self, ok, n, like, stream):
         if ok is None:
-            return _empty_rows(n, None, like)
+            return _empty_rows(n, None, like, stream=stream)
         _check_array(ok, "ok", n, self.device)
         return ok
 
@@ -122,7 +122,7 @@ class PageCache:
         ct = self._tables(tables)
         B, add_ptr = self._count(add, "add", ct.rows)
         base = _check_array(lens, "lens", B, self.device)
-        ok = self._ok(ok, B, add)
+        ok = self._ok(ok, B, add, stream)
         st = self.lib.ss_cache_reserve(self.handle, ctypes.byref(ct), base, add_ptr, B,
                                        ok.data_ptr(), _stream_on(stream, self.device))
         if st != SS_OK:
@@ -135,7 +135,7 @@ class PageCache:
         ct = self._tables(tables)
         n, src_ptr = self._count(src, "src", ct.rows)
         dst_ptr = self._vec(dst, "dst", n)
-        ok = self._ok(ok, n, src)
+        ok = self._ok(ok, n, src, stream)
         st = self.lib.ss_cache_fork(self.handle, ctypes.byref(ct), src_ptr, dst_ptr, n,
                                     ok.data_ptr(), _stream_on(stream, self.device))
         if st != SS_OK:
@@ -167,7 +167,7 @@ class PageCache:
             if not 1 <= N <= 64 or stride < N:
                 raise ValueError("nodes must be [B, N] with N in 1 .. 64 and rows that do not overlap")
             at = nodes.data_ptr()
-        ok = self._ok(ok, B, num_accepted)
+        ok = self._ok(ok, B, num_accepted, stream)
         st = self.lib.ss_cache_commit_reserved(self.handle, ctypes.byref(ct), base, at, stride, N,
                                                acc, B, 1 if release else 0, reserved,
                                                ok.data_ptr(), _stream_on(stream, self.device))
@@ -197,7 +197,7 @@ class PageCache:
         other = self if src_cache is None else src_cache
         n, src_ptr = self._count(src, "src", 65535)
         dst_ptr = self._vec(dst, "dst", n)
-        ok = self._ok(ok, n, src)
+        ok = self._ok(ok, n, src, stream)
         st = self.lib.ss_cache_copy_pages(other.handle, src_ptr, self.handle, dst_ptr, n,
                                           ok.data_ptr(), _stream_on(stream, self.device))
         if st != SS_OK:

@@ -188,8 +188,19 @@ _empty_strided = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", N
 _current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
-def _empty_rows(n, m, like, dtype=torch.int32):
-    """An uninitialised [n, m] array (m None: [n]) on the device of `like`."""
+def _empty_rows(n, m, like, dtype=torch.int32, stream=None):
+    """An uninitialised [n, m] array (m None: [n]) on the device of `like`, for a call
+    on `stream` (None: the current one). What another stream writes is allocated
+    there, so that its memory is never one that earlier work of the current stream
+    still uses, and returns to that stream once neither is at work on it."""
+    if stream is not None and stream.cuda_stream != _raw_stream(like.get_device()):
+        device = like.device
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+        with torch.cuda.stream(stream):
+            out = like.new_empty(n if m is None else (n, m), dtype=dtype)
+        out.record_stream(torch.cuda.current_stream(device))
+        return out
     if _empty_strided is not None and _current_device is not None and \
             _current_device() == like.get_device():
         if m is None:
@@ -439,7 +450,7 @@ class Sampler:
         B, V = logits.shape
         _require(V == self.vocab_size, f"logits have {V} columns, the sampler {self.vocab_size}")
         if out is None:
-            out = torch.empty(B, dtype=torch.int32, device=logits.device)
+            out = _empty_rows(B, None, logits, stream=stream)
         _check_vec(out, "out", B, torch.int32, self.device)
         if debug is not None:
             for name, cols in (("processed_logits", V), ("probs", V)):
@@ -488,11 +499,10 @@ class Sampler:
         _check_dev(draft_tokens, "draft_tokens", (torch.int32,), self.device)
         _require(tuple(draft_tokens.shape) == (B, G) and draft_tokens.is_contiguous(),
                  "draft_tokens must be a contiguous [B, G] int32 array")
-        dev = target_logits.device
         if out_tokens is None:
-            out_tokens = torch.empty(B, G1, dtype=torch.int32, device=dev)
+            out_tokens = _empty_rows(B, G1, target_logits, stream=stream)
         if out_num_accepted is None:
-            out_num_accepted = torch.empty(B, dtype=torch.int32, device=dev)
+            out_num_accepted = _empty_rows(B, None, target_logits, stream=stream)
         _check_dev(out_tokens, "out_tokens", (torch.int32,), self.device)
         _require(tuple(out_tokens.shape) == (B, G1) and out_tokens.is_contiguous(),
                  "out_tokens must be a contiguous [B, G+1] int32 array")
@@ -531,13 +541,12 @@ class Sampler:
             _check_dev(t, name, (torch.int32,), self.device)
             _require(tuple(t.shape) == (B, N) and t.is_contiguous(),
                      f"{name} must be a contiguous [B, N] int32 array")
-        dev = target_logits.device
         if out_tokens is None:
-            out_tokens = torch.empty(B, N, dtype=torch.int32, device=dev)
+            out_tokens = _empty_rows(B, N, target_logits, stream=stream)
         if out_nodes is None:
-            out_nodes = torch.empty(B, N, dtype=torch.int32, device=dev)
+            out_nodes = _empty_rows(B, N, target_logits, stream=stream)
         if out_num_accepted is None:
-            out_num_accepted = torch.empty(B, dtype=torch.int32, device=dev)
+            out_num_accepted = _empty_rows(B, None, target_logits, stream=stream)
         for name, t in (("out_tokens", out_tokens), ("out_nodes", out_nodes)):
             _check_dev(t, name, (torch.int32,), self.device)
             _require(tuple(t.shape) == (B, N) and t.is_contiguous(),
@@ -564,7 +573,7 @@ class Sampler:
         _require(tuple(weight.shape) == (self.vocab_size, K) and weight.is_contiguous(),
                  f"weight must be a contiguous [{self.vocab_size}, {K}] array")
         if out is None:
-            out = torch.empty(B, dtype=torch.int32, device=hidden.device)
+            out = _empty_rows(B, None, hidden, stream=stream)
         _check_vec(out, "out", B, torch.int32, self.device)
         _check_vec(path, "path", B, torch.int32, self.device)
         cp = params.to_c(params.validate(B, self.vocab_size, self.device))
@@ -587,7 +596,7 @@ class Sampler:
         _check_vec(request_ids, "request_ids", B, torch.int32, self.device)
         _check_vec(positions, "positions", B, torch.int32, self.device)
         if out is None:
-            out = torch.empty(B, dtype=torch.int32, device=hidden.device)
+            out = _empty_rows(B, None, hidden, stream=stream)
         _check_vec(out, "out", B, torch.int32, self.device)
         if debug_logits is not None:
             _check_dev(debug_logits, "debug_logits", (torch.float32,), self.device)
@@ -632,11 +641,11 @@ class Sampler:
         u = _check_block(uniforms, "uniforms", (B, G1), torch.float32, dev)
         n = _check_array(draft_len, "draft_len", B, dev)
         if out_tokens is None:
-            out_tokens = _empty_rows(B, G1, uniforms)
+            out_tokens = _empty_rows(B, G1, uniforms, stream=stream)
         else:
             _check_block(out_tokens, "out_tokens", (B, G1), torch.int32, dev)
         if out_num_accepted is None:
-            out_num_accepted = _empty_rows(B, None, uniforms)
+            out_num_accepted = _empty_rows(B, None, uniforms, stream=stream)
         else:
             _check_array(out_num_accepted, "out_num_accepted", B, dev)
         seq = None
@@ -686,7 +695,7 @@ class Sampler:
         if out is None:
             if out_dtype is not torch.float32 and out_dtype is not torch.bfloat16:
                 raise ValueError("out_dtype must be float32 or bfloat16")
-            out = _empty_rows(B, V, hidden, out_dtype)
+            out = _empty_rows(B, V, hidden, out_dtype, stream)
             stride = V
         else:
             _check_rows(out, "out", B, (torch.float32, torch.bfloat16), dev)
@@ -711,7 +720,7 @@ def sample_noalloc(logits, params: SamplingParams, out=None, stream=None):
     _check_rows(logits, "logits", 0, (torch.float32, torch.bfloat16), dev)
     B, V = logits.shape
     if out is None:
-        out = torch.empty(B, dtype=torch.int32, device=logits.device)
+        out = _empty_rows(B, None, logits, stream=stream)
     _check_vec(out, "out", B, torch.int32, dev)
     cp = params.to_c(params.validate(B, V, dev))
     with torch.cuda.device(dev):
