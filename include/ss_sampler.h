@@ -502,15 +502,16 @@ int64_t ss_cache_workspace_bytes(const ss_cache* c);
 
 /* ss_cache_reserve -- make slots [base_b, base_b + add_b) of rows 0 .. B-1 writable.
  *   base    [B] int32, or NULL: t->len.   add  [B] int32 >= 0.
- *   out_ok  NULL, or [B] int32: 1 served (add = 0 at base >= 0 always is), 0 refused.
+ *   out_ok  NULL, or [B] int32: 1 served, 0 refused.
  * Every table entry those slots lie on that holds no page, or one that others
  * hold as well, gets a fresh page; of a shared page that holds slots before
  * base_b those slots are copied along (all planes), and its count falls by one.
  * Fresh pages are the lowest-numbered free ones, in row order, then table order;
  * counts are those at the call's start, so rows that share a page and both
- * reserve on it both leave it. Rows are served in order while their pages
- * suffice: once one does not fit, later rows that need pages are refused too. A
- * negative base or add, or slots behind max_blocks pages, is refused by itself.
+ * reserve on it both leave it. Rows are served in order while the pages suffice:
+ * once a row does not fit, every later row is refused too, one that needs no page
+ * (add = 0, or slots on pages of its own) as well. A negative base or add, or slots
+ * behind max_blocks pages, is refused by itself and takes nothing from later rows.
  * A refused row is left as it was. Two kernels. */
 ss_status ss_cache_reserve(ss_cache* c, const ss_block_tables* t, const int32_t* base,
                            const int32_t* add, int32_t B, int32_t* out_ok, void* stream);

@@ -117,8 +117,9 @@ class PageCache:
     def reserve(self, tables: BlockTables, add, lens=None, ok=None, stream=None):
         """Make slots [lens, lens + add) of rows 0 .. B-1 writable (add [B] int32;
         lens None: tables.lens): fresh pages where none is held, and in place of
-        shared ones (copy on write). Returns ok [B] int32 (0: not enough pages,
-        row unchanged)."""
+        shared ones (copy on write). Rows are served in order: behind one that does
+        not fit none is, whatever it needs. Returns ok [B] int32 (0: refused, row
+        unchanged); commit takes it as reserved."""
         ct = self._tables(tables)
         B, add_ptr = self._count(add, "add", ct.rows)
         base = _check_array(lens, "lens", B, self.device)

@@ -506,3 +506,14 @@ def test_captured_commit_with_verdicts():
         c.same(("replay", turn))
         seen += r
     assert 0 in seen and 1 in seen
+
+
+def test_reserve_serves_rows_in_order():
+    """Behind a row that does not fit none is served, also where it needs no page."""
+    c = Pair(1, 5, 2, 1, 8, 5, 6)
+    for add, base, want in (([2, 4, 1, 0, 0], None, [1] * 5), ([6, 4, 2, 0, 1], None, [0] * 5),
+                            ([13, 4, 2, 0, 1], None, [0, 1, 1, 1, 1]),
+                            ([-1, 4, 2, 0, 0], [0, 0, 0, 99, -1], [0, 1, 1, 1, 0])):
+        got = c.cache.reserve(c.bt, i32(add), lens=None if base is None else i32(base))
+        assert got.tolist() == want, (add, base)
+        c.same(("reserve", add, base), got, c.o.reserve(add, base))

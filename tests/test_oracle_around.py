@@ -128,3 +128,15 @@ def test_commit_reads_counts_as_they_were():
         assert c.commit([0, 0], base=base) == want
         assert c.ref == [1, 1, 1] and c.lens[stays] == 5 and c.lens[leaves] == 1 and c.consistent()
         assert c.commit([0, 0], base=base) == [1, 1]
+
+
+def test_reserve_serves_rows_in_order():
+    """Behind a row that does not fit none is served, also where it needs no page; a
+    row refused by itself takes nothing from later ones."""
+    c = OC.Pages(np.zeros((1, 5, 2, 1, 1)), rows=5, max_blocks=6)
+    assert c.reserve([2, 4, 1, 0, 0]) == [1] * 5 and c.ref == [1, 1, 1, 1, 0]
+    # row 0 needs two pages of one; the slots of rows 1 and 2 are their own; row 3 adds none
+    assert c.reserve([6, 4, 2, 0, 1]) == [0, 0, 0, 0, 0]
+    assert c.reserve([13, 4, 2, 0, 1]) == [0, 1, 1, 1, 1]   # behind the table, by itself
+    assert c.reserve([-1, 4, 2, 0, 0], base=[0, 0, 0, 99, -1]) == [0, 1, 1, 1, 0]
+    assert c.ref == [1] * 5 and c.consistent()
