@@ -115,11 +115,16 @@ _samplers = {}
 
 
 def _sampler(**limits):
-    """The sampler handle of a program with these limits: made once, kept."""
+    """The sampler handle of a program with these limits on this device and stream
+    (calls that overlap in time need handles of their own): made once, kept. Of more
+    than four the one made first is let go; states that use it keep it."""
     from speculative_decoding_verification_pipeline_amd.sampler import Sampler
-    key = tuple(sorted(limits.items()))
+    device = torch.cuda.current_device()
+    key = (device, torch.cuda.current_stream().cuda_stream, *sorted(limits.items()))
     if key not in _samplers:
-        _samplers[key] = Sampler(**limits)
+        if len(_samplers) == 4:
+            del _samplers[next(iter(_samplers))]
+        _samplers[key] = Sampler(device=device, **limits)
     return _samplers[key]
 
 
