@@ -62,6 +62,7 @@ constexpr int64_t kAlign = 256;
 constexpr int64_t align_up(int64_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Device pointers for every per-request parameter: an absent one points at the
 // handle's default array (so the kernels read every parameter unconditionally).
@@ -575,6 +576,9 @@ ss_status ss_spec_verify_probs(ss_sampler* s, const void* target_probs, ss_dtype
     if (draft_probs && ((reinterpret_cast<uintptr_t>(draft_probs) & low) || draft_stride < V))
         return SS_ERR_INVALID_ARG;
     if ((G > 0 && !draft_tokens) || !uniforms || !out_tokens || !out_num_accepted)
+        return SS_ERR_INVALID_ARG;
+    if (!aligned4(draft_tokens) || !aligned4(draft_len) || !aligned4(uniforms) ||
+        !aligned4(out_tokens) || !aligned4(out_num_accepted))
         return SS_ERR_INVALID_ARG;
     if (seq && (!seq->tokens || !seq->len || seq->capacity < 0 || seq->stride < seq->capacity))
         return SS_ERR_INVALID_ARG;

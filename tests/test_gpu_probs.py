@@ -331,3 +331,30 @@ def test_the_most_requests():
         s.spec_verify_probs(p, None, none, u)
     assert e.value.status == SM.SS_ERR_UNSUPPORTED
     s.close()
+
+
+def test_misaligned_arrays_are_refused():
+    """Arrays of 32-bit entries that start between entries, as the header says."""
+    B, G, V = 2, 3, 64
+    s = SM.Sampler(B, V, max_draft=G, device=0)
+    target, draft, tokens, u, n = make(B, G, V, torch.float32, True, True, 1)
+    out = torch.zeros(B, G + 1, dtype=torch.int32, device=device())
+    acc = torch.zeros(B, dtype=torch.int32, device=device())
+    good = [t.data_ptr() for t in (tokens, n, u, out, acc)]
+    before = out.clone(), acc.clone()
+
+    def raw(tok, length, uni, o, a):
+        return s.lib.ss_spec_verify_probs(s.handle, target.data_ptr(), SM.SS_F32, V, draft.data_ptr(),
+                                          V, tok, length, uni, B, G, o, a, None, None)
+
+    for i in range(5):
+        for by in (1, 2, 3):
+            at = list(good)
+            at[i] += by
+            assert raw(*at) == SM.SS_ERR_INVALID_ARG, (i, by)
+    torch.cuda.synchronize()
+    assert torch.equal(out, before[0]) and torch.equal(acc, before[1])
+    assert raw(*good) == SM.SS_OK
+    torch.cuda.synchronize()
+    assert np.array_equal(out.cpu().numpy(), expect(target, draft, tokens, u, n)[0])
+    s.close()
