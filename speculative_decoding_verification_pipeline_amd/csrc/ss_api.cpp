@@ -29,7 +29,7 @@ struct ss_sampler {
     ss::LmCut* lm_cut;
     double* probs_part;      // [max_batch * n_wt]
     int32_t* probs_arrived;  // [max_batch * PROBS_COUNTER]: 0 between calls
-    uint64_t* quant_part;    // [QUANT_CUS * QUANT_PART_BYTES]
+    uint64_t* quant_part;    // quant_part_bytes, in the rows' scratch
     int32_t* quant_arrived;  // [QUANT_CUS * QUANT_COUNTER]: 0 between calls
     ss::LaunchEvents events;
     // defaults substituted for absent per-request parameters, [max_batch] each
@@ -60,6 +60,8 @@ namespace {
 constexpr int64_t kAlign = 256;
 
 constexpr int64_t align_up(int64_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+constexpr int QUANT_MOST_K = 1 << 24;  // 32-bit offsets within a tile
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -280,7 +282,12 @@ ss_status ss_sampler_create(const ss_sampler_config* cfg, ss_sampler** out) {
     const int64_t o_info = take(R * (int64_t)sizeof(ss::RowInfo));
     const int64_t o_acc = take(R * 4);
     const int64_t o_restile = take((int64_t)B * nt * (int64_t)sizeof(double2));
-    const int64_t o_scratch = take(R * (int64_t)V * 4);
+    // the 4-bit head's parts lie where the other calls keep whole rows: calls on a
+    // handle follow each other
+    const int64_t scratch = R * (int64_t)V * 4;
+    const bool quant = cfg->hidden_size > 0 && cfg->hidden_size <= QUANT_MOST_K;
+    const int64_t parts = quant ? ss::quant_part_bytes(V, cfg->hidden_size, B) : 0;
+    const int64_t o_scratch = take(scratch > parts ? scratch : parts);
     const int64_t o_bins = take((int64_t)B * nw * ss::NBIN * 4);
     const int64_t dmax = cfg->max_draft > 0 ? cfg->max_draft : 1;
     const int64_t o_tpath = take(R * dmax * 4);
@@ -292,7 +299,6 @@ ss_status ss_sampler_create(const ss_sampler_config* cfg, ss_sampler** out) {
     const int64_t o_lmunres = cfg->hidden_size > 0 ? take(64 * 4) : 0;
     const int64_t o_lmcut = cfg->hidden_size > 0 ? take(64 * (int64_t)sizeof(ss::LmCut)) : 0;
     const int64_t o_probs = take((int64_t)B * nw * (int64_t)sizeof(double));
-    const int64_t o_quant = cfg->hidden_size > 0 ? take(ss::QUANT_CUS * ss::QUANT_PART_BYTES) : 0;
     // counters of 0, filled together with the defaults
     const size_t n_quant = cfg->hidden_size > 0 ? ss::QUANT_CUS * ss::QUANT_COUNTER : 0;
     const size_t n_filled = (4 + ss::PROBS_COUNTER) * (size_t)B + n_quant;
@@ -331,7 +337,7 @@ ss_status ss_sampler_create(const ss_sampler_config* cfg, ss_sampler** out) {
         s->def_one_f = reinterpret_cast<float*>(d + 2 * B);
         s->def_iota = d + 3 * B;
         s->probs_arrived = d + 4 * (size_t)B;
-        s->quant_part = cfg->hidden_size > 0 ? reinterpret_cast<uint64_t*>(b + o_quant) : nullptr;
+        s->quant_part = cfg->hidden_size > 0 ? reinterpret_cast<uint64_t*>(b + o_scratch) : nullptr;
         s->quant_arrived = s->probs_arrived + ss::PROBS_COUNTER * (size_t)B;
         int32_t* h = new (std::nothrow) int32_t[n_filled]();
         if (!h) {
@@ -626,7 +632,7 @@ ss_status ss_lmhead_quant_logits(ss_sampler* s, const uint16_t* hidden, const ui
         (reinterpret_cast<uintptr_t>(out_logits) & (out_dtype == SS_F32 ? 3u : 1u)))
         return SS_ERR_INVALID_ARG;
     if (group != 32 && group != 64 && group != 128) return SS_ERR_UNSUPPORTED;
-    if (s->cfg.hidden_size > (1 << 24)) return SS_ERR_UNSUPPORTED;  // 32-bit offsets within a tile
+    if (s->cfg.hidden_size > QUANT_MOST_K) return SS_ERR_UNSUPPORTED;
     if (!aligned16(hidden) || !aligned16(qweight)) return SS_ERR_UNSUPPORTED;
     ss::QuantArgs a;
     std::memset(&a, 0, sizeof(a));

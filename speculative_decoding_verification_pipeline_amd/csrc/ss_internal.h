@@ -248,14 +248,13 @@ struct QuantArgs {
     int64_t out_stride;
     // row blocks whose K is cut in parts, behind the whole ones (set by the launch)
     int whole_blocks, split_blocks, split, split_stages;
-    uint64_t* part;            // [QUANT_CUS * QUANT_PART_BYTES]: the parts' sums
+    uint64_t* part;            // [quant_part_bytes]: the parts' sums
     int32_t* arrived;          // [QUANT_CUS * QUANT_COUNTER]: parts of each row block that have left
                                //   their sums; 0 between calls
 };
 constexpr int QUANT_CUS = 256;
 constexpr int QUANT_COUNTER = 64;  // integers between counters
 constexpr int QUANT_SPLIT = 8;     // parts of a row block at most; of all, one a CU
-constexpr int64_t QUANT_PART_BYTES = 64 << 10;  // one part's sums at most
 struct QuantSplit {
     int whole_blocks, split_blocks, split, sets;
 };
@@ -386,6 +385,8 @@ hipError_t launch_lmhead(const LmheadArgs& a, hipStream_t st, const LaunchEvents
 hipError_t launch_lmhead_params(const LmheadArgs& a, hipStream_t st, const LaunchEvents& le);
 hipError_t launch_probs(const ProbsArgs& a, ss_dtype dt, hipStream_t st, const LaunchEvents& le);
 hipError_t launch_quant(const QuantArgs& a, hipStream_t st, const LaunchEvents& le);
+// what the parts' sums of any call with these limits take
+int64_t quant_part_bytes(int V, int K, int max_batch);
 hipError_t launch_cache_reserve(const CacheReserve& a, const CacheCopy& g, hipStream_t st);
 hipError_t launch_cache_truncate(const CacheTruncate& a, hipStream_t st);
 hipError_t launch_cache_fork(const CacheFork& a, hipStream_t st);

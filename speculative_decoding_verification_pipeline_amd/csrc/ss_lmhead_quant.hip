@@ -559,23 +559,28 @@ static QuantSplit quant_split(int blocks, int resident, int sets) {
     return s;
 }
 
+// A choice of tiles: what its launch needs and what its parts' sums take.
 template <int GROUP, int NT, int RT, int KW, int WAVES, int BPS, int S>
-static void launch_quant_t(const QuantArgs& a, hipStream_t st, const LaunchEvents& le) {
-    constexpr int rows = WAVES / KW * RT * 16;
-    const int blocks = (a.V + rows - 1) / rows;
-    QuantArgs b = a;
-    constexpr int GPS = LQ_KB / GROUP * BPS, SET = (GPS < 4 ? 4 / GPS : 1) * KW;
-    constexpr int LDS = S * BPS * (KW * NT * 4096 + WAVES * RT * 1024);
-    static_assert(WAVES / KW * RT * NT * WAVE * 16 <= QUANT_PART_BYTES, "a part's sums fit the workspace");
-    const int all = (a.K + LQ_KB * BPS - 1) / (LQ_KB * BPS);
-    const QuantSplit s = quant_split(blocks, 160 * 1024 / LDS, (all + SET - 1) / SET);
-    b.whole_blocks = s.whole_blocks;
-    b.split_blocks = s.split_blocks;
-    b.split = s.split;
-    b.split_stages = s.sets * SET;
-    launch_k(le, 0, k_lmhead_quant<GROUP, NT, RT, KW, WAVES, BPS, S>,
-             dim3(b.whole_blocks + b.split_blocks * b.split), dim3(WAVES * WAVE), st, b);
-}
+struct QuantTiles {
+    static constexpr int rows = WAVES / KW * RT * 16;
+    static constexpr int part_bytes = rows * NT * 16 * 4;
+    static constexpr int GPS = LQ_KB / GROUP * BPS, SET = (GPS < 4 ? 4 / GPS : 1) * KW;
+    static constexpr int LDS = S * BPS * (KW * NT * 4096 + WAVES * RT * 1024);
+    static QuantSplit split(int V, int K) {
+        const int all = (K + LQ_KB * BPS - 1) / (LQ_KB * BPS);
+        return quant_split((V + rows - 1) / rows, 160 * 1024 / LDS, (all + SET - 1) / SET);
+    }
+    static void launch(const QuantArgs& a, hipStream_t st, const LaunchEvents& le) {
+        QuantArgs b = a;
+        const QuantSplit s = split(a.V, a.K);
+        b.whole_blocks = s.whole_blocks;
+        b.split_blocks = s.split_blocks;
+        b.split = s.split;
+        b.split_stages = s.sets * SET;
+        launch_k(le, 0, k_lmhead_quant<GROUP, NT, RT, KW, WAVES, BPS, S>,
+                 dim3(b.whole_blocks + b.split_blocks * b.split), dim3(WAVES * WAVE), st, b);
+    }
+};
 
 // ---------------------------------------------------------------------------
 // one batch row: no matrix cores
@@ -704,6 +709,37 @@ static void launch_rows_t(const QuantArgs& a, hipStream_t st, const LaunchEvents
         hipLaunchKernelGGL((k_quant_rows<GROUP>), grid, dim3(QR_NT), lds, st, a);
 }
 
+// Calls f with the tiles of B rows. Fewer, larger workgroups share a stage of x and
+// widen a weight for more batch rows; where they are few, smaller ones, with K in
+// two ranges where those are few as well.
+template <int GROUP, class F>
+static void quant_choose(int B, int V, F f) {
+    if (B <= 16) {
+        // V = 20000, K = 4096: 17.0 us (one range: 19.1), V = 50257, K = 4160: 44.8 (36.8)
+        if (V <= 32768) f(QuantTiles<GROUP, 1, 1, 2, 8, 2, 2>{});
+        else f(QuantTiles<GROUP, 1, 1, 1, 4, 2, 2>{});
+    } else if (B <= 32) {
+        // V = 32000, K = 2048: 16.8 us (one range: 22.9), V = 50257, K = 4160: 57.7 (45.1;
+        // two row tiles a wave: 46.2), V = 128256, K = 4096: two row tiles 98 (one: 112)
+        if (V <= 32768) f(QuantTiles<GROUP, 2, 1, 2, 8, 1, 2>{});
+        else if (V <= 53248) f(QuantTiles<GROUP, 2, 1, 1, 4, 2, 2>{});
+        else f(QuantTiles<GROUP, 2, 2, 1, 4, 2, 2>{});
+    } else if (V <= 16384) {
+        // V = 16000, K = 4096: 23.2 us (one range: 31.7), V = 24000, K = 2048: 23.1 (21.1)
+        f(QuantTiles<GROUP, 4, 1, 2, 8, 1, 2>{});
+    } else if (V <= 32768 || GROUP == 32) {
+        // V = 32000, K = 2048: 26.5 us (two row tiles a wave: 28.8). Groups of 32 end
+        // with every MFMA: with two row tiles their accumulators do not fit.
+        f(QuantTiles<GROUP, 4, 1, 1, 4, 1, 2>{});
+    } else if constexpr (GROUP >= 64) {
+        // V = 66000, K = 4096: 70 us (256 rows a workgroup: 74); groups of 128, by whole
+        // lines: V = 128256: 114 (128 rows: 121), V = 200000: 176 (191); groups of 64 by
+        // half lines, 128 rows: V = 128256: 140 (256 rows: 154, by whole lines 246)
+        if (GROUP == 64 || V <= 65536) f(QuantTiles<GROUP, 4, 2, 1, 4, 1, 2>{});
+        else if constexpr (GROUP == 128) f(QuantTiles<GROUP, 4, 2, 1, 8, 2, 2>{});
+    }
+}
+
 template <int GROUP>
 static void launch_quant_g(const QuantArgs& a, hipStream_t st, const LaunchEvents& le) {
     // One row: whole rows by v_dot2, where at least four fifths of the lanes have k
@@ -711,37 +747,29 @@ static void launch_quant_g(const QuantArgs& a, hipStream_t st, const LaunchEvent
     // groups of 128: 111 (127), V = 32000, K = 2048: 10.2 (14.1); K = 4160, of three
     // chunks the last nearly empty: 40 (36).
     const int chunks = (a.K + QR_K - 1) / QR_K;
-    if (a.B == 1 && (int64_t)a.K * 5 >= (int64_t)chunks * QR_K * 4 && a.K <= QR_MOST_K) {
+    if (a.B == 1 && (int64_t)a.K * 5 >= (int64_t)chunks * QR_K * 4 && a.K <= QR_MOST_K)
         launch_rows_t<GROUP>(a, st, le);
-        return;
+    else
+        quant_choose<GROUP>(a.B, a.V, [&](auto tiles) { tiles.launch(a, st, le); });
+}
+
+template <int GROUP>
+static int64_t quant_part_bytes_g(int V, int K, int max_batch) {
+    int64_t most = 0;
+    for (const int B : {16, 32, 64}) {  // the last batch of each choice
+        quant_choose<GROUP>(max_batch < B ? max_batch : B, V, [&](auto tiles) {
+            const QuantSplit s = tiles.split(V, K);
+            const int64_t n = (int64_t)s.split_blocks * s.split * tiles.part_bytes;
+            if (n > most) most = n;
+        });
     }
-    // Fewer, larger workgroups share a stage of x and widen a weight for more batch
-    // rows; where they are few, smaller ones, with K in two ranges where those are few
-    // as well.
-    if (a.B <= 16) {
-        // V = 20000, K = 4096: 17.0 us (one range: 19.1), V = 50257, K = 4160: 44.8 (36.8)
-        if (a.V <= 32768) launch_quant_t<GROUP, 1, 1, 2, 8, 2, 2>(a, st, le);
-        else launch_quant_t<GROUP, 1, 1, 1, 4, 2, 2>(a, st, le);
-    } else if (a.B <= 32) {
-        // V = 32000, K = 2048: 16.8 us (one range: 22.9), V = 50257, K = 4160: 57.7 (45.1;
-        // two row tiles a wave: 46.2), V = 128256, K = 4096: two row tiles 98 (one: 112)
-        if (a.V <= 32768) launch_quant_t<GROUP, 2, 1, 2, 8, 1, 2>(a, st, le);
-        else if (a.V <= 53248) launch_quant_t<GROUP, 2, 1, 1, 4, 2, 2>(a, st, le);
-        else launch_quant_t<GROUP, 2, 2, 1, 4, 2, 2>(a, st, le);
-    } else if (a.V <= 16384) {
-        // V = 16000, K = 4096: 23.2 us (one range: 31.7), V = 24000, K = 2048: 23.1 (21.1)
-        launch_quant_t<GROUP, 4, 1, 2, 8, 1, 2>(a, st, le);
-    } else if (a.V <= 32768 || GROUP == 32) {
-        // V = 32000, K = 2048: 26.5 us (two row tiles a wave: 28.8). Groups of 32 end
-        // with every MFMA: with two row tiles their accumulators do not fit.
-        launch_quant_t<GROUP, 4, 1, 1, 4, 1, 2>(a, st, le);
-    } else if constexpr (GROUP >= 64) {
-        // V = 66000, K = 4096: 70 us (256 rows a workgroup: 74); groups of 128, by whole
-        // lines: V = 128256: 114 (128 rows: 121), V = 200000: 176 (191); groups of 64 by
-        // half lines, 128 rows: V = 128256: 140 (256 rows: 154, by whole lines 246)
-        if (GROUP == 64 || a.V <= 65536) launch_quant_t<GROUP, 4, 2, 1, 4, 1, 2>(a, st, le);
-        else if constexpr (GROUP == 128) launch_quant_t<GROUP, 4, 2, 1, 8, 2, 2>(a, st, le);
-    }
+    return most;
+}
+
+int64_t quant_part_bytes(int V, int K, int max_batch) {
+    const int64_t a = quant_part_bytes_g<32>(V, K, max_batch), b = quant_part_bytes_g<64>(V, K, max_batch);
+    const int64_t c = quant_part_bytes_g<128>(V, K, max_batch);
+    return a > b ? (a > c ? a : c) : (b > c ? b : c);
 }
 
 hipError_t launch_quant(const QuantArgs& a, hipStream_t st, const LaunchEvents& le) {

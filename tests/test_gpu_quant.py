@@ -278,3 +278,31 @@ def test_refusals():
     plain.close()
     assert raw() == SM.SS_OK
     s.close()
+
+
+def test_the_parts_take_no_workspace_of_their_own():
+    """Partial sums lie in the scratch of whole rows, which the other calls use between
+    them; only what ss_lmhead_sample needs (8 + 64 bytes per row and 128 vocabulary
+    rows) and the counters come with a hidden size."""
+    for V, B in ((128256, 64), (32000, 64)):
+        with_head, without = (SM.Sampler(B, V, hidden_size=k, device=0) for k in (8192, 0))
+        extra = with_head.workspace_bytes() - without.workspace_bytes()
+        assert 0 < extra <= 64 * 72 * -(-V // 128) + (256 << 10)
+        with_head.close()
+        without.close()
+    V, K = 3000, 1024
+    for B in (1, 7, 30, 64):
+        log(f"quant: shared scratch B={B}")
+        x, q, sc, z = make(B, V, K, 64, True, torch.float16, B)
+        s, fresh = SM.Sampler(B, V, hidden_size=K, device=0), SM.Sampler(B, V, device=0)
+        want = call(s, x, q, sc, z, 64).clone()
+        # rows whose filters keep more than the candidates: selected over their scratch
+        p = SM.SamplingParams(temperature=torch.full((B,), 5.0, device=device()),
+                              top_p=torch.full((B,), 0.999, device=device()), seed=5)
+        wide = torch.randn(B, V, generator=torch.Generator().manual_seed(B)).to(device())
+        tokens = fresh.sample(wide, p)
+        for turn in range(3):
+            assert torch.equal(call(s, x, q, sc, z, 64), want)
+            assert torch.equal(s.sample(wide, p), tokens)
+        s.close()
+        fresh.close()
