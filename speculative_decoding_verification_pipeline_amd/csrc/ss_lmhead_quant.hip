@@ -19,9 +19,9 @@
 //    (vocabulary rows as columns): a lane's accumulators then belong to the
 //    vocabulary row whose weights it widens, so the scale is one value per lane
 //    and row tile.
-//  * Operands go from memory to LDS by global_load_lds_dwordx4, S - 1 stages of
-//    128 BPS k ahead, so the stream stays in flight without registers. Each stage is
-//    an LDS object of its own: the compiler then orders a read against the
+//  * Operands go from memory to LDS by global_load_lds_dwordx4, a stage of 128 BPS k
+//    ahead, so the stream stays in flight without registers. Each of the two stages
+//    is an LDS object of its own: the compiler then orders a read against the
 //    copies into its own stage only, which the explicit wait has seen land. A
 //    wave copies the weights it uses and its share of x. What lies behind K is
 //    copied as zeros of x, so no block is special.
@@ -51,8 +51,7 @@ constexpr int LQ_KB = 128;   // k per block: 16 bytes of weights per lane and ro
 
 #define LQ_LDS(x) ((__attribute__((address_space(3))) void*)(x))
 
-// s_waitcnt with vmcnt n, lgkmcnt 0, expcnt free (gfx9 encoding).
-constexpr int lq_wait(int n) { return (n & 15) | (n >> 4 & 3) << 14 | 0x0070; }
+constexpr int LQ_WAIT = 0x0070;  // s_waitcnt with vmcnt 0, lgkmcnt 0, expcnt free (gfx9 encoding)
 
 // Word of eight nibbles -> eight bfloat16 16 + n, in order. mask and exponent come
 // in vector registers: one v_and_or_b32 takes them, literals would take two
@@ -180,9 +179,8 @@ __device__ __forceinline__ uint64_t lq_pair(float lo, float hi) {
 
 __device__ const u32x4 lq_zero = {0u, 0u, 0u, 0u};
 
-template <int GROUP, int NT, int RT, int KW, int WAVES, int BPS, int S>
+template <int GROUP, int NT, int RT, int KW, int WAVES, int BPS>
 __global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
-    static_assert(S >= 2 && S <= 4, "stages");
     constexpr int RW = WAVES / KW;
     constexpr int ROWS = RW * RT * 16;           // vocabulary rows per workgroup
     constexpr int GPB = LQ_KB / GROUP;           // groups per block
@@ -195,11 +193,8 @@ __global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
     constexpr int XB = KW * NT * XT;             // bytes of x, of weights per stage
     constexpr int WB = WAVES * RT * WT_;
     constexpr int XC = NT * KW * 4 * BPS / WAVES;  // copies of x per wave and stage
-    constexpr int COPIES = RT * BPS + XC;
     __shared__ __attribute__((aligned(1024))) uint8_t b0[XB + WB];
     __shared__ __attribute__((aligned(1024))) uint8_t b1[XB + WB];
-    __shared__ __attribute__((aligned(1024))) uint8_t b2[S > 2 ? XB + WB : 16];
-    __shared__ __attribute__((aligned(1024))) uint8_t b3[S > 3 ? XB + WB : 16];
     __shared__ float s_sum[2 * SPS][KW][4][NT * 16];  // sums of x over a set's groups
     __shared__ float s_scale[WAVES][SPS][4][RT * 16];
     const int tid = threadIdx.x;
@@ -271,7 +266,7 @@ __global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
         const int row = c * RPC + lane / LPR;
         xoff[c] = (uint32_t)min(xtile * 16 + row, a.B - 1) * (uint32_t)K * 2 + unit_of(row) * 16;
     }
-    // Copies of a stage: always COPIES of them, from addresses kept in bounds.
+    // Copies of a stage, from addresses kept in bounds.
     auto copy = [&](uint8_t* buf, int j) {
         uint8_t* ws = buf + XB + wave * RT * WT_;
         const int at = place(j);
@@ -406,9 +401,7 @@ __global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
 
     load_scales(0);
     copy(b0, 0);
-    if (S > 2 && 1 < stages) copy(b1, 1);
-    if (S > 3 && 2 < stages) copy(b2, 2);
-    constexpr int U = S == 3 ? 3 * SET : S > SET ? S : SET;  // a multiple of both
+    constexpr int U = SET > 2 ? SET : 2;  // a multiple of the two stages and of a set
     for (int j0 = 0; j0 < stages; j0 += U) {
         auto stage = [&](auto uc) {
             constexpr int u = decltype(uc)::value;
@@ -416,13 +409,12 @@ __global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
             if (j >= stages) return;
             // this stage has landed for every wave, and the one before has been read
             asm volatile("" ::: "memory");
-            if (j + S - 1 <= stages) __builtin_amdgcn_s_waitcnt(lq_wait((S - 2) * COPIES));
-            else __builtin_amdgcn_s_waitcnt(lq_wait(0));
+            __builtin_amdgcn_s_waitcnt(LQ_WAIT);
             // the builtins say nothing about memory: no access may cross them
             asm volatile("" ::: "memory");
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
-            uint8_t* const bufs[4] = {b0, b1, b2, b3};
+            uint8_t* const bufs[2] = {b0, b1};
             if (u % SET == 0) {
 #pragma unroll
                 for (int h = 0; h < SPS; ++h)
@@ -435,12 +427,12 @@ __global__ __launch_bounds__(WAVES* WAVE, 2) void k_lmhead_quant(QuantArgs a) {
                     }
                 if (j + SET < stages) load_scales(j + SET);
             }
-            if (j + S - 1 < stages) copy(bufs[(u + S - 1) % S], j + S - 1);
+            if (j + 1 < stages) copy(bufs[(u + 1) % 2], j + 1);
             const int slot = SPS == 2 ? j % 2 * 2 : j / SET % 2;
             auto one = [&](auto hc) {
                 constexpr int h = decltype(hc)::value;
                 constexpr int g = (u % SET * GPS + h * GPB) % 4;  // place of its first group
-                block(bufs[u % S], slot + h % SPS, hc, std::integral_constant<int, g>{});
+                block(bufs[u % 2], slot + h % SPS, hc, std::integral_constant<int, g>{});
             };
             lq_each(one, std::make_integer_sequence<int, BPS>{});
             if (u % SET == 0 && j > 0) add_sums(j, c_before);
@@ -560,12 +552,12 @@ static QuantSplit quant_split(int blocks, int resident, int sets) {
 }
 
 // A choice of tiles: what its launch needs and what its parts' sums take.
-template <int GROUP, int NT, int RT, int KW, int WAVES, int BPS, int S>
+template <int GROUP, int NT, int RT, int KW, int WAVES, int BPS>
 struct QuantTiles {
     static constexpr int rows = WAVES / KW * RT * 16;
     static constexpr int part_bytes = rows * NT * 16 * 4;
     static constexpr int GPS = LQ_KB / GROUP * BPS, SET = (GPS < 4 ? 4 / GPS : 1) * KW;
-    static constexpr int LDS = S * BPS * (KW * NT * 4096 + WAVES * RT * 1024);
+    static constexpr int LDS = 2 * BPS * (KW * NT * 4096 + WAVES * RT * 1024);
     static QuantSplit split(int V, int K) {
         const int all = (K + LQ_KB * BPS - 1) / (LQ_KB * BPS);
         return quant_split((V + rows - 1) / rows, 160 * 1024 / LDS, (all + SET - 1) / SET);
@@ -577,7 +569,7 @@ struct QuantTiles {
         b.split_blocks = s.split_blocks;
         b.split = s.split;
         b.split_stages = s.sets * SET;
-        launch_k(le, 0, k_lmhead_quant<GROUP, NT, RT, KW, WAVES, BPS, S>,
+        launch_k(le, 0, k_lmhead_quant<GROUP, NT, RT, KW, WAVES, BPS>,
                  dim3(b.whole_blocks + b.split_blocks * b.split), dim3(WAVES * WAVE), st, b);
     }
 };
@@ -716,27 +708,27 @@ template <int GROUP, class F>
 static void quant_choose(int B, int V, F f) {
     if (B <= 16) {
         // V = 20000, K = 4096: 17.0 us (one range: 19.1), V = 50257, K = 4160: 44.8 (36.8)
-        if (V <= 32768) f(QuantTiles<GROUP, 1, 1, 2, 8, 2, 2>{});
-        else f(QuantTiles<GROUP, 1, 1, 1, 4, 2, 2>{});
+        if (V <= 32768) f(QuantTiles<GROUP, 1, 1, 2, 8, 2>{});
+        else f(QuantTiles<GROUP, 1, 1, 1, 4, 2>{});
     } else if (B <= 32) {
         // V = 32000, K = 2048: 16.8 us (one range: 22.9), V = 50257, K = 4160: 57.7 (45.1;
         // two row tiles a wave: 46.2), V = 128256, K = 4096: two row tiles 98 (one: 112)
-        if (V <= 32768) f(QuantTiles<GROUP, 2, 1, 2, 8, 1, 2>{});
-        else if (V <= 53248) f(QuantTiles<GROUP, 2, 1, 1, 4, 2, 2>{});
-        else f(QuantTiles<GROUP, 2, 2, 1, 4, 2, 2>{});
+        if (V <= 32768) f(QuantTiles<GROUP, 2, 1, 2, 8, 1>{});
+        else if (V <= 53248) f(QuantTiles<GROUP, 2, 1, 1, 4, 2>{});
+        else f(QuantTiles<GROUP, 2, 2, 1, 4, 2>{});
     } else if (V <= 16384) {
         // V = 16000, K = 4096: 23.2 us (one range: 31.7), V = 24000, K = 2048: 23.1 (21.1)
-        f(QuantTiles<GROUP, 4, 1, 2, 8, 1, 2>{});
+        f(QuantTiles<GROUP, 4, 1, 2, 8, 1>{});
     } else if (V <= 32768 || GROUP == 32) {
         // V = 32000, K = 2048: 26.5 us (two row tiles a wave: 28.8). Groups of 32 end
         // with every MFMA: with two row tiles their accumulators do not fit.
-        f(QuantTiles<GROUP, 4, 1, 1, 4, 1, 2>{});
+        f(QuantTiles<GROUP, 4, 1, 1, 4, 1>{});
     } else if constexpr (GROUP >= 64) {
         // V = 66000, K = 4096: 70 us (256 rows a workgroup: 74); groups of 128, by whole
         // lines: V = 128256: 114 (128 rows: 121), V = 200000: 176 (191); groups of 64 by
         // half lines, 128 rows: V = 128256: 140 (256 rows: 154, by whole lines 246)
-        if (GROUP == 64 || V <= 65536) f(QuantTiles<GROUP, 4, 2, 1, 4, 1, 2>{});
-        else if constexpr (GROUP == 128) f(QuantTiles<GROUP, 4, 2, 1, 8, 2, 2>{});
+        if (GROUP == 64 || V <= 65536) f(QuantTiles<GROUP, 4, 2, 1, 4, 1>{});
+        else if constexpr (GROUP == 128) f(QuantTiles<GROUP, 4, 2, 1, 8, 2>{});
     }
 }
 
