@@ -140,7 +140,8 @@ ss_status ss_cache_create(const ss_cache_config* cfg, void* const* planes, ss_ca
     };
     // the plane pointers and the counters of 0, filled by one copy
     const int64_t o_planes = take((int64_t)cfg->num_planes * sizeof(char*));
-    const int64_t o_arrived = take(((int64_t)cfg->max_batch + 2) * ss::CACHE_COUNTER * 4);
+    const int64_t o_arrived =
+        take(((int64_t)cfg->max_batch + 1 + ss::CACHE_GROUPS + 1) * ss::CACHE_COUNTER * 4);
     const int64_t filled = off;
     const int64_t o_ids = take((int64_t)c->n_chunks * ss::CACHE_REF_CHUNK * 4);
     const int64_t o_cnt = take((int64_t)c->n_chunks * 4);
@@ -163,8 +164,9 @@ ss_status ss_cache_create(const ss_cache_config* cfg, void* const* planes, ss_ca
     c->ws.mark = reinterpret_cast<int32_t*>(b + o_mark);
     c->ws.pair_ok = reinterpret_cast<int32_t*>(b + o_pair);
     c->ws.arrived = reinterpret_cast<int32_t*>(b + o_arrived);
-    c->ws.settled = c->ws.arrived + (int64_t)cfg->max_batch * ss::CACHE_COUNTER;
-    c->ws.n_left = c->ws.settled + ss::CACHE_COUNTER;
+    int32_t* settled = c->ws.arrived + (int64_t)cfg->max_batch * ss::CACHE_COUNTER;
+    c->ws.settled = reinterpret_cast<unsigned long long*>(settled);
+    c->ws.n_left = settled + (1 + ss::CACHE_GROUPS) * ss::CACHE_COUNTER;
     char* h = new (std::nothrow) char[(size_t)filled]();
     if (!h) {
         (void)hipFree(c->ws_base);
@@ -275,6 +277,9 @@ ss_status ss_cache_commit_reserved(ss_cache* c, const ss_block_tables* t, const 
     a.settled = c->ws.settled;
     a.n_left = c->ws.n_left;
     a.left = c->ws.mark;
+    // about as many groups as rows in one, from 32 rows on: 65535 rows in 256 of 256
+    a.group = 32;
+    while (a.group * a.group < B) a.group *= 2;
     a.out_ok = out_ok;
     a.num_pages = c->cfg.num_pages;
     a.num_planes = c->cfg.num_planes;

@@ -266,6 +266,7 @@ constexpr int CACHE_REF_CHUNK = 4096;   // page counts listed by one workgroup
 constexpr int CACHE_MAX_CHUNKS = 1024;
 constexpr int CACHE_COUNTER = 64;       // integers between counters: in one line they would be
                                         //   counted one by one
+constexpr int CACHE_GROUPS = 256;       // groups of rows whose settling is counted apart
 constexpr int CACHE_MAX_PAGES = CACHE_REF_CHUNK * CACHE_MAX_CHUNKS;
 
 struct CacheTables {
@@ -298,8 +299,10 @@ struct CacheWork {
     int32_t* pair_ok;   // [num_pages]
     int32_t* arrived;   // [max_batch * CACHE_COUNTER]: workgroups of each row that have read its
                         //   table; 0 between calls
-    int32_t* settled;   // rows of a commit that are settled; 0 between calls
-    int32_t* n_left;    // entries of the list in mark; 0 between calls
+    unsigned long long* settled;  // [1 + CACHE_GROUPS], CACHE_COUNTER integers apart: groups of a
+                        //   commit, and rows of each group, that are settled (low half) and the
+                        //   entries that they left (high half); 0 between calls
+    int32_t* n_left;    // places taken in the list in mark; 0 between calls
 };
 
 struct CacheReserve {
@@ -340,9 +343,10 @@ struct CacheCommit {
     int release;
     const int32_t* reserved;  // [B] or null: the reserve's verdicts
     int32_t* arrived;
-    int32_t* settled;
+    unsigned long long* settled;
     int32_t* n_left;
     int32_t* left;
+    int group;               // rows per group of the counters in settled
     int32_t* out_ok;
     int num_pages, num_planes, page_size, max_blocks;
 };

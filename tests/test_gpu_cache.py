@@ -517,3 +517,39 @@ def test_reserve_serves_rows_in_order():
         got = c.cache.reserve(c.bt, i32(add), lens=None if base is None else i32(base))
         assert got.tolist() == want, (add, base)
         c.same(("reserve", add, base), got, c.o.reserve(add, base))
+
+
+@pytest.mark.parametrize("rows", [32, 33, 1000, 1025, 5000])
+def test_commit_of_many_rows(rows):
+    """Rows are settled in groups: all of them leave a page that one of them holds."""
+    c = Pair(1, 3 * rows + 8, 2, 1, 8, rows, 3)
+    stays = rows // 2
+    others = [b for b in range(rows) if b != stays]
+    for turn in range(2):
+        c.truncate()
+        add = [0] * rows
+        add[stays] = 5
+        c.reserve(add)
+        c.commit([n - 1 for n in add])
+        c.fork([stays] * len(others), others)
+        base = [5 if b == stays else 0 for b in range(rows)]
+        c.reserve([int(b != stays) for b in range(rows)], base=base)
+        c.commit([0] * rows, [[-1, -1]] * rows if turn else None, base=base)
+        assert max(c.o.ref) == 1 and c.o.lens[stays] == 5 and sum(c.o.lens) == rows + 4
+
+
+def test_commit_of_more_pages_than_lanes():
+    """Every kept slot's page is looked at: a shared one far behind the others is found."""
+    n = 200
+    c = Pair(1, 2 * n, 1, 1, 8, 2, n + 3)
+    c.reserve([n, 0])
+    c.commit([n - 1, -1])
+    c.fork([0], [1])
+    c.reserve([0, 150], base=[0, 0])   # slots 0 .. 149 of row 1 are its own
+    for acc in (n - 1, 150, 170, 149):
+        c.commit([-1, acc], base=[0, 0], release=acc != 149)
+        assert c.o.lens == [n, n if acc > 149 else 150]
+    c.commit([-1, 63], base=[0, 86])
+    c.commit([-1, 64], base=[0, 85])
+    c.commit([-1, 0], base=[0, 150])   # its page is row 0's as well, but was given back
+    assert c.o.lens == [n, 150]
