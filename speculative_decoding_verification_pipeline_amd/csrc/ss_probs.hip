@@ -326,10 +326,11 @@ static void launch_probs_p(const ProbsArgs& a, hipStream_t st, const LaunchEvent
 
 template <class T>
 static void launch_probs_t(const ProbsArgs& a, hipStream_t st, const LaunchEvents& le) {
-    // A chunk a workgroup while all of them are resident at once: [1, 4, 32000] f32
-    // 5.4 us (two chunks: 5.8), [48, 5, 50257] 7.4 (7.6). Beyond, two: [32, 4, 128256]
-    // f32 9.6 us (one: 10.6, four: 10.1), [64, 7, 152064] bf16 12.5 (17.5, 12.8).
-    if ((int64_t)a.n_chunks * a.B <= 1536) launch_probs_p<T, 1>(a, st, le);
+    // A chunk a workgroup up to two workgroups a CU. Measured over 16 to 2016 chunks with
+    // draft rows in f32 and bf16 and without, G = 4: 16 chunks 5.7 us (two a workgroup:
+    // 6.2), 256 5.8 (6.2), 504 6.3 (6.4), 600 6.5 (6.4), 800 6.9 (6.7), 1200 7.5 (7.0),
+    // 1512 8.8 (7.4), 2016 10.1 (8.4); [64, 7, 152064] bf16, 4800: 17.5 (12.5, four 12.8).
+    if ((int64_t)a.n_chunks * a.B <= 512) launch_probs_p<T, 1>(a, st, le);
     else launch_probs_p<T, 2>(a, st, le);
 }
 
