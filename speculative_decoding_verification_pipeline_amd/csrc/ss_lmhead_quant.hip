@@ -703,30 +703,38 @@ static void launch_rows_t(const QuantArgs& a, hipStream_t st, const LaunchEvents
 
 // Calls f with the tiles of B rows. Fewer, larger workgroups share a stage of x and
 // widen a weight for more batch rows; where they are few, smaller ones, with K in
-// two ranges where those are few as well.
+// two ranges where those are few as well. The borders are sizes V alone. Over K =
+// 2048, 4096 and 8192, 13 sizes V from 8000 to 128256 and 13, 24 and 64 rows, each
+// choice timed, the one made here was the fastest or within a tenth of it but at
+//  - 24 rows, V = 40000 and 50257: up to 12 % behind two ranges or two row tiles;
+//  - 64 rows, groups of 128, V = 72000 and 100000, K <= 4096: 17 to 22 % behind 128
+//    rows a workgroup (with 256, 282 and 391 blocks leave CUs idle in the last round);
+//  - 64 rows, V = 20000, K = 8192: 10 to 17 % behind two ranges or 256 rows;
+//  - 64 rows, V = 40000, K = 2048: 11 % behind 64 rows a workgroup.
 template <int GROUP, class F>
 static void quant_choose(int B, int V, F f) {
     if (B <= 16) {
-        // V = 20000, K = 4096: 17.0 us (one range: 19.1), V = 50257, K = 4160: 44.8 (36.8)
+        // K = 4096: V = 20000 14.0 us (one range: 17.9), V = 50257 31.0 (27.0)
         if (V <= 32768) f(QuantTiles<GROUP, 1, 1, 2, 8, 2>{});
         else f(QuantTiles<GROUP, 1, 1, 1, 4, 2>{});
     } else if (B <= 32) {
-        // V = 32000, K = 2048: 16.8 us (one range: 22.9), V = 50257, K = 4160: 57.7 (45.1;
-        // two row tiles a wave: 46.2), V = 128256, K = 4096: two row tiles 98 (one: 112)
+        // K = 4096, two ranges, one, two row tiles a wave: V = 32000 21.9 us, 26.1, 28.1;
+        // V = 40000 28.5, 29.5, 30.5; V = 56000 36.7, 42.1, 36.4; V = 128256 86.2, 85.7, 74.0
         if (V <= 32768) f(QuantTiles<GROUP, 2, 1, 2, 8, 1>{});
         else if (V <= 53248) f(QuantTiles<GROUP, 2, 1, 1, 4, 2>{});
         else f(QuantTiles<GROUP, 2, 2, 1, 4, 2>{});
     } else if (V <= 16384) {
-        // V = 16000, K = 4096: 23.2 us (one range: 31.7), V = 24000, K = 2048: 23.1 (21.1)
+        // groups of 128: V = 16000, K = 4096: 21.1 us (one range: 27.5), V = 24000: 33.9 (32.3)
         f(QuantTiles<GROUP, 4, 1, 2, 8, 1>{});
     } else if (V <= 32768 || GROUP == 32) {
-        // V = 32000, K = 2048: 26.5 us (two row tiles a wave: 28.8). Groups of 32 end
-        // with every MFMA: with two row tiles their accumulators do not fit.
+        // groups of 128, K = 4096: V = 32000 35.0 us (two row tiles a wave: 38.2), V = 50257
+        // 51.5 (48.2). Groups of 32 end with every MFMA: with two row tiles their
+        // accumulators do not fit.
         f(QuantTiles<GROUP, 4, 1, 1, 4, 1>{});
     } else if constexpr (GROUP >= 64) {
-        // V = 66000, K = 4096: 70 us (256 rows a workgroup: 74); groups of 128, by whole
-        // lines: V = 128256: 114 (128 rows: 121), V = 200000: 176 (191); groups of 64 by
-        // half lines, 128 rows: V = 128256: 140 (256 rows: 154, by whole lines 246)
+        // K = 4096: groups of 128, 256 rows a workgroup by whole lines: V = 64000 53.5 us (128
+        // rows: 50.3), V = 128256 104.5 (107.9), V = 200000 176 (191); groups of 64 by half
+        // lines, 128 rows: V = 128256 123 (64 rows: 150; 256 rows and whole lines were slower)
         if (GROUP == 64 || V <= 65536) f(QuantTiles<GROUP, 4, 2, 1, 4, 1>{});
         else if constexpr (GROUP == 128) f(QuantTiles<GROUP, 4, 2, 1, 8, 2>{});
     }
