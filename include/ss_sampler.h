@@ -521,7 +521,9 @@ ss_status ss_cache_reserve(ss_cache* c, const ss_block_tables* t, const int32_t*
  * before is given back.
  *   src, dst  [n] int32 rows, n <= rows.   out_ok  NULL, or [n] int32.
  * A pair is refused (out_ok 0, nothing changed) if a row is out of range, or its
- * dst is named by another pair's dst or by any pair's src. One kernel. */
+ * dst is named by another pair's dst or by any pair's src. A row is forked between
+ * steps: after it the page of slot len is shared, and a draft that was reserved and
+ * written before is refused by commit for both rows. One kernel. */
 ss_status ss_cache_fork(ss_cache* c, const ss_block_tables* t, const int32_t* src,
                         const int32_t* dst, int32_t n, int32_t* out_ok, void* stream);
 

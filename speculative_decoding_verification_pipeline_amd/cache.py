@@ -132,7 +132,8 @@ class PageCache:
 
     def fork(self, tables: BlockTables, src, dst, ok=None, stream=None):
         """Rows dst become copies of rows src (int32 [n]) that share their pages;
-        what dst held is given back. Returns ok [n] int32."""
+        what dst held is given back. Fork between steps, not between a row's reserve
+        and its commit, which would refuse it. Returns ok [n] int32."""
         ct = self._tables(tables)
         n, src_ptr = self._count(src, "src", ct.rows)
         dst_ptr = self._vec(dst, "dst", n)

@@ -553,3 +553,18 @@ def test_commit_of_more_pages_than_lanes():
     c.commit([-1, 64], base=[0, 85])
     c.commit([-1, 0], base=[0, 150])   # its page is row 0's as well, but was given back
     assert c.o.lens == [n, 150]
+
+
+def test_a_fork_within_a_step_is_refused_by_commit():
+    """The page that a step writes is shared by then: neither row may write to it."""
+    c = Pair(2, 12, 4, 2, 8, 3, 4)
+    c.reserve([2, 2, 2])
+    c.commit([1, 1, 1])
+    c.reserve([5, 5, 5])
+    c.fork([0], [1])
+    nodes = [[2, 4, -1, -1, -1]] * 3
+    c.commit([2, 2, 2], nodes)
+    assert c.o.lens == [2, 2, 5]
+    c.reserve([5, 5, 0])          # the next step: each on a page of its own
+    c.commit([2, 2, -1], nodes)
+    assert c.o.lens == [5, 5, 5]
