@@ -588,6 +588,140 @@ ss_status ss_cache_truncate(ss_cache* c, const ss_block_tables* t, const int32_t
 ss_status ss_cache_copy_pages(ss_cache* src_cache, const int32_t* src, ss_cache* dst_cache,
                               const int32_t* dst, int32_t n, int32_t* out_ok, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Attention over a cache held in 8 bits
+ *
+ * A scaled cache holds keys and values as 8-bit floats (1 sign, 4 exponent and 3
+ * mantissa bits, largest value 448, one NaN pattern per sign) with a power of two
+ * for each block of slots and head: a byte q under the scale byte s stands for
+ * q 2^(s - 127). Its pages are those of ss_cache_*, which carry the scales along:
+ * reserve and copy_pages copy them with the slots, and commit, where an accepted
+ * node moves to a block of another scale, gives the block the largest of the scales
+ * that its kept slots had and rounds them to it. */
+
+/* The scales: planes of num_pages pages of page_size / block blocks of heads bytes. */
+typedef struct {
+    int32_t block;        /* slots that share a scale: 16, 32 or 64; divides page_size */
+    int64_t page_stride;  /* bytes between pages, blocks and heads: any order, as long */
+    int64_t block_stride; /*   as no two bytes coincide; a dimension of one entry may */
+    int64_t head_stride;  /*   have any stride */
+} ss_cache_scales;
+
+/* Creates the handle of a scaled cache: as ss_cache_create, with piece_bytes the head's
+ * size (a multiple of 16 up to 256), page_size a multiple of 16, and planes and strides
+ * aligned to 16 bytes (SS_ERR_UNSUPPORTED otherwise). scales: HOST array of num_planes
+ * device pointers, read during the call; no two arrays may share bytes. Scale bytes lie
+ * in 67 .. 187 (2^-60 .. 2^60), as ss_cache_write leaves them. */
+ss_status ss_cache_create_scaled(const ss_cache_config* cfg, void* const* planes,
+                                 uint8_t* const* scales, const ss_cache_scales* layout,
+                                 ss_cache** out);
+
+/* A [B, N, heads, dim] array of 16-bit floats (device, 16-byte aligned); strides in
+ * elements, multiples of 8, the head's entries side by side. */
+typedef struct {
+    void* data;
+    int64_t row_stride, token_stride, head_stride;
+} ss_heads;
+
+/* The tokens of a step: request b has the n_b = min(max(counts[b], 0), N) tokens behind
+ * base_b, token i in slot base_b + i. All pointers device, 4-byte aligned. */
+typedef struct {
+    int32_t B;                /* rows 0 .. B-1 of the tables */
+    int32_t N;                /* 1 .. max_blocks * page_size; with parents 1 .. 64 */
+    const int32_t* base;      /* [B], or NULL: t->len. A row with a negative base or one
+                                 behind its max_blocks pages has no tokens */
+    const int32_t* counts;    /* [B], or NULL: N */
+    const int32_t* parents;   /* [B, N] as ss_tree_verify's, or NULL: each token follows
+                                 the one before it */
+    const int32_t* reserved;  /* [B], or NULL: ss_cache_reserve's out_ok; rows with 0
+                                 there have no tokens */
+} ss_cache_step;
+
+/* A rotation of heads by position. Pair i of the first dim entries of a head, (x[2i],
+ * x[2i+1]) if interleaved, else (x[i], x[i + dim/2]), is turned by turns[i] whole turns
+ * per position and multiplied by magnitude; the entries behind dim stay. Angles are
+ * formed in binary64. */
+typedef struct {
+    const double* turns;  /* [dim / 2] device, 8-byte aligned */
+    int32_t dim;          /* even, 2 .. the head's size */
+    int32_t interleaved;  /* nonzero: neighbours are pairs */
+    double magnitude;
+} ss_rotary;
+
+/* ss_rotate -- turn queries and keys by their positions, on any device.
+ *   queries, out_queries  [B, N, q_heads, head_dim] of dtype (SS_BF16 or SS_F16).
+ *   keys, out_keys        [B, N, k_heads, head_dim], or NULL (k_heads 0).
+ *   positions             [B, N] int32.
+ * Here arrays need only be aligned to their elements and strides may be any, as long as
+ * the outputs' entries do not coincide. An output may be its input (same data and
+ * strides), and must not overlap an input otherwise. Each value is rounded once, from
+ * binary32. One kernel; no handle and no workspace, so calls may overlap in time.
+ * Errors: SS_ERR_INVALID_ARG for a null or misaligned pointer, another dtype, or a size
+ * out of range (head_dim 1 .. 65536, heads of both 1 .. 65536, B * N below 2^31). */
+ss_status ss_rotate(int32_t device, const ss_rotary* rotary, ss_dtype dtype, int32_t B, int32_t N,
+                    int32_t head_dim, const int32_t* positions, const ss_heads* queries,
+                    const ss_heads* out_queries, int32_t q_heads, const ss_heads* keys,
+                    const ss_heads* out_keys, int32_t k_heads, void* stream);
+
+/* ss_cache_write -- write a step's keys and values into planes k_plane and v_plane.
+ *   keys, values  [B, N, heads, dim] of dtype (SS_BF16 or SS_F16), heads and dim those of
+ *                 the cache.
+ *   rotary        NULL, or the rotation of the keys (and queries) before they are written:
+ *                 its dim and the halves of its pairs multiples of 16 and 8.
+ *   positions     [B, N] int32 positions for the rotation, or NULL: base_b + i, in a tree
+ *                 base_b + the node's depth.
+ *   queries       NULL, or [B, N, q_heads, dim] turned along into out_queries (which may
+ *                 be the same array); rows of tokens that there are not become 0.
+ * A block's scale is the least power of two, from 2^-60 to 2^60, under which its finite
+ * entries are at most 448; where the block holds slots before base_b, the larger of that
+ * and its old one, to which those slots are rounded again (a shift of the exponent: exact
+ * but for values that fall below 2^-6). Entries become the nearest 8-bit float, ties to
+ * even; larger ones the largest, infinities and NaN a NaN. Turned keys are rounded once,
+ * from binary64. Slots on no page, or on one that others hold as well, are not written.
+ * One kernel. */
+ss_status ss_cache_write(ss_cache* c, const ss_block_tables* t, const ss_cache_step* step,
+                         int32_t k_plane, int32_t v_plane, ss_dtype dtype, const ss_heads* keys,
+                         const ss_heads* values, const ss_rotary* rotary,
+                         const int32_t* positions, const ss_heads* queries,
+                         const ss_heads* out_queries, int32_t q_heads, void* stream);
+
+/* ss_cache_read -- the values of slots start_b .. start_b + n_b - 1 of rows 0 .. B-1.
+ *   start   [B] int32, or NULL: 0.   counts  [B] int32, or NULL: N.
+ *   out_keys, out_values  [B, N, heads, dim] of dtype (SS_BF16, SS_F16), either may be
+ *           NULL. Entries behind n_b = min(max(counts[b], 0), N), and of slots that lie
+ *           on no page or before 0, are 0.
+ * Values are exact in bfloat16; in float16 they are rounded to nearest, to an infinity
+ * from 65520 on. One kernel. */
+ss_status ss_cache_read(ss_cache* c, const ss_block_tables* t, const int32_t* start,
+                        const int32_t* counts, int32_t B, int32_t N, int32_t k_plane,
+                        int32_t v_plane, ss_dtype dtype, const ss_heads* out_keys,
+                        const ss_heads* out_values, void* stream);
+
+/* ss_cache_attend -- attention of a step's tokens over the cache.
+ *   queries, out  [B, N, q_heads, dim] of dtype (SS_BF16 or SS_F16); q_heads a multiple of
+ *                 the cache's heads: queries h read head h / (q_heads / heads).
+ *   scale         positive: what dot products are multiplied by.
+ *   out_lse       NULL, or [B, N, q_heads] float32: the logarithm of the sum of
+ *                 exponentials, -inf where a token sees nothing.
+ * Token i of request b sees the slots before base_b and, of the step's, its own and those
+ * before it; in a tree its own and those of the nodes above it. Slots on no page are not
+ * seen. A token that sees nothing (behind n_b, below no root, of a row without tokens or
+ * pages), or scores of -inf alone, gets 0. Whatever slots hold that a token does not see, NaN among it, does not reach it.
+ * Products are exact, sums and the softmax's statistics binary32; weights are rounded to
+ * float16 under a running power of two before they meet the values, the result once more.
+ * Results do not depend on the order in which workgroups run. One kernel; it counts in
+ * the handle's workspace.
+ *
+ * Errors of the calls on a scaled cache, before any launch: as of the other ss_cache
+ * calls, and SS_ERR_INVALID_ARG for a handle without scales, planes out of range or the
+ * same twice, another dtype, sizes out of range or a rotary without turns;
+ * SS_ERR_UNSUPPORTED for data or strides that are not aligned and a rotary whose sizes
+ * are not multiples as said. */
+ss_status ss_cache_attend(ss_cache* c, const ss_block_tables* t, const ss_cache_step* step,
+                          int32_t k_plane, int32_t v_plane, ss_dtype dtype,
+                          const ss_heads* queries, const ss_heads* out, int32_t q_heads,
+                          float scale, float* out_lse, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

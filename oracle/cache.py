@@ -27,6 +27,16 @@ class Pages:
                 self.ref[self.tables[row][i]] -= 1
             self.tables[row][i] = -1
 
+    def _carry(self, new, old, slots):
+        self.pool[:, new, :slots] = self.pool[:, old, :slots]
+
+    def _move(self, moves):
+        for sp, s, dp, d in moves:
+            self.pool[:, dp, d] = self.pool[:, sp, s]
+
+    def _copy(self, dst, src):
+        self.pool[:, dst] = self.pool[:, src]
+
     def reserve(self, add, base=None):
         base = list(self.lens if base is None else base)
         before = list(self.ref)
@@ -49,8 +59,7 @@ class Pages:
                 if self.held(old):
                     self.ref[old] -= 1
                     if i == lo:
-                        r = base[b] % self.ps
-                        self.pool[:, new, :r] = self.pool[:, old, :r]
+                        self._carry(new, old, base[b] % self.ps)
                 self.ref[new] += 1
                 tab[i] = new
         return ok
@@ -102,8 +111,7 @@ class Pages:
             ok.append(int(good))
             if not good:
                 continue
-            for sp, s, dp, d in moves:
-                self.pool[:, dp, d] = self.pool[:, sp, s]
+            self._move(moves)
             self.lens[b] = base[b] + 1 + n
             if release:
                 self._drop(b, self.pages_of(self.lens[b]))
@@ -123,7 +131,7 @@ class Pages:
               for s, d in zip(src, dst)]
         for s, d, good in zip(src, dst, ok):
             if good:
-                self.pool[:, d] = self.pool[:, s]
+                self._copy(d, s)
         return ok
 
     def consistent(self):

@@ -18,7 +18,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libss_sampler.so")
 SOURCES = ["ss_api.cpp", "ss_cache_api.cpp", "ss_rows.hip", "ss_lmhead.hip", "ss_lmhead_quant.hip",
-           "ss_probs.hip", "ss_cache.hip"]
+           "ss_probs.hip", "ss_cache.hip", "ss_kv8.hip", "ss_attend.hip"]
 ARCH = "gfx950"
 
 CFLAGS = [

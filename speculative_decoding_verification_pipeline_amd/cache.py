@@ -3,7 +3,9 @@
 A PageCache names the planes (a layer's keys, a layer's values, ...) that share
 page numbers; BlockTables holds the device arrays that say which request holds
 which pages. The pages around a verification step: reserve slots for the draft,
-run the model, verify, commit what was accepted. Nothing is read back to the
+run the model, verify, commit what was accepted. A cache whose pages hold 8-bit
+floats with a scale for each block of slots and head also writes a step's keys
+and values, attends over them and reads them back. Nothing is read back to the
 host; everything is computed in the HIP library.
 """
 from __future__ import annotations
@@ -13,8 +15,9 @@ from dataclasses import dataclass
 
 import torch
 
-from .sampler import (SS_OK, CacheConfig, CBlockTables, _check, _check_array, _check_block,
-                      _check_dev, _check_rows, _empty_rows, _require, _stream_on, load_library)
+from .sampler import (_HALF_DTYPES, SS_OK, CacheConfig, CacheScales, CBlockTables, CCacheStep, _check,
+                      _check_array, _check_block, _check_dev, _check_out_heads, _check_rows, _empty,
+                      _empty_rows, _heads, _require, _stream_on, load_library)
 
 
 @dataclass
@@ -30,9 +33,16 @@ class PageCache:
     heads, dim] tensor, or a list of [num_pages, page_size, heads, dim] tensors
     of one dtype, shape and stride. The last dimension has unit stride, the
     others any (a transposed view of pages that hold heads outside slots is
-    fine) as long as no two pieces overlap. The planes are kept referenced."""
+    fine) as long as no two pieces overlap. The planes are kept referenced.
 
-    def __init__(self, planes, max_batch, max_blocks):
+    scales: a cache held in 8 bits (write, read, attend). The planes are then
+    float8_e4m3fn or uint8, plane 2 l the keys and 2 l + 1 the values of layer l,
+    and scales a [num_planes, num_pages, page_size / block, heads] uint8 tensor (or
+    a list) for blocks of 16, 32 or 64 slots: a byte q under the scale byte s
+    stands for q 2^(s - 127). dim is a multiple of 16 up to 256, page_size a
+    multiple of the block."""
+
+    def __init__(self, planes, max_batch, max_blocks, scales=None):
         self.handle = None
         self.lib = load_library()
         planes = list(planes.unbind(0)) if isinstance(planes, torch.Tensor) else list(planes)
@@ -52,9 +62,30 @@ class PageCache:
                           max_blocks, p.device.index)
         ptrs = (ctypes.c_void_p * len(planes))(*[q.data_ptr() for q in planes])
         h = ctypes.c_void_p()
-        _check("ss_cache_create", self.lib.ss_cache_create(ctypes.byref(cfg), ptrs, ctypes.byref(h)))
+        if scales is None:
+            _check("ss_cache_create",
+                   self.lib.ss_cache_create(ctypes.byref(cfg), ptrs, ctypes.byref(h)))
+        else:
+            scales = list(scales.unbind(0)) if isinstance(scales, torch.Tensor) else list(scales)
+            _require(p.dtype in (torch.float8_e4m3fn, torch.uint8),
+                     "planes with scales must be float8_e4m3fn or uint8")
+            _require(len(scales) == len(planes), "scales must be one for each plane")
+            x = scales[0]
+            for q in scales:
+                _check_dev(q, "scales", (torch.uint8,), p.device.index)
+                _require(q.dim() == 3 and q.shape == x.shape and q.stride() == x.stride(),
+                         "all scales must have one shape and one stride")
+            _require(x.shape[0] == p.shape[0] and x.shape[2] == p.shape[2] and x.shape[1] > 0 and
+                     p.shape[1] % x.shape[1] == 0,
+                     "scales must be [num_planes, num_pages, page_size / block, heads]")
+            lay = CacheScales(p.shape[1] // x.shape[1], x.stride(0), x.stride(1), x.stride(2))
+            xptrs = (ctypes.c_void_p * len(scales))(*[q.data_ptr() for q in scales])
+            _check("ss_cache_create_scaled",
+                   self.lib.ss_cache_create_scaled(ctypes.byref(cfg), ptrs, xptrs, ctypes.byref(lay),
+                                                   ctypes.byref(h)))
         self.handle = h
-        self.planes = planes
+        self.planes, self.scales = planes, scales
+        self.heads, self.dim = p.shape[2], p.shape[3]
         self.num_pages, self.page_size = p.shape[0], p.shape[1]
         self.max_batch, self.max_blocks = max_batch, max_blocks
         self.device = p.device.index
@@ -205,3 +236,145 @@ class PageCache:
         if st != SS_OK:
             _check("ss_cache_copy_pages", st)
         return ok
+
+    def _step(self, tables, like, lens, counts, parents, reserved):
+        """A step's tokens as the ABI takes them; like: [B, N, ...]."""
+        ct = self._tables(tables)
+        B, N = like.shape[0], like.shape[1]
+        _require(B <= ct.rows, f"the step has {B} rows, the tables {ct.rows}")
+        _require(1 <= N <= self.max_blocks * self.page_size,
+                 f"a step has 1 .. {self.max_blocks * self.page_size} tokens a row")
+        at = None
+        if parents is not None:
+            _require(N <= 64, "a draft tree has at most 64 nodes")
+            at = _check_block(parents, "parents", (B, N), torch.int32, self.device)
+        return ct, CCacheStep(B, N, _check_array(lens, "lens", B, self.device),
+                              _check_array(counts, "counts", B, self.device), at,
+                              _check_array(reserved, "reserved", B, self.device))
+
+    def _layer(self, layer):
+        _require(self.scales is not None, "the cache has no scales")
+        _require(0 <= layer and 2 * layer + 1 < len(self.planes),
+                 f"layer must be in 0 .. {len(self.planes) // 2 - 1}")
+        return 2 * layer, 2 * layer + 1
+
+    def _dtype(self, t, name):
+        code = _HALF_DTYPES.get(getattr(t, "dtype", None))
+        _require(code is not None and t.dim() == 4,
+                 f"{name} must be a [B, N, heads, dim] array of bfloat16 or float16")
+        return code
+
+    def _like(self, out, name, t, stream):
+        """The given output of t's shape and type, else a new one."""
+        if out is None:
+            return _empty(tuple(t.shape), t, t.dtype, stream)
+        _heads(out, name, t.shape, t.dtype, self.device)
+        _check_out_heads(out, name)
+        return out
+
+    def write(self, tables: BlockTables, layer, keys, values, lens=None, counts=None, parents=None,
+              reserved=None, rotary=None, positions=None, queries=None, out_queries=None,
+              stream=None):
+        """Write a step's keys and values [B, N, heads, dim] (bfloat16 or float16) into
+        the slots behind lens (None: tables.lens), in 8 bits: token i of row b into
+        slot lens[b] + i, the first counts[b] of them (None: all N). reserved: what
+        reserve returned; rows with 0 there write nothing.
+
+        rotary (a Rotary whose dim is a multiple of 16): the keys are turned by their
+        positions first: positions [B, N] int32, else lens + i, with parents [B, N]
+        (a draft tree as tree_verify takes it) lens + the node's depth. queries
+        [B, N, q_heads, dim] are turned along, into out_queries, which is returned
+        (None: a new array; queries itself: in place); rows of tokens that there are
+        not become 0."""
+        k_plane, v_plane = self._layer(layer)
+        code = self._dtype(keys, "keys")
+        ct, step = self._step(tables, keys, lens, counts, parents, reserved)
+        shape = (step.B, step.N, self.heads, self.dim)
+        k = _heads(keys, "keys", shape, keys.dtype, self.device)
+        v = _heads(values, "values", shape, keys.dtype, self.device)
+        at = None
+        if positions is not None:
+            at = _check_block(positions, "positions", shape[:2], torch.int32, self.device)
+        r = q = o = None
+        q_heads = 0
+        if rotary is not None:
+            r = ctypes.byref(rotary.on(self.device))
+        if queries is not None:
+            _require(rotary is not None, "queries are turned along: give a rotary")
+            q = _heads(queries, "queries", None, keys.dtype, self.device)
+            q_heads = queries.shape[2]
+            _require(queries.shape == (step.B, step.N, q_heads, self.dim) and q_heads > 0,
+                     "queries must be [B, N, q_heads, dim]")
+            out_queries = self._like(out_queries, "out_queries", queries, stream)
+            o = _heads(out_queries, "out_queries", queries.shape, keys.dtype, self.device)
+        st = self.lib.ss_cache_write(self.handle, ctypes.byref(ct), ctypes.byref(step), k_plane,
+                                     v_plane, code, ctypes.byref(k), ctypes.byref(v), r, at, q, o,
+                                     q_heads, _stream_on(stream, self.device))
+        if st != SS_OK:
+            _check("ss_cache_write", st)
+        return out_queries if q is not None else None
+
+    def read(self, tables: BlockTables, layer, N, start=None, counts=None, dtype=torch.bfloat16,
+             out_keys=None, out_values=None, stream=None):
+        """The keys and values of slots start .. start + N - 1 of rows 0 .. B-1 (start
+        [B] int32, None: 0 of every row) as two [B, N, heads, dim] arrays of dtype
+        (bfloat16: exactly; float16). Entries behind counts[b] (None: N) and of slots
+        on no page are 0."""
+        k_plane, v_plane = self._layer(layer)
+        code = _HALF_DTYPES.get(dtype)
+        _require(code is not None, "dtype must be bfloat16 or float16")
+        ct = self._tables(tables)
+        B = ct.rows if start is None and counts is None else \
+            (start if start is not None else counts).shape[0]
+        _require(B <= ct.rows, f"start has {B} rows, the tables {ct.rows}")
+        _require(1 <= N <= self.max_blocks * self.page_size,
+                 f"N must be in 1 .. {self.max_blocks * self.page_size}")
+        first = _check_array(start, "start", B, self.device)
+        n = _check_array(counts, "counts", B, self.device)
+        shape = (B, N, self.heads, self.dim)
+        out = []
+        for t, name in ((out_keys, "out_keys"), (out_values, "out_values")):
+            if t is None:
+                t = _empty(shape, tables.tables, dtype, stream)
+            else:
+                _heads(t, name, shape, dtype, self.device)
+                _check_out_heads(t, name)
+            out.append(t)
+        k, v = (_heads(t, "out", shape, dtype, self.device) for t in out)
+        st = self.lib.ss_cache_read(self.handle, ctypes.byref(ct), first, n, B, N, k_plane, v_plane,
+                                    code, ctypes.byref(k), ctypes.byref(v),
+                                    _stream_on(stream, self.device))
+        if st != SS_OK:
+            _check("ss_cache_read", st)
+        return out[0], out[1]
+
+    def attend(self, tables: BlockTables, layer, queries, lens=None, counts=None, parents=None,
+               reserved=None, scale=None, out=None, lse=None, stream=None):
+        """Attention of a step's queries [B, N, q_heads, dim] (bfloat16 or float16) over
+        the cache; q_heads is a multiple of its heads. Token i of row b stands in slot
+        lens[b] + i (None: tables.lens) and sees the slots before lens[b] and, of the
+        step's, its own and those before it; with parents [B, N] (a draft tree as
+        tree_verify takes it) its own and those of the nodes above it. counts and
+        reserved as for write. scale: None is 1 / sqrt(dim). Returns out, like queries
+        (None: a new array); a token that sees nothing gets 0. lse: None, or a
+        contiguous [B, N, q_heads] float32 array for the logarithms of the sums of
+        exponentials."""
+        k_plane, v_plane = self._layer(layer)
+        code = self._dtype(queries, "queries")
+        ct, step = self._step(tables, queries, lens, counts, parents, reserved)
+        q = _heads(queries, "queries", None, queries.dtype, self.device)
+        q_heads = queries.shape[2]
+        _require(queries.shape[3] == self.dim and q_heads > 0 and q_heads % self.heads == 0,
+                 f"queries must be [B, N, a multiple of {self.heads}, {self.dim}]")
+        out = self._like(out, "out", queries, stream)
+        o = _heads(out, "out", queries.shape, queries.dtype, self.device)
+        at = None
+        if lse is not None:
+            at = _check_block(lse, "lse", (step.B, step.N, q_heads), torch.float32, self.device)
+        st = self.lib.ss_cache_attend(self.handle, ctypes.byref(ct), ctypes.byref(step), k_plane,
+                                      v_plane, code, ctypes.byref(q), ctypes.byref(o), q_heads,
+                                      self.dim ** -0.5 if scale is None else scale, at,
+                                      _stream_on(stream, self.device))
+        if st != SS_OK:
+            _check("ss_cache_attend", st)
+        return out

@@ -1,0 +1,662 @@
+// Attention over a cache held in 8 bits (ss_cache_attend).
+//
+// o = sum_j softmax_j(scale q k_j) v_j over the slots j that a token sees, where a slot's
+// key and value are 8-bit floats q8 under a power of two 2^x for each block of slots and
+// head. One pass over the slots with a running maximum and sum.
+//
+// A wave takes steps of 32 slots and 16 * MT rows, a row being a query head of a token:
+// the query heads that share a head of the cache and the step's tokens stand in one
+// product. It forms S^T = K Q^T and O^T = V^T P^T with v_mfma_f32_16x16x32, keys and
+// values as the A operands, straight from the cache's pages in registers:
+//  * S^T: a lane holds slot (lane & 15) of a tile of 16 and, with each load of 16 bytes,
+//    two runs of 8 of its dimensions; which dimension a lane group's k index names is free
+//    as long as Q is loaded by the same rule, so loads are 16 bytes and neighbouring lane
+//    groups read neighbouring pieces.
+//  * The result, four slots of one row a lane, is the B operand of the second product as it
+//    is: its k index g * 8 + j names slot g * 4 + j of the first tile for j < 4 and
+//    g * 4 + j - 4 of the second beyond. Nothing crosses lanes.
+//  * V^T: a lane holds DP / 16 neighbouring dimensions of the 8 slots of its group, read as
+//    they lie, and pairs slots with byte permutes after widening. The product's rows are
+//    then dimensions (row * DP / 16 + tile), and a lane ends with 4 * DP / 16 neighbouring
+//    entries of one row of the output.
+// An 8-bit float is exact in float16 and bfloat16, so the scales never meet the operands: a
+// key's is a factor on S, and a value's joins the weight's exponent,
+//     p_j = 2^(s_j + x_j - R),   o = sum_j p_j q8_j / sum_j p_j 2^(-x_j),
+// R the running reference of a row. Weights are rounded to float16 (11 bits, where bfloat16
+// has 8): a reference is set to 2^8 below the largest exponent and kept until one passes
+// 2^15, so a weight keeps its bits down to 2^-22 of the largest.
+#include <limits.h>
+
+#include "ss_device.h"
+#include "ss_internal.h"
+
+namespace ss {
+
+constexpr int AT_NT = 256;
+constexpr int AT_WAVES = AT_NT / WAVE;
+constexpr int AT_STEP = 32;                   // slots of a wave's step
+constexpr int AT_UNIT = AT_STEP * AT_WAVES;   // pieces of a row are multiples of it
+constexpr float AT_NONE = -3.0e38f;           // reference of a row that has seen nothing
+constexpr float AT_SET = 8.0f, AT_MOST = 15.0f;
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 h16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 h16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 b16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 b16x8 __attribute__((ext_vector_type(8)));
+typedef const __attribute__((address_space(4))) int32_t* const_i32;  // what no kernel writes meanwhile
+
+template <class T, class F>
+__device__ __forceinline__ T as(F f) {
+    static_assert(sizeof(T) == sizeof(F), "bits");
+    return __builtin_bit_cast(T, f);
+}
+
+template <int N>
+struct Words;
+template <>
+struct Words<1> { typedef uint32_t type; };
+template <>
+struct Words<2> { typedef u32x2 type; };
+template <>
+struct Words<4> { typedef u32x4 type; };
+
+// Two 8-bit floats (the low or high pair of a word) widened exactly.
+template <bool F16>
+__device__ __forceinline__ uint32_t widen(uint32_t w, bool high) {
+    if constexpr (F16)
+        return high ? as<uint32_t>(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true))
+                    : as<uint32_t>(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false));
+    else
+        return high ? as<uint32_t>(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true))
+                    : as<uint32_t>(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
+}
+
+template <bool F16>
+__device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+    if constexpr (F16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(as<h16x8>(a), as<h16x8>(b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as<b16x8>(a), as<b16x8>(b), c, 0, 0, 0);
+}
+
+// Rows of one request as this launch sees them.
+struct AttendRow {
+    int base;   // committed slots
+    int count;  // tokens of the step
+    int end;    // slots that any of them may see
+};
+
+__device__ __forceinline__ AttendRow attend_row(const Kv8Attend& a, int b) {
+    AttendRow r;
+    const int cap = a.g.max_blocks * a.g.page_size;
+    r.base = ((const_i32)a.s.base)[b];
+    r.count = a.s.counts ? min(max(((const_i32)a.s.counts)[b], 0), a.s.N) : a.s.N;
+    if (r.base < 0 || r.base > cap || (a.s.reserved && ((const_i32)a.s.reserved)[b] == 0)) {
+        r.base = 0;
+        r.count = 0;
+    }
+    r.end = r.count ? (int)min((int64_t)r.base + r.count, (int64_t)cap) : 0;
+    return r;
+}
+
+// A scale byte, held to what ss_cache_write leaves: whatever a block holds that nothing was
+// written to, its factors are finite and not 0, and masked slots stay masked.
+__device__ __forceinline__ uint32_t clamp_scale(uint32_t x) {
+    return min(max(x, (uint32_t)(127 + KV8_XMIN)), (uint32_t)(127 + KV8_XMAX));
+}
+
+// 32 slots of keys and values as they lie in the pages.
+template <int DP>
+struct AttendStep {
+    u32x4 k[2][DP / 64];
+    typename Words<DP / 64>::type v[8];
+    uint32_t ks[2], vs[2];  // scale bytes of the two tiles
+    bool ok[2];             // whether the tile lies on a page
+};
+
+// Where a wave stands in its row's table: tile of 16 slots by tile.
+struct AttendCursor {
+    const_i32 table;
+    int block, inner;  // table entry, tile within its page
+    int tiles;         // tiles of a page
+    int left;          // tiles up to the row's last
+    __device__ __forceinline__ void next() {
+        if (++inner == tiles) {
+            inner = 0;
+            ++block;
+        }
+        --left;
+    }
+};
+
+template <int DP>
+__device__ __forceinline__ void attend_load(const Kv8Attend& a, AttendCursor& at, int h,
+                                            uint32_t k_lane, uint32_t v_lane, bool k_on[],
+                                            bool v_on, AttendStep<DP>& x) {
+    const uint32_t slot = (uint32_t)a.g.slot;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        int page = -1;
+        if (at.left > 0) page = at.table[at.block];
+        x.ok[t] = (unsigned)page < (unsigned)a.g.num_pages;
+        const int64_t p = x.ok[t] ? page : 0;
+        const int off = x.ok[t] ? at.inner * 16 : 0;
+        const int64_t from = p * a.g.page + off * a.g.slot + h * a.g.head;
+        const char* kp = a.k.data + from;
+        const char* vp = a.v.data + from;
+#pragma unroll
+        for (int c = 0; c < DP / 64; ++c) {
+            x.k[t][c] = u32x4{0, 0, 0, 0};
+            if (k_on[c]) x.k[t][c] = *reinterpret_cast<const u32x4*>(kp + (k_lane + c * 64));
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            typename Words<DP / 64>::type v = {};
+            if (v_on)
+                v = *reinterpret_cast<const typename Words<DP / 64>::type*>(vp + (v_lane + j * slot));
+            x.v[t * 4 + j] = v;
+        }
+        const int64_t sc = p * a.g.sc_page + off / a.g.block * a.g.sc_block + h * a.g.sc_head;
+        x.ks[t] = clamp_scale(a.k.scales[sc]);
+        x.vs[t] = clamp_scale(a.v.scales[sc]);
+        at.next();
+    }
+}
+
+// What a wave holds of its rows.
+template <int DP, int MT>
+struct AttendState {
+    u32x4 q[MT][DP / 32];
+    f32x4 o[MT][DP / 16];
+    float l[MT];               // this lane's share of the sum
+    float ref[MT];             // the same in the four lanes of a row
+    int n[MT];                 // the row's token
+    unsigned long long up[MT]; // in a tree: the nodes that it sees
+};
+
+template <int DP>
+__device__ __forceinline__ uint32_t word_of(const typename Words<DP / 64>::type& v, int w) {
+    if constexpr (DP == 64) return v;
+    else return v[w];
+}
+
+template <int DP>
+__device__ __forceinline__ void set_word(typename Words<DP / 64>::type& v, int w, uint32_t to) {
+    if constexpr (DP == 64) v = to;
+    else v[w] = to;
+}
+
+// Bytes of a word that are a NaN, as 0x80 each.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+    return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
+// One step. MASK: slots of it that some row does not see: those of the step's own tokens,
+// behind the last one, or on no page.
+template <int DP, int MT, bool F16, bool MASK>
+__device__ __forceinline__ void attend_step(const Kv8Attend& a, AttendStep<DP>& x, int rel, int end_rel,
+                                            AttendState<DP, MT>& w) {
+    constexpr int KS = DP / 32;
+    const int g = (threadIdx.x & (WAVE - 1)) >> 4;
+    f32x4 s[2][MT];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) s[t][m] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int st = 0; st < KS; ++st) {
+            const u32x4 b = x.k[t][st / 2];
+            const uint32_t w0 = b[st % 2 * 2], w1 = b[st % 2 * 2 + 1];
+            const u32x4 k = {widen<F16>(w0, false), widen<F16>(w0, true), widen<F16>(w1, false),
+                             widen<F16>(w1, true)};
+#pragma unroll
+            for (int m = 0; m < MT; ++m) s[t][m] = mfma<F16>(k, w.q[m][st], s[t][m]);
+        }
+    }
+    uint32_t vis[MT];  // bit 4 t + i: slot i of this lane in tile t is seen
+    if constexpr (MASK) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            vis[m] = 0;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = rel + t * 16 + g * 4 + i;  // behind the committed slots
+                    const bool own = a.s.parents ? r < 64 && (w.up[m] >> (r & 63) & 1) : r <= w.n[m];
+                    const bool sees = x.ok[t] && r < end_rel && (r < 0 || own);
+                    vis[m] |= (sees ? 1u : 0u) << (4 * t + i);
+                    if (!sees) s[t][m][i] = -INFINITY;
+                }
+            }
+        }
+        // values that no row sees are not numbers to be multiplied by 0
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const bool there = x.ok[j / 4] && rel + j / 4 * 16 + g * 4 + j % 4 < end_rel;
+#pragma unroll
+            for (int c = 0; c < DP / 64; ++c)
+                set_word<DP>(x.v[j], c, there ? word_of<DP>(x.v[j], c) : 0u);
+        }
+    }
+    float fk[2], xv[2], inv[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        fk[t] = as<float>(x.ks[t] << 23) * a.scale_log2;
+        xv[t] = (float)((int)x.vs[t] - 127);
+        inv[t] = as<float>((254u - x.vs[t]) << 23);
+    }
+    float top[MT];
+    bool grows = false;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        top[m] = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const float most = fmaxf(fmaxf(s[t][m][0], s[t][m][1]), fmaxf(s[t][m][2], s[t][m][3]));
+            top[m] = fmaxf(top[m], __builtin_fmaf(most, fk[t], xv[t]));
+        }
+        grows |= top[m] > w.ref[m] + AT_MOST;
+    }
+    if (__any(grows)) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            top[m] = fmaxf(top[m], xor_lane_f<16>(top[m]));
+            top[m] = fmaxf(top[m], xor_lane_f<32>(top[m]));
+            if (top[m] > w.ref[m] + AT_MOST) {
+                const float to = top[m] - AT_SET;
+                const float f = __builtin_amdgcn_exp2f(w.ref[m] - to);
+                w.ref[m] = to;
+                w.l[m] *= f;
+#pragma unroll
+                for (int d = 0; d < DP / 16; ++d) w.o[m][d] *= f;
+            }
+        }
+    }
+    u32x4 p[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const float c = xv[t] - w.ref[m];
+            float e[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][m][i], fk[t], c));
+            w.l[m] = __builtin_fmaf((e[0] + e[1]) + (e[2] + e[3]), inv[t], w.l[m]);
+            p[m][2 * t] = as<uint32_t>(__builtin_convertvector((f32x2{e[0], e[1]}), h16x2));
+            p[m][2 * t + 1] = as<uint32_t>(__builtin_convertvector((f32x2{e[2], e[3]}), h16x2));
+        }
+    }
+    if constexpr (MASK) {
+        // A NaN among the values reaches the rows that see it and no others: it is
+        // counted where it is seen, and taken out of the product.
+        uint32_t any = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int c = 0; c < DP / 64; ++c) any |= nan_bytes(word_of<DP>(x.v[j], c));
+        if (__any(any != 0)) {
+#pragma unroll
+            for (int c = 0; c < DP / 64; ++c) {
+                uint32_t nan[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t word = word_of<DP>(x.v[j], c);
+                    nan[j] = nan_bytes(word);
+                    set_word<DP>(x.v[j], c, word & ~((nan[j] >> 7) * 0xffu));
+                }
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    u32x4 hot;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        hot[j] = ((nan[2 * j] >> (8 * d + 7)) & 1) * 0x3c00u |
+                                 ((nan[2 * j + 1] >> (8 * d + 7)) & 1) * 0x3c000000u;
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        u32x4 sees;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            sees[j] = (vis[m] >> (2 * j) & 1) * 0x3c00u | (vis[m] >> (2 * j + 1) & 1) * 0x3c000000u;
+                        const f32x4 n = mfma<true>(hot, sees, f32x4{0, 0, 0, 0});
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (n[i] > 0) w.o[m][c * 4 + d][i] = NAN;
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < DP / 64; ++c) {
+        uint32_t lo[8], hi[8];  // dimensions 0 and 1, 2 and 3 of the word
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            lo[j] = widen<true>(word_of<DP>(x.v[j], c), false);
+            hi[j] = widen<true>(word_of<DP>(x.v[j], c), true);
+        }
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            u32x4 v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t u0 = d < 2 ? lo[2 * j] : hi[2 * j], u1 = d < 2 ? lo[2 * j + 1] : hi[2 * j + 1];
+                v[j] = __builtin_amdgcn_perm(u1, u0, d % 2 ? 0x07060302u : 0x05040100u);
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) w.o[m][c * 4 + d] = mfma<true>(v, p[m], w.o[m][c * 4 + d]);
+        }
+    }
+}
+
+// Where workgroup `item` of a head and block of rows works: row b, piece c of its n. Rows
+// are cut into pieces of equal size, about as many over all rows as a.pieces; every wave
+// finds its own by itself.
+struct AttendPiece {
+    int b, c, n, units;  // units of AT_UNIT slots of a piece
+};
+
+__device__ __forceinline__ AttendPiece attend_piece(const Kv8Attend& a, int item) {
+    if (a.pieces == 0) return {item, 0, 1, INT_MAX / AT_UNIT};
+    const int lane = threadIdx.x & (WAVE - 1);
+    int total = 0;
+    for (int b0 = 0; b0 < a.s.B; b0 += WAVE) {
+        const int b = b0 + lane;
+        if (b < a.s.B) total += max(1, (int)(((int64_t)attend_row(a, b).end + AT_UNIT - 1) / AT_UNIT));
+    }
+    total = wave_sum_i(total);
+    const int units = (total + a.pieces - 1) / a.pieces;
+    int before = 0;
+    for (int b0 = 0; b0 < a.s.B; b0 += WAVE) {
+        const int b = b0 + lane;
+        int n = 0;
+        if (b < a.s.B) {
+            const int u = max(1, (int)(((int64_t)attend_row(a, b).end + AT_UNIT - 1) / AT_UNIT));
+            n = (u + units - 1) / units;
+        }
+        const int to = before + wave_incl_scan_i(n);
+        const unsigned long long m = __ballot(item < to);
+        if (m) {
+            const int l = __builtin_ctzll(m);
+            const int nl = __shfl(n, l);
+            return {b0 + l, item - (__shfl(to, l) - nl), nl, units};
+        }
+        before = __shfl(to, WAVE - 1);
+    }
+    return {-1, 0, 0, 0};
+}
+
+// Values that other workgroups, on other XCDs, wrote in this launch or will read in it.
+__device__ __forceinline__ void put(float* p, float a, float b) {
+    __hip_atomic_store(reinterpret_cast<unsigned long long*>(p), as<unsigned long long>(f32x2{a, b}),
+                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ f32x2 get(const float* p) {
+    return as<f32x2>(__hip_atomic_load(reinterpret_cast<const unsigned long long*>(p), __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_AGENT));
+}
+
+// Writes D neighbouring entries of a row of the output from entry d0 on.
+template <int D, bool F16>
+__device__ __forceinline__ void attend_out(const Kv8Attend& a, int b, int n, int head, int d0,
+                                           const float* o, float f) {
+    uint32_t r[D / 2];
+#pragma unroll
+    for (int i = 0; i < D / 2; ++i) {
+        const f32x2 v = {o[2 * i] * f, o[2 * i + 1] * f};
+        if constexpr (F16) r[i] = as<uint32_t>(__builtin_convertvector(v, h16x2));
+        else r[i] = as<uint32_t>(__builtin_convertvector(v, b16x2));
+    }
+    uint16_t* to = a.out.data + b * a.out.row + n * a.out.token + head * a.out.head + d0;
+    typedef typename Words<D / 2 < 4 ? D / 2 : 4>::type V;
+#pragma unroll
+    for (int i = 0; i < D / 2; i += sizeof(V) / 4) {
+        V v;
+#pragma unroll
+        for (unsigned k = 0; k < sizeof(V) / 4; ++k) v[k] = r[i + k];
+        *reinterpret_cast<V*>(to + 2 * i) = v;
+    }
+}
+
+// The factor on a row's output: 0 where it has seen nothing, or scores of -inf alone.
+__device__ __forceinline__ float attend_factor(float l, bool live) {
+    return live && l != 0.0f ? 1.0f / l : 0.0f;
+}
+
+template <int DP, int MT, bool F16>
+__global__ __launch_bounds__(AT_NT) void k_attend(Kv8Attend a) {
+    constexpr int DT = DP / 16;
+    constexpr int PAD = 4;
+    constexpr int SLOT = MT * 16 * (DP + 2);  // floats that a piece leaves
+    __shared__ float s_o[AT_WAVES][16][DP + PAD];
+    __shared__ float s_ref[AT_WAVES][MT * 16], s_l[AT_WAVES][MT * 16];
+    __shared__ int s_live[MT * 16];
+    __shared__ int s_last;
+    const int tid = threadIdx.x;
+    const int lane = tid & (WAVE - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
+    const int g = lane >> 4, col = lane & 15;
+    const int items = a.s.B + a.pieces;
+    const int item = blockIdx.x % items;
+    const int y = blockIdx.x / items;
+    const int h = y / a.blocks;
+    const int first = (y - h * a.blocks) * (MT * 16);  // row of this block
+    const int rows = min(a.s.N * a.group - first, MT * 16);
+    AttendPiece pc = attend_piece(a, item);
+    pc.b = __builtin_amdgcn_readfirstlane(pc.b);
+    pc.c = __builtin_amdgcn_readfirstlane(pc.c);
+    pc.n = __builtin_amdgcn_readfirstlane(pc.n);
+    pc.units = __builtin_amdgcn_readfirstlane(pc.units);
+    if (pc.b < 0) return;
+    const AttendRow row = attend_row(a, pc.b);
+
+    AttendState<DP, MT> w;
+    unsigned long long above = 0;
+    if (a.s.parents) above = tree_node(a.s.parents + (int64_t)pc.b * a.s.N, a.s.N).above;
+    bool k_on[DP / 64];
+#pragma unroll
+    for (int c = 0; c < DP / 64; ++c) k_on[c] = c * 64 + g * 16 < a.g.dim;
+    const bool v_on = col * DT < a.g.dim;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        const int r = first + min(m * 16 + col, rows - 1);
+        const int n = r / a.group;
+        w.n[m] = n;
+        w.l[m] = 0.0f;
+        w.ref[m] = AT_NONE;
+        w.up[m] = 0;
+        if (a.s.parents)
+            w.up[m] = (unsigned long long)(uint32_t)__shfl((int)(above >> 32), n) << 32 |
+                      (uint32_t)__shfl((int)above, n);
+        const bool live = n < row.count && (!a.s.parents || w.up[m] != 0);
+        if (wave == 0 && g == 0) s_live[m * 16 + col] = live;
+        const uint16_t* q = a.q.data + pc.b * a.q.row + n * a.q.token +
+                            (h * a.group + r - n * a.group) * a.q.head + g * 16;
+#pragma unroll
+        for (int st = 0; st < DP / 32; ++st) {
+            w.q[m][st] = u32x4{0, 0, 0, 0};
+            if (k_on[st / 2])
+                w.q[m][st] = *reinterpret_cast<const u32x4*>(q + st / 2 * 64 + st % 2 * 8);
+        }
+#pragma unroll
+        for (int d = 0; d < DT; ++d) w.o[m][d] = f32x4{0, 0, 0, 0};
+    }
+
+    // the slots of this piece, and of this wave of it, in steps
+    int see = row.end;
+    int full = min(row.base, row.end);  // slots before it all rows see
+    if (!a.s.parents && row.count) {
+        see = (int)min((int64_t)see, (int64_t)row.base + (first + rows - 1) / a.group + 1);
+        full = (int)min((int64_t)row.end, (int64_t)row.base + first / a.group + 1);
+    }
+    const int steps = (int)(((int64_t)see + AT_STEP - 1) / AT_STEP);
+    const int s0 = (int)min((int64_t)pc.c * pc.units * AT_WAVES, (int64_t)steps);
+    const int s1 = (int)min((int64_t)(pc.c + 1) * pc.units * AT_WAVES, (int64_t)steps);
+    const int per = (s1 - s0 + AT_WAVES - 1) / AT_WAVES;
+    const int from = min(s0 + wave * per, s1), to = min(from + per, s1);
+    if (from < to) {
+        AttendCursor at;
+        at.table = (const_i32)(a.s.t.tables + (int64_t)pc.b * a.s.t.stride);
+        at.tiles = a.g.page_size / 16;
+        at.block = from * 2 / at.tiles;
+        at.inner = from * 2 - at.block * at.tiles;
+        at.left = (row.end + 15) / 16 - from * 2;
+        const uint32_t k_lane = (uint32_t)col * (uint32_t)a.g.slot + g * 16;
+        const uint32_t v_lane = (uint32_t)g * 4 * (uint32_t)a.g.slot + col * DT;
+        AttendStep<DP> cur, nxt;
+        attend_load<DP>(a, at, h, k_lane, v_lane, k_on, v_on, cur);
+        for (int s = from; s < to; ++s) {
+            if (s + 1 < to) attend_load<DP>(a, at, h, k_lane, v_lane, k_on, v_on, nxt);
+            const int rel = s * AT_STEP - row.base;
+            if (s * AT_STEP + AT_STEP <= full && cur.ok[0] && cur.ok[1])
+                attend_step<DP, MT, F16, false>(a, cur, rel, row.end - row.base, w);
+            else
+                attend_step<DP, MT, F16, true>(a, cur, rel, row.end - row.base, w);
+            cur = nxt;
+        }
+    }
+
+    // the waves' sums to one reference
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        w.l[m] += xor_lane_f<16>(w.l[m]);
+        w.l[m] += xor_lane_f<32>(w.l[m]);
+        if (g == 0) {
+            s_ref[wave][m * 16 + col] = w.ref[m];
+            s_l[wave][m * 16 + col] = w.l[m];
+        }
+    }
+    const int r16 = tid / 16, part = tid % 16;  // what a thread sums up: DT entries of a row
+    float* slot = a.part + (int64_t)blockIdx.x * SLOT;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        __syncthreads();
+        float ref = s_ref[0][m * 16 + col];
+#pragma unroll
+        for (int v = 1; v < AT_WAVES; ++v) ref = fmaxf(ref, s_ref[v][m * 16 + col]);
+        const float f = __builtin_amdgcn_exp2f(w.ref[m] - ref);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int d = 0; d < DT; d += 4) {
+                const f32x4 v = {w.o[m][d][i] * f, w.o[m][d + 1][i] * f, w.o[m][d + 2][i] * f,
+                                 w.o[m][d + 3][i] * f};
+                *reinterpret_cast<f32x4*>(&s_o[wave][col][(g * 4 + i) * DT + d]) = v;
+            }
+        __syncthreads();
+        const int rr = m * 16 + r16;
+        ref = s_ref[0][rr];
+#pragma unroll
+        for (int v = 1; v < AT_WAVES; ++v) ref = fmaxf(ref, s_ref[v][rr]);
+        float l = 0.0f;
+        float o[DT] = {};
+#pragma unroll
+        for (int v = 0; v < AT_WAVES; ++v) {
+            l = __builtin_fmaf(s_l[v][rr], __builtin_amdgcn_exp2f(s_ref[v][rr] - ref), l);
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[d] += s_o[v][r16][part * DT + d];
+        }
+        if (rr >= rows) continue;
+        if (pc.n > 1) {
+            if (part == 0) put(slot + rr * 2, ref, l);
+#pragma unroll
+            for (int d = 0; d < DT; d += 2) put(slot + MT * 32 + rr * DP + part * DT + d, o[d], o[d + 1]);
+        } else {
+            const int r = first + rr, n = r / a.group, head = h * a.group + r - n * a.group;
+            const bool live = s_live[rr] != 0;
+            if (!live) {
+#pragma unroll
+                for (int d = 0; d < DT; ++d) o[d] = 0.0f;
+            }
+            if (part * DT < a.g.dim)
+                attend_out<DT, F16>(a, pc.b, n, head, part * DT, o, attend_factor(l, live));
+            if (a.lse && part == 0)
+                a.lse[((int64_t)pc.b * a.s.N + n) * a.q_heads + head] =
+                    live ? (ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        }
+    }
+    if (pc.n <= 1) return;
+
+    // the last piece of a row adds them all, in their order
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (tid == 0) {
+        int32_t* arrived = a.arrived + ((int64_t)y * a.s.B + pc.b) * KV8_COUNTER;
+        s_last = __hip_atomic_fetch_add(arrived, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == pc.n - 1;
+        if (s_last) __hip_atomic_store(arrived, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    if (!s_last) return;
+    const float* all = a.part + (int64_t)(blockIdx.x - pc.c) * SLOT;  // pieces of a row follow each other
+    for (int rr = r16; rr < rows; rr += 16) {
+        float ref = AT_NONE;
+        for (int c = 0; c < pc.n; ++c) ref = fmaxf(ref, get(all + (int64_t)c * SLOT + rr * 2)[0]);
+        float l = 0.0f;
+        float o[DT] = {};
+#pragma unroll 4
+        for (int c = 0; c < pc.n; ++c) {
+            const float* p = all + (int64_t)c * SLOT;
+            const f32x2 s = get(p + rr * 2);
+            const float f = __builtin_amdgcn_exp2f(s[0] - ref);
+            l = __builtin_fmaf(s[1], f, l);
+#pragma unroll
+            for (int d = 0; d < DT; d += 2) {
+                const f32x2 v = get(p + MT * 32 + rr * DP + part * DT + d);
+                o[d] = __builtin_fmaf(v[0], f, o[d]);
+                o[d + 1] = __builtin_fmaf(v[1], f, o[d + 1]);
+            }
+        }
+        const int r = first + rr, n = r / a.group, head = h * a.group + r - n * a.group;
+        const bool live = s_live[rr] != 0;
+        if (!live) {
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[d] = 0.0f;
+        }
+        if (part * DT < a.g.dim)
+            attend_out<DT, F16>(a, pc.b, n, head, part * DT, o, attend_factor(l, live));
+        if (a.lse && part == 0)
+            a.lse[((int64_t)pc.b * a.s.N + n) * a.q_heads + head] =
+                live ? (ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    }
+}
+
+// How many rows a workgroup takes, and into how many pieces rows are cut.
+template <int DP, int MT, bool F16>
+static hipError_t launch_attend(Kv8Attend a, hipStream_t st) {
+    constexpr int64_t SLOT = MT * 16 * (DP + 2);
+    a.blocks = (int)(((int64_t)a.s.N * a.group + MT * 16 - 1) / (MT * 16));
+    const int64_t y = (int64_t)a.g.heads * a.blocks;
+    // rows are cut where whole ones leave the card's CUs idle or uneven
+    const int64_t most = KV8_PART_FLOATS / SLOT < KV8_SPLITS ? KV8_PART_FLOATS / SLOT : KV8_SPLITS;
+    a.pieces = y * a.s.B <= most / 2 ? (int)(most / 2 / y) : 0;
+    const int64_t grid = y * (a.s.B + a.pieces);
+    if (grid > INT_MAX) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((k_attend<DP, MT, F16>), dim3((unsigned)grid), dim3(AT_NT), 0, st, a);
+    return hipGetLastError();
+}
+
+template <int DP, bool F16>
+static hipError_t launch_attend_rows(const Kv8Attend& a, hipStream_t st) {
+    const int64_t rows = (int64_t)a.s.N * a.group;
+    if (rows <= 16) return launch_attend<DP, 1, F16>(a, st);
+    if (rows <= 32 || DP == 256) return launch_attend<DP, 2, F16>(a, st);
+    return launch_attend<DP, DP == 256 ? 2 : 4, F16>(a, st);
+}
+
+template <bool F16>
+static hipError_t launch_attend_dim(const Kv8Attend& a, hipStream_t st) {
+    if (a.g.dim <= 64) return launch_attend_rows<64, F16>(a, st);
+    if (a.g.dim <= 128) return launch_attend_rows<128, F16>(a, st);
+    return launch_attend_rows<256, F16>(a, st);
+}
+
+hipError_t launch_kv8_attend(const Kv8Attend& a, ss_dtype dt, hipStream_t st) {
+    return dt == SS_F16 ? launch_attend_dim<true>(a, st) : launch_attend_dim<false>(a, st);
+}
+
+}  // namespace ss

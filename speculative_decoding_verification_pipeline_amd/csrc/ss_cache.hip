@@ -22,6 +22,7 @@
 
 #include "ss_device.h"
 #include "ss_internal.h"
+#include "ss_kv8.h"
 
 namespace ss {
 
@@ -29,6 +30,7 @@ constexpr int CA_NT = 256;
 constexpr int CA_WAVES = CA_NT / WAVE;
 constexpr int CA_REF_EPT = CACHE_REF_CHUNK / CA_NT;  // counts per thread of a free-page chunk
 constexpr int CA_UNROLL = 8;
+constexpr int CA_RUNS = 5;       // blocks of 16 slots that 63 neighbouring slots touch
 static_assert(CA_REF_EPT == 16, "four vector loads of counts per thread");
 constexpr int CACHE_COMPARED = 1024;  // pairs that every copying workgroup compares itself
 
@@ -84,6 +86,15 @@ __device__ __forceinline__ void copy_slots(const CacheCopy& g, const char* __res
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             if (u0 + k * CA_NT < total) *reinterpret_cast<V*>(dst + to[k]) = v[k];
+    }
+}
+
+// Copies the scales of the first n blocks of a page of one plane.
+__device__ __forceinline__ void copy_scales(const ScaleCopy& g, const uint8_t* __restrict__ src,
+                                            uint8_t* __restrict__ dst, int n) {
+    for (int i = threadIdx.x; i < n * g.heads; i += CA_NT) {
+        const int k = i / g.heads, h = i - k * g.heads;
+        dst[k * g.dst_block + h * g.dst_head] = src[k * g.src_block + h * g.src_head];
     }
 }
 
@@ -162,7 +173,7 @@ __global__ __launch_bounds__(CA_NT) void k_cache_plan(CacheReserve a) {
 // plane each. Every workgroup finds by itself where its request's pages start
 // in the list of free pages.
 template <int VEC>
-__global__ __launch_bounds__(CA_NT) void k_cache_take(CacheReserve a, CacheCopy g) {
+__global__ __launch_bounds__(CA_NT) void k_cache_take(CacheReserve a, CacheCopy g, ScaleCopy sc) {
     __shared__ RedT<CA_NT> red;
     __shared__ int s_end[CACHE_MAX_CHUNKS];  // free pages up to and including each chunk
     const int tid = threadIdx.x;
@@ -199,8 +210,14 @@ __global__ __launch_bounds__(CA_NT) void k_cache_take(CacheReserve a, CacheCopy 
         if (!ok) return;
         const int plane = blockIdx.x - 1;
         char* p = g.dst_planes[plane];
-        copy_slots<VEC>(g, p + carry * g.src_page, p + fresh(before) * g.dst_page,
-                        (int)((unsigned)a.base[b] % (unsigned)a.page_size));
+        const int to = fresh(before);
+        const int slots = (int)((unsigned)a.base[b] % (unsigned)a.page_size);
+        copy_slots<VEC>(g, p + carry * g.src_page, p + to * g.dst_page, slots);
+        if (sc.src_planes) {
+            uint8_t* q = sc.dst_planes[plane];
+            copy_scales(sc, q + carry * sc.src_page, q + to * sc.dst_page,
+                        (slots + sc.block - 1) / sc.block);
+        }
         return;
     }
     if (tid == 0 && a.out_ok) a.out_ok[b] = ok ? 1 : 0;
@@ -295,11 +312,15 @@ struct CommitRow {
     int acc;
     int len;           // base + 1 + acc
     int64_t src, dst;  // page * src_page + slot * src_slot of lane i's move
+    int64_t src_scale, dst_scale;  // of a scaled cache: where the blocks' scales lie
+    int dst_in;        // and the slot moved to within its block
     bool moves;
     int kept, moved;   // counts: of the kept slots' pages, of the page moved from
 };
 
-__device__ __forceinline__ CommitRow commit_row(const CacheCommit& a, const CacheCopy& g, int b) {
+template <bool SCALED>
+__device__ __forceinline__ CommitRow commit_row(const CacheCommit& a, const CacheCopy& g,
+                                                const ScaleCopy& sc, int b) {
     const int lane = threadIdx.x & (WAVE - 1);
     CommitRow r;
     // what does not depend on anything is loaded together
@@ -312,7 +333,8 @@ __device__ __forceinline__ CommitRow commit_row(const CacheCommit& a, const Cach
         node = nodes[lane];
         prev = lane ? nodes[lane - 1] : 0;
     }
-    r.src = r.dst = 0;
+    r.src = r.dst = r.src_scale = r.dst_scale = 0;
+    r.dst_in = 0;
     r.moves = false;
     r.len = r.kept = r.moved = 0;
     const int64_t room = (int64_t)a.max_blocks * a.page_size;
@@ -342,6 +364,12 @@ __device__ __forceinline__ CommitRow commit_row(const CacheCommit& a, const Cach
             } else {
                 r.src = sp * g.src_page + (s % page_size) * g.src_slot;
                 r.dst = dp * g.dst_page + (d % page_size) * g.dst_slot;
+                if constexpr (SCALED) {
+                    const unsigned block = sc.block;
+                    r.src_scale = sp * sc.src_page + s % page_size / block * sc.src_block;
+                    r.dst_scale = dp * sc.dst_page + d % page_size / block * sc.dst_block;
+                    r.dst_in = (int)(d % block);
+                }
                 r.moves = true;
             }
         }
@@ -386,8 +414,79 @@ __device__ __forceinline__ bool settle(unsigned long long* counter, int all, uns
     return true;
 }
 
-template <int VEC>
-__global__ __launch_bounds__(CA_NT) void k_cache_commit(CacheCommit a, CacheCopy g) {
+// The moves of a scaled cache. A workgroup takes whole heads of planes, a lane one vector of
+// a head, so that nobody else reads or writes the head's scales; they are written when
+// all of them are read. The slots that move fill blocks one after the other; a block's
+// scale becomes the largest that its slots had: the moved ones' and, where it holds slots
+// before them, its own. Slots of a smaller scale are rounded again to it.
+__device__ __forceinline__ void move_scaled(const CacheCommit& a, const CacheCopy& g, const ScaleCopy& sc,
+                                            const CommitRow& r, unsigned long long moves,
+                                            uint8_t (*s_scale)[CA_RUNS]) {
+    const int tid = threadIdx.x;
+    const int here = CA_NT / sc.piece;  // heads of this workgroup
+    const int hh = tid / sc.piece, u = tid - hh * sc.piece;
+    const unsigned head = blockIdx.x * (unsigned)here + hh;
+    const unsigned plane = head / (unsigned)sc.heads, h = head - plane * sc.heads;
+    const bool on = hh < here && plane < (unsigned)a.num_planes;
+    char* p = nullptr;
+    uint8_t* q = nullptr;
+    if (on) {
+        p = g.dst_planes[plane] + h * g.dst_head + u * 16;
+        q = sc.dst_planes[plane] + h * sc.dst_head;
+    }
+    int runs = 0;
+    for (int i0 = __builtin_ctzll(moves); i0 < r.acc; ++runs) {
+        const int64_t to = __shfl(r.dst_scale, i0);
+        const int in = __shfl(r.dst_in, i0);
+        const int n = min(r.acc - i0, sc.block - in);  // slots of this block
+        int own = 0, most = 0;
+        if (on) {
+            if (in > 0) most = own = q[to];
+        }
+        for (int k = 0; k < n; ++k) {
+            const int64_t from = __shfl(r.src_scale, i0 + k);
+            if (on) most = max(most, (int)q[from]);
+        }
+        if (on && u == 0) s_scale[hh][runs] = (uint8_t)most;
+        const int64_t first = __shfl(r.dst, i0) - in * g.dst_slot;
+        if (on && own < most) {
+            for (int k = 0; k < in; ++k) {
+                kv8x16* at = reinterpret_cast<kv8x16*>(p + first + k * g.dst_slot);
+                *at = kv8_shift(*at, own - most);
+            }
+        }
+        for (int k0 = 0; k0 < n; k0 += CA_UNROLL) {
+            kv8x16 v[CA_UNROLL];
+            int by[CA_UNROLL];
+#pragma unroll
+            for (int k = 0; k < CA_UNROLL; ++k) {
+                const int64_t at = __shfl(r.src, i0 + k0 + k), x = __shfl(r.src_scale, i0 + k0 + k);
+                if (on && k0 + k < n) {
+                    v[k] = *reinterpret_cast<const kv8x16*>(p + at);
+                    by[k] = (int)q[x] - most;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < CA_UNROLL; ++k) {
+                const int64_t at = __shfl(r.dst, i0 + k0 + k);
+                if (on && k0 + k < n)
+                    *reinterpret_cast<kv8x16*>(p + at) = by[k] < 0 ? kv8_shift(v[k], by[k]) : v[k];
+            }
+        }
+        i0 += n;
+    }
+    __syncthreads();
+    runs = 0;
+    for (int i0 = __builtin_ctzll(moves); i0 < r.acc; ++runs) {
+        const int64_t to = __shfl(r.dst_scale, i0);
+        const int in = __shfl(r.dst_in, i0);
+        if (on && u == 0) q[to] = s_scale[hh][runs];
+        i0 += min(r.acc - i0, sc.block - in);
+    }
+}
+
+template <int VEC, bool SCALED>
+__global__ __launch_bounds__(CA_NT) void k_cache_commit(CacheCommit a, CacheCopy g, ScaleCopy sc) {
     typedef typename CacheVec<VEC>::type V;
     __shared__ int s_settles, s_left;
     const int b = blockIdx.y;
@@ -397,7 +496,7 @@ __global__ __launch_bounds__(CA_NT) void k_cache_commit(CacheCommit a, CacheCopy
     const unsigned plane = u / per_plane;
     const bool on = plane < (unsigned)a.num_planes;
     char* p = on ? g.dst_planes[plane] : nullptr;
-    CommitRow r = commit_row(a, g, b);
+    CommitRow r = commit_row<SCALED>(a, g, sc, b);
     const unsigned long long moves = r.ok ? __ballot(r.moves) : 0;
     int i0 = moves ? __builtin_ctzll(moves) : r.acc;
     V v[CA_UNROLL];
@@ -408,7 +507,7 @@ __global__ __launch_bounds__(CA_NT) void k_cache_commit(CacheCommit a, CacheCopy
             if (on && i0 + k < r.acc) v[k] = *reinterpret_cast<const V*>(p + s);
         }
     };
-    if (moves) {
+    if (moves && !SCALED) {
         const unsigned w = u - plane * per_plane;
         const unsigned h = w / g.units;
         if (on) p += h * g.dst_head + (int64_t)(w - h * g.units) * VEC;
@@ -421,7 +520,10 @@ __global__ __launch_bounds__(CA_NT) void k_cache_commit(CacheCommit a, CacheCopy
     int32_t* arrived = a.arrived + b * CACHE_COUNTER;
     int before = 0;
     if (tid == 0) before = __hip_atomic_fetch_add(arrived, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (moves && r.ok) {
+    if constexpr (SCALED) {
+        __shared__ uint8_t s_scale[CA_NT][CA_RUNS];  // of a workgroup's heads and the blocks they fill
+        if (moves && r.ok) move_scaled(a, g, sc, r, moves, s_scale);
+    } else if (moves && r.ok) {
         for (;;) {
 #pragma unroll
             for (int k = 0; k < CA_UNROLL; ++k) {
@@ -502,7 +604,7 @@ __global__ __launch_bounds__(CA_NT) void k_cache_pairs(CachePages a) {
 // longer). Few pairs are compared by every workgroup that copies: one launch
 // instead of two.
 template <int VEC, bool COMPARE>
-__global__ __launch_bounds__(CA_NT) void k_cache_copy(CachePages a, CacheCopy g) {
+__global__ __launch_bounds__(CA_NT) void k_cache_copy(CachePages a, CacheCopy g, ScaleCopy sc) {
     const int i = blockIdx.x;
     const int plane = blockIdx.y;
     const bool ok = COMPARE ? !__syncthreads_or(pair_bad(a, i, threadIdx.x, CA_NT)) : a.pair_ok[i] != 0;
@@ -510,17 +612,21 @@ __global__ __launch_bounds__(CA_NT) void k_cache_copy(CachePages a, CacheCopy g)
     if (!ok) return;
     copy_slots<VEC>(g, g.src_planes[plane] + a.src[i] * g.src_page,
                     g.dst_planes[plane] + a.dst[i] * g.dst_page, a.page_size);
+    if (sc.src_planes)
+        copy_scales(sc, sc.src_planes[plane] + a.src[i] * sc.src_page,
+                    sc.dst_planes[plane] + a.dst[i] * sc.dst_page, a.page_size / sc.block);
 }
 
 // ---------------------------------------------------------------------------
 
-hipError_t launch_cache_reserve(const CacheReserve& a, const CacheCopy& g, hipStream_t st) {
+hipError_t launch_cache_reserve(const CacheReserve& a, const CacheCopy& g, const ScaleCopy& sc,
+                                hipStream_t st) {
     const int nb = a.n_chunks + (a.B + CA_WAVES - 1) / CA_WAVES;
     hipLaunchKernelGGL(k_cache_plan, dim3(nb), dim3(CA_NT), 0, st, a);
     const dim3 grid(1 + a.num_planes, a.B);
-    if (g.vec == 16) hipLaunchKernelGGL(k_cache_take<16>, grid, dim3(CA_NT), 0, st, a, g);
-    else if (g.vec == 4) hipLaunchKernelGGL(k_cache_take<4>, grid, dim3(CA_NT), 0, st, a, g);
-    else hipLaunchKernelGGL(k_cache_take<1>, grid, dim3(CA_NT), 0, st, a, g);
+    if (g.vec == 16) hipLaunchKernelGGL(k_cache_take<16>, grid, dim3(CA_NT), 0, st, a, g, sc);
+    else if (g.vec == 4) hipLaunchKernelGGL(k_cache_take<4>, grid, dim3(CA_NT), 0, st, a, g, sc);
+    else hipLaunchKernelGGL(k_cache_take<1>, grid, dim3(CA_NT), 0, st, a, g, sc);
     return hipGetLastError();
 }
 
@@ -534,30 +640,40 @@ hipError_t launch_cache_fork(const CacheFork& a, hipStream_t st) {
     return hipGetLastError();
 }
 
-hipError_t launch_cache_commit(const CacheCommit& a, const CacheCopy& g, hipStream_t st) {
+hipError_t launch_cache_commit(const CacheCommit& a, const CacheCopy& g, const ScaleCopy& sc,
+                               hipStream_t st) {
+    if (a.nodes && sc.src_planes) {
+        const int here = CA_NT / sc.piece;
+        const int64_t heads = (int64_t)a.num_planes * sc.heads;
+        const dim3 grid((unsigned)((heads + here - 1) / here), a.B);
+        hipLaunchKernelGGL((k_cache_commit<16, true>), grid, dim3(CA_NT), 0, st, a, g, sc);
+        return hipGetLastError();
+    }
     const int64_t units = a.nodes ? (int64_t)a.num_planes * g.heads * g.units : 1;
     const dim3 grid((unsigned)((units + CA_NT - 1) / CA_NT), a.B);
-    if (g.vec == 16) hipLaunchKernelGGL(k_cache_commit<16>, grid, dim3(CA_NT), 0, st, a, g);
-    else if (g.vec == 4) hipLaunchKernelGGL(k_cache_commit<4>, grid, dim3(CA_NT), 0, st, a, g);
-    else hipLaunchKernelGGL(k_cache_commit<1>, grid, dim3(CA_NT), 0, st, a, g);
+    if (g.vec == 16) hipLaunchKernelGGL((k_cache_commit<16, false>), grid, dim3(CA_NT), 0, st, a, g, sc);
+    else if (g.vec == 4) hipLaunchKernelGGL((k_cache_commit<4, false>), grid, dim3(CA_NT), 0, st, a, g, sc);
+    else hipLaunchKernelGGL((k_cache_commit<1, false>), grid, dim3(CA_NT), 0, st, a, g, sc);
     return hipGetLastError();
 }
 
 template <int VEC>
-static void launch_cache_copy_v(const CachePages& a, const CacheCopy& g, hipStream_t st) {
+static void launch_cache_copy_v(const CachePages& a, const CacheCopy& g, const ScaleCopy& sc,
+                                hipStream_t st) {
     const dim3 grid(a.n, a.num_planes);
     if (a.n <= CACHE_COMPARED) {
-        hipLaunchKernelGGL((k_cache_copy<VEC, true>), grid, dim3(CA_NT), 0, st, a, g);
+        hipLaunchKernelGGL((k_cache_copy<VEC, true>), grid, dim3(CA_NT), 0, st, a, g, sc);
     } else {
         hipLaunchKernelGGL(k_cache_pairs, dim3((a.n + CA_WAVES - 1) / CA_WAVES), dim3(CA_NT), 0, st, a);
-        hipLaunchKernelGGL((k_cache_copy<VEC, false>), grid, dim3(CA_NT), 0, st, a, g);
+        hipLaunchKernelGGL((k_cache_copy<VEC, false>), grid, dim3(CA_NT), 0, st, a, g, sc);
     }
 }
 
-hipError_t launch_cache_copy(const CachePages& a, const CacheCopy& g, hipStream_t st) {
-    if (g.vec == 16) launch_cache_copy_v<16>(a, g, st);
-    else if (g.vec == 4) launch_cache_copy_v<4>(a, g, st);
-    else launch_cache_copy_v<1>(a, g, st);
+hipError_t launch_cache_copy(const CachePages& a, const CacheCopy& g, const ScaleCopy& sc,
+                             hipStream_t st) {
+    if (g.vec == 16) launch_cache_copy_v<16>(a, g, sc, st);
+    else if (g.vec == 4) launch_cache_copy_v<4>(a, g, sc, st);
+    else launch_cache_copy_v<1>(a, g, sc, st);
     return hipGetLastError();
 }
 

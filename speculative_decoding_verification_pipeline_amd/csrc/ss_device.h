@@ -313,6 +313,37 @@ __device__ __forceinline__ unsigned long long wave_incl_scan_u64(unsigned long l
     return v;
 }
 
+// ---------------------------------------------------------------------------
+// draft trees of up to 64 nodes, node `lane` in a lane: parents stand before their
+// children, so pointers that double reach the root in six steps
+
+struct TreeNode {
+    unsigned long long above;  // the nodes above it and itself, a bit each; 0: below no root
+    int depth;                 // edges up to the root, or to the node that hangs below none
+};
+
+__device__ __forceinline__ TreeNode tree_node(const int32_t* parents, int N) {
+    const int lane = threadIdx.x & (WAVE - 1);
+    int up = 0, depth = 0;
+    bool lost = false;
+    if (lane > 0 && lane < N) {
+        up = parents[lane];
+        lost = up < 0 || up >= lane;
+        if (lost) up = lane;
+        else depth = 1;
+    }
+    uint32_t lo = lane < 32 ? 1u << lane : 0, hi = lane < 32 ? 0 : 1u << (lane - 32);
+#pragma unroll
+    for (int i = 0; i < 6; ++i) {
+        lo |= __shfl(lo, up);
+        hi |= __shfl(hi, up);
+        depth += __shfl(depth, up);
+        lost |= __shfl((int)lost, up) != 0;
+        up = __shfl(up, up);
+    }
+    return {lost || lane >= N ? 0 : (unsigned long long)hi << 32 | lo, depth};
+}
+
 // Scratch for workgroup-level reductions over NB threads (NB / WAVE waves).
 template <int NB>
 struct RedT {

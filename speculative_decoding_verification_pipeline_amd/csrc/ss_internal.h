@@ -290,6 +290,17 @@ struct CacheCopy {
     int joined;  // consecutive slots of a head follow each other on both sides
 };
 
+// The scales of a cache held in 8 bits, both sides of a copy (src null: it has none).
+struct ScaleCopy {
+    const uint8_t* const* src_planes;  // device array
+    uint8_t* const* dst_planes;
+    int64_t src_page, src_block, src_head;  // bytes
+    int64_t dst_page, dst_block, dst_head;
+    int block;   // slots that share a scale
+    int heads;
+    int piece;   // vectors of 16 bytes of a slot's head
+};
+
 struct CacheWork {
     int32_t* free_ids;  // [chunks * CACHE_REF_CHUNK]: free pages, ascending within a chunk
     int32_t* free_cnt;  // [chunks]
@@ -362,6 +373,98 @@ struct CachePages {
     int32_t* out_ok;
 };
 
+// ---------------------------------------------------------------------------
+// a cache held in 8 bits
+
+constexpr int KV8_XMIN = -60, KV8_XMAX = 60;  // exponents of a block's scale
+
+// One plane of a scaled cache with its scales, all strides in bytes.
+struct Kv8Plane {
+    char* data;
+    uint8_t* scales;
+};
+
+struct Kv8Geo {
+    int64_t page, slot, head;      // of the planes
+    int64_t sc_page, sc_block, sc_head;
+    int page_size, block, heads, dim;
+    int num_pages, max_blocks;
+};
+
+// A step's tokens (ss_cache_step with what the handle knows).
+struct Kv8Step {
+    CacheTables t;
+    int B, N;
+    const int32_t* base;
+    const int32_t* counts;
+    const int32_t* parents;
+    const int32_t* reserved;
+};
+
+struct Heads {  // strides in elements
+    uint16_t* data;
+    int64_t row, token, head;
+};
+
+struct Rotary {
+    const double* turns;
+    int dim;
+    int interleaved;
+    double magnitude;
+};
+
+struct RotateArgs {
+    Rotary r;
+    const int32_t* positions;
+    int B, N, head_dim, q_heads, k_heads;
+    Heads q, q_out, k, k_out;
+    int vectors;  // pieces of 16 bytes; else single entries
+};
+
+struct Kv8Write {
+    Kv8Geo g;
+    Kv8Step s;
+    Kv8Plane k, v;
+    Heads keys, values, q, q_out;
+    int q_heads;      // 0: no queries
+    Rotary r;         // turns null: keys stay
+    const int32_t* positions;
+};
+
+struct Kv8Read {
+    Kv8Geo g;
+    CacheTables t;
+    Kv8Plane p[2];
+    Heads out[2];
+    int planes;
+    const int32_t* start;
+    const int32_t* counts;
+    int B, N;
+};
+
+// Attention: a workgroup takes a piece of one row's slots, one head of the cache and
+// 16 * tiles rows (query heads of tokens). What splits leave for the last of a row lies
+// in `part`.
+struct Kv8Attend {
+    Kv8Geo g;
+    Kv8Step s;
+    Kv8Plane k, v;
+    Heads q, out;
+    float* lse;
+    int q_heads;
+    int group;        // query heads per head of the cache
+    int blocks;       // blocks of rows of one row and head
+    int pieces;       // pieces that all rows of one head and block are cut into at most, beyond
+                      //   one each; 0: rows are not cut
+    float scale_log2; // scale * log2(e)
+    float* part;
+    int32_t* arrived;
+};
+
+constexpr int KV8_COUNTER = 64;       // integers between counters
+constexpr int KV8_SPLITS = 2048;      // rows, heads and blocks that are cut, at most
+constexpr int64_t KV8_PART_FLOATS = 8 << 20;  // what pieces leave, at most
+
 // Optional timing events of a call (see ss_sampler_set_launch_events): launch
 // k is bracketed by ev[2k] (its start) and ev[2k + 1] (its end), recorded by
 // the dispatch itself.
@@ -391,11 +494,18 @@ hipError_t launch_probs(const ProbsArgs& a, ss_dtype dt, hipStream_t st, const L
 hipError_t launch_quant(const QuantArgs& a, hipStream_t st, const LaunchEvents& le);
 // what the parts' sums of any call with these limits take
 int64_t quant_part_bytes(int V, int K, int max_batch);
-hipError_t launch_cache_reserve(const CacheReserve& a, const CacheCopy& g, hipStream_t st);
+hipError_t launch_cache_reserve(const CacheReserve& a, const CacheCopy& g, const ScaleCopy& sc,
+                                hipStream_t st);
 hipError_t launch_cache_truncate(const CacheTruncate& a, hipStream_t st);
 hipError_t launch_cache_fork(const CacheFork& a, hipStream_t st);
-hipError_t launch_cache_commit(const CacheCommit& a, const CacheCopy& g, hipStream_t st);
-hipError_t launch_cache_copy(const CachePages& a, const CacheCopy& g, hipStream_t st);
+hipError_t launch_cache_commit(const CacheCommit& a, const CacheCopy& g, const ScaleCopy& sc,
+                                hipStream_t st);
+hipError_t launch_cache_copy(const CachePages& a, const CacheCopy& g, const ScaleCopy& sc,
+                                hipStream_t st);
+hipError_t launch_rotate(const RotateArgs& a, ss_dtype dt, hipStream_t st);
+hipError_t launch_kv8_write(const Kv8Write& a, ss_dtype dt, hipStream_t st);
+hipError_t launch_kv8_read(const Kv8Read& a, ss_dtype dt, hipStream_t st);
+hipError_t launch_kv8_attend(const Kv8Attend& a, ss_dtype dt, hipStream_t st);
 // the row kernels of ss_lmhead_sample_params (in the row-kernel source)
 void launch_lm_merge(const LmheadArgs& a, hipStream_t st, const LaunchEvents& le, int k);
 void launch_lm_slow(const LmheadArgs& a, hipStream_t st, const LaunchEvents& le, int k);

@@ -31,7 +31,9 @@ EXPORTED = ("ss_sampler_create", "ss_sampler_destroy", "ss_status_string",
             "ss_lmhead_sample_params", "ss_sample_noalloc", "ss_spec_verify_probs",
             "ss_lmhead_quant_logits", "ss_cache_create", "ss_cache_destroy",
             "ss_cache_workspace_bytes", "ss_cache_reserve", "ss_cache_fork", "ss_cache_commit",
-            "ss_cache_commit_reserved", "ss_cache_truncate", "ss_cache_copy_pages")
+            "ss_cache_commit_reserved", "ss_cache_truncate", "ss_cache_copy_pages",
+            "ss_cache_create_scaled", "ss_cache_write", "ss_cache_read", "ss_cache_attend",
+            "ss_rotate")
 NOALLOC_MAX_BATCH = 64
 NOALLOC_MAX_ENTRIES = 1 << 23
 
@@ -78,6 +80,27 @@ class CacheConfig(ctypes.Structure):
 class CBlockTables(ctypes.Structure):
     _fields_ = [("tables", ctypes.c_void_p), ("stride", ctypes.c_int64),
                 ("rows", ctypes.c_int32), ("ref", ctypes.c_void_p), ("len", ctypes.c_void_p)]
+
+
+class CacheScales(ctypes.Structure):
+    _fields_ = [("block", ctypes.c_int32), ("page_stride", ctypes.c_int64),
+                ("block_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class CHeads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class CCacheStep(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("N", ctypes.c_int32), ("base", ctypes.c_void_p),
+                ("counts", ctypes.c_void_p), ("parents", ctypes.c_void_p),
+                ("reserved", ctypes.c_void_p)]
+
+
+class CRotary(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("magnitude", ctypes.c_double)]
 
 
 class SamplerError(RuntimeError):
@@ -153,6 +176,22 @@ def load_library(path=None):
     lib.ss_cache_truncate.restype = i32
     lib.ss_cache_copy_pages.argtypes = [vp, vp, vp, vp, i32, vp, vp]
     lib.ss_cache_copy_pages.restype = i32
+    heads, step, rotary = (ctypes.POINTER(x) for x in (CHeads, CCacheStep, CRotary))
+    lib.ss_cache_create_scaled.argtypes = [ctypes.POINTER(CacheConfig), ctypes.POINTER(vp),
+                                           ctypes.POINTER(vp), ctypes.POINTER(CacheScales),
+                                           ctypes.POINTER(vp)]
+    lib.ss_cache_create_scaled.restype = i32
+    lib.ss_rotate.argtypes = [i32, rotary, i32, i32, i32, i32, vp, heads, heads, i32, heads, heads,
+                              i32, vp]
+    lib.ss_rotate.restype = i32
+    lib.ss_cache_write.argtypes = [vp, tables, step, i32, i32, i32, heads, heads, rotary, vp, heads,
+                                   heads, i32, vp]
+    lib.ss_cache_write.restype = i32
+    lib.ss_cache_read.argtypes = [vp, tables, vp, vp, i32, i32, i32, i32, i32, heads, heads, vp]
+    lib.ss_cache_read.restype = i32
+    lib.ss_cache_attend.argtypes = [vp, tables, step, i32, i32, i32, heads, heads, i32,
+                                    ctypes.c_float, vp, vp]
+    lib.ss_cache_attend.restype = i32
     _lib = lib
     return lib
 
@@ -190,23 +229,33 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 def _empty_rows(n, m, like, dtype=torch.int32, stream=None):
     """An uninitialised [n, m] array (m None: [n]) on the device of `like`, for a call
-    on `stream` (None: the current one). What another stream writes is allocated
-    there, so that its memory is never one that earlier work of the current stream
-    still uses, and returns to that stream once neither is at work on it."""
+    on `stream` (None: the current one)."""
+    return _empty((n,) if m is None else (n, m), like, dtype, stream)
+
+
+def _empty(shape, like, dtype, stream=None):
+    """An uninitialised contiguous array on the device of `like`. What another stream
+    writes is allocated there, so that its memory is never one that earlier work of
+    the current stream still uses, and returns to that stream once neither is at
+    work on it."""
     if stream is not None and stream.cuda_stream != _raw_stream(like.get_device()):
         device = like.device
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
         with torch.cuda.stream(stream):
-            out = like.new_empty(n if m is None else (n, m), dtype=dtype)
+            out = like.new_empty(shape, dtype=dtype)
         out.record_stream(torch.cuda.current_stream(device))
         return out
     if _empty_strided is not None and _current_device is not None and \
             _current_device() == like.get_device():
-        if m is None:
-            return _empty_strided((n,), (1,), dtype)
-        return _empty_strided((n, m), (m, 1), dtype)
-    return like.new_empty(n if m is None else (n, m), dtype=dtype)
+        if len(shape) == 1:
+            return _empty_strided(shape, (1,), dtype)
+        if len(shape) == 2:
+            return _empty_strided(shape, (shape[1], 1), dtype)
+        if len(shape) == 4:
+            _, n, h, d = shape
+            return _empty_strided(shape, (n * h * d, h * d, d, 1), dtype)
+    return like.new_empty(shape, dtype=dtype)
 
 
 def _require(cond, msg):
@@ -266,6 +315,33 @@ def _check_rank3(t, name, shape, dtype, device):
             t.shape == shape):
         _check_dev(t, name, (dtype,), device)
         raise ValueError(f"{name} must be {list(shape)}")
+
+
+_HALF_DTYPES = {torch.bfloat16: SS_BF16, torch.float16: SS_F16}
+
+
+def _heads(t, name, shape, dtype, device):
+    """A [B, N, heads, dim] array of 16-bit floats as the ABI takes it; shape None: any.
+    The last dimension has unit stride, the others any."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and
+            t.dim() == 4 and (shape is None or t.shape == shape)):
+        _check_dev(t, name, (dtype,), device)
+        raise ValueError(f"{name} must be {'[B, N, heads, dim]' if shape is None else list(shape)}")
+    b, n, h, one = t.stride()
+    if one != 1 and t.shape[3] > 1:
+        raise ValueError(f"{name} must have unit stride along its last dim")
+    # a dimension of one entry is never stepped, whatever its stride
+    B, N, H, _ = t.shape
+    return CHeads(t.data_ptr(), b if B > 1 else 0, n if N > 1 else 0, h if H > 1 else 0)
+
+
+def _check_out_heads(t, name):
+    """An output whose entries lie apart: strides, sorted, each span what lies within."""
+    span = t.shape[3]
+    for stride, n in sorted(zip(t.stride()[:3], t.shape[:3])):
+        if n > 1:
+            _require(stride >= span, f"{name} must not hold an entry twice")
+            span += stride * (n - 1)
 
 
 def _row_stride(t, name):
