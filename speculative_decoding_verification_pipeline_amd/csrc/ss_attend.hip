@@ -133,9 +133,10 @@ struct AttendCursor {
     }
 };
 
+// The next 32 slots. A tile on no page becomes zeros whose weights are 2^-inf.
 template <int DP>
 __device__ __forceinline__ void attend_load(const Kv8Attend& a, AttendCursor& at, int h,
-                                            uint32_t k_lane, uint32_t v_lane, bool k_on[],
+                                            uint32_t k_lane, uint32_t v_lane, uint32_t k_on,
                                             bool v_on, AttendStep<DP>& x) {
     const uint32_t slot = (uint32_t)a.g.slot;
 #pragma unroll
@@ -143,26 +144,34 @@ __device__ __forceinline__ void attend_load(const Kv8Attend& a, AttendCursor& at
         int page = -1;
         if (at.left > 0) page = at.table[at.block];
         x.ok[t] = (unsigned)page < (unsigned)a.g.num_pages;
-        const int64_t p = x.ok[t] ? page : 0;
-        const int off = x.ok[t] ? at.inner * 16 : 0;
-        const int64_t from = p * a.g.page + off * a.g.slot + h * a.g.head;
-        const char* kp = a.k.data + from;
-        const char* vp = a.v.data + from;
+        if (x.ok[t]) {
+            const int64_t p = page;
+            const int off = at.inner * 16;
+            const int64_t from = p * a.g.page + off * a.g.slot + h * a.g.head;
+            const char* kp = a.k.data + from;
+            const char* vp = a.v.data + from;
 #pragma unroll
-        for (int c = 0; c < DP / 64; ++c) {
-            x.k[t][c] = u32x4{0, 0, 0, 0};
-            if (k_on[c]) x.k[t][c] = *reinterpret_cast<const u32x4*>(kp + (k_lane + c * 64));
-        }
+            for (int c = 0; c < DP / 64; ++c) {
+                x.k[t][c] = u32x4{0, 0, 0, 0};
+                if (k_on >> c & 1) x.k[t][c] = *reinterpret_cast<const u32x4*>(kp + (k_lane + c * 64));
+            }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            typename Words<DP / 64>::type v = {};
-            if (v_on)
-                v = *reinterpret_cast<const typename Words<DP / 64>::type*>(vp + (v_lane + j * slot));
-            x.v[t * 4 + j] = v;
+            for (int j = 0; j < 4; ++j) {
+                typename Words<DP / 64>::type v = {};
+                if (v_on)
+                    v = *reinterpret_cast<const typename Words<DP / 64>::type*>(vp + (v_lane + j * slot));
+                x.v[t * 4 + j] = v;
+            }
+            const int64_t sc = p * a.g.sc_page + off / a.g.block * a.g.sc_block + h * a.g.sc_head;
+            x.ks[t] = clamp_scale(a.k.scales[sc]);
+            x.vs[t] = clamp_scale(a.v.scales[sc]);
+        } else {
+#pragma unroll
+            for (int c = 0; c < DP / 64; ++c) x.k[t][c] = u32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x.v[t * 4 + j] = {};
+            x.ks[t] = x.vs[t] = 127;
         }
-        const int64_t sc = p * a.g.sc_page + off / a.g.block * a.g.sc_block + h * a.g.sc_head;
-        x.ks[t] = clamp_scale(a.k.scales[sc]);
-        x.vs[t] = clamp_scale(a.v.scales[sc]);
         at.next();
     }
 }
@@ -174,9 +183,17 @@ struct AttendState {
     f32x4 o[MT][DP / 16];
     float l[MT];               // this lane's share of the sum
     float ref[MT];             // the same in the four lanes of a row
-    int n[MT];                 // the row's token
-    unsigned long long up[MT]; // in a tree: the nodes that it sees
 };
+
+// The slots that a row sees of a lane's four from `at` on (behind the committed ones), a bit
+// each: of a tree's nodes those in `up`, else those up to token n; `end` bounds all.
+__device__ __forceinline__ uint32_t attend_sees(bool tree, unsigned long long up, int n, int at, int end) {
+    const int below = min(max(-at, 0), 4);  // committed slots, seen by all
+    uint32_t own;
+    if (tree) own = at >= 64 ? 0 : at >= 0 ? (uint32_t)(up >> at) : (uint32_t)up << below;
+    else own = (1u << min(max(n + 1 - at, 0), 4)) - 1;
+    return (own | ((1u << below) - 1)) & ((1u << min(max(end - at, 0), 4)) - 1);
+}
 
 template <int DP>
 __device__ __forceinline__ uint32_t word_of(const typename Words<DP / 64>::type& v, int w) {
@@ -195,13 +212,12 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
     return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
-// One step. MASK: slots of it that some row does not see: those of the step's own tokens,
-// behind the last one, or on no page.
+// One step. MASK: it has slots that some row does not see, of the step's own tokens or behind
+// the last one; vis: those seen of this lane's, bit 4 t + i slot i of tile t.
 template <int DP, int MT, bool F16, bool MASK>
-__device__ __forceinline__ void attend_step(const Kv8Attend& a, AttendStep<DP>& x, int rel, int end_rel,
+__device__ __forceinline__ void attend_step(const Kv8Attend& a, AttendStep<DP>& x, const uint32_t (&vis)[MT],
                                             AttendState<DP, MT>& w) {
     constexpr int KS = DP / 32;
-    const int g = (threadIdx.x & (WAVE - 1)) >> 4;
     f32x4 s[2][MT];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -217,37 +233,20 @@ __device__ __forceinline__ void attend_step(const Kv8Attend& a, AttendStep<DP>& 
             for (int m = 0; m < MT; ++m) s[t][m] = mfma<F16>(k, w.q[m][st], s[t][m]);
         }
     }
-    uint32_t vis[MT];  // bit 4 t + i: slot i of this lane in tile t is seen
     if constexpr (MASK) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            vis[m] = 0;
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = rel + t * 16 + g * 4 + i;  // behind the committed slots
-                    const bool own = a.s.parents ? r < 64 && (w.up[m] >> (r & 63) & 1) : r <= w.n[m];
-                    const bool sees = x.ok[t] && r < end_rel && (r < 0 || own);
-                    vis[m] |= (sees ? 1u : 0u) << (4 * t + i);
-                    if (!sees) s[t][m][i] = -INFINITY;
-                }
-            }
-        }
-        // values that no row sees are not numbers to be multiplied by 0
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const bool there = x.ok[j / 4] && rel + j / 4 * 16 + g * 4 + j % 4 < end_rel;
-#pragma unroll
-            for (int c = 0; c < DP / 64; ++c)
-                set_word<DP>(x.v[j], c, there ? word_of<DP>(x.v[j], c) : 0u);
-        }
+                for (int i = 0; i < 4; ++i)
+                    if (!(vis[m] >> (4 * t + i) & 1)) s[t][m][i] = -INFINITY;
     }
     float fk[2], xv[2], inv[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         fk[t] = as<float>(x.ks[t] << 23) * a.scale_log2;
-        xv[t] = (float)((int)x.vs[t] - 127);
+        xv[t] = x.ok[t] ? (float)((int)x.vs[t] - 127) : -INFINITY;
         inv[t] = as<float>((254u - x.vs[t]) << 23);
     }
     float top[MT];
@@ -456,31 +455,26 @@ __global__ __launch_bounds__(AT_NT) void k_attend(Kv8Attend a) {
     const AttendRow row = attend_row(a, pc.b);
 
     AttendState<DP, MT> w;
-    unsigned long long above = 0;
-    if (a.s.parents) above = tree_node(a.s.parents + (int64_t)pc.b * a.s.N, a.s.N).above;
-    bool k_on[DP / 64];
+    unsigned long long rooted = 0;  // nodes that hang below the root
+    if (a.s.parents) rooted = __ballot(tree_node(a.s.parents + (int64_t)pc.b * a.s.N, a.s.N).above != 0);
+    uint32_t k_on = 0;  // the pieces of 64 dimensions that reach into the head's
 #pragma unroll
-    for (int c = 0; c < DP / 64; ++c) k_on[c] = c * 64 + g * 16 < a.g.dim;
+    for (int c = 0; c < DP / 64; ++c) k_on |= (c * 64 + g * 16 < a.g.dim ? 1u : 0u) << c;
     const bool v_on = col * DT < a.g.dim;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
         const int r = first + min(m * 16 + col, rows - 1);
         const int n = r / a.group;
-        w.n[m] = n;
         w.l[m] = 0.0f;
         w.ref[m] = AT_NONE;
-        w.up[m] = 0;
-        if (a.s.parents)
-            w.up[m] = (unsigned long long)(uint32_t)__shfl((int)(above >> 32), n) << 32 |
-                      (uint32_t)__shfl((int)above, n);
-        const bool live = n < row.count && (!a.s.parents || w.up[m] != 0);
+        const bool live = n < row.count && (!a.s.parents || (rooted >> (n & 63) & 1));
         if (wave == 0 && g == 0) s_live[m * 16 + col] = live;
         const uint16_t* q = a.q.data + pc.b * a.q.row + n * a.q.token +
                             (h * a.group + r - n * a.group) * a.q.head + g * 16;
 #pragma unroll
         for (int st = 0; st < DP / 32; ++st) {
             w.q[m][st] = u32x4{0, 0, 0, 0};
-            if (k_on[st / 2])
+            if (k_on >> (st / 2) & 1)
                 w.q[m][st] = *reinterpret_cast<const u32x4*>(q + st / 2 * 64 + st % 2 * 8);
         }
 #pragma unroll
@@ -499,6 +493,7 @@ __global__ __launch_bounds__(AT_NT) void k_attend(Kv8Attend a) {
     const int s1 = (int)min((int64_t)(pc.c + 1) * pc.units * AT_WAVES, (int64_t)steps);
     const int per = (s1 - s0 + AT_WAVES - 1) / AT_WAVES;
     const int from = min(s0 + wave * per, s1), to = min(from + per, s1);
+    const int plain = max(min(to, full / AT_STEP), from);  // steps before it need no mask
     if (from < to) {
         AttendCursor at;
         at.table = (const_i32)(a.s.t.tables + (int64_t)pc.b * a.s.t.stride);
@@ -508,16 +503,44 @@ __global__ __launch_bounds__(AT_NT) void k_attend(Kv8Attend a) {
         at.left = (row.end + 15) / 16 - from * 2;
         const uint32_t k_lane = (uint32_t)col * (uint32_t)a.g.slot + g * 16;
         const uint32_t v_lane = (uint32_t)g * 4 * (uint32_t)a.g.slot + col * DT;
-        AttendStep<DP> cur, nxt;
-        attend_load<DP>(a, at, h, k_lane, v_lane, k_on, v_on, cur);
-        for (int s = from; s < to; ++s) {
-            if (s + 1 < to) attend_load<DP>(a, at, h, k_lane, v_lane, k_on, v_on, nxt);
-            const int rel = s * AT_STEP - row.base;
-            if (s * AT_STEP + AT_STEP <= full && cur.ok[0] && cur.ok[1])
-                attend_step<DP, MT, F16, false>(a, cur, rel, row.end - row.base, w);
-            else
-                attend_step<DP, MT, F16, true>(a, cur, rel, row.end - row.base, w);
-            cur = nxt;
+        AttendStep<DP> x, y;
+        uint32_t vis[MT] = {};
+        if (from < plain) {
+            attend_load<DP>(a, at, h, k_lane, v_lane, k_on, v_on, x);
+            int s = from;
+            for (; s + 1 < plain; s += 2) {
+                attend_load<DP>(a, at, h, k_lane, v_lane, k_on, v_on, y);
+                attend_step<DP, MT, F16, false>(a, x, vis, w);
+                if (s + 2 < plain) attend_load<DP>(a, at, h, k_lane, v_lane, k_on, v_on, x);
+                attend_step<DP, MT, F16, false>(a, y, vis, w);
+            }
+            if (s < plain) attend_step<DP, MT, F16, false>(a, x, vis, w);
+        }
+        unsigned long long above = 0;
+        if (a.s.parents && plain < to)
+            above = tree_node(a.s.parents + (int64_t)pc.b * a.s.N, a.s.N).above;
+#pragma clang loop unroll(disable)
+        for (int s = plain; s < to; ++s) {
+            attend_load<DP>(a, at, h, k_lane, v_lane, k_on, v_on, x);
+            const int rel = s * AT_STEP - row.base + g * 4, end = row.end - row.base;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const int n = (first + min(m * 16 + col, rows - 1)) / a.group;
+                const unsigned long long up =
+                    (unsigned long long)(uint32_t)__shfl((int)(above >> 32), n & 63) << 32 |
+                    (uint32_t)__shfl((int)above, n & 63);
+                vis[m] = attend_sees(a.s.parents, up, n, rel, end) |
+                         attend_sees(a.s.parents, up, n, rel + 16, end) << 4;
+            }
+            // values behind the last token are not numbers to be multiplied by 0
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const bool there = rel + j / 4 * 16 + j % 4 < end;
+#pragma unroll
+                for (int c = 0; c < DP / 64; ++c)
+                    set_word<DP>(x.v[j], c, there ? word_of<DP>(x.v[j], c) : 0u);
+            }
+            attend_step<DP, MT, F16, true>(a, x, vis, w);
         }
     }
 
