@@ -26,16 +26,14 @@
 // has 8): a reference is set to 2^8 below the largest exponent and kept until one passes
 // 2^15, so a weight keeps its bits down to 2^-22 of the largest.
 #include <limits.h>
+#include <stdlib.h>
 
 #include "ss_device.h"
 #include "ss_internal.h"
 
 namespace ss {
 
-constexpr int AT_NT = 256;
-constexpr int AT_WAVES = AT_NT / WAVE;
 constexpr int AT_STEP = 32;                   // slots of a wave's step
-constexpr int AT_UNIT = AT_STEP * AT_WAVES;   // pieces of a row are multiples of it
 constexpr float AT_NONE = -3.0e38f;           // reference of a row that has seen nothing
 constexpr float AT_SET = 8.0f, AT_MOST = 15.0f;
 
@@ -103,76 +101,114 @@ __device__ __forceinline__ AttendRow attend_row(const Kv8Attend& a, int b) {
     return r;
 }
 
+// A byte that all lanes read, as a scalar load of the word it lies in: a vector load would be
+// waited for with the loads before it.
+__device__ __forceinline__ uint32_t scale_byte(const uint8_t* at) {
+    const uint64_t p = reinterpret_cast<uint64_t>(at);
+    return (uint32_t)*(const_i32)(p & ~3ull) >> ((uint32_t)p % 4 * 8) & 0xffu;
+}
+
 // A scale byte, held to what ss_cache_write leaves: whatever a block holds that nothing was
 // written to, its factors are finite and not 0, and masked slots stay masked.
 __device__ __forceinline__ uint32_t clamp_scale(uint32_t x) {
     return min(max(x, (uint32_t)(127 + KV8_XMIN)), (uint32_t)(127 + KV8_XMAX));
 }
 
-// 32 slots of keys and values as they lie in the pages.
+// The keys or the values of 32 slots as they lie in the pages, and their two tiles' scales.
 template <int DP>
-struct AttendStep {
+struct AttendKeys {
     u32x4 k[2][DP / 64];
+    uint32_t s[2];
+    bool ok[2];  // whether a tile lies on a page
+};
+template <int DP>
+struct AttendValues {
     typename Words<DP / 64>::type v[8];
-    uint32_t ks[2], vs[2];  // scale bytes of the two tiles
-    bool ok[2];             // whether the tile lies on a page
+    uint32_t s[2];
 };
 
-// Where a wave stands in its row's table: tile of 16 slots by tile.
+// Where a wave stands in its row: a step of two tiles after the other. The pages of the next
+// step are looked up a step ahead.
 struct AttendCursor {
     const_i32 table;
-    int block, inner;  // table entry, tile within its page
+    int block, inner;  // table entry of the tile after the pages below, and its place there
     int tiles;         // tiles of a page
-    int left;          // tiles up to the row's last
-    __device__ __forceinline__ void next() {
-        if (++inner == tiles) {
-            inner = 0;
-            ++block;
-        }
-        --left;
-    }
+    int left;          // tiles from there up to the row's last
+    int page[2], at[2];
 };
 
-// The next 32 slots. A tile on no page becomes zeros whose weights are 2^-inf.
-template <int DP>
-__device__ __forceinline__ void attend_load(const Kv8Attend& a, AttendCursor& at, int h,
-                                            uint32_t k_lane, uint32_t v_lane, uint32_t k_on,
-                                            bool v_on, AttendStep<DP>& x) {
-    const uint32_t slot = (uint32_t)a.g.slot;
+__device__ __forceinline__ void attend_look(AttendCursor& c) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-        int page = -1;
-        if (at.left > 0) page = at.table[at.block];
-        x.ok[t] = (unsigned)page < (unsigned)a.g.num_pages;
-        if (x.ok[t]) {
-            const int64_t p = page;
-            const int off = at.inner * 16;
-            const int64_t from = p * a.g.page + off * a.g.slot + h * a.g.head;
-            const char* kp = a.k.data + from;
-            const char* vp = a.v.data + from;
+        c.page[t] = -1;
+        c.at[t] = c.inner;
+        if (c.left > 0) c.page[t] = c.table[c.block];
+        --c.left;
+        const bool over = ++c.inner == c.tiles;
+        c.block += over ? 1 : 0;
+        c.inner = over ? 0 : c.inner;
+    }
+}
+
+// Two tiles' places in the planes and in their scales. One on no page is read where page 0
+// lies, and then put out.
+struct AttendPlace {
+    int64_t at[2], scale[2];
+    bool ok[2];
+};
+
+__device__ __forceinline__ AttendPlace attend_next(const Kv8Attend& a, AttendCursor& c, int h) {
+    AttendPlace p;
 #pragma unroll
-            for (int c = 0; c < DP / 64; ++c) {
-                x.k[t][c] = u32x4{0, 0, 0, 0};
-                if (k_on >> c & 1) x.k[t][c] = *reinterpret_cast<const u32x4*>(kp + (k_lane + c * 64));
-            }
+    for (int t = 0; t < 2; ++t) {
+        p.ok[t] = (unsigned)c.page[t] < (unsigned)a.g.num_pages;
+        const int64_t page = p.ok[t] ? c.page[t] : 0;
+        const int off = c.at[t] * 16;
+        p.at[t] = page * a.g.page + off * a.g.slot + h * a.g.head;
+        p.scale[t] = page * a.g.sc_page + (off >> a.g.block_bits) * a.g.sc_block + h * a.g.sc_head;
+    }
+    attend_look(c);
+    return p;
+}
+
+// k_at: where this lane's pieces of 64 dimensions lie, those behind the head's last at the
+// first: they meet zeros of Q.
+template <int DP>
+__device__ __forceinline__ void load_keys(const Kv8Attend& a, const AttendPlace& p,
+                                          const uint32_t (&k_at)[DP / 64], AttendKeys<DP>& x) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                typename Words<DP / 64>::type v = {};
-                if (v_on)
-                    v = *reinterpret_cast<const typename Words<DP / 64>::type*>(vp + (v_lane + j * slot));
-                x.v[t * 4 + j] = v;
-            }
-            const int64_t sc = p * a.g.sc_page + off / a.g.block * a.g.sc_block + h * a.g.sc_head;
-            x.ks[t] = clamp_scale(a.k.scales[sc]);
-            x.vs[t] = clamp_scale(a.v.scales[sc]);
-        } else {
+    for (int t = 0; t < 2; ++t) {
+        const char* from = a.k.data + p.at[t];
 #pragma unroll
-            for (int c = 0; c < DP / 64; ++c) x.k[t][c] = u32x4{0, 0, 0, 0};
+        for (int c = 0; c < DP / 64; ++c) x.k[t][c] = *reinterpret_cast<const u32x4*>(from + k_at[c]);
+        x.s[t] = scale_byte(a.k.scales + p.scale[t]);
+        x.ok[t] = p.ok[t];
+    }
+}
+
+template <int DP>
+__device__ __forceinline__ void load_values(const Kv8Attend& a, const AttendPlace& p,
+                                            const uint32_t (&v_at)[4], AttendValues<DP>& x) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x.v[t * 4 + j] = {};
-            x.ks[t] = x.vs[t] = 127;
-        }
-        at.next();
+    for (int t = 0; t < 2; ++t) {
+        const char* from = a.v.data + p.at[t];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            x.v[t * 4 + j] = *reinterpret_cast<const typename Words<DP / 64>::type*>(from + v_at[j]);
+        x.s[t] = scale_byte(a.v.scales + p.scale[t]);
+    }
+}
+
+// Tiles on no page are zeros; their weights become 2^-inf.
+template <int DP>
+__device__ __forceinline__ void put_out(AttendKeys<DP>& k, AttendValues<DP>& v) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        if (k.ok[t]) continue;
+#pragma unroll
+        for (int c = 0; c < DP / 64; ++c) k.k[t][c] = u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v.v[t * 4 + j] = {};
     }
 }
 
@@ -207,24 +243,28 @@ __device__ __forceinline__ void set_word(typename Words<DP / 64>::type& v, int w
     else v[w] = to;
 }
 
+// The word if the bit is set, else the other, without a condition a lane (masks of many of
+// them took the scalar registers).
+__device__ __forceinline__ uint32_t keep_if(uint32_t bits, int bit, uint32_t w, uint32_t other) {
+    const uint32_t m = (uint32_t)((int32_t)(bits << (31 - bit)) >> 31);
+    return (w & m) | (other & ~m);
+}
+
 // Bytes of a word that are a NaN, as 0x80 each.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
     return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
-// One step. MASK: it has slots that some row does not see, of the step's own tokens or behind
-// the last one; vis: those seen of this lane's, bit 4 t + i slot i of tile t.
-template <int DP, int MT, bool F16, bool MASK>
-__device__ __forceinline__ void attend_step(const Kv8Attend& a, AttendStep<DP>& x, const uint32_t (&vis)[MT],
-                                            AttendState<DP, MT>& w) {
-    constexpr int KS = DP / 32;
-    f32x4 s[2][MT];
+// S^T of one step.
+template <int DP, int MT, bool F16>
+__device__ __forceinline__ void attend_scores(const AttendKeys<DP>& x, const AttendState<DP, MT>& w,
+                                              f32x4 (&s)[2][MT]) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) s[t][m] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int st = 0; st < KS; ++st) {
+        for (int st = 0; st < DP / 32; ++st) {
             const u32x4 b = x.k[t][st / 2];
             const uint32_t w0 = b[st % 2 * 2], w1 = b[st % 2 * 2 + 1];
             const u32x4 k = {widen<F16>(w0, false), widen<F16>(w0, true), widen<F16>(w1, false),
@@ -233,21 +273,20 @@ __device__ __forceinline__ void attend_step(const Kv8Attend& a, AttendStep<DP>& 
             for (int m = 0; m < MT; ++m) s[t][m] = mfma<F16>(k, w.q[m][st], s[t][m]);
         }
     }
-    if constexpr (MASK) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (!(vis[m] >> (4 * t + i) & 1)) s[t][m][i] = -INFINITY;
-    }
+}
+
+// Weights of one step: s becomes them, under the rows' references, which may grow.
+template <int DP, int MT>
+__device__ __forceinline__ void attend_weights(const Kv8Attend& a, const uint32_t (&ks)[2],
+                                               const uint32_t (&vs)[2], const bool (&ok)[2], const f32x4 (&s)[2][MT],
+                                               AttendState<DP, MT>& w, u32x4 (&p)[MT]) {
     float fk[2], xv[2], inv[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-        fk[t] = as<float>(x.ks[t] << 23) * a.scale_log2;
-        xv[t] = x.ok[t] ? (float)((int)x.vs[t] - 127) : -INFINITY;
-        inv[t] = as<float>((254u - x.vs[t]) << 23);
+        const uint32_t v = clamp_scale(vs[t]);
+        fk[t] = as<float>(clamp_scale(ks[t]) << 23) * a.scale_log2;
+        xv[t] = ok[t] ? (float)((int)v - 127) : -INFINITY;
+        inv[t] = as<float>((254u - v) << 23);
     }
     float top[MT];
     bool grows = false;
@@ -276,7 +315,6 @@ __device__ __forceinline__ void attend_step(const Kv8Attend& a, AttendStep<DP>& 
             }
         }
     }
-    u32x4 p[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
 #pragma unroll
@@ -291,46 +329,12 @@ __device__ __forceinline__ void attend_step(const Kv8Attend& a, AttendStep<DP>& 
             p[m][2 * t + 1] = as<uint32_t>(__builtin_convertvector((f32x2{e[2], e[3]}), h16x2));
         }
     }
-    if constexpr (MASK) {
-        // A NaN among the values reaches the rows that see it and no others: it is
-        // counted where it is seen, and taken out of the product.
-        uint32_t any = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int c = 0; c < DP / 64; ++c) any |= nan_bytes(word_of<DP>(x.v[j], c));
-        if (__any(any != 0)) {
-#pragma unroll
-            for (int c = 0; c < DP / 64; ++c) {
-                uint32_t nan[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t word = word_of<DP>(x.v[j], c);
-                    nan[j] = nan_bytes(word);
-                    set_word<DP>(x.v[j], c, word & ~((nan[j] >> 7) * 0xffu));
-                }
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    u32x4 hot;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        hot[j] = ((nan[2 * j] >> (8 * d + 7)) & 1) * 0x3c00u |
-                                 ((nan[2 * j + 1] >> (8 * d + 7)) & 1) * 0x3c000000u;
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        u32x4 sees;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            sees[j] = (vis[m] >> (2 * j) & 1) * 0x3c00u | (vis[m] >> (2 * j + 1) & 1) * 0x3c000000u;
-                        const f32x4 n = mfma<true>(hot, sees, f32x4{0, 0, 0, 0});
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (n[i] > 0) w.o[m][c * 4 + d][i] = NAN;
-                    }
-                }
-            }
-        }
-    }
+}
+
+// O^T of one step.
+template <int DP, int MT>
+__device__ __forceinline__ void attend_values(const AttendValues<DP>& x, const u32x4 (&p)[MT],
+                                              AttendState<DP, MT>& w) {
 #pragma unroll
     for (int c = 0; c < DP / 64; ++c) {
         uint32_t lo[8], hi[8];  // dimensions 0 and 1, 2 and 3 of the word
@@ -353,20 +357,63 @@ __device__ __forceinline__ void attend_step(const Kv8Attend& a, AttendStep<DP>& 
     }
 }
 
+// A NaN among the values reaches the rows that see it and no others: it is counted where it
+// is seen, and taken out of the product.
+template <int DP, int MT>
+__device__ __forceinline__ void attend_nans(AttendValues<DP>& x, const uint32_t (&vis)[MT],
+                                            AttendState<DP, MT>& w) {
+    uint32_t any = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int c = 0; c < DP / 64; ++c) any |= nan_bytes(word_of<DP>(x.v[j], c));
+    if (!__any(any != 0)) return;
+#pragma unroll
+    for (int c = 0; c < DP / 64; ++c) {
+        uint32_t nan[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t word = word_of<DP>(x.v[j], c);
+            nan[j] = nan_bytes(word);
+            set_word<DP>(x.v[j], c, word & ~((nan[j] >> 7) * 0xffu));
+        }
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            u32x4 hot;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                hot[j] = ((nan[2 * j] >> (8 * d + 7)) & 1) * 0x3c00u |
+                         ((nan[2 * j + 1] >> (8 * d + 7)) & 1) * 0x3c000000u;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                u32x4 sees;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    sees[j] = (vis[m] >> (2 * j) & 1) * 0x3c00u | (vis[m] >> (2 * j + 1) & 1) * 0x3c000000u;
+                const f32x4 n = mfma<true>(hot, sees, f32x4{0, 0, 0, 0});
+#pragma unroll
+                for (int i = 0; i < 4; ++i)  // n is 0 or at least 1
+                    w.o[m][c * 4 + d][i] += n[i] * (as<float>(as<uint32_t>((float)n[i]) ? 0x7fc00000u : 0u));
+            }
+        }
+    }
+}
+
 // Where workgroup `item` of a head and block of rows works: row b, piece c of its n. Rows
 // are cut into pieces of equal size, about as many over all rows as a.pieces; every wave
 // finds its own by itself.
 struct AttendPiece {
-    int b, c, n, units;  // units of AT_UNIT slots of a piece
+    int b, c, n, units;  // units of UNIT slots of a piece
 };
 
+template <int UNIT>
 __device__ __forceinline__ AttendPiece attend_piece(const Kv8Attend& a, int item) {
-    if (a.pieces == 0) return {item, 0, 1, INT_MAX / AT_UNIT};
+    if (a.pieces == 0) return {item, 0, 1, INT_MAX / UNIT};
     const int lane = threadIdx.x & (WAVE - 1);
     int total = 0;
     for (int b0 = 0; b0 < a.s.B; b0 += WAVE) {
         const int b = b0 + lane;
-        if (b < a.s.B) total += max(1, (int)(((int64_t)attend_row(a, b).end + AT_UNIT - 1) / AT_UNIT));
+        if (b < a.s.B) total += max(1, (int)(((int64_t)attend_row(a, b).end + UNIT - 1) / UNIT));
     }
     total = wave_sum_i(total);
     const int units = (total + a.pieces - 1) / a.pieces;
@@ -375,7 +422,7 @@ __device__ __forceinline__ AttendPiece attend_piece(const Kv8Attend& a, int item
         const int b = b0 + lane;
         int n = 0;
         if (b < a.s.B) {
-            const int u = max(1, (int)(((int64_t)attend_row(a, b).end + AT_UNIT - 1) / AT_UNIT));
+            const int u = max(1, (int)(((int64_t)attend_row(a, b).end + UNIT - 1) / UNIT));
             n = (u + units - 1) / units;
         }
         const int to = before + wave_incl_scan_i(n);
@@ -416,24 +463,68 @@ __device__ __forceinline__ void attend_out(const Kv8Attend& a, int b, int n, int
 #pragma unroll
     for (int i = 0; i < D / 2; i += sizeof(V) / 4) {
         V v;
+        if constexpr (sizeof(V) == 4) {
+            v = r[i];
+        } else {
 #pragma unroll
-        for (unsigned k = 0; k < sizeof(V) / 4; ++k) v[k] = r[i + k];
+            for (unsigned k = 0; k < sizeof(V) / 4; ++k) v[k] = r[i + k];
+        }
         *reinterpret_cast<V*>(to + 2 * i) = v;
     }
 }
 
-// The factor on a row's output: 0 where it has seen nothing, or scores of -inf alone.
-__device__ __forceinline__ float attend_factor(float l, bool live) {
-    return live && l != 0.0f ? 1.0f / l : 0.0f;
+// A row's sums under one reference, of the entries that a thread has.
+template <int PT>
+struct AttendSum {
+    float ref, l;
+    float o[PT];
+};
+
+// Adds the waves' sums of row r (of the 16 from m on), which lie under the waves' largest
+// reference.
+template <int DP, int PT, int WAVES, class O, class S>
+__device__ __forceinline__ AttendSum<PT> add_waves(const O& s_o, const S& s_ref, const S& s_l, int m, int r,
+                                                   int part) {
+    AttendSum<PT> s;
+    s.ref = s_ref[0][m + r];
+#pragma unroll
+    for (int v = 1; v < WAVES; ++v) s.ref = fmaxf(s.ref, s_ref[v][m + r]);
+    s.l = 0.0f;
+#pragma unroll
+    for (int d = 0; d < PT; ++d) s.o[d] = 0.0f;
+#pragma unroll
+    for (int v = 0; v < WAVES; ++v) {
+        s.l = __builtin_fmaf(s_l[v][m + r], __builtin_amdgcn_exp2f(s_ref[v][m + r] - s.ref), s.l);
+#pragma unroll
+        for (int d = 0; d < PT; ++d) s.o[d] += s_o[v][r][part * PT + d];
+    }
+    return s;
 }
 
-template <int DP, int MT, bool F16>
-__global__ __launch_bounds__(AT_NT) void k_attend(Kv8Attend a) {
+// Row r of a head of the cache to the output: 0 where it has seen nothing, or scores of -inf
+// alone.
+template <int PT, bool F16>
+__device__ __forceinline__ void attend_result(const Kv8Attend& a, AttendSum<PT> s, int b, int h, int r,
+                                              int part, bool live) {
+    const int n = r / a.group, head = h * a.group + r - n * a.group;
+    if (!live) {
+#pragma unroll
+        for (int d = 0; d < PT; ++d) s.o[d] = 0.0f;
+    }
+    if (part * PT < a.g.dim)
+        attend_out<PT, F16>(a, b, n, head, part * PT, s.o, live && s.l != 0.0f ? 1.0f / s.l : 0.0f);
+    if (a.lse && part == 0)
+        a.lse[((int64_t)b * a.s.N + n) * a.q_heads + head] =
+            live ? (s.ref + log2f(s.l)) * 0.69314718055994531f : -INFINITY;
+}
+
+template <int DP, int MT, bool F16, int WAVES>
+__global__ __launch_bounds__(WAVES* WAVE, DP == 256 || MT == 4 ? 1 : MT == 2 ? 2 : DP == 128 ? 3 : 4) void k_attend(Kv8Attend a) {
     constexpr int DT = DP / 16;
-    constexpr int PAD = 4;
+    constexpr int PT = DP / (WAVES * 4);      // entries of a row that a thread adds
     constexpr int SLOT = MT * 16 * (DP + 2);  // floats that a piece leaves
-    __shared__ float s_o[AT_WAVES][16][DP + PAD];
-    __shared__ float s_ref[AT_WAVES][MT * 16], s_l[AT_WAVES][MT * 16];
+    __shared__ float s_o[WAVES][16][DP + 4];
+    __shared__ float s_ref[WAVES][MT * 16], s_l[WAVES][MT * 16];
     __shared__ int s_live[MT * 16];
     __shared__ int s_last;
     const int tid = threadIdx.x;
@@ -446,7 +537,7 @@ __global__ __launch_bounds__(AT_NT) void k_attend(Kv8Attend a) {
     const int h = y / a.blocks;
     const int first = (y - h * a.blocks) * (MT * 16);  // row of this block
     const int rows = min(a.s.N * a.group - first, MT * 16);
-    AttendPiece pc = attend_piece(a, item);
+    AttendPiece pc = attend_piece<AT_STEP * WAVES>(a, item);
     pc.b = __builtin_amdgcn_readfirstlane(pc.b);
     pc.c = __builtin_amdgcn_readfirstlane(pc.c);
     pc.n = __builtin_amdgcn_readfirstlane(pc.n);
@@ -460,7 +551,6 @@ __global__ __launch_bounds__(AT_NT) void k_attend(Kv8Attend a) {
     uint32_t k_on = 0;  // the pieces of 64 dimensions that reach into the head's
 #pragma unroll
     for (int c = 0; c < DP / 64; ++c) k_on |= (c * 64 + g * 16 < a.g.dim ? 1u : 0u) << c;
-    const bool v_on = col * DT < a.g.dim;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
         const int r = first + min(m * 16 + col, rows - 1);
@@ -489,9 +579,9 @@ __global__ __launch_bounds__(AT_NT) void k_attend(Kv8Attend a) {
         full = (int)min((int64_t)row.end, (int64_t)row.base + first / a.group + 1);
     }
     const int steps = (int)(((int64_t)see + AT_STEP - 1) / AT_STEP);
-    const int s0 = (int)min((int64_t)pc.c * pc.units * AT_WAVES, (int64_t)steps);
-    const int s1 = (int)min((int64_t)(pc.c + 1) * pc.units * AT_WAVES, (int64_t)steps);
-    const int per = (s1 - s0 + AT_WAVES - 1) / AT_WAVES;
+    const int s0 = (int)min((int64_t)pc.c * pc.units * WAVES, (int64_t)steps);
+    const int s1 = (int)min((int64_t)(pc.c + 1) * pc.units * WAVES, (int64_t)steps);
+    const int per = (s1 - s0 + WAVES - 1) / WAVES;
     const int from = min(s0 + wave * per, s1), to = min(from + per, s1);
     const int plain = max(min(to, full / AT_STEP), from);  // steps before it need no mask
     if (from < to) {
@@ -501,28 +591,48 @@ __global__ __launch_bounds__(AT_NT) void k_attend(Kv8Attend a) {
         at.block = from * 2 / at.tiles;
         at.inner = from * 2 - at.block * at.tiles;
         at.left = (row.end + 15) / 16 - from * 2;
-        const uint32_t k_lane = (uint32_t)col * (uint32_t)a.g.slot + g * 16;
-        const uint32_t v_lane = (uint32_t)g * 4 * (uint32_t)a.g.slot + col * DT;
-        AttendStep<DP> x, y;
-        uint32_t vis[MT] = {};
-        if (from < plain) {
-            attend_load<DP>(a, at, h, k_lane, v_lane, k_on, v_on, x);
-            int s = from;
-            for (; s + 1 < plain; s += 2) {
-                attend_load<DP>(a, at, h, k_lane, v_lane, k_on, v_on, y);
-                attend_step<DP, MT, F16, false>(a, x, vis, w);
-                if (s + 2 < plain) attend_load<DP>(a, at, h, k_lane, v_lane, k_on, v_on, x);
-                attend_step<DP, MT, F16, false>(a, y, vis, w);
-            }
-            if (s < plain) attend_step<DP, MT, F16, false>(a, x, vis, w);
+        uint32_t k_at[DP / 64], v_at[4];
+#pragma unroll
+        for (int c = 0; c < DP / 64; ++c)
+            k_at[c] = (uint32_t)col * (uint32_t)a.g.slot + (k_on >> c & 1 ? c * 64 + g * 16 : 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v_at[j] = (uint32_t)(g * 4 + j) * (uint32_t)a.g.slot + (col * DT < a.g.dim ? col * DT : 0);
+        AttendKeys<DP> k;
+        AttendValues<DP> v;
+        f32x4 e[2][MT];
+        u32x4 p[MT];
+        attend_look(at);
+        AttendPlace place = attend_next(a, at, h);
+        load_keys<DP>(a, place, k_at, k);
+        // keys of the next step are on their way while this one's weights and values are
+        // worked on, values while its scores are
+        for (int s = from; s < plain; ++s) {
+            load_values<DP>(a, place, v_at, v);
+            if (!(k.ok[0] && k.ok[1])) put_out<DP>(k, v);
+            attend_scores<DP, MT, F16>(k, w, e);
+            const uint32_t ks[2] = {k.s[0], k.s[1]};
+            const bool ok[2] = {k.ok[0], k.ok[1]};
+            place = attend_next(a, at, h);  // behind the last step: page 0
+            load_keys<DP>(a, place, k_at, k);
+            attend_weights<DP, MT>(a, ks, v.s, ok, e, w, p);
+            attend_values<DP, MT>(v, p, w);
         }
         unsigned long long above = 0;
         if (a.s.parents && plain < to)
             above = tree_node(a.s.parents + (int64_t)pc.b * a.s.N, a.s.N).above;
+        // steps with slots that some row does not see
 #pragma clang loop unroll(disable)
         for (int s = plain; s < to; ++s) {
-            attend_load<DP>(a, at, h, k_lane, v_lane, k_on, v_on, x);
+            if (s > plain) {
+                place = attend_next(a, at, h);
+                load_keys<DP>(a, place, k_at, k);
+            }
+            load_values<DP>(a, place, v_at, v);
+            if (!(k.ok[0] && k.ok[1])) put_out<DP>(k, v);
+            attend_scores<DP, MT, F16>(k, w, e);
             const int rel = s * AT_STEP - row.base + g * 4, end = row.end - row.base;
+            uint32_t vis[MT];  // bit 4 t + i: slot i of this lane's in tile t is seen
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 const int n = (first + min(m * 16 + col, rows - 1)) / a.group;
@@ -531,16 +641,24 @@ __global__ __launch_bounds__(AT_NT) void k_attend(Kv8Attend a) {
                     (uint32_t)__shfl((int)above, n & 63);
                 vis[m] = attend_sees(a.s.parents, up, n, rel, end) |
                          attend_sees(a.s.parents, up, n, rel + 16, end) << 4;
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        e[t][m][i] = as<float>(keep_if(vis[m], 4 * t + i, as<uint32_t>((float)e[t][m][i]), 0xff800000u));
             }
             // values behind the last token are not numbers to be multiplied by 0
+            const uint32_t there = ((1u << min(max(end - rel, 0), 4)) - 1) |
+                                   ((1u << min(max(end - rel - 16, 0), 4)) - 1) << 4;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const bool there = rel + j / 4 * 16 + j % 4 < end;
 #pragma unroll
                 for (int c = 0; c < DP / 64; ++c)
-                    set_word<DP>(x.v[j], c, there ? word_of<DP>(x.v[j], c) : 0u);
+                    set_word<DP>(v.v[j], c, keep_if(there, j, word_of<DP>(v.v[j], c), 0u));
             }
-            attend_step<DP, MT, F16, true>(a, x, vis, w);
+            attend_weights<DP, MT>(a, k.s, v.s, k.ok, e, w, p);
+            attend_nans<DP, MT>(v, vis, w);
+            attend_values<DP, MT>(v, p, w);
         }
     }
 
@@ -554,14 +672,14 @@ __global__ __launch_bounds__(AT_NT) void k_attend(Kv8Attend a) {
             s_l[wave][m * 16 + col] = w.l[m];
         }
     }
-    const int r16 = tid / 16, part = tid % 16;  // what a thread sums up: DT entries of a row
+    const int r16 = tid / (DP / PT), part = tid % (DP / PT);
     float* slot = a.part + (int64_t)blockIdx.x * SLOT;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
         __syncthreads();
         float ref = s_ref[0][m * 16 + col];
 #pragma unroll
-        for (int v = 1; v < AT_WAVES; ++v) ref = fmaxf(ref, s_ref[v][m * 16 + col]);
+        for (int v = 1; v < WAVES; ++v) ref = fmaxf(ref, s_ref[v][m * 16 + col]);
         const float f = __builtin_amdgcn_exp2f(w.ref[m] - ref);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -572,40 +690,21 @@ __global__ __launch_bounds__(AT_NT) void k_attend(Kv8Attend a) {
                 *reinterpret_cast<f32x4*>(&s_o[wave][col][(g * 4 + i) * DT + d]) = v;
             }
         __syncthreads();
+        if (m * 16 + r16 >= rows) continue;
+        AttendSum<PT> sum = add_waves<DP, PT, WAVES>(s_o, s_ref, s_l, m * 16, r16, part);
         const int rr = m * 16 + r16;
-        ref = s_ref[0][rr];
-#pragma unroll
-        for (int v = 1; v < AT_WAVES; ++v) ref = fmaxf(ref, s_ref[v][rr]);
-        float l = 0.0f;
-        float o[DT] = {};
-#pragma unroll
-        for (int v = 0; v < AT_WAVES; ++v) {
-            l = __builtin_fmaf(s_l[v][rr], __builtin_amdgcn_exp2f(s_ref[v][rr] - ref), l);
-#pragma unroll
-            for (int d = 0; d < DT; ++d) o[d] += s_o[v][r16][part * DT + d];
-        }
-        if (rr >= rows) continue;
         if (pc.n > 1) {
-            if (part == 0) put(slot + rr * 2, ref, l);
+            if (part == 0) put(slot + rr * 2, sum.ref, sum.l);
 #pragma unroll
-            for (int d = 0; d < DT; d += 2) put(slot + MT * 32 + rr * DP + part * DT + d, o[d], o[d + 1]);
+            for (int d = 0; d < PT; d += 2)
+                put(slot + MT * 32 + rr * DP + part * PT + d, sum.o[d], sum.o[d + 1]);
         } else {
-            const int r = first + rr, n = r / a.group, head = h * a.group + r - n * a.group;
-            const bool live = s_live[rr] != 0;
-            if (!live) {
-#pragma unroll
-                for (int d = 0; d < DT; ++d) o[d] = 0.0f;
-            }
-            if (part * DT < a.g.dim)
-                attend_out<DT, F16>(a, pc.b, n, head, part * DT, o, attend_factor(l, live));
-            if (a.lse && part == 0)
-                a.lse[((int64_t)pc.b * a.s.N + n) * a.q_heads + head] =
-                    live ? (ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
+            attend_result<PT, F16>(a, sum, pc.b, h, first + rr, part, s_live[rr] != 0);
         }
     }
     if (pc.n <= 1) return;
 
-    // the last piece of a row adds them all, in their order
+    // the last piece of a row adds them all, in their order: a wave every WAVES-th of them
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (tid == 0) {
@@ -616,59 +715,86 @@ __global__ __launch_bounds__(AT_NT) void k_attend(Kv8Attend a) {
     __syncthreads();
     if (!s_last) return;
     const float* all = a.part + (int64_t)(blockIdx.x - pc.c) * SLOT;  // pieces of a row follow each other
-    for (int rr = r16; rr < rows; rr += 16) {
-        float ref = AT_NONE;
-        for (int c = 0; c < pc.n; ++c) ref = fmaxf(ref, get(all + (int64_t)c * SLOT + rr * 2)[0]);
-        float l = 0.0f;
-        float o[DT] = {};
-#pragma unroll 4
-        for (int c = 0; c < pc.n; ++c) {
-            const float* p = all + (int64_t)c * SLOT;
-            const f32x2 s = get(p + rr * 2);
-            const float f = __builtin_amdgcn_exp2f(s[0] - ref);
-            l = __builtin_fmaf(s[1], f, l);
+    for (int r0 = 0; r0 < rows; r0 += 8) {
+        constexpr int ET = DP / 8;  // entries of a row that a lane adds
+        const int r = lane / 8, e0 = lane % 8 * ET;
+        const int rc = min(r0 + r, rows - 1);  // lanes behind the last row add it again
+        AttendSum<ET> sum;
+        sum.ref = AT_NONE;
+        sum.l = 0.0f;
 #pragma unroll
-            for (int d = 0; d < DT; d += 2) {
-                const f32x2 v = get(p + MT * 32 + rr * DP + part * DT + d);
-                o[d] = __builtin_fmaf(v[0], f, o[d]);
-                o[d + 1] = __builtin_fmaf(v[1], f, o[d + 1]);
+        for (int d = 0; d < ET; ++d) sum.o[d] = 0.0f;
+        constexpr int AT_ONCE = 64 / ET < 4 ? 64 / ET : 4;
+        for (int c0 = wave; c0 < pc.n; c0 += AT_ONCE * WAVES) {
+            f32x2 s[AT_ONCE], v[AT_ONCE][ET / 2];
+#pragma unroll
+            for (int k = 0; k < AT_ONCE; ++k) {
+                const float* p = all + (int64_t)min(c0 + k * WAVES, pc.n - 1) * SLOT;
+                s[k] = get(p + rc * 2);
+#pragma unroll
+                for (int d = 0; d < ET / 2; ++d) v[k][d] = get(p + MT * 32 + rc * DP + e0 + 2 * d);
+            }
+            float ref = sum.ref;
+#pragma unroll
+            for (int k = 0; k < AT_ONCE; ++k) ref = fmaxf(ref, s[k][0]);
+            const float f = __builtin_amdgcn_exp2f(sum.ref - ref);
+            sum.ref = ref;
+            sum.l *= f;
+#pragma unroll
+            for (int d = 0; d < ET; ++d) sum.o[d] *= f;
+#pragma unroll
+            for (int k = 0; k < AT_ONCE; ++k) {
+                // behind the last piece nothing is added
+                const float fk = c0 + k * WAVES < pc.n ? __builtin_amdgcn_exp2f(s[k][0] - ref) : 0.0f;
+                sum.l = __builtin_fmaf(s[k][1], fk, sum.l);
+#pragma unroll
+                for (int d = 0; d < ET; ++d) sum.o[d] = __builtin_fmaf(v[k][d / 2][d % 2], fk, sum.o[d]);
             }
         }
-        const int r = first + rr, n = r / a.group, head = h * a.group + r - n * a.group;
-        const bool live = s_live[rr] != 0;
-        if (!live) {
-#pragma unroll
-            for (int d = 0; d < DT; ++d) o[d] = 0.0f;
+        __syncthreads();  // the sums of the rows before are read
+        if (lane % 8 == 0) {
+            s_ref[wave][r] = sum.ref;
+            s_l[wave][r] = sum.l;
         }
-        if (part * DT < a.g.dim)
-            attend_out<DT, F16>(a, pc.b, n, head, part * DT, o, attend_factor(l, live));
-        if (a.lse && part == 0)
-            a.lse[((int64_t)pc.b * a.s.N + n) * a.q_heads + head] =
-                live ? (ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        __syncthreads();
+        float ref = s_ref[0][r];
+#pragma unroll
+        for (int v = 1; v < WAVES; ++v) ref = fmaxf(ref, s_ref[v][r]);
+        const float f = __builtin_amdgcn_exp2f(sum.ref - ref);
+#pragma unroll
+        for (int d = 0; d < ET; d += 4) {
+            const f32x4 v = {sum.o[d] * f, sum.o[d + 1] * f, sum.o[d + 2] * f, sum.o[d + 3] * f};
+            *reinterpret_cast<f32x4*>(&s_o[wave][r][e0 + d]) = v;
+        }
+        __syncthreads();
+        if (r16 < 8 && r0 + r16 < rows)
+            attend_result<PT, F16>(a, add_waves<DP, PT, WAVES>(s_o, s_ref, s_l, 0, r16, part), pc.b, h,
+                                   first + r0 + r16, part, s_live[r0 + r16] != 0);
     }
 }
 
 // How many rows a workgroup takes, and into how many pieces rows are cut.
-template <int DP, int MT, bool F16>
+template <int DP, int MT, bool F16, int WAVES>
 static hipError_t launch_attend(Kv8Attend a, hipStream_t st) {
     constexpr int64_t SLOT = MT * 16 * (DP + 2);
     a.blocks = (int)(((int64_t)a.s.N * a.group + MT * 16 - 1) / (MT * 16));
     const int64_t y = (int64_t)a.g.heads * a.blocks;
     // rows are cut where whole ones leave the card's CUs idle or uneven
     const int64_t most = KV8_PART_FLOATS / SLOT < KV8_SPLITS ? KV8_PART_FLOATS / SLOT : KV8_SPLITS;
-    a.pieces = y * a.s.B <= most / 2 ? (int)(most / 2 / y) : 0;
+    static const int target = getenv("AT_TARGET") ? atoi(getenv("AT_TARGET")) : 512;
+    a.pieces = y * a.s.B <= most / 2 ? (int)((most / 2 < target ? most / 2 : target) / y) : 0;
     const int64_t grid = y * (a.s.B + a.pieces);
     if (grid > INT_MAX) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_attend<DP, MT, F16>), dim3((unsigned)grid), dim3(AT_NT), 0, st, a);
+    hipLaunchKernelGGL((k_attend<DP, MT, F16, WAVES>), dim3((unsigned)grid), dim3(WAVES * WAVE), 0, st, a);
     return hipGetLastError();
 }
 
 template <int DP, bool F16>
 static hipError_t launch_attend_rows(const Kv8Attend& a, hipStream_t st) {
     const int64_t rows = (int64_t)a.s.N * a.group;
-    if (rows <= 16) return launch_attend<DP, 1, F16>(a, st);
-    if (rows <= 32 || DP == 256) return launch_attend<DP, 2, F16>(a, st);
-    return launch_attend<DP, DP == 256 ? 2 : 4, F16>(a, st);
+    if (rows <= 16) return launch_attend<DP, 1, F16, 4>(a, st);
+    if (rows <= 32 || DP == 256) return launch_attend<DP, 2, F16, 4>(a, st);
+    return launch_attend<DP, DP == 256 ? 2 : 4, F16, 4>(a, st);
 }
 
 template <bool F16>

@@ -165,6 +165,7 @@ ss::Kv8Geo geo_of(const ss_cache* c) {
     g.sc_head = c->cfg.heads > 1 ? c->scales.head_stride : 0;
     g.page_size = c->cfg.page_size;
     g.block = c->scales.block;
+    g.block_bits = c->scales.block == 16 ? 4 : c->scales.block == 32 ? 5 : 6;
     g.heads = c->cfg.heads;
     g.dim = c->cfg.piece_bytes;
     g.num_pages = c->cfg.num_pages;

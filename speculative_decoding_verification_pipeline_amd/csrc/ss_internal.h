@@ -387,7 +387,7 @@ struct Kv8Plane {
 struct Kv8Geo {
     int64_t page, slot, head;      // of the planes
     int64_t sc_page, sc_block, sc_head;
-    int page_size, block, heads, dim;
+    int page_size, block, block_bits, heads, dim;  // a block has 2^block_bits slots
     int num_pages, max_blocks;
 };
 
