@@ -250,9 +250,24 @@ __device__ __forceinline__ uint32_t keep_if(uint32_t bits, int bit, uint32_t w, 
     return (w & m) | (other & ~m);
 }
 
-// Bytes of a word that are a NaN, as 0x80 each.
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
-    return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+// Puts out the scores of a step's slots that a row does not see. rel: this lane's first slot
+// behind the committed ones; vis: those seen, bit 4 t + i slot i of tile t.
+template <int MT>
+__device__ __forceinline__ void attend_mask(const Kv8Attend& a, unsigned long long above, int first, int rows,
+                                            int rel, int end, f32x4 (&s)[2][MT], uint32_t (&vis)[MT]) {
+    const int col = threadIdx.x & 15;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        const int n = (first + min(m * 16 + col, rows - 1)) / a.group;
+        const unsigned long long up = (unsigned long long)(uint32_t)__shfl((int)(above >> 32), n & 63) << 32 |
+                                      (uint32_t)__shfl((int)above, n & 63);
+        vis[m] = attend_sees(a.s.parents, up, n, rel, end) | attend_sees(a.s.parents, up, n, rel + 16, end) << 4;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                s[t][m][i] = as<float>(keep_if(vis[m], 4 * t + i, as<uint32_t>((float)s[t][m][i]), 0xff800000u));
+    }
 }
 
 // S^T of one step.
@@ -275,19 +290,29 @@ __device__ __forceinline__ void attend_scores(const AttendKeys<DP>& x, const Att
     }
 }
 
-// Weights of one step: s becomes them, under the rows' references, which may grow.
-template <int DP, int MT>
-__device__ __forceinline__ void attend_weights(const Kv8Attend& a, const uint32_t (&ks)[2],
-                                               const uint32_t (&vs)[2], const bool (&ok)[2], const f32x4 (&s)[2][MT],
-                                               AttendState<DP, MT>& w, u32x4 (&p)[MT]) {
+// What two tiles' scales come to: the factor on S with the softmax's scale, the exponent that
+// a value's scale adds to its weight, and the factor that takes it off again.
+struct AttendScales {
     float fk[2], xv[2], inv[2];
+};
+
+__device__ __forceinline__ AttendScales scales_of(const Kv8Attend& a, const uint32_t (&ks)[2],
+                                                  const uint32_t (&vs)[2], const bool (&ok)[2]) {
+    AttendScales x;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         const uint32_t v = clamp_scale(vs[t]);
-        fk[t] = as<float>(clamp_scale(ks[t]) << 23) * a.scale_log2;
-        xv[t] = ok[t] ? (float)((int)v - 127) : -INFINITY;
-        inv[t] = as<float>((254u - v) << 23);
+        x.fk[t] = as<float>(clamp_scale(ks[t]) << 23) * a.scale_log2;
+        x.xv[t] = ok[t] ? (float)((int)v - 127) : -INFINITY;
+        x.inv[t] = as<float>((254u - v) << 23);
     }
+    return x;
+}
+
+// Weights of one step, under the rows' references, which may grow.
+template <int DP, int MT>
+__device__ __forceinline__ void attend_weights(const AttendScales& x, const f32x4 (&s)[2][MT],
+                                               AttendState<DP, MT>& w, u32x4 (&p)[MT]) {
     float top[MT];
     bool grows = false;
 #pragma unroll
@@ -296,7 +321,7 @@ __device__ __forceinline__ void attend_weights(const Kv8Attend& a, const uint32_
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const float most = fmaxf(fmaxf(s[t][m][0], s[t][m][1]), fmaxf(s[t][m][2], s[t][m][3]));
-            top[m] = fmaxf(top[m], __builtin_fmaf(most, fk[t], xv[t]));
+            top[m] = fmaxf(top[m], __builtin_fmaf(most, x.fk[t], x.xv[t]));
         }
         grows |= top[m] > w.ref[m] + AT_MOST;
     }
@@ -319,22 +344,56 @@ __device__ __forceinline__ void attend_weights(const Kv8Attend& a, const uint32_
     for (int m = 0; m < MT; ++m) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const float c = xv[t] - w.ref[m];
+            const float c = x.xv[t] - w.ref[m];
             float e[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][m][i], fk[t], c));
-            w.l[m] = __builtin_fmaf((e[0] + e[1]) + (e[2] + e[3]), inv[t], w.l[m]);
+                e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][m][i], x.fk[t], c));
+            w.l[m] = __builtin_fmaf((e[0] + e[1]) + (e[2] + e[3]), x.inv[t], w.l[m]);
             p[m][2 * t] = as<uint32_t>(__builtin_convertvector((f32x2{e[0], e[1]}), h16x2));
             p[m][2 * t + 1] = as<uint32_t>(__builtin_convertvector((f32x2{e[2], e[3]}), h16x2));
         }
     }
 }
 
+// A NaN among the values of one dimension reaches the rows that see it and no others: it is
+// counted where it is seen, and taken out of the product. v: eight slots of a lane's, widened;
+// vis: those that a row sees, bit by bit; o: the rows' sums of this dimension tile.
+template <int MT>
+__device__ __forceinline__ u32x4 take_nans(u32x4 v, const uint32_t (&vis)[MT], f32x4* (&o)[MT]) {
+    u32x4 nan;
+    uint32_t any = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        nan[j] = ((v[j] & 0x7fff7fffu) + 0x03ff03ffu) & 0x80008000u;
+        any |= nan[j];
+    }
+    if (__any(any != 0)) {
+        u32x4 hot;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            hot[j] = (nan[j] >> 15) * 0x3c00u;
+            v[j] &= ~((nan[j] >> 15) * 0xffffu);
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            u32x4 sees;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                sees[j] = (vis[m] >> (2 * j) & 1) * 0x3c00u | (vis[m] >> (2 * j + 1) & 1) * 0x3c000000u;
+            const f32x4 n = mfma<true>(hot, sees, f32x4{0, 0, 0, 0});
+#pragma unroll
+            for (int i = 0; i < 4; ++i)  // n is 0 or at least 1
+                (*o[m])[i] += n[i] * as<float>(as<uint32_t>((float)n[i]) ? 0x7fc00000u : 0u);
+        }
+    }
+    return v;
+}
+
 // O^T of one step.
-template <int DP, int MT>
+template <int DP, int MT, bool MASK>
 __device__ __forceinline__ void attend_values(const AttendValues<DP>& x, const u32x4 (&p)[MT],
-                                              AttendState<DP, MT>& w) {
+                                              const uint32_t (&vis)[MT], AttendState<DP, MT>& w) {
 #pragma unroll
     for (int c = 0; c < DP / 64; ++c) {
         uint32_t lo[8], hi[8];  // dimensions 0 and 1, 2 and 3 of the word
@@ -351,50 +410,14 @@ __device__ __forceinline__ void attend_values(const AttendValues<DP>& x, const u
                 const uint32_t u0 = d < 2 ? lo[2 * j] : hi[2 * j], u1 = d < 2 ? lo[2 * j + 1] : hi[2 * j + 1];
                 v[j] = __builtin_amdgcn_perm(u1, u0, d % 2 ? 0x07060302u : 0x05040100u);
             }
+            if constexpr (MASK) {
+                f32x4* o[MT];
+#pragma unroll
+                for (int m = 0; m < MT; ++m) o[m] = &w.o[m][c * 4 + d];
+                v = take_nans<MT>(v, vis, o);
+            }
 #pragma unroll
             for (int m = 0; m < MT; ++m) w.o[m][c * 4 + d] = mfma<true>(v, p[m], w.o[m][c * 4 + d]);
-        }
-    }
-}
-
-// A NaN among the values reaches the rows that see it and no others: it is counted where it
-// is seen, and taken out of the product.
-template <int DP, int MT>
-__device__ __forceinline__ void attend_nans(AttendValues<DP>& x, const uint32_t (&vis)[MT],
-                                            AttendState<DP, MT>& w) {
-    uint32_t any = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int c = 0; c < DP / 64; ++c) any |= nan_bytes(word_of<DP>(x.v[j], c));
-    if (!__any(any != 0)) return;
-#pragma unroll
-    for (int c = 0; c < DP / 64; ++c) {
-        uint32_t nan[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t word = word_of<DP>(x.v[j], c);
-            nan[j] = nan_bytes(word);
-            set_word<DP>(x.v[j], c, word & ~((nan[j] >> 7) * 0xffu));
-        }
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-            u32x4 hot;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                hot[j] = ((nan[2 * j] >> (8 * d + 7)) & 1) * 0x3c00u |
-                         ((nan[2 * j + 1] >> (8 * d + 7)) & 1) * 0x3c000000u;
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                u32x4 sees;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    sees[j] = (vis[m] >> (2 * j) & 1) * 0x3c00u | (vis[m] >> (2 * j + 1) & 1) * 0x3c000000u;
-                const f32x4 n = mfma<true>(hot, sees, f32x4{0, 0, 0, 0});
-#pragma unroll
-                for (int i = 0; i < 4; ++i)  // n is 0 or at least 1
-                    w.o[m][c * 4 + d][i] += n[i] * (as<float>(as<uint32_t>((float)n[i]) ? 0x7fc00000u : 0u));
-            }
         }
     }
 }
@@ -447,86 +470,160 @@ __device__ __forceinline__ f32x2 get(const float* p) {
                                        __HIP_MEMORY_SCOPE_AGENT));
 }
 
-// Writes D neighbouring entries of a row of the output from entry d0 on.
-template <int D, bool F16>
-__device__ __forceinline__ void attend_out(const Kv8Attend& a, int b, int n, int head, int d0,
-                                           const float* o, float f) {
-    uint32_t r[D / 2];
-#pragma unroll
-    for (int i = 0; i < D / 2; ++i) {
-        const f32x2 v = {o[2 * i] * f, o[2 * i + 1] * f};
-        if constexpr (F16) r[i] = as<uint32_t>(__builtin_convertvector(v, h16x2));
-        else r[i] = as<uint32_t>(__builtin_convertvector(v, b16x2));
-    }
-    uint16_t* to = a.out.data + b * a.out.row + n * a.out.token + head * a.out.head + d0;
-    typedef typename Words<D / 2 < 4 ? D / 2 : 4>::type V;
-#pragma unroll
-    for (int i = 0; i < D / 2; i += sizeof(V) / 4) {
-        V v;
-        if constexpr (sizeof(V) == 4) {
-            v = r[i];
-        } else {
-#pragma unroll
-            for (unsigned k = 0; k < sizeof(V) / 4; ++k) v[k] = r[i + k];
-        }
-        *reinterpret_cast<V*>(to + 2 * i) = v;
-    }
+// Two floats as the output's type.
+template <bool F16>
+__device__ __forceinline__ uint32_t narrow(float a, float b) {
+    const f32x2 v = {a, b};
+    if constexpr (F16) return as<uint32_t>(__builtin_convertvector(v, h16x2));
+    else return as<uint32_t>(__builtin_convertvector(v, b16x2));
 }
 
-// A row's sums under one reference, of the entries that a thread has.
-template <int PT>
-struct AttendSum {
-    float ref, l;
-    float o[PT];
+// A row of a head of the cache (a query head of a token) in the output.
+struct AttendOut {
+    uint16_t* to;
+    int64_t lse;
 };
 
-// Adds the waves' sums of row r (of the 16 from m on), which lie under the waves' largest
-// reference.
-template <int DP, int PT, int WAVES, class O, class S>
-__device__ __forceinline__ AttendSum<PT> add_waves(const O& s_o, const S& s_ref, const S& s_l, int m, int r,
-                                                   int part) {
-    AttendSum<PT> s;
-    s.ref = s_ref[0][m + r];
-#pragma unroll
-    for (int v = 1; v < WAVES; ++v) s.ref = fmaxf(s.ref, s_ref[v][m + r]);
-    s.l = 0.0f;
-#pragma unroll
-    for (int d = 0; d < PT; ++d) s.o[d] = 0.0f;
-#pragma unroll
-    for (int v = 0; v < WAVES; ++v) {
-        s.l = __builtin_fmaf(s_l[v][m + r], __builtin_amdgcn_exp2f(s_ref[v][m + r] - s.ref), s.l);
-#pragma unroll
-        for (int d = 0; d < PT; ++d) s.o[d] += s_o[v][r][part * PT + d];
-    }
-    return s;
+__device__ __forceinline__ AttendOut attend_out(const Kv8Attend& a, int b, int h, int r) {
+    const int n = r / a.group, head = h * a.group + r - n * a.group;
+    return {a.out.data + b * a.out.row + n * a.out.token + head * a.out.head,
+            ((int64_t)b * a.s.N + n) * a.q_heads + head};
 }
 
-// Row r of a head of the cache to the output: 0 where it has seen nothing, or scores of -inf
-// alone.
-template <int PT, bool F16>
-__device__ __forceinline__ void attend_result(const Kv8Attend& a, AttendSum<PT> s, int b, int h, int r,
-                                              int part, bool live) {
-    const int n = r / a.group, head = h * a.group + r - n * a.group;
-    if (!live) {
-#pragma unroll
-        for (int d = 0; d < PT; ++d) s.o[d] = 0.0f;
+// The factor on a row's sums: 0 where it has seen nothing, or scores of -inf alone.
+__device__ __forceinline__ float attend_factor(float l, bool live) { return live && l != 0.0f ? 1.0f / l : 0.0f; }
+
+__device__ __forceinline__ float attend_lse(float ref, float l, bool live) {
+    return live ? (ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+// Two entries of a row; what a row that is not live has summed up may be anything.
+template <bool F16>
+__device__ __forceinline__ void put_pair(uint16_t* to, float a, float b, float f, bool live) {
+    *reinterpret_cast<uint32_t*>(to) = live ? narrow<F16>(a * f, b * f) : 0u;
+}
+
+// Floats that a piece of `rows` rows leaves: references and sums, then their outputs.
+constexpr int attend_slot(int dp, int rows) { return rows * (dp + 2); }
+
+// Counts a piece that has left its sums. The one that counts last of a row adds them all, in
+// their order, eight rows a wave at a time, a lane two neighbouring entries of each 128: whole
+// lines a load, four pieces on their way at once. Of few rows the pieces are dealt out to the
+// waves, which meet in LDS.
+template <int DP, int ROWS, bool F16, int WAVES>
+__device__ __forceinline__ void add_pieces(const Kv8Attend& a, int b, int c, int n, int y, int h, int first,
+                                           int rows, float* s_mem, const int* s_live) {
+    constexpr int PAIRS = 8 * DP / 128;  // of a lane's, over eight rows
+    constexpr int ONCE = PAIRS >= 16 ? 2 : 4;
+    const int tid = threadIdx.x;
+    const int lane = tid & (WAVE - 1);
+    const int wave = tid / WAVE;
+    __shared__ int s_last;
+    // what it left has reached the agent's point of coherence before it counts
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (tid == 0) {
+        int32_t* arrived = a.arrived + ((int64_t)y * a.s.B + b) * KV8_COUNTER;
+        s_last = __hip_atomic_fetch_add(arrived, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == n - 1;
+        if (s_last) __hip_atomic_store(arrived, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    if (part * PT < a.g.dim)
-        attend_out<PT, F16>(a, b, n, head, part * PT, s.o, live && s.l != 0.0f ? 1.0f / s.l : 0.0f);
-    if (a.lse && part == 0)
-        a.lse[((int64_t)b * a.s.N + n) * a.q_heads + head] =
-            live ? (s.ref + log2f(s.l)) * 0.69314718055994531f : -INFINITY;
+    __syncthreads();
+    if (!s_last) return;
+    // pieces of a row follow each other
+    const float* all = a.part + (int64_t)(blockIdx.x - c) * attend_slot(DP, ROWS);
+    const int groups = (rows + 7) / 8;
+    const int share = groups == 1 ? WAVES : groups == 2 ? WAVES / 2 : 1;  // waves of a group
+    const int sub = wave % share;
+    auto row_of = [&](int k) { return (k * WAVE + lane) * 2 / DP; };
+    for (int r0 = wave / share * 8; r0 < groups * 8; r0 += WAVES / share * 8) {
+        const int mine = min(r0 + lane % 8, rows - 1);  // whose sums this lane has; of a wave's last rows any
+        float ref = AT_NONE, l = 0.0f;
+        f32x2 o[PAIRS];
+#pragma unroll
+        for (int k = 0; k < PAIRS; ++k) o[k] = f32x2{0.0f, 0.0f};
+        for (int c0 = sub; c0 < n; c0 += ONCE * share) {
+            f32x2 s[ONCE], v[ONCE][PAIRS];
+#pragma unroll
+            for (int i = 0; i < ONCE; ++i) {
+                const float* p = all + (int64_t)min(c0 + i * share, n - 1) * attend_slot(DP, ROWS);
+                s[i] = get(p + mine * 2);
+#pragma unroll
+                for (int k = 0; k < PAIRS; ++k) v[i][k] = get(p + 2 * ROWS + r0 * DP + (k * WAVE + lane) * 2);
+            }
+            float to = ref;
+#pragma unroll
+            for (int i = 0; i < ONCE; ++i) to = fmaxf(to, s[i][0]);
+            const float f = __builtin_amdgcn_exp2f(ref - to);
+            ref = to;
+            l *= f;
+#pragma unroll
+            for (int k = 0; k < PAIRS; ++k) o[k] *= __shfl(f, row_of(k));
+#pragma unroll
+            for (int i = 0; i < ONCE; ++i) {
+                // behind the last piece nothing is added
+                const float g = c0 + i * share < n ? __builtin_amdgcn_exp2f(s[i][0] - ref) : 0.0f;
+                l = __builtin_fmaf(s[i][1], g, l);
+#pragma unroll
+                for (int k = 0; k < PAIRS; ++k) {
+                    const float gk = __shfl(g, row_of(k));
+                    o[k][0] = __builtin_fmaf(v[i][k][0], gk, o[k][0]);
+                    o[k][1] = __builtin_fmaf(v[i][k][1], gk, o[k][1]);
+                }
+            }
+        }
+        if (share > 1) {  // one round for all waves
+            float* s_o = s_mem + wave * 8 * DP;
+            float* s_s = s_mem + WAVES * 8 * DP;
+#pragma unroll
+            for (int k = 0; k < PAIRS; ++k) *reinterpret_cast<f32x2*>(s_o + (k * WAVE + lane) * 2) = o[k];
+            if (lane < 8) {
+                s_s[(wave * 8 + lane) * 2] = ref;
+                s_s[(wave * 8 + lane) * 2 + 1] = l;
+            }
+            __syncthreads();
+            if (sub) continue;
+            float to = ref;
+            for (int i = 1; i < share; ++i) to = fmaxf(to, s_s[((wave + i) * 8 + lane % 8) * 2]);
+            const float f = __builtin_amdgcn_exp2f(ref - to);
+            ref = to;
+            l *= f;
+#pragma unroll
+            for (int k = 0; k < PAIRS; ++k) o[k] *= __shfl(f, row_of(k));
+            for (int i = 1; i < share; ++i) {
+                const float* other = s_s + ((wave + i) * 8 + lane % 8) * 2;
+                const float g = __builtin_amdgcn_exp2f(other[0] - ref);
+                l = __builtin_fmaf(other[1], g, l);
+#pragma unroll
+                for (int k = 0; k < PAIRS; ++k) {
+                    const f32x2 v = *reinterpret_cast<const f32x2*>(s_o + i * 8 * DP + (k * WAVE + lane) * 2);
+                    const float gk = __shfl(g, row_of(k));
+                    o[k][0] = __builtin_fmaf(v[0], gk, o[k][0]);
+                    o[k][1] = __builtin_fmaf(v[1], gk, o[k][1]);
+                }
+            }
+        }
+        const bool live = s_live[mine] != 0;
+        const float f = attend_factor(l, live);
+        if (a.lse && lane < 8 && r0 + lane < rows)
+            a.lse[attend_out(a, b, h, first + r0 + lane).lse] = attend_lse(ref, l, live);
+#pragma unroll
+        for (int k = 0; k < PAIRS; ++k) {
+            const int r = r0 + row_of(k), e = (k * WAVE + lane) * 2 % DP;
+            const float fk = __shfl(f, row_of(k));
+            const bool on = __shfl((int)live, row_of(k));
+            if (r < rows && e < a.g.dim)
+                put_pair<F16>(attend_out(a, b, h, first + r).to + e, o[k][0], o[k][1], fk, on);
+        }
+    }
 }
 
 template <int DP, int MT, bool F16, int WAVES>
 __global__ __launch_bounds__(WAVES* WAVE, DP == 256 || MT == 4 ? 1 : MT == 2 ? 2 : DP == 128 ? 3 : 4) void k_attend(Kv8Attend a) {
     constexpr int DT = DP / 16;
-    constexpr int PT = DP / (WAVES * 4);      // entries of a row that a thread adds
-    constexpr int SLOT = MT * 16 * (DP + 2);  // floats that a piece leaves
+    constexpr int SLOT = attend_slot(DP, MT * 16);
     __shared__ float s_o[WAVES][16][DP + 4];
     __shared__ float s_ref[WAVES][MT * 16], s_l[WAVES][MT * 16];
     __shared__ int s_live[MT * 16];
-    __shared__ int s_last;
     const int tid = threadIdx.x;
     const int lane = tid & (WAVE - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
@@ -602,6 +699,7 @@ __global__ __launch_bounds__(WAVES* WAVE, DP == 256 || MT == 4 ? 1 : MT == 2 ? 2
         AttendValues<DP> v;
         f32x4 e[2][MT];
         u32x4 p[MT];
+        const uint32_t none[MT] = {};
         attend_look(at);
         AttendPlace place = attend_next(a, at, h);
         load_keys<DP>(a, place, k_at, k);
@@ -615,8 +713,8 @@ __global__ __launch_bounds__(WAVES* WAVE, DP == 256 || MT == 4 ? 1 : MT == 2 ? 2
             const bool ok[2] = {k.ok[0], k.ok[1]};
             place = attend_next(a, at, h);  // behind the last step: page 0
             load_keys<DP>(a, place, k_at, k);
-            attend_weights<DP, MT>(a, ks, v.s, ok, e, w, p);
-            attend_values<DP, MT>(v, p, w);
+            attend_weights<DP, MT>(scales_of(a, ks, v.s, ok), e, w, p);
+            attend_values<DP, MT, false>(v, p, none, w);
         }
         unsigned long long above = 0;
         if (a.s.parents && plain < to)
@@ -632,21 +730,8 @@ __global__ __launch_bounds__(WAVES* WAVE, DP == 256 || MT == 4 ? 1 : MT == 2 ? 2
             if (!(k.ok[0] && k.ok[1])) put_out<DP>(k, v);
             attend_scores<DP, MT, F16>(k, w, e);
             const int rel = s * AT_STEP - row.base + g * 4, end = row.end - row.base;
-            uint32_t vis[MT];  // bit 4 t + i: slot i of this lane's in tile t is seen
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const int n = (first + min(m * 16 + col, rows - 1)) / a.group;
-                const unsigned long long up =
-                    (unsigned long long)(uint32_t)__shfl((int)(above >> 32), n & 63) << 32 |
-                    (uint32_t)__shfl((int)above, n & 63);
-                vis[m] = attend_sees(a.s.parents, up, n, rel, end) |
-                         attend_sees(a.s.parents, up, n, rel + 16, end) << 4;
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        e[t][m][i] = as<float>(keep_if(vis[m], 4 * t + i, as<uint32_t>((float)e[t][m][i]), 0xff800000u));
-            }
+            uint32_t vis[MT];
+            attend_mask<MT>(a, above, first, rows, rel, end, e, vis);
             // values behind the last token are not numbers to be multiplied by 0
             const uint32_t there = ((1u << min(max(end - rel, 0), 4)) - 1) |
                                    ((1u << min(max(end - rel - 16, 0), 4)) - 1) << 4;
@@ -656,9 +741,8 @@ __global__ __launch_bounds__(WAVES* WAVE, DP == 256 || MT == 4 ? 1 : MT == 2 ? 2
                 for (int c = 0; c < DP / 64; ++c)
                     set_word<DP>(v.v[j], c, keep_if(there, j, word_of<DP>(v.v[j], c), 0u));
             }
-            attend_weights<DP, MT>(a, k.s, v.s, k.ok, e, w, p);
-            attend_nans<DP, MT>(v, vis, w);
-            attend_values<DP, MT>(v, p, w);
+            attend_weights<DP, MT>(scales_of(a, k.s, v.s, k.ok), e, w, p);
+            attend_values<DP, MT, true>(v, p, vis, w);
         }
     }
 
@@ -672,7 +756,9 @@ __global__ __launch_bounds__(WAVES* WAVE, DP == 256 || MT == 4 ? 1 : MT == 2 ? 2
             s_l[wave][m * 16 + col] = w.l[m];
         }
     }
-    const int r16 = tid / (DP / PT), part = tid % (DP / PT);
+    // a thread adds pairs of entries of a row, neighbours' pairs side by side
+    constexpr int PER_ROW = WAVES * 4;
+    const int r16 = tid / PER_ROW, part = tid % PER_ROW;
     float* slot = a.part + (int64_t)blockIdx.x * SLOT;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -690,87 +776,323 @@ __global__ __launch_bounds__(WAVES* WAVE, DP == 256 || MT == 4 ? 1 : MT == 2 ? 2
                 *reinterpret_cast<f32x4*>(&s_o[wave][col][(g * 4 + i) * DT + d]) = v;
             }
         __syncthreads();
-        if (m * 16 + r16 >= rows) continue;
-        AttendSum<PT> sum = add_waves<DP, PT, WAVES>(s_o, s_ref, s_l, m * 16, r16, part);
         const int rr = m * 16 + r16;
-        if (pc.n > 1) {
-            if (part == 0) put(slot + rr * 2, sum.ref, sum.l);
+        if (rr >= rows) continue;
+        ref = s_ref[0][rr];
 #pragma unroll
-            for (int d = 0; d < PT; d += 2)
-                put(slot + MT * 32 + rr * DP + part * PT + d, sum.o[d], sum.o[d + 1]);
-        } else {
-            attend_result<PT, F16>(a, sum, pc.b, h, first + rr, part, s_live[rr] != 0);
+        for (int v = 1; v < WAVES; ++v) ref = fmaxf(ref, s_ref[v][rr]);
+        float l = 0.0f;
+#pragma unroll
+        for (int v = 0; v < WAVES; ++v)
+            l = __builtin_fmaf(s_l[v][rr], __builtin_amdgcn_exp2f(s_ref[v][rr] - ref), l);
+        const bool live = s_live[rr] != 0;
+        const AttendOut out = attend_out(a, pc.b, h, first + rr);
+        const float to = attend_factor(l, live);
+        if (part == 0) {
+            if (pc.n > 1) put(slot + rr * 2, ref, l);
+            else if (a.lse) a.lse[out.lse] = attend_lse(ref, l, live);
+        }
+#pragma unroll
+        for (int k = 0; k < DP / 2 / PER_ROW; ++k) {
+            const int e = (k * PER_ROW + part) * 2;
+            f32x2 o = {0.0f, 0.0f};
+#pragma unroll
+            for (int v = 0; v < WAVES; ++v) o += *reinterpret_cast<const f32x2*>(&s_o[v][r16][e]);
+            if (pc.n > 1) put(slot + 2 * MT * 16 + rr * DP + e, o[0], o[1]);
+            else if (e < a.g.dim) put_pair<F16>(out.to + e, o[0], o[1], to, live);
         }
     }
-    if (pc.n <= 1) return;
+    if (pc.n > 1)
+        add_pieces<DP, MT * 16, F16, WAVES>(a, pc.b, pc.c, pc.n, y, h, first, rows, &s_o[0][0][0], s_live);
+}
 
-    // the last piece of a row adds them all, in their order: a wave every WAVES-th of them
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (tid == 0) {
-        int32_t* arrived = a.arrived + ((int64_t)y * a.s.B + pc.b) * KV8_COUNTER;
-        s_last = __hip_atomic_fetch_add(arrived, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == pc.n - 1;
-        if (s_last) __hip_atomic_store(arrived, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// ---------------------------------------------------------------------------
+// Many rows: the waves of a workgroup take rows of their own, 16 * MT each, and share keys and
+// values. Of a tile of 64 slots every wave widens 16 and leaves them in LDS as the operands'
+// registers hold them, 16 bytes a lane, so that neither its writes nor the reads meet in a
+// bank. Two tiles take turns: one is read while the next is left, with a barrier a tile; the
+// one after that is on its way from memory meanwhile.
+
+constexpr int AT_TILE = 64;
+
+template <int DP>
+struct AttendTile {
+    u32x4 k[4][DP / 32][WAVE];  // by tile of 16 slots and step of 32 dimensions
+    u32x4 v[2][DP / 16][WAVE];  // by step of 32 slots and tile of 16 dimensions
+    f32x4 x[4];                 // factor on S, exponent of the weights, its inverse
+};
+
+// A wave's 16 slots of the next tile, as they lie in the page.
+template <int DP>
+struct AttendRaw {
+    u32x4 k[DP / 64];
+    typename Words<DP / 64>::type v[4];
+    uint32_t ks, vs;
+    bool ok;
+    int there;  // its slots up to the row's last
+};
+
+// Where a wave's 16 slots of a tile lie in its row.
+struct AttendWalk {
+    const_i32 table;
+    int block, inner;        // table entry, tile of 16 within its page
+    int tiles, over, ahead;  // tiles of a page; table entries and tiles from one tile of 64 to the next
+    int left;                // slots from there up to the row's last
+};
+
+template <int DP>
+__device__ __forceinline__ void load_raw(const Kv8Attend& a, AttendWalk& c, int h, const uint32_t (&k_at)[DP / 64],
+                                         const uint32_t (&v_at)[4], AttendRaw<DP>& x) {
+    int page = -1;
+    if (c.left > 0) page = c.table[c.block];
+    x.ok = (unsigned)page < (unsigned)a.g.num_pages;
+    x.there = c.left;
+    const int64_t p = x.ok ? page : 0;
+    const int off = c.inner * 16;
+    const int64_t at = p * a.g.page + off * a.g.slot + h * a.g.head;
+    const int64_t sc = p * a.g.sc_page + (off >> a.g.block_bits) * a.g.sc_block + h * a.g.sc_head;
+#pragma unroll
+    for (int i = 0; i < DP / 64; ++i) x.k[i] = *reinterpret_cast<const u32x4*>(a.k.data + at + k_at[i]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        x.v[j] = *reinterpret_cast<const typename Words<DP / 64>::type*>(a.v.data + at + v_at[j]);
+    x.ks = scale_byte(a.k.scales + sc);
+    x.vs = scale_byte(a.v.scales + sc);
+    c.left -= AT_TILE;
+    c.block += c.over;
+    c.inner += c.ahead;
+    if (c.inner >= c.tiles) {
+        c.inner -= c.tiles;
+        ++c.block;
     }
-    __syncthreads();
-    if (!s_last) return;
-    const float* all = a.part + (int64_t)(blockIdx.x - pc.c) * SLOT;  // pieces of a row follow each other
-    for (int r0 = 0; r0 < rows; r0 += 8) {
-        constexpr int ET = DP / 8;  // entries of a row that a lane adds
-        const int r = lane / 8, e0 = lane % 8 * ET;
-        const int rc = min(r0 + r, rows - 1);  // lanes behind the last row add it again
-        AttendSum<ET> sum;
-        sum.ref = AT_NONE;
-        sum.l = 0.0f;
+}
+
+// Widens them into the tile, as its wave-th 16.
+template <int DP, bool F16>
+__device__ __forceinline__ void leave_raw(const Kv8Attend& a, AttendRaw<DP>& x, int wave, AttendTile<DP>& t) {
+    const int lane = threadIdx.x & (WAVE - 1);
+    if (!x.ok || x.there < 16) {  // values behind the last token are not numbers to be multiplied by 0
+        const int g = lane >> 4;
 #pragma unroll
-        for (int d = 0; d < ET; ++d) sum.o[d] = 0.0f;
-        constexpr int AT_ONCE = 64 / ET < 4 ? 64 / ET : 4;
-        for (int c0 = wave; c0 < pc.n; c0 += AT_ONCE * WAVES) {
-            f32x2 s[AT_ONCE], v[AT_ONCE][ET / 2];
+        for (int c = 0; c < DP / 64; ++c)
+            if (!x.ok) x.k[c] = u32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int k = 0; k < AT_ONCE; ++k) {
-                const float* p = all + (int64_t)min(c0 + k * WAVES, pc.n - 1) * SLOT;
-                s[k] = get(p + rc * 2);
-#pragma unroll
-                for (int d = 0; d < ET / 2; ++d) v[k][d] = get(p + MT * 32 + rc * DP + e0 + 2 * d);
-            }
-            float ref = sum.ref;
-#pragma unroll
-            for (int k = 0; k < AT_ONCE; ++k) ref = fmaxf(ref, s[k][0]);
-            const float f = __builtin_amdgcn_exp2f(sum.ref - ref);
-            sum.ref = ref;
-            sum.l *= f;
-#pragma unroll
-            for (int d = 0; d < ET; ++d) sum.o[d] *= f;
-#pragma unroll
-            for (int k = 0; k < AT_ONCE; ++k) {
-                // behind the last piece nothing is added
-                const float fk = c0 + k * WAVES < pc.n ? __builtin_amdgcn_exp2f(s[k][0] - ref) : 0.0f;
-                sum.l = __builtin_fmaf(s[k][1], fk, sum.l);
-#pragma unroll
-                for (int d = 0; d < ET; ++d) sum.o[d] = __builtin_fmaf(v[k][d / 2][d % 2], fk, sum.o[d]);
-            }
-        }
-        __syncthreads();  // the sums of the rows before are read
-        if (lane % 8 == 0) {
-            s_ref[wave][r] = sum.ref;
-            s_l[wave][r] = sum.l;
-        }
-        __syncthreads();
-        float ref = s_ref[0][r];
-#pragma unroll
-        for (int v = 1; v < WAVES; ++v) ref = fmaxf(ref, s_ref[v][r]);
-        const float f = __builtin_amdgcn_exp2f(sum.ref - ref);
-#pragma unroll
-        for (int d = 0; d < ET; d += 4) {
-            const f32x4 v = {sum.o[d] * f, sum.o[d + 1] * f, sum.o[d + 2] * f, sum.o[d + 3] * f};
-            *reinterpret_cast<f32x4*>(&s_o[wave][r][e0 + d]) = v;
-        }
-        __syncthreads();
-        if (r16 < 8 && r0 + r16 < rows)
-            attend_result<PT, F16>(a, add_waves<DP, PT, WAVES>(s_o, s_ref, s_l, 0, r16, part), pc.b, h,
-                                   first + r0 + r16, part, s_live[r0 + r16] != 0);
+        for (int j = 0; j < 4; ++j)
+            if (!x.ok || g * 4 + j >= x.there) x.v[j] = {};
     }
+#pragma unroll
+    for (int st = 0; st < DP / 32; ++st) {
+        const uint32_t w0 = x.k[st / 2][st % 2 * 2], w1 = x.k[st / 2][st % 2 * 2 + 1];
+        t.k[wave][st][lane] = u32x4{widen<F16>(w0, false), widen<F16>(w0, true), widen<F16>(w1, false),
+                                    widen<F16>(w1, true)};
+    }
+#pragma unroll
+    for (int c = 0; c < DP / 64; ++c) {
+        uint32_t lo[4], hi[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            lo[j] = widen<true>(word_of<DP>(x.v[j], c), false);
+            hi[j] = widen<true>(word_of<DP>(x.v[j], c), true);
+        }
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            u32x2 v;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t u0 = d < 2 ? lo[2 * j] : hi[2 * j], u1 = d < 2 ? lo[2 * j + 1] : hi[2 * j + 1];
+                v[j] = __builtin_amdgcn_perm(u1, u0, d % 2 ? 0x07060302u : 0x05040100u);
+            }
+            reinterpret_cast<u32x2*>(&t.v[wave / 2][c * 4 + d][lane])[wave % 2] = v;
+        }
+    }
+    if (lane == 0) {
+        const uint32_t v = clamp_scale(x.vs);
+        t.x[wave] = f32x4{as<float>(clamp_scale(x.ks) << 23) * a.scale_log2,
+                          x.ok ? (float)((int)v - 127) : -INFINITY, as<float>((254u - v) << 23), 0.0f};
+    }
+}
+
+template <int DP, int MT, bool F16>
+__global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attend_rows(Kv8Attend a) {
+    constexpr int WAVES = 4;
+    constexpr int DT = DP / 16;
+    constexpr int ROWS = WAVES * MT * 16;
+    constexpr int SLOT = attend_slot(DP, ROWS);
+    union Shared {
+        AttendTile<DP> t[2];
+        float o[WAVES][16][DP + 4];
+    };
+    __shared__ Shared sh;
+    __shared__ int s_live[ROWS];
+    const int tid = threadIdx.x;
+    const int lane = tid & (WAVE - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
+    const int g = lane >> 4, col = lane & 15;
+    const int items = a.s.B + a.pieces;
+    const int item = blockIdx.x % items;
+    const int y = blockIdx.x / items;
+    const int h = y / a.blocks;
+    const int first = (y - h * a.blocks) * ROWS;  // row of this block
+    const int rows = min(a.s.N * a.group - first, ROWS);
+    AttendPiece pc = attend_piece<AT_TILE>(a, item);
+    pc.b = __builtin_amdgcn_readfirstlane(pc.b);
+    pc.c = __builtin_amdgcn_readfirstlane(pc.c);
+    pc.n = __builtin_amdgcn_readfirstlane(pc.n);
+    pc.units = __builtin_amdgcn_readfirstlane(pc.units);
+    if (pc.b < 0) return;
+    const AttendRow row = attend_row(a, pc.b);
+
+    const int mine = first + wave * MT * 16;                       // rows of this wave
+    const int count = min(max(rows - wave * MT * 16, 0), MT * 16);
+    unsigned long long above = 0, rooted = 0;
+    if (a.s.parents) {
+        above = tree_node(a.s.parents + (int64_t)pc.b * a.s.N, a.s.N).above;
+        rooted = __ballot(above != 0);
+    }
+    AttendState<DP, MT> w;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        const int r = mine + min(m * 16 + col, max(count, 1) - 1);
+        const int rc = min(r, first + rows - 1);
+        const int n = rc / a.group;
+        w.l[m] = 0.0f;
+        w.ref[m] = AT_NONE;
+        if (g == 0)
+            s_live[wave * MT * 16 + m * 16 + col] = n < row.count && (!a.s.parents || (rooted >> (n & 63) & 1));
+        const uint16_t* q = a.q.data + pc.b * a.q.row + n * a.q.token +
+                            (h * a.group + rc - n * a.group) * a.q.head + g * 16;
+#pragma unroll
+        for (int st = 0; st < DP / 32; ++st) {
+            w.q[m][st] = u32x4{0, 0, 0, 0};
+            if (st / 2 * 64 + g * 16 < a.g.dim)
+                w.q[m][st] = *reinterpret_cast<const u32x4*>(q + st / 2 * 64 + st % 2 * 8);
+        }
+#pragma unroll
+        for (int d = 0; d < DT; ++d) w.o[m][d] = f32x4{0, 0, 0, 0};
+    }
+
+    // tiles of this piece that some row sees, and what this wave's rows see of them
+    int see = row.end, see_all = row.end;
+    int full = min(row.base, row.end);
+    if (!a.s.parents && row.count) {
+        see_all = (int)min((int64_t)row.end, (int64_t)row.base + (first + rows - 1) / a.group + 1);
+        see = (int)min((int64_t)row.end, (int64_t)row.base + (mine + count - 1) / a.group + 1);
+        full = (int)min((int64_t)row.end, (int64_t)row.base + mine / a.group + 1);
+    }
+    if (!count) see = 0;
+    const int tiles = (int)(((int64_t)see_all + AT_TILE - 1) / AT_TILE);
+    const int t0 = (int)min((int64_t)pc.c * pc.units, (int64_t)tiles);
+    const int t1 = (int)min((int64_t)(pc.c + 1) * pc.units, (int64_t)tiles);
+    if (t0 < t1) {
+        AttendWalk at;
+        at.table = (const_i32)(a.s.t.tables + (int64_t)pc.b * a.s.t.stride);
+        at.tiles = a.g.page_size / 16;
+        at.over = 4 / at.tiles;
+        at.ahead = 4 - at.over * at.tiles;
+        at.block = (t0 * 4 + wave) / at.tiles;
+        at.inner = t0 * 4 + wave - at.block * at.tiles;
+        at.left = row.end - (t0 * AT_TILE + wave * 16);
+        uint32_t k_at[DP / 64], v_at[4];
+#pragma unroll
+        for (int c = 0; c < DP / 64; ++c)
+            k_at[c] = (uint32_t)col * (uint32_t)a.g.slot + (c * 64 + g * 16 < a.g.dim ? c * 64 + g * 16 : 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v_at[j] = (uint32_t)(g * 4 + j) * (uint32_t)a.g.slot + (col * DT < a.g.dim ? col * DT : 0);
+        AttendRaw<DP> raw;
+        load_raw<DP>(a, at, h, k_at, v_at, raw);
+        leave_raw<DP, F16>(a, raw, wave, sh.t[0]);
+        load_raw<DP>(a, at, h, k_at, v_at, raw);
+        for (int i = t0; i < t1; ++i) {
+            const AttendTile<DP>& t = sh.t[(i - t0) & 1];
+            __syncthreads();
+            if (i + 1 < t1) {
+                leave_raw<DP, F16>(a, raw, wave, sh.t[(i - t0 + 1) & 1]);
+                load_raw<DP>(a, at, h, k_at, v_at, raw);
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int s0 = i * AT_TILE + half * AT_STEP;
+                if (s0 >= see) continue;
+                f32x4 e[2][MT];
+                u32x4 p[MT];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) e[k][m] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                    for (int st = 0; st < DP / 32; ++st) {
+                        const u32x4 f = t.k[half * 2 + k][st][lane];
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) e[k][m] = mfma<F16>(f, w.q[m][st], e[k][m]);
+                    }
+                }
+                const f32x4 x0 = t.x[half * 2], x1 = t.x[half * 2 + 1];
+                const AttendScales x = {{x0[0], x1[0]}, {x0[1], x1[1]}, {x0[2], x1[2]}};
+                const bool masked = s0 + AT_STEP > full;
+                uint32_t vis[MT] = {};
+                if (masked)
+                    attend_mask<MT>(a, above, mine, max(count, 1), s0 - row.base + g * 4, row.end - row.base, e, vis);
+                attend_weights<DP, MT>(x, e, w, p);
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    u32x4 v = t.v[half][d][lane];
+                    if (masked) {
+                        f32x4* o[MT];
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) o[m] = &w.o[m][d];
+                        v = take_nans<MT>(v, vis, o);
+                    }
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) w.o[m][d] = mfma<true>(v, p[m], w.o[m][d]);
+                }
+            }
+        }
+    }
+
+    float* slot = a.part + (int64_t)blockIdx.x * SLOT;
+    if (pc.n > 1) __syncthreads();  // the tiles are read; what pieces leave goes through LDS, in whole lines
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        w.l[m] += xor_lane_f<16>(w.l[m]);
+        w.l[m] += xor_lane_f<32>(w.l[m]);
+        const int r0 = wave * MT * 16 + m * 16, rr = r0 + col;
+        if (pc.n > 1) {
+            if (g == 0 && rr < rows) put(slot + rr * 2, w.ref[m], w.l[m]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int d = 0; d < DT; d += 4)
+                    *reinterpret_cast<f32x4*>(&sh.o[wave][col][(g * 4 + k) * DT + d]) =
+                        f32x4{w.o[m][d][k], w.o[m][d + 1][k], w.o[m][d + 2][k], w.o[m][d + 3][k]};
+            __builtin_amdgcn_wave_barrier();  // a wave's own part: its LDS operations stay in order
+#pragma unroll
+            for (int k = 0; k < DP / 8; ++k) {
+                const int r = (k * WAVE + lane) * 2 / DP, e = (k * WAVE + lane) * 2 % DP;
+                const f32x2 o = *reinterpret_cast<const f32x2*>(&sh.o[wave][r][e]);
+                if (r0 + r < rows) put(slot + 2 * ROWS + (r0 + r) * DP + e, o[0], o[1]);
+            }
+            __builtin_amdgcn_wave_barrier();
+        } else if (rr < rows) {  // a lane has 4 * DT neighbouring entries of a row
+            const bool live = s_live[rr] != 0;
+            const float f = attend_factor(w.l[m], live);
+            const AttendOut out = attend_out(a, pc.b, h, first + rr);
+            if (a.lse && g == 0) a.lse[out.lse] = attend_lse(w.ref[m], w.l[m], live);
+#pragma unroll
+            for (int e = 0; e < 4 * DT; e += 8) {
+                if (g * 4 * DT + e >= a.g.dim) break;
+                u32x4 v;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int x = e + 2 * k;
+                    v[k] = live ? narrow<F16>(w.o[m][x % DT][x / DT] * f, w.o[m][x % DT + 1][x / DT] * f) : 0u;
+                }
+                *reinterpret_cast<u32x4*>(out.to + g * 4 * DT + e) = v;
+            }
+        }
+    }
+    if (pc.n > 1)
+        add_pieces<DP, ROWS, F16, WAVES>(a, pc.b, pc.c, pc.n, y, h, first, rows, &sh.o[0][0][0], s_live);
 }
 
 // How many rows a workgroup takes, and into how many pieces rows are cut.
@@ -789,9 +1111,29 @@ static hipError_t launch_attend(Kv8Attend a, hipStream_t st) {
     return hipGetLastError();
 }
 
+template <int DP, int MT, bool F16>
+static hipError_t launch_shared(Kv8Attend a, hipStream_t st) {
+    constexpr int ROWS = 64 * MT;
+    constexpr int64_t SLOT = attend_slot(DP, ROWS);
+    a.blocks = (int)(((int64_t)a.s.N * a.group + ROWS - 1) / ROWS);
+    const int64_t y = (int64_t)a.g.heads * a.blocks;
+    const int64_t most = KV8_PART_FLOATS / SLOT < KV8_SPLITS ? KV8_PART_FLOATS / SLOT : KV8_SPLITS;
+    static const int target = getenv("AT_TARGET2") ? atoi(getenv("AT_TARGET2")) : 512;
+    a.pieces = y * a.s.B <= most / 2 ? (int)((most / 2 < target ? most / 2 : target) / y) : 0;
+    const int64_t grid = y * (a.s.B + a.pieces);
+    if (grid > INT_MAX) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((k_attend_rows<DP, MT, F16>), dim3((unsigned)grid), dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
 template <int DP, bool F16>
 static hipError_t launch_attend_rows(const Kv8Attend& a, hipStream_t st) {
     const int64_t rows = (int64_t)a.s.N * a.group;
+    static const int sh = getenv("AT_SHARED") ? atoi(getenv("AT_SHARED")) : 1;
+    if (sh && rows > 32) {
+        if (rows <= 64 || DP == 256 || sh == 2) return launch_shared<DP, 1, F16>(a, st);
+        return launch_shared<DP, DP == 256 ? 1 : 2, F16>(a, st);
+    }
     if (rows <= 16) return launch_attend<DP, 1, F16, 4>(a, st);
     if (rows <= 32 || DP == 256) return launch_attend<DP, 2, F16, 4>(a, st);
     return launch_attend<DP, DP == 256 ? 2 : 4, F16, 4>(a, st);
