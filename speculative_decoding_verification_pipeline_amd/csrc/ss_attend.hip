@@ -35,7 +35,8 @@ namespace ss {
 
 constexpr int AT_STEP = 32;                   // slots of a wave's step
 constexpr float AT_NONE = -3.0e38f;           // reference of a row that has seen nothing
-constexpr float AT_SET = 8.0f, AT_MOST = 15.0f;
+constexpr float AT_SET = 8.0f;                // a reference is set so far below the largest exponent
+constexpr float AT_MOST = 32768.0f;           // and moves when a lane's four weights sum up to more
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -290,15 +291,16 @@ __device__ __forceinline__ void attend_scores(const AttendKeys<DP>& x, const Att
     }
 }
 
-// What two tiles' scales come to: the factor on S with the softmax's scale, the exponent that
+// What tiles' scales come to: the factor on S with the softmax's scale, the exponent that
 // a value's scale adds to its weight, and the factor that takes it off again.
+template <int NT>
 struct AttendScales {
-    float fk[2], xv[2], inv[2];
+    float fk[NT], xv[NT], inv[NT];
 };
 
-__device__ __forceinline__ AttendScales scales_of(const Kv8Attend& a, const uint32_t (&ks)[2],
+__device__ __forceinline__ AttendScales<2> scales_of(const Kv8Attend& a, const uint32_t (&ks)[2],
                                                   const uint32_t (&vs)[2], const bool (&ok)[2]) {
-    AttendScales x;
+    AttendScales<2> x;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         const uint32_t v = clamp_scale(vs[t]);
@@ -309,51 +311,58 @@ __device__ __forceinline__ AttendScales scales_of(const Kv8Attend& a, const uint
     return x;
 }
 
-// Weights of one step, under the rows' references, which may grow.
-template <int DP, int MT>
-__device__ __forceinline__ void attend_weights(const AttendScales& x, const f32x4 (&s)[2][MT],
-                                               AttendState<DP, MT>& w, u32x4 (&p)[MT]) {
-    float top[MT];
-    bool grows = false;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        top[m] = -INFINITY;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const float most = fmaxf(fmaxf(s[t][m][0], s[t][m][1]), fmaxf(s[t][m][2], s[t][m][3]));
-            top[m] = fmaxf(top[m], __builtin_fmaf(most, x.fk[t], x.xv[t]));
-        }
-        grows |= top[m] > w.ref[m] + AT_MOST;
-    }
-    if (__any(grows)) {
+// Weights of NT tiles under the rows' references. A lane's sums, which the rows need anyway,
+// tell whether a weight has passed 2^15; a row's reference then moves to its largest exponent
+// less 8, and the weights are formed again. (Looking for the largest exponent at every step
+// took a third of the vector instructions.)
+template <int DP, int MT, int NT>
+__device__ __forceinline__ void attend_weights(const AttendScales<NT>& x, const f32x4 (&s)[NT][MT],
+                                               AttendState<DP, MT>& w, u32x4 (&p)[NT / 2][MT]) {
+    float sum[NT][MT];
+    auto form = [&] {
+        float most = 0.0f;
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            top[m] = fmaxf(top[m], xor_lane_f<16>(top[m]));
-            top[m] = fmaxf(top[m], xor_lane_f<32>(top[m]));
-            if (top[m] > w.ref[m] + AT_MOST) {
-                const float to = top[m] - AT_SET;
-                const float f = __builtin_amdgcn_exp2f(w.ref[m] - to);
-                w.ref[m] = to;
-                w.l[m] *= f;
 #pragma unroll
-                for (int d = 0; d < DP / 16; ++d) w.o[m][d] *= f;
+            for (int t = 0; t < NT; ++t) {
+                const float c = x.xv[t] - w.ref[m];
+                float e[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][m][i], x.fk[t], c));
+                sum[t][m] = (e[0] + e[1]) + (e[2] + e[3]);
+                most = fmaxf(most, sum[t][m]);
+                p[t / 2][m][t % 2 * 2] = as<uint32_t>(__builtin_convertvector((f32x2{e[0], e[1]}), h16x2));
+                p[t / 2][m][t % 2 * 2 + 1] = as<uint32_t>(__builtin_convertvector((f32x2{e[2], e[3]}), h16x2));
             }
         }
-    }
+        return most;
+    };
+    if (__any(form() > AT_MOST)) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+        for (int m = 0; m < MT; ++m) {
+            float top = -INFINITY;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const float c = x.xv[t] - w.ref[m];
-            float e[4];
+            for (int t = 0; t < NT; ++t) {
+                const float most = fmaxf(fmaxf(s[t][m][0], s[t][m][1]), fmaxf(s[t][m][2], s[t][m][3]));
+                top = fmaxf(top, __builtin_fmaf(most, x.fk[t], x.xv[t]));
+            }
+            top = fmaxf(top, xor_lane_f<16>(top));
+            top = fmaxf(top, xor_lane_f<32>(top)) - AT_SET;
+            // rows below their reference keep it, bit by bit
+            const float to = fmaxf(w.ref[m], top);
+            const float f = __builtin_amdgcn_exp2f(w.ref[m] - to);
+            w.ref[m] = to;
+            w.l[m] *= f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][m][i], x.fk[t], c));
-            w.l[m] = __builtin_fmaf((e[0] + e[1]) + (e[2] + e[3]), x.inv[t], w.l[m]);
-            p[m][2 * t] = as<uint32_t>(__builtin_convertvector((f32x2{e[0], e[1]}), h16x2));
-            p[m][2 * t + 1] = as<uint32_t>(__builtin_convertvector((f32x2{e[2], e[3]}), h16x2));
+            for (int d = 0; d < DP / 16; ++d) w.o[m][d] *= f;
         }
+        form();
     }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) w.l[m] = __builtin_fmaf(sum[t][m], x.inv[t], w.l[m]);
 }
 
 // A NaN among the values of one dimension reaches the rows that see it and no others: it is
@@ -422,42 +431,112 @@ __device__ __forceinline__ void attend_values(const AttendValues<DP>& x, const u
     }
 }
 
-// Where workgroup `item` of a head and block of rows works: row b, piece c of its n. Rows
-// are cut into pieces of equal size, about as many over all rows as a.pieces; every wave
-// finds its own by itself.
+// Which work a workgroup takes. All requests' slots that a head of the cache and a block of
+// rows see, in units of UNIT, are one line, and a.shares workgroups take equal shares of it: the end of one request's slots, whole requests, the start
+// of the next one's. So all are done at the same time, however uneven the contexts, and as many
+// requests are cut as there are shares. With a.shares = 0 there are requests enough, and each is
+// a workgroup's.
+//
+// Neighbouring workgroups, which run on different XCDs, take different heads of one share: they
+// read the same pages at about the same time, and with eight heads an XCD's cache holds the
+// pages of one. Later blocks of rows, which see more, come first.
 struct AttendPiece {
-    int b, c, n, units;  // units of UNIT slots of a piece
+    int h, first;         // head of the cache, first row
+    int line, p;          // of heads and blocks of rows, and the share of it
+    uint32_t share;       // its units
+    uint32_t at, end;     // those of the line that it takes, from the present request on
+    int b;                // the request
+    uint32_t before, of;  // units of the requests before it, and its own
+    int from, to;         // units of it that this share takes
+    int c, n;             // the c-th of the n shares that it lies in
 };
 
+__device__ __forceinline__ int attend_see(const Kv8Attend& a, const AttendRow& row, int last) {
+    if (a.s.parents || !row.count) return row.end;
+    return (int)min((int64_t)row.end, (int64_t)row.base + last + 1);
+}
+
+// Units of UNIT slots that rows up to token `last` of a request see; one where they see none.
 template <int UNIT>
-__device__ __forceinline__ AttendPiece attend_piece(const Kv8Attend& a, int item) {
-    if (a.pieces == 0) return {item, 0, 1, INT_MAX / UNIT};
+__device__ __forceinline__ uint32_t attend_units(const Kv8Attend& a, int b, int last) {
+    return max(((uint32_t)attend_see(a, attend_row(a, b), last) + UNIT - 1) / UNIT, 1u);
+}
+
+__device__ __forceinline__ void attend_part(AttendPiece& x) {
+    x.from = (int)(x.at - x.before);
+    x.to = (int)min(x.end - x.before, x.of);
+    const uint32_t first = x.before / x.share;
+    x.n = (int)((x.before + x.of - 1) / x.share - first) + 1;
+    x.c = x.p - (int)first;
+}
+
+template <int ROWS>
+__device__ __forceinline__ int attend_last(const Kv8Attend& a, int first) {
+    return (min(a.s.N * a.group, first + ROWS) - 1) / a.group;
+}
+
+// False: nothing is left for this workgroup.
+template <int UNIT, int ROWS>
+__device__ __forceinline__ bool attend_share(const Kv8Attend& a, AttendPiece& x) {
     const int lane = threadIdx.x & (WAVE - 1);
-    int total = 0;
-    for (int b0 = 0; b0 < a.s.B; b0 += WAVE) {
-        const int b = b0 + lane;
-        if (b < a.s.B) total += max(1, (int)(((int64_t)attend_row(a, b).end + UNIT - 1) / UNIT));
+    const int lines = a.g.heads * a.blocks;
+    x.p = blockIdx.x / lines;
+    x.line = blockIdx.x - x.p * lines;
+    const int block = x.line / a.g.heads;
+    x.h = x.line - block * a.g.heads;
+    x.first = (a.blocks - 1 - block) * ROWS;
+    x.c = x.from = 0;
+    x.n = 1;
+    x.at = x.before = 0;
+    if (a.shares == 0) {
+        x.b = x.p;
+        x.to = INT_MAX / UNIT;
+        x.of = x.end = x.share = 1;
+        return true;
     }
-    total = wave_sum_i(total);
-    const int units = (total + a.pieces - 1) / a.pieces;
-    int before = 0;
-    for (int b0 = 0; b0 < a.s.B; b0 += WAVE) {
-        const int b = b0 + lane;
-        int n = 0;
-        if (b < a.s.B) {
-            const int u = max(1, (int)(((int64_t)attend_row(a, b).end + UNIT - 1) / UNIT));
-            n = (u + units - 1) / units;
-        }
-        const int to = before + wave_incl_scan_i(n);
-        const unsigned long long m = __ballot(item < to);
+    const int last = attend_last<ROWS>(a, x.first);
+    // 32 bits hold the units of all: the host has seen to it
+    uint32_t total = 0;
+    for (int b0 = 0; b0 < a.s.B; b0 += WAVE)
+        if (b0 + lane < a.s.B) total += attend_units<UNIT>(a, b0 + lane, last);
+    total = (uint32_t)__builtin_amdgcn_readfirstlane(wave_sum_i((int)total));
+    x.share = max((total + a.shares - 1) / a.shares, (uint32_t)a.least);
+    x.at = x.p * x.share;
+    if (x.at >= total) return false;
+    x.end = min(x.at + x.share, total);
+    for (int b0 = 0;; b0 += WAVE) {
+        const uint32_t u = b0 + lane < a.s.B ? attend_units<UNIT>(a, b0 + lane, last) : 0;
+        const uint32_t to = x.before + (uint32_t)wave_incl_scan_i((int)u);
+        const unsigned long long m = __ballot(x.at < to);
         if (m) {
             const int l = __builtin_ctzll(m);
-            const int nl = __shfl(n, l);
-            return {b0 + l, item - (__shfl(to, l) - nl), nl, units};
+            x.b = __builtin_amdgcn_readfirstlane(b0 + l);
+            x.of = (uint32_t)__builtin_amdgcn_readlane((int)u, l);
+            x.before = (uint32_t)__builtin_amdgcn_readlane((int)to, l) - x.of;
+            attend_part(x);
+            return true;
         }
-        before = __shfl(to, WAVE - 1);
+        x.before = (uint32_t)__builtin_amdgcn_readlane((int)to, WAVE - 1);
     }
-    return {-1, 0, 0, 0};
+}
+
+// On to the next request of the share; false: it ends.
+template <int UNIT, int ROWS>
+__device__ __forceinline__ bool attend_on(const Kv8Attend& a, AttendPiece& x) {
+    x.at = x.before + x.of;
+    if (x.at >= x.end) return false;
+    x.before = x.at;
+    ++x.b;
+    x.of = (uint32_t)__builtin_amdgcn_readfirstlane(
+        (int)attend_units<UNIT>(a, x.b, attend_last<ROWS>(a, x.first)));
+    attend_part(x);
+    return true;
+}
+
+// Where a line's share p leaves the sums of the request that it ends with (which = 1), or of the
+// one that began before it (0).
+__device__ __forceinline__ int attend_left(const Kv8Attend& a, const AttendPiece& x, int p, int which) {
+    return (x.line * a.shares + p) * 2 + which;
 }
 
 // Values that other workgroups, on other XCDs, wrote in this launch or will read in it.
@@ -510,11 +589,13 @@ constexpr int attend_slot(int dp, int rows) { return rows * (dp + 2); }
 // their order, eight rows a wave at a time, a lane two neighbouring entries of each 128: whole
 // lines a load, four pieces on their way at once. Of few rows the pieces are dealt out to the
 // waves, which meet in LDS.
-template <int DP, int ROWS, bool F16, int WAVES>
-__device__ __forceinline__ void add_pieces(const Kv8Attend& a, int b, int c, int n, int y, int h, int first,
-                                           int rows, float* s_mem, const int* s_live) {
+template <int DP, int ROWS, bool F16>
+__device__ __forceinline__ void add_pieces(const Kv8Attend& a, const AttendPiece& pc, int rows, float* s_mem,
+                                           const int* s_live) {
+    constexpr int WAVES = 4;
     constexpr int PAIRS = 8 * DP / 128;  // of a lane's, over eight rows
     constexpr int ONCE = PAIRS >= 16 ? 2 : 4;
+    const int b = pc.b, n = pc.n, h = pc.h, first = pc.first;
     const int tid = threadIdx.x;
     const int lane = tid & (WAVE - 1);
     const int wave = tid / WAVE;
@@ -523,14 +604,16 @@ __device__ __forceinline__ void add_pieces(const Kv8Attend& a, int b, int c, int
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (tid == 0) {
-        int32_t* arrived = a.arrived + ((int64_t)y * a.s.B + b) * KV8_COUNTER;
+        // a share begins one request at most that others go on with: its counter is the share's
+        int32_t* arrived = a.arrived + (int64_t)(pc.line * a.shares + pc.p - pc.c) * KV8_COUNTER;
         s_last = __hip_atomic_fetch_add(arrived, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == n - 1;
         if (s_last) __hip_atomic_store(arrived, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     __syncthreads();
     if (!s_last) return;
-    // pieces of a row follow each other
-    const float* all = a.part + (int64_t)(blockIdx.x - c) * attend_slot(DP, ROWS);
+    auto left = [&](int i) {  // what the i-th piece has left
+        return a.part + (int64_t)attend_left(a, pc, pc.p - pc.c + i, i == 0) * attend_slot(DP, ROWS);
+    };
     const int groups = (rows + 7) / 8;
     const int share = groups == 1 ? WAVES : groups == 2 ? WAVES / 2 : 1;  // waves of a group
     const int sub = wave % share;
@@ -545,7 +628,7 @@ __device__ __forceinline__ void add_pieces(const Kv8Attend& a, int b, int c, int
             f32x2 s[ONCE], v[ONCE][PAIRS];
 #pragma unroll
             for (int i = 0; i < ONCE; ++i) {
-                const float* p = all + (int64_t)min(c0 + i * share, n - 1) * attend_slot(DP, ROWS);
+                const float* p = left(min(c0 + i * share, n - 1));
                 s[i] = get(p + mine * 2);
 #pragma unroll
                 for (int k = 0; k < PAIRS; ++k) v[i][k] = get(p + 2 * ROWS + r0 * DP + (k * WAVE + lane) * 2);
@@ -617,29 +700,44 @@ __device__ __forceinline__ void add_pieces(const Kv8Attend& a, int b, int c, int
     }
 }
 
-template <int DP, int MT, bool F16, int WAVES>
-__global__ __launch_bounds__(WAVES* WAVE, DP == 256 || MT == 4 ? 1 : MT == 2 ? 2 : DP == 128 ? 3 : 4) void k_attend(Kv8Attend a) {
+// For a loop over requests: what does not change from one to the next (addresses, sizes, lanes'
+// places) is formed again for each, as if it did. Kept instead, it took 40 vector registers and
+// a hundred spilled scalar ones.
+struct ArgsAgain {
+    const __attribute__((address_space(4))) Kv8Attend* p;
+    int tid;
+    __device__ __forceinline__ ArgsAgain()
+        : p((const __attribute__((address_space(4))) Kv8Attend*)__builtin_amdgcn_kernarg_segment_ptr()),
+          tid(threadIdx.x) {}
+    __device__ __forceinline__ const Kv8Attend& args() {
+        asm volatile("" : "+s"(p));
+        asm volatile("" : "+v"(tid));
+        return *(const Kv8Attend*)p;
+    }
+    __device__ __forceinline__ int thread() const { return tid; }
+};
+
+// Few rows: the four waves take a share's slots each a run of them, and meet in LDS.
+template <int DP, int MT, bool F16>
+__global__ __launch_bounds__(256, DP == 256 ? 1 : MT == 2 || DP == 128 ? 2 : 3) void k_attend(Kv8Attend args) {
+    constexpr int WAVES = 4;
     constexpr int DT = DP / 16;
     constexpr int SLOT = attend_slot(DP, MT * 16);
+    constexpr int UNIT = AT_STEP * WAVES;
     __shared__ float s_o[WAVES][16][DP + 4];
     __shared__ float s_ref[WAVES][MT * 16], s_l[WAVES][MT * 16];
     __shared__ int s_live[MT * 16];
-    const int tid = threadIdx.x;
-    const int lane = tid & (WAVE - 1);
+    AttendPiece pc;
+    if (!attend_share<UNIT, MT * 16>(args, pc)) return;
+    ArgsAgain again;
+    do {
+    const Kv8Attend& a = again.args();
+    const int lane = again.thread() & (WAVE - 1);
+    const int tid = again.thread();
     const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
     const int g = lane >> 4, col = lane & 15;
-    const int items = a.s.B + a.pieces;
-    const int item = blockIdx.x % items;
-    const int y = blockIdx.x / items;
-    const int h = y / a.blocks;
-    const int first = (y - h * a.blocks) * (MT * 16);  // row of this block
+    const int h = pc.h, first = pc.first;
     const int rows = min(a.s.N * a.group - first, MT * 16);
-    AttendPiece pc = attend_piece<AT_STEP * WAVES>(a, item);
-    pc.b = __builtin_amdgcn_readfirstlane(pc.b);
-    pc.c = __builtin_amdgcn_readfirstlane(pc.c);
-    pc.n = __builtin_amdgcn_readfirstlane(pc.n);
-    pc.units = __builtin_amdgcn_readfirstlane(pc.units);
-    if (pc.b < 0) return;
     const AttendRow row = attend_row(a, pc.b);
 
     AttendState<DP, MT> w;
@@ -669,15 +767,12 @@ __global__ __launch_bounds__(WAVES* WAVE, DP == 256 || MT == 4 ? 1 : MT == 2 ? 2
     }
 
     // the slots of this piece, and of this wave of it, in steps
-    int see = row.end;
+    const int see = attend_see(a, row, (first + rows - 1) / a.group);
     int full = min(row.base, row.end);  // slots before it all rows see
-    if (!a.s.parents && row.count) {
-        see = (int)min((int64_t)see, (int64_t)row.base + (first + rows - 1) / a.group + 1);
-        full = (int)min((int64_t)row.end, (int64_t)row.base + first / a.group + 1);
-    }
+    if (!a.s.parents && row.count) full = (int)min((int64_t)row.end, (int64_t)row.base + first / a.group + 1);
     const int steps = (int)(((int64_t)see + AT_STEP - 1) / AT_STEP);
-    const int s0 = (int)min((int64_t)pc.c * pc.units * WAVES, (int64_t)steps);
-    const int s1 = (int)min((int64_t)(pc.c + 1) * pc.units * WAVES, (int64_t)steps);
+    const int s0 = (int)min((int64_t)pc.from * WAVES, (int64_t)steps);
+    const int s1 = (int)min((int64_t)pc.to * WAVES, (int64_t)steps);
     const int per = (s1 - s0 + WAVES - 1) / WAVES;
     const int from = min(s0 + wave * per, s1), to = min(from + per, s1);
     const int plain = max(min(to, full / AT_STEP), from);  // steps before it need no mask
@@ -698,13 +793,14 @@ __global__ __launch_bounds__(WAVES* WAVE, DP == 256 || MT == 4 ? 1 : MT == 2 ? 2
         AttendKeys<DP> k;
         AttendValues<DP> v;
         f32x4 e[2][MT];
-        u32x4 p[MT];
+        u32x4 p[1][MT];
         const uint32_t none[MT] = {};
         attend_look(at);
         AttendPlace place = attend_next(a, at, h);
         load_keys<DP>(a, place, k_at, k);
         // keys of the next step are on their way while this one's weights and values are
-        // worked on, values while its scores are
+        // worked on, values while its scores are (a step's values loaded a step ahead as well,
+        // into registers of their own: 1 to 3 % slower)
         for (int s = from; s < plain; ++s) {
             load_values<DP>(a, place, v_at, v);
             if (!(k.ok[0] && k.ok[1])) put_out<DP>(k, v);
@@ -713,8 +809,8 @@ __global__ __launch_bounds__(WAVES* WAVE, DP == 256 || MT == 4 ? 1 : MT == 2 ? 2
             const bool ok[2] = {k.ok[0], k.ok[1]};
             place = attend_next(a, at, h);  // behind the last step: page 0
             load_keys<DP>(a, place, k_at, k);
-            attend_weights<DP, MT>(scales_of(a, ks, v.s, ok), e, w, p);
-            attend_values<DP, MT, false>(v, p, none, w);
+            attend_weights<DP, MT, 2>(scales_of(a, ks, v.s, ok), e, w, p);
+            attend_values<DP, MT, false>(v, p[0], none, w);
         }
         unsigned long long above = 0;
         if (a.s.parents && plain < to)
@@ -741,8 +837,8 @@ __global__ __launch_bounds__(WAVES* WAVE, DP == 256 || MT == 4 ? 1 : MT == 2 ? 2
                 for (int c = 0; c < DP / 64; ++c)
                     set_word<DP>(v.v[j], c, keep_if(there, j, word_of<DP>(v.v[j], c), 0u));
             }
-            attend_weights<DP, MT>(scales_of(a, k.s, v.s, k.ok), e, w, p);
-            attend_values<DP, MT, true>(v, p, vis, w);
+            attend_weights<DP, MT, 2>(scales_of(a, k.s, v.s, k.ok), e, w, p);
+            attend_values<DP, MT, true>(v, p[0], vis, w);
         }
     }
 
@@ -759,7 +855,7 @@ __global__ __launch_bounds__(WAVES* WAVE, DP == 256 || MT == 4 ? 1 : MT == 2 ? 2
     // a thread adds pairs of entries of a row, neighbours' pairs side by side
     constexpr int PER_ROW = WAVES * 4;
     const int r16 = tid / PER_ROW, part = tid % PER_ROW;
-    float* slot = a.part + (int64_t)blockIdx.x * SLOT;
+    float* slot = a.part + (int64_t)attend_left(a, pc, pc.p, pc.c == 0) * SLOT;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
         __syncthreads();
@@ -802,8 +898,9 @@ __global__ __launch_bounds__(WAVES* WAVE, DP == 256 || MT == 4 ? 1 : MT == 2 ? 2
             else if (e < a.g.dim) put_pair<F16>(out.to + e, o[0], o[1], to, live);
         }
     }
-    if (pc.n > 1)
-        add_pieces<DP, MT * 16, F16, WAVES>(a, pc.b, pc.c, pc.n, y, h, first, rows, &s_o[0][0][0], s_live);
+    if (pc.n > 1) add_pieces<DP, MT * 16, F16>(a, pc, rows, &s_o[0][0][0], s_live);
+    __syncthreads();  // LDS is read
+    } while (attend_on<UNIT, MT * 16>(args, pc));
 }
 
 // ---------------------------------------------------------------------------
@@ -912,8 +1009,53 @@ __device__ __forceinline__ void leave_raw(const Kv8Attend& a, AttendRaw<DP>& x, 
     }
 }
 
+// NT tiles of 16 slots of the tile in LDS: all four, or two that need a mask, the half-th. rel
+// and end as attend_mask has them, for the wave's rows from `first` on.
+template <int DP, int MT, bool F16, int NT, bool MASK>
+__device__ __forceinline__ void attend_tile(const Kv8Attend& a, const AttendTile<DP>& t, int half, int rel,
+                                            int end, unsigned long long above, int first, int rows,
+                                            AttendState<DP, MT>& w) {
+    const int lane = threadIdx.x & (WAVE - 1);
+    f32x4 e[NT][MT];
+    u32x4 p[NT / 2][MT];
+    AttendScales<NT> x;
+#pragma unroll
+    for (int k = 0; k < NT; ++k) {
+        const f32x4 v = t.x[half * 2 + k];
+        x.fk[k] = v[0];
+        x.xv[k] = v[1];
+        x.inv[k] = v[2];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) e[k][m] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int st = 0; st < DP / 32; ++st) {
+            const u32x4 f = t.k[half * 2 + k][st][lane];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) e[k][m] = mfma<F16>(f, w.q[m][st], e[k][m]);
+        }
+    }
+    uint32_t vis[MT] = {};
+    if constexpr (MASK) attend_mask<MT>(a, above, first, rows, rel, end, e, vis);
+    attend_weights<DP, MT, NT>(x, e, w, p);
+#pragma unroll
+    for (int k = 0; k < NT / 2; ++k) {
+#pragma unroll
+        for (int d = 0; d < DP / 16; ++d) {
+            u32x4 v = t.v[half + k][d][lane];
+            if constexpr (MASK) {
+                f32x4* o[MT];
+#pragma unroll
+                for (int m = 0; m < MT; ++m) o[m] = &w.o[m][d];
+                v = take_nans<MT>(v, vis, o);
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) w.o[m][d] = mfma<true>(v, p[k][m], w.o[m][d]);
+        }
+    }
+}
+
 template <int DP, int MT, bool F16>
-__global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attend_rows(Kv8Attend a) {
+__global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attend_rows(Kv8Attend args) {
     constexpr int WAVES = 4;
     constexpr int DT = DP / 16;
     constexpr int ROWS = WAVES * MT * 16;
@@ -924,22 +1066,16 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attend_rows(Kv8Atten
     };
     __shared__ Shared sh;
     __shared__ int s_live[ROWS];
-    const int tid = threadIdx.x;
-    const int lane = tid & (WAVE - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
+    AttendPiece pc;
+    if (!attend_share<AT_TILE, ROWS>(args, pc)) return;
+    ArgsAgain again;
+    do {
+    const Kv8Attend& a = again.args();
+    const int lane = again.thread() & (WAVE - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(again.thread() / WAVE);
     const int g = lane >> 4, col = lane & 15;
-    const int items = a.s.B + a.pieces;
-    const int item = blockIdx.x % items;
-    const int y = blockIdx.x / items;
-    const int h = y / a.blocks;
-    const int first = (y - h * a.blocks) * ROWS;  // row of this block
+    const int h = pc.h, first = pc.first;
     const int rows = min(a.s.N * a.group - first, ROWS);
-    AttendPiece pc = attend_piece<AT_TILE>(a, item);
-    pc.b = __builtin_amdgcn_readfirstlane(pc.b);
-    pc.c = __builtin_amdgcn_readfirstlane(pc.c);
-    pc.n = __builtin_amdgcn_readfirstlane(pc.n);
-    pc.units = __builtin_amdgcn_readfirstlane(pc.units);
-    if (pc.b < 0) return;
     const AttendRow row = attend_row(a, pc.b);
 
     const int mine = first + wave * MT * 16;                       // rows of this wave
@@ -971,18 +1107,12 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attend_rows(Kv8Atten
         for (int d = 0; d < DT; ++d) w.o[m][d] = f32x4{0, 0, 0, 0};
     }
 
-    // tiles of this piece that some row sees, and what this wave's rows see of them
-    int see = row.end, see_all = row.end;
+    // tiles of this piece, and what this wave's rows see of them
+    const int see = count ? attend_see(a, row, (mine + count - 1) / a.group) : 0;
     int full = min(row.base, row.end);
-    if (!a.s.parents && row.count) {
-        see_all = (int)min((int64_t)row.end, (int64_t)row.base + (first + rows - 1) / a.group + 1);
-        see = (int)min((int64_t)row.end, (int64_t)row.base + (mine + count - 1) / a.group + 1);
-        full = (int)min((int64_t)row.end, (int64_t)row.base + mine / a.group + 1);
-    }
-    if (!count) see = 0;
-    const int tiles = (int)(((int64_t)see_all + AT_TILE - 1) / AT_TILE);
-    const int t0 = (int)min((int64_t)pc.c * pc.units, (int64_t)tiles);
-    const int t1 = (int)min((int64_t)(pc.c + 1) * pc.units, (int64_t)tiles);
+    if (!a.s.parents && row.count) full = (int)min((int64_t)row.end, (int64_t)row.base + mine / a.group + 1);
+    const int t0 = pc.from;
+    const int t1 = min(pc.to, (int)(((int64_t)attend_see(a, row, (first + rows - 1) / a.group) + AT_TILE - 1) / AT_TILE));
     if (t0 < t1) {
         AttendWalk at;
         at.table = (const_i32)(a.s.t.tables + (int64_t)pc.b * a.s.t.stride);
@@ -1010,47 +1140,21 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attend_rows(Kv8Atten
                 leave_raw<DP, F16>(a, raw, wave, sh.t[(i - t0 + 1) & 1]);
                 load_raw<DP>(a, at, h, k_at, v_at, raw);
             }
+            const int s0 = i * AT_TILE;
+            if (s0 + AT_TILE <= full) {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int s0 = i * AT_TILE + half * AT_STEP;
-                if (s0 >= see) continue;
-                f32x4 e[2][MT];
-                u32x4 p[MT];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) e[k][m] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                    for (int st = 0; st < DP / 32; ++st) {
-                        const u32x4 f = t.k[half * 2 + k][st][lane];
-#pragma unroll
-                        for (int m = 0; m < MT; ++m) e[k][m] = mfma<F16>(f, w.q[m][st], e[k][m]);
-                    }
-                }
-                const f32x4 x0 = t.x[half * 2], x1 = t.x[half * 2 + 1];
-                const AttendScales x = {{x0[0], x1[0]}, {x0[1], x1[1]}, {x0[2], x1[2]}};
-                const bool masked = s0 + AT_STEP > full;
-                uint32_t vis[MT] = {};
-                if (masked)
-                    attend_mask<MT>(a, above, mine, max(count, 1), s0 - row.base + g * 4, row.end - row.base, e, vis);
-                attend_weights<DP, MT>(x, e, w, p);
-#pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    u32x4 v = t.v[half][d][lane];
-                    if (masked) {
-                        f32x4* o[MT];
-#pragma unroll
-                        for (int m = 0; m < MT; ++m) o[m] = &w.o[m][d];
-                        v = take_nans<MT>(v, vis, o);
-                    }
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) w.o[m][d] = mfma<true>(v, p[m], w.o[m][d]);
-                }
+                for (int k = 0; k < 2; ++k)
+                    attend_tile<DP, MT, F16, 2, false>(a, t, k, 0, 0, above, mine, count, w);
+            } else {  // slots that some row does not see
+#pragma clang loop unroll(disable)
+                for (int k = 0; k < 2 && s0 + k * AT_STEP < see; ++k)
+                    attend_tile<DP, MT, F16, 2, true>(a, t, k, s0 + k * AT_STEP - row.base + g * 4,
+                                                      row.end - row.base, above, mine, count, w);
             }
         }
     }
 
-    float* slot = a.part + (int64_t)blockIdx.x * SLOT;
+    float* slot = a.part + (int64_t)attend_left(a, pc, pc.p, pc.c == 0) * SLOT;
     if (pc.n > 1) __syncthreads();  // the tiles are read; what pieces leave goes through LDS, in whole lines
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -1091,59 +1195,64 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attend_rows(Kv8Atten
             }
         }
     }
-    if (pc.n > 1)
-        add_pieces<DP, ROWS, F16, WAVES>(a, pc.b, pc.c, pc.n, y, h, first, rows, &sh.o[0][0][0], s_live);
+    if (pc.n > 1) add_pieces<DP, ROWS, F16>(a, pc, rows, &sh.o[0][0][0], s_live);
+    __syncthreads();  // LDS is read
+    } while (attend_on<AT_TILE, ROWS>(args, pc));
 }
 
-// How many rows a workgroup takes, and into how many pieces rows are cut.
-template <int DP, int MT, bool F16, int WAVES>
+// Into how many shares the slots of a head and block of rows are cut.
+template <int ROWS>
+static int64_t attend_grid(Kv8Attend& a, int dp, int target) {
+    a.blocks = (int)(((int64_t)a.s.N * a.group + ROWS - 1) / ROWS);
+    const int64_t lines = (int64_t)a.g.heads * a.blocks;
+    const int64_t most = KV8_PART_FLOATS / (2 * attend_slot(dp, ROWS));
+    if (target > most) target = (int)most;
+    a.shares = (int)(target / lines);
+    // whole requests where there are many, or where the card is full of blocks of rows
+    if (lines * a.s.B >= 4 * target || a.s.B * ((int64_t)a.g.max_blocks * a.g.page_size / 64 + 1) > INT_MAX)
+        a.shares = 0;
+    return lines * (a.shares ? a.shares : a.s.B);
+}
+
+template <int DP, int MT, bool F16>
 static hipError_t launch_attend(Kv8Attend a, hipStream_t st) {
-    constexpr int64_t SLOT = MT * 16 * (DP + 2);
-    a.blocks = (int)(((int64_t)a.s.N * a.group + MT * 16 - 1) / (MT * 16));
-    const int64_t y = (int64_t)a.g.heads * a.blocks;
-    // rows are cut where whole ones leave the card's CUs idle or uneven
-    const int64_t most = KV8_PART_FLOATS / SLOT < KV8_SPLITS ? KV8_PART_FLOATS / SLOT : KV8_SPLITS;
-    static const int target = getenv("AT_TARGET") ? atoi(getenv("AT_TARGET")) : 512;
-    a.pieces = y * a.s.B <= most / 2 ? (int)((most / 2 < target ? most / 2 : target) / y) : 0;
-    const int64_t grid = y * (a.s.B + a.pieces);
+    static const int target = getenv("AT_TARGET") ? atoi(getenv("AT_TARGET")) : 256;
+    static const int least = getenv("AT_LEAST") ? atoi(getenv("AT_LEAST")) : 1;
+    a.least = least;
+    const int64_t grid = attend_grid<MT * 16>(a, DP, target);
     if (grid > INT_MAX) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_attend<DP, MT, F16, WAVES>), dim3((unsigned)grid), dim3(WAVES * WAVE), 0, st, a);
+    hipLaunchKernelGGL((k_attend<DP, MT, F16>), dim3((unsigned)grid), dim3(256), 0, st, a);
     return hipGetLastError();
 }
 
 template <int DP, int MT, bool F16>
-static hipError_t launch_shared(Kv8Attend a, hipStream_t st) {
-    constexpr int ROWS = 64 * MT;
-    constexpr int64_t SLOT = attend_slot(DP, ROWS);
-    a.blocks = (int)(((int64_t)a.s.N * a.group + ROWS - 1) / ROWS);
-    const int64_t y = (int64_t)a.g.heads * a.blocks;
-    const int64_t most = KV8_PART_FLOATS / SLOT < KV8_SPLITS ? KV8_PART_FLOATS / SLOT : KV8_SPLITS;
+static hipError_t launch_rows(Kv8Attend a, hipStream_t st) {
     static const int target = getenv("AT_TARGET2") ? atoi(getenv("AT_TARGET2")) : 512;
-    a.pieces = y * a.s.B <= most / 2 ? (int)((most / 2 < target ? most / 2 : target) / y) : 0;
-    const int64_t grid = y * (a.s.B + a.pieces);
+    static const int least = getenv("AT_LEAST2") ? atoi(getenv("AT_LEAST2")) : 1;
+    a.least = least;
+    const int64_t grid = attend_grid<MT * 64>(a, DP, target);
     if (grid > INT_MAX) return hipErrorInvalidValue;
     hipLaunchKernelGGL((k_attend_rows<DP, MT, F16>), dim3((unsigned)grid), dim3(256), 0, st, a);
     return hipGetLastError();
 }
 
 template <int DP, bool F16>
-static hipError_t launch_attend_rows(const Kv8Attend& a, hipStream_t st) {
+static hipError_t launch_attend_by_rows(const Kv8Attend& a, hipStream_t st) {
     const int64_t rows = (int64_t)a.s.N * a.group;
-    static const int sh = getenv("AT_SHARED") ? atoi(getenv("AT_SHARED")) : 1;
-    if (sh && rows > 32) {
-        if (rows <= 64 || DP == 256 || sh == 2) return launch_shared<DP, 1, F16>(a, st);
-        return launch_shared<DP, DP == 256 ? 1 : 2, F16>(a, st);
+    static const int sh = getenv("AT_SHARED") ? atoi(getenv("AT_SHARED")) : 32;
+    if (rows > sh) {
+        if (rows <= 64 || DP == 256) return launch_rows<DP, 1, F16>(a, st);
+        return launch_rows<DP, DP == 256 ? 1 : 2, F16>(a, st);
     }
-    if (rows <= 16) return launch_attend<DP, 1, F16, 4>(a, st);
-    if (rows <= 32 || DP == 256) return launch_attend<DP, 2, F16, 4>(a, st);
-    return launch_attend<DP, DP == 256 ? 2 : 4, F16, 4>(a, st);
+    if (rows <= 16) return launch_attend<DP, 1, F16>(a, st);
+    return launch_attend<DP, 2, F16>(a, st);
 }
 
 template <bool F16>
 static hipError_t launch_attend_dim(const Kv8Attend& a, hipStream_t st) {
-    if (a.g.dim <= 64) return launch_attend_rows<64, F16>(a, st);
-    if (a.g.dim <= 128) return launch_attend_rows<128, F16>(a, st);
-    return launch_attend_rows<256, F16>(a, st);
+    if (a.g.dim <= 64) return launch_attend_by_rows<64, F16>(a, st);
+    if (a.g.dim <= 128) return launch_attend_by_rows<128, F16>(a, st);
+    return launch_attend_by_rows<256, F16>(a, st);
 }
 
 hipError_t launch_kv8_attend(const Kv8Attend& a, ss_dtype dt, hipStream_t st) {

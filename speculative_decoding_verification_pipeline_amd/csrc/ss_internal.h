@@ -453,17 +453,18 @@ struct Kv8Attend {
     float* lse;
     int q_heads;
     int group;        // query heads per head of the cache
-    int blocks;       // blocks of rows of one row and head
-    int pieces;       // pieces that all rows of one head and block are cut into at most, beyond
-                      //   one each; 0: rows are not cut
+    int blocks;       // blocks of rows of one request and head
+    int shares;       // that the slots of a head and block of rows over all requests are cut
+                      //   into; 0: none is cut
+    int least;        // units of a share, at least
     float scale_log2; // scale * log2(e)
     float* part;
     int32_t* arrived;
 };
 
 constexpr int KV8_COUNTER = 64;       // integers between counters
-constexpr int KV8_SPLITS = 2048;      // rows, heads and blocks that are cut, at most
-constexpr int64_t KV8_PART_FLOATS = 8 << 20;  // what pieces leave, at most
+constexpr int KV8_SPLITS = 1024;      // shares, over heads and blocks of rows, at most
+constexpr int64_t KV8_PART_FLOATS = 9 << 20;  // what shares leave, at most
 
 // Optional timing events of a call (see ss_sampler_set_launch_events): launch
 // k is bracketed by ev[2k] (its start) and ev[2k + 1] (its end), recorded by
