@@ -15,9 +15,9 @@ from dataclasses import dataclass
 
 import torch
 
-from .sampler import (_HALF_DTYPES, SS_OK, CacheConfig, CacheScales, CBlockTables, CCacheStep, _check,
-                      _check_array, _check_block, _check_dev, _check_out_heads, _check_rows, _empty,
-                      _empty_rows, _heads, _require, _stream_on, load_library)
+from .sampler import (_HALF_DTYPES, SS_OK, CacheConfig, CacheScales, CBlockTables, _check, _check_array,
+                      _check_block, _check_dev, _check_rows, _empty_rows, _heads, _out_heads, _pack_step,
+                      _pack_tables, _require, _stream_on, load_library)
 
 
 @dataclass
@@ -110,8 +110,12 @@ class PageCache:
                            torch.zeros(rows, dtype=torch.int32, device=dev))
 
     def _tables(self, t):
-        """The tables as the ABI takes them, checked by what costs least; the
-        messages are formed on failure only."""
+        """The tables as the ABI takes them."""
+        return CBlockTables(*self._table_words(t))
+
+    def _table_words(self, t):
+        """The tables' fields, checked by what costs least; the messages are formed on
+        failure only."""
         dev, tab = self.device, t.tables
         shape = getattr(tab, "shape", ())
         if not (len(shape) == 2 and isinstance(tab, torch.Tensor) and tab.dtype is torch.int32 and
@@ -123,9 +127,9 @@ class PageCache:
             _require(tab.shape[0] <= 1 or tab.stride(0) >= self.max_blocks,
                      "tables rows must not overlap")
         rows, cols = shape
-        return CBlockTables(tab.data_ptr(), tab.stride(0) if rows > 1 else cols, rows,
-                            _check_array(t.ref, "ref", self.num_pages, dev),
-                            _check_array(t.lens, "lens", rows, dev))
+        return (tab.data_ptr(), tab.stride(0) if rows > 1 else cols, rows,
+                _check_array(t.ref, "ref", self.num_pages, dev),
+                _check_array(t.lens, "lens", rows, dev))
 
     def _count(self, v, name, most):
         """Entries of a contiguous 1-D int32 array of at most `most`, and its address."""
@@ -237,40 +241,34 @@ class PageCache:
             _check("ss_cache_copy_pages", st)
         return ok
 
-    def _step(self, tables, like, lens, counts, parents, reserved):
-        """A step's tokens as the ABI takes them; like: [B, N, ...]."""
-        ct = self._tables(tables)
-        B, N = like.shape[0], like.shape[1]
-        _require(B <= ct.rows, f"the step has {B} rows, the tables {ct.rows}")
-        _require(1 <= N <= self.max_blocks * self.page_size,
-                 f"a step has 1 .. {self.max_blocks * self.page_size} tokens a row")
-        at = None
+    def _step(self, tables, shape, lens, counts, parents, reserved):
+        """The tables and a step's tokens [B, N, ...] as the ABI takes them."""
+        words = self._table_words(tables)
+        B, N = shape[0], shape[1]
+        if B > words[2] or not 1 <= N <= self.max_blocks * self.page_size:
+            raise ValueError(f"a step has at most {words[2]} rows of 1 .. "
+                             f"{self.max_blocks * self.page_size} tokens")
+        dev, at = self.device, 0
         if parents is not None:
-            _require(N <= 64, "a draft tree has at most 64 nodes")
-            at = _check_block(parents, "parents", (B, N), torch.int32, self.device)
-        return ct, CCacheStep(B, N, _check_array(lens, "lens", B, self.device),
-                              _check_array(counts, "counts", B, self.device), at,
-                              _check_array(reserved, "reserved", B, self.device))
+            if N > 64:
+                raise ValueError("a draft tree has at most 64 nodes")
+            at = _check_block(parents, "parents", (B, N), torch.int32, dev)
+        return _pack_tables(*words), _pack_step(B, N, _check_array(lens, "lens", B, dev) or 0,
+                                                _check_array(counts, "counts", B, dev) or 0, at,
+                                                _check_array(reserved, "reserved", B, dev) or 0)
 
     def _layer(self, layer):
-        _require(self.scales is not None, "the cache has no scales")
-        _require(0 <= layer and 2 * layer + 1 < len(self.planes),
-                 f"layer must be in 0 .. {len(self.planes) // 2 - 1}")
+        if self.scales is None:
+            raise ValueError("the cache has no scales")
+        if not 0 <= 2 * layer < len(self.planes) - 1:
+            raise ValueError(f"layer must be in 0 .. {len(self.planes) // 2 - 1}")
         return 2 * layer, 2 * layer + 1
 
     def _dtype(self, t, name):
         code = _HALF_DTYPES.get(getattr(t, "dtype", None))
-        _require(code is not None and t.dim() == 4,
-                 f"{name} must be a [B, N, heads, dim] array of bfloat16 or float16")
+        if code is None or t.dim() != 4:
+            raise ValueError(f"{name} must be a [B, N, heads, dim] array of bfloat16 or float16")
         return code
-
-    def _like(self, out, name, t, stream):
-        """The given output of t's shape and type, else a new one."""
-        if out is None:
-            return _empty(tuple(t.shape), t, t.dtype, stream)
-        _heads(out, name, t.shape, t.dtype, self.device)
-        _check_out_heads(out, name)
-        return out
 
     def write(self, tables: BlockTables, layer, keys, values, lens=None, counts=None, parents=None,
               reserved=None, rotary=None, positions=None, queries=None, out_queries=None,
@@ -288,8 +286,8 @@ class PageCache:
         not become 0."""
         k_plane, v_plane = self._layer(layer)
         code = self._dtype(keys, "keys")
-        ct, step = self._step(tables, keys, lens, counts, parents, reserved)
-        shape = (step.B, step.N, self.heads, self.dim)
+        shape = (*keys.shape[:2], self.heads, self.dim)
+        ct, step = self._step(tables, shape, lens, counts, parents, reserved)
         k = _heads(keys, "keys", shape, keys.dtype, self.device)
         v = _heads(values, "values", shape, keys.dtype, self.device)
         at = None
@@ -298,17 +296,16 @@ class PageCache:
         r = q = o = None
         q_heads = 0
         if rotary is not None:
-            r = ctypes.byref(rotary.on(self.device))
+            r = rotary.on(self.device)
         if queries is not None:
-            _require(rotary is not None, "queries are turned along: give a rotary")
+            if rotary is None:
+                raise ValueError("queries are turned along: give a rotary")
             q = _heads(queries, "queries", None, keys.dtype, self.device)
-            q_heads = queries.shape[2]
-            _require(queries.shape == (step.B, step.N, q_heads, self.dim) and q_heads > 0,
-                     "queries must be [B, N, q_heads, dim]")
-            out_queries = self._like(out_queries, "out_queries", queries, stream)
-            o = _heads(out_queries, "out_queries", queries.shape, keys.dtype, self.device)
-        st = self.lib.ss_cache_write(self.handle, ctypes.byref(ct), ctypes.byref(step), k_plane,
-                                     v_plane, code, ctypes.byref(k), ctypes.byref(v), r, at, q, o,
+            q_heads = queries.shape[2] if queries.dim() == 4 else 0
+            if q_heads < 1 or queries.shape != (*shape[:2], q_heads, self.dim):
+                raise ValueError("queries must be [B, N, q_heads, dim]")
+            out_queries, o = _out_heads(out_queries, "out_queries", queries.shape, queries, keys.dtype, stream)
+        st = self.lib.ss_cache_write(self.handle, ct, step, k_plane, v_plane, code, k, v, r, at, q, o,
                                      q_heads, _stream_on(stream, self.device))
         if st != SS_OK:
             _check("ss_cache_write", st)
@@ -322,31 +319,25 @@ class PageCache:
         on no page are 0."""
         k_plane, v_plane = self._layer(layer)
         code = _HALF_DTYPES.get(dtype)
-        _require(code is not None, "dtype must be bfloat16 or float16")
-        ct = self._tables(tables)
-        B = ct.rows if start is None and counts is None else \
+        if code is None:
+            raise ValueError("dtype must be bfloat16 or float16")
+        words = self._table_words(tables)
+        B = words[2] if start is None and counts is None else \
             (start if start is not None else counts).shape[0]
-        _require(B <= ct.rows, f"start has {B} rows, the tables {ct.rows}")
-        _require(1 <= N <= self.max_blocks * self.page_size,
-                 f"N must be in 1 .. {self.max_blocks * self.page_size}")
+        if B > words[2] or not 1 <= N <= self.max_blocks * self.page_size:
+            raise ValueError(f"at most {words[2]} rows of 1 .. {self.max_blocks * self.page_size} "
+                             f"slots are read")
         first = _check_array(start, "start", B, self.device)
         n = _check_array(counts, "counts", B, self.device)
         shape = (B, N, self.heads, self.dim)
-        out = []
-        for t, name in ((out_keys, "out_keys"), (out_values, "out_values")):
-            if t is None:
-                t = _empty(shape, tables.tables, dtype, stream)
-            else:
-                _heads(t, name, shape, dtype, self.device)
-                _check_out_heads(t, name)
-            out.append(t)
-        k, v = (_heads(t, "out", shape, dtype, self.device) for t in out)
-        st = self.lib.ss_cache_read(self.handle, ctypes.byref(ct), first, n, B, N, k_plane, v_plane,
-                                    code, ctypes.byref(k), ctypes.byref(v),
-                                    _stream_on(stream, self.device))
+        like = tables.tables
+        out_keys, k = _out_heads(out_keys, "out_keys", shape, like, dtype, stream)
+        out_values, v = _out_heads(out_values, "out_values", shape, like, dtype, stream)
+        st = self.lib.ss_cache_read(self.handle, _pack_tables(*words), first, n, B, N, k_plane, v_plane,
+                                    code, k, v, _stream_on(stream, self.device))
         if st != SS_OK:
             _check("ss_cache_read", st)
-        return out[0], out[1]
+        return out_keys, out_values
 
     def attend(self, tables: BlockTables, layer, queries, lens=None, counts=None, parents=None,
                reserved=None, scale=None, out=None, lse=None, stream=None):
@@ -361,18 +352,17 @@ class PageCache:
         exponentials."""
         k_plane, v_plane = self._layer(layer)
         code = self._dtype(queries, "queries")
-        ct, step = self._step(tables, queries, lens, counts, parents, reserved)
+        shape = queries.shape
+        ct, step = self._step(tables, shape, lens, counts, parents, reserved)
         q = _heads(queries, "queries", None, queries.dtype, self.device)
-        q_heads = queries.shape[2]
-        _require(queries.shape[3] == self.dim and q_heads > 0 and q_heads % self.heads == 0,
-                 f"queries must be [B, N, a multiple of {self.heads}, {self.dim}]")
-        out = self._like(out, "out", queries, stream)
-        o = _heads(out, "out", queries.shape, queries.dtype, self.device)
+        q_heads = shape[2]
+        if shape[3] != self.dim or q_heads < 1 or q_heads % self.heads:
+            raise ValueError(f"queries must be [B, N, a multiple of {self.heads}, {self.dim}]")
+        out, o = _out_heads(out, "out", shape, queries, queries.dtype, stream)
         at = None
         if lse is not None:
-            at = _check_block(lse, "lse", (step.B, step.N, q_heads), torch.float32, self.device)
-        st = self.lib.ss_cache_attend(self.handle, ctypes.byref(ct), ctypes.byref(step), k_plane,
-                                      v_plane, code, ctypes.byref(q), ctypes.byref(o), q_heads,
+            at = _check_block(lse, "lse", shape[:3], torch.float32, self.device)
+        st = self.lib.ss_cache_attend(self.handle, ct, step, k_plane, v_plane, code, q, o, q_heads,
                                       self.dim ** -0.5 if scale is None else scale, at,
                                       _stream_on(stream, self.device))
         if st != SS_OK:

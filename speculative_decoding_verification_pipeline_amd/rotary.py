@@ -8,13 +8,12 @@ them.
 """
 from __future__ import annotations
 
-import ctypes
 import math
 
 import torch
 
-from .sampler import (_HALF_DTYPES, SS_OK, CRotary, _check, _check_block, _check_out_heads, _empty,
-                      _heads, _require, _stream_on, load_library)
+from .sampler import (_HALF_DTYPES, SS_OK, _check, _check_block, _heads, _out_heads, _pack_rotary,
+                      _require, _stream_on, load_library)
 
 
 def frequencies(dim, base=10000.0, scaling=None, factor=1.0, original=None, fast=32.0, slow=1.0):
@@ -76,7 +75,7 @@ class Rotary:
                                   device="cuda" if device is None else device)
         _require(self.turns.is_cuda, "a Rotary lives on a GPU")
         self.device = self.turns.device.index
-        self._c = CRotary(self.turns.data_ptr(), dim, int(self.interleaved), self.magnitude)
+        self._c = _pack_rotary(self.turns.data_ptr(), dim, int(self.interleaved), self.magnitude)
 
     def on(self, device):
         """The rotation as the ABI takes it, for calls on this device."""
@@ -91,36 +90,27 @@ class Rotary:
         is turned in place. Returns out_queries, or (out_queries, out_keys)."""
         dev = self.device
         code = _HALF_DTYPES.get(getattr(queries, "dtype", None))
-        _require(code is not None and queries.dim() in (3, 4),
-                 "queries must be [T, heads, dim] or [B, N, heads, dim] of bfloat16 or float16")
-        lead = queries.shape[:-2]
-        _require(self.dim <= queries.shape[-1], f"heads must have at least {self.dim} entries")
+        if code is None or queries.dim() not in (3, 4):
+            raise ValueError("queries must be [T, heads, dim] or [B, N, heads, dim] of bfloat16 or float16")
+        shape, dtype = queries.shape, queries.dtype
+        lead, dim = shape[:-2], shape[-1]
+        if self.dim > dim:
+            raise ValueError(f"heads must have at least {self.dim} entries")
         pos = _check_block(positions, "positions", lead, torch.int32, dev)
-        if out_queries is None:
-            out_queries = _empty(tuple(queries.shape), queries, queries.dtype, stream)
-        arrays = [(queries, "queries", queries), (out_queries, "out_queries", queries)]
+        q = _heads(queries, "queries", None, dtype, dev)
+        out_queries, oq = _out_heads(out_queries, "out_queries", shape, queries, dtype, stream)
+        k = ok = None
+        k_heads = 0
         if keys is not None:
-            _require(keys.dim() == queries.dim() and keys.shape[:-2] == lead and
-                     keys.shape[-1] == queries.shape[-1],
-                     "keys must match queries but for the number of heads")
-            if out_keys is None:
-                out_keys = _empty(tuple(keys.shape), keys, keys.dtype, stream)
-            arrays += [(keys, "keys", keys), (out_keys, "out_keys", keys)]
-        else:
-            _require(out_keys is None, "out_keys needs keys")
-        c = []
-        for i, (t, name, like) in enumerate(arrays):
-            _require(isinstance(t, torch.Tensor) and t.shape == like.shape,
-                     f"{name} must be {list(like.shape)}")
-            if t.dim() == 3:
-                t = t.unsqueeze(0)
-            c.append(_heads(t, name, None, queries.dtype, dev))
-            if i % 2:
-                _check_out_heads(t, name)
-        q, oq, k, ok = [ctypes.byref(x) for x in c] + [None] * (4 - len(c))
-        B, N = (1, lead[0]) if len(lead) == 1 else lead
-        st = self.lib.ss_rotate(dev, ctypes.byref(self._c), code, B, N, queries.shape[-1], pos, q, oq,
-                                queries.shape[-2], k, ok, 0 if keys is None else keys.shape[-2],
+            k_heads = keys.shape[-2]
+            if keys.shape != (*lead, k_heads, dim):
+                raise ValueError("keys must match queries but for the number of heads")
+            k = _heads(keys, "keys", None, dtype, dev)
+            out_keys, ok = _out_heads(out_keys, "out_keys", keys.shape, keys, dtype, stream)
+        elif out_keys is not None:
+            raise ValueError("out_keys needs keys")
+        B, N = lead if len(lead) == 2 else (1, lead[0])
+        st = self.lib.ss_rotate(dev, self._c, code, B, N, dim, pos, q, oq, shape[-2], k, ok, k_heads,
                                 _stream_on(stream, dev))
         if st != SS_OK:
             _check("ss_rotate", st)

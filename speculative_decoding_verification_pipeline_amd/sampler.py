@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -87,22 +88,6 @@ class CacheScales(ctypes.Structure):
                 ("block_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
-class CHeads(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
-                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
-
-
-class CCacheStep(ctypes.Structure):
-    _fields_ = [("B", ctypes.c_int32), ("N", ctypes.c_int32), ("base", ctypes.c_void_p),
-                ("counts", ctypes.c_void_p), ("parents", ctypes.c_void_p),
-                ("reserved", ctypes.c_void_p)]
-
-
-class CRotary(ctypes.Structure):
-    _fields_ = [("turns", ctypes.c_void_p), ("dim", ctypes.c_int32),
-                ("interleaved", ctypes.c_int32), ("magnitude", ctypes.c_double)]
-
-
 class SamplerError(RuntimeError):
     def __init__(self, fn, status, msg):
         super().__init__(f"{fn} failed: {msg} ({status})")
@@ -176,21 +161,18 @@ def load_library(path=None):
     lib.ss_cache_truncate.restype = i32
     lib.ss_cache_copy_pages.argtypes = [vp, vp, vp, vp, i32, vp, vp]
     lib.ss_cache_copy_pages.restype = i32
-    heads, step, rotary = (ctypes.POINTER(x) for x in (CHeads, CCacheStep, CRotary))
     lib.ss_cache_create_scaled.argtypes = [ctypes.POINTER(CacheConfig), ctypes.POINTER(vp),
                                            ctypes.POINTER(vp), ctypes.POINTER(CacheScales),
                                            ctypes.POINTER(vp)]
     lib.ss_cache_create_scaled.restype = i32
-    lib.ss_rotate.argtypes = [i32, rotary, i32, i32, i32, i32, vp, heads, heads, i32, heads, heads,
-                              i32, vp]
+    # structures come as bytes: see _pack_heads
+    lib.ss_rotate.argtypes = [i32, vp, i32, i32, i32, i32, vp, vp, vp, i32, vp, vp, i32, vp]
     lib.ss_rotate.restype = i32
-    lib.ss_cache_write.argtypes = [vp, tables, step, i32, i32, i32, heads, heads, rotary, vp, heads,
-                                   heads, i32, vp]
+    lib.ss_cache_write.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, i32, vp]
     lib.ss_cache_write.restype = i32
-    lib.ss_cache_read.argtypes = [vp, tables, vp, vp, i32, i32, i32, i32, i32, heads, heads, vp]
+    lib.ss_cache_read.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp]
     lib.ss_cache_read.restype = i32
-    lib.ss_cache_attend.argtypes = [vp, tables, step, i32, i32, i32, heads, heads, i32,
-                                    ctypes.c_float, vp, vp]
+    lib.ss_cache_attend.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, i32, ctypes.c_float, vp, vp]
     lib.ss_cache_attend.restype = i32
     _lib = lib
     return lib
@@ -252,6 +234,9 @@ def _empty(shape, like, dtype, stream=None):
             return _empty_strided(shape, (1,), dtype)
         if len(shape) == 2:
             return _empty_strided(shape, (shape[1], 1), dtype)
+        if len(shape) == 3:
+            _, h, d = shape
+            return _empty_strided(shape, (h * d, d, 1), dtype)
         if len(shape) == 4:
             _, n, h, d = shape
             return _empty_strided(shape, (n * h * d, h * d, d, 1), dtype)
@@ -319,26 +304,55 @@ def _check_rank3(t, name, shape, dtype, device):
 
 _HALF_DTYPES = {torch.bfloat16: SS_BF16, torch.float16: SS_F16}
 
+# ss_heads, ss_block_tables, ss_cache_step and ss_rotary as bytes, which ctypes passes by
+# their address: a structure of its own takes 1 us a call, these 0.3
+_pack_heads = struct.Struct("@P3q").pack
+_pack_tables = struct.Struct("@PqixxxxPP").pack
+_pack_step = struct.Struct("@iiPPPP").pack
+_pack_rotary = struct.Struct("@Piid").pack
+
 
 def _heads(t, name, shape, dtype, device):
     """A [B, N, heads, dim] array of 16-bit floats as the ABI takes it; shape None: any.
-    The last dimension has unit stride, the others any."""
+    The last dimension has unit stride, the others any. [T, heads, dim] is a batch of one."""
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and
-            t.dim() == 4 and (shape is None or t.shape == shape)):
+            (shape is None or t.shape == shape)):
         _check_dev(t, name, (dtype,), device)
         raise ValueError(f"{name} must be {'[B, N, heads, dim]' if shape is None else list(shape)}")
-    b, n, h, one = t.stride()
-    if one != 1 and t.shape[3] > 1:
+    strides = t.stride()
+    if strides[-1] != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must have unit stride along its last dim")
-    # a dimension of one entry is never stepped, whatever its stride
-    B, N, H, _ = t.shape
-    return CHeads(t.data_ptr(), b if B > 1 else 0, n if N > 1 else 0, h if H > 1 else 0)
+    if t.is_contiguous():  # a dimension of one entry may have any stride: it is not stepped
+        _, N, H, D = t.shape if len(strides) == 4 else (1, *t.shape)
+        return _pack_heads(t.data_ptr(), N * H * D, H * D, D)
+    b, n, h, _ = strides if len(strides) == 4 else (0, *strides)
+    B, N, H, _ = t.shape if len(strides) == 4 else (1, *t.shape)
+    return _pack_heads(t.data_ptr(), b if B > 1 else 0, n if N > 1 else 0, h if H > 1 else 0)
+
+
+def _new_heads(shape, like, dtype, stream):
+    """A new [..., N, heads, dim] array, and as the ABI takes it."""
+    out = _empty(tuple(shape), like, dtype, stream)
+    n, h, d = shape[-3:]
+    h *= d
+    return out, _pack_heads(out.data_ptr(), n * h, h, d)
+
+
+def _out_heads(out, name, shape, like, dtype, stream):
+    """The given output, of this shape and type, or a new one (None), and as the ABI takes it."""
+    if out is None:
+        return _new_heads(shape, like, dtype, stream)
+    words = _heads(out, name, shape, dtype, like.get_device())
+    _check_out_heads(out, name)
+    return out, words
 
 
 def _check_out_heads(t, name):
     """An output whose entries lie apart: strides, sorted, each span what lies within."""
-    span = t.shape[3]
-    for stride, n in sorted(zip(t.stride()[:3], t.shape[:3])):
+    if t.is_contiguous():
+        return
+    span = t.shape[-1]
+    for stride, n in sorted(zip(t.stride()[:-1], t.shape[:-1])):
         if n > 1:
             _require(stride >= span, f"{name} must not hold an entry twice")
             span += stride * (n - 1)
