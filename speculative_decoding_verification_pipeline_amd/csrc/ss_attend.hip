@@ -1110,9 +1110,10 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attend_rows(Kv8Atten
     // tiles of this piece, and what this wave's rows see of them
     const int see = count ? attend_see(a, row, (mine + count - 1) / a.group) : 0;
     int full = min(row.base, row.end);
-    if (!a.s.parents && row.count) full = (int)min((int64_t)row.end, (int64_t)row.base + mine / a.group + 1);
+    if (!a.s.parents && row.count) full = (int)min((int64_t)row.end, (int64_t)row.base + first / a.group + 1);
     const int t0 = pc.from;
     const int t1 = min(pc.to, (int)(((int64_t)attend_see(a, row, (first + rows - 1) / a.group) + AT_TILE - 1) / AT_TILE));
+    const int t2 = max(min(full / AT_TILE, t1), t0);  // tiles before it need no mask
     if (t0 < t1) {
         AttendWalk at;
         at.table = (const_i32)(a.s.t.tables + (int64_t)pc.b * a.s.t.stride);
@@ -1133,24 +1134,30 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attend_rows(Kv8Atten
         load_raw<DP>(a, at, h, k_at, v_at, raw);
         leave_raw<DP, F16>(a, raw, wave, sh.t[0]);
         load_raw<DP>(a, at, h, k_at, v_at, raw);
-        for (int i = t0; i < t1; ++i) {
-            const AttendTile<DP>& t = sh.t[(i - t0) & 1];
+        auto next = [&](int i) {
             __syncthreads();
             if (i + 1 < t1) {
                 leave_raw<DP, F16>(a, raw, wave, sh.t[(i - t0 + 1) & 1]);
                 load_raw<DP>(a, at, h, k_at, v_at, raw);
             }
-            const int s0 = i * AT_TILE;
-            if (s0 + AT_TILE <= full) {
+        };
+        // tiles that all rows see
+        for (int i = t0; i < t2; ++i) {
+            next(i);
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    attend_tile<DP, MT, F16, 2, false>(a, t, k, 0, 0, above, mine, count, w);
-            } else {  // slots that some row does not see
+            for (int k = 0; k < 2; ++k)
+                attend_tile<DP, MT, F16, 2, false>(a, sh.t[(i - t0) & 1], k, 0, 0, 0, mine, count, w);
+        }
+        // those that some row does not see, of the step's own tokens or behind the last one: in a
+        // loop of their own, or what they need is kept, in scratch memory, through the other
 #pragma clang loop unroll(disable)
-                for (int k = 0; k < 2 && s0 + k * AT_STEP < see; ++k)
-                    attend_tile<DP, MT, F16, 2, true>(a, t, k, s0 + k * AT_STEP - row.base + g * 4,
-                                                      row.end - row.base, above, mine, count, w);
-            }
+        for (int i = t2; i < t1; ++i) {
+            next(i);
+            const int s0 = i * AT_TILE;
+#pragma clang loop unroll(disable)
+            for (int k = 0; k < 2 && s0 + k * AT_STEP < see; ++k)
+                attend_tile<DP, MT, F16, 2, true>(a, sh.t[(i - t0) & 1], k, s0 + k * AT_STEP - row.base + g * 4,
+                                                  row.end - row.base, above, mine, count, w);
         }
     }
 
