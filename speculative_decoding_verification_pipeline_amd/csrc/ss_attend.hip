@@ -26,7 +26,6 @@
 // has 8): a reference is set to 2^8 below the largest exponent and kept until one passes
 // 2^15, so a weight keeps its bits down to 2^-22 of the largest.
 #include <limits.h>
-#include <stdlib.h>
 
 #include "ss_device.h"
 #include "ss_internal.h"
@@ -34,6 +33,7 @@
 namespace ss {
 
 constexpr int AT_STEP = 32;                   // slots of a wave's step
+constexpr int AT_CUS = 256;
 constexpr float AT_NONE = -3.0e38f;           // reference of a row that has seen nothing
 constexpr float AT_SET = 8.0f;                // a reference is set so far below the largest exponent
 constexpr float AT_MOST = 32768.0f;           // and moves when a lane's four weights sum up to more
@@ -291,16 +291,15 @@ __device__ __forceinline__ void attend_scores(const AttendKeys<DP>& x, const Att
     }
 }
 
-// What tiles' scales come to: the factor on S with the softmax's scale, the exponent that
+// What two tiles' scales come to: the factor on S with the softmax's scale, the exponent that
 // a value's scale adds to its weight, and the factor that takes it off again.
-template <int NT>
 struct AttendScales {
-    float fk[NT], xv[NT], inv[NT];
+    float fk[2], xv[2], inv[2];
 };
 
-__device__ __forceinline__ AttendScales<2> scales_of(const Kv8Attend& a, const uint32_t (&ks)[2],
+__device__ __forceinline__ AttendScales scales_of(const Kv8Attend& a, const uint32_t (&ks)[2],
                                                   const uint32_t (&vs)[2], const bool (&ok)[2]) {
-    AttendScales<2> x;
+    AttendScales x;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         const uint32_t v = clamp_scale(vs[t]);
@@ -311,20 +310,20 @@ __device__ __forceinline__ AttendScales<2> scales_of(const Kv8Attend& a, const u
     return x;
 }
 
-// Weights of NT tiles under the rows' references. A lane's sums, which the rows need anyway,
+// Weights of two tiles under the rows' references. A lane's sums, which the rows need anyway,
 // tell whether a weight has passed 2^15; a row's reference then moves to its largest exponent
 // less 8, and the weights are formed again. (Looking for the largest exponent at every step
 // took a third of the vector instructions.)
-template <int DP, int MT, int NT>
-__device__ __forceinline__ void attend_weights(const AttendScales<NT>& x, const f32x4 (&s)[NT][MT],
-                                               AttendState<DP, MT>& w, u32x4 (&p)[NT / 2][MT]) {
-    float sum[NT][MT];
+template <int DP, int MT>
+__device__ __forceinline__ void attend_weights(const AttendScales& x, const f32x4 (&s)[2][MT],
+                                               AttendState<DP, MT>& w, u32x4 (&p)[MT]) {
+    float sum[2][MT];
     auto form = [&] {
         float most = 0.0f;
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
+            for (int t = 0; t < 2; ++t) {
                 const float c = x.xv[t] - w.ref[m];
                 float e[4];
 #pragma unroll
@@ -332,8 +331,8 @@ __device__ __forceinline__ void attend_weights(const AttendScales<NT>& x, const 
                     e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][m][i], x.fk[t], c));
                 sum[t][m] = (e[0] + e[1]) + (e[2] + e[3]);
                 most = fmaxf(most, sum[t][m]);
-                p[t / 2][m][t % 2 * 2] = as<uint32_t>(__builtin_convertvector((f32x2{e[0], e[1]}), h16x2));
-                p[t / 2][m][t % 2 * 2 + 1] = as<uint32_t>(__builtin_convertvector((f32x2{e[2], e[3]}), h16x2));
+                p[m][2 * t] = as<uint32_t>(__builtin_convertvector((f32x2{e[0], e[1]}), h16x2));
+                p[m][2 * t + 1] = as<uint32_t>(__builtin_convertvector((f32x2{e[2], e[3]}), h16x2));
             }
         }
         return most;
@@ -343,7 +342,7 @@ __device__ __forceinline__ void attend_weights(const AttendScales<NT>& x, const 
         for (int m = 0; m < MT; ++m) {
             float top = -INFINITY;
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
+            for (int t = 0; t < 2; ++t) {
                 const float most = fmaxf(fmaxf(s[t][m][0], s[t][m][1]), fmaxf(s[t][m][2], s[t][m][3]));
                 top = fmaxf(top, __builtin_fmaf(most, x.fk[t], x.xv[t]));
             }
@@ -362,7 +361,7 @@ __device__ __forceinline__ void attend_weights(const AttendScales<NT>& x, const 
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) w.l[m] = __builtin_fmaf(sum[t][m], x.inv[t], w.l[m]);
+        for (int t = 0; t < 2; ++t) w.l[m] = __builtin_fmaf(sum[t][m], x.inv[t], w.l[m]);
 }
 
 // A NaN among the values of one dimension reaches the rows that see it and no others: it is
@@ -500,11 +499,11 @@ __device__ __forceinline__ bool attend_share(const Kv8Attend& a, AttendPiece& x)
     for (int b0 = 0; b0 < a.s.B; b0 += WAVE)
         if (b0 + lane < a.s.B) total += attend_units<UNIT>(a, b0 + lane, last);
     total = (uint32_t)__builtin_amdgcn_readfirstlane(wave_sum_i((int)total));
-    x.share = max((total + a.shares - 1) / a.shares, (uint32_t)a.least);
+    x.share = (total + a.shares - 1) / a.shares;
     x.at = x.p * x.share;
     if (x.at >= total) return false;
     x.end = min(x.at + x.share, total);
-    for (int b0 = 0;; b0 += WAVE) {
+    for (int b0 = 0; b0 < a.s.B; b0 += WAVE) {
         const uint32_t u = b0 + lane < a.s.B ? attend_units<UNIT>(a, b0 + lane, last) : 0;
         const uint32_t to = x.before + (uint32_t)wave_incl_scan_i((int)u);
         const unsigned long long m = __ballot(x.at < to);
@@ -518,15 +517,15 @@ __device__ __forceinline__ bool attend_share(const Kv8Attend& a, AttendPiece& x)
         }
         x.before = (uint32_t)__builtin_amdgcn_readlane((int)to, WAVE - 1);
     }
+    return false;
 }
 
 // On to the next request of the share; false: it ends.
 template <int UNIT, int ROWS>
 __device__ __forceinline__ bool attend_on(const Kv8Attend& a, AttendPiece& x) {
     x.at = x.before + x.of;
-    if (x.at >= x.end) return false;
+    if (x.at >= x.end || ++x.b >= a.s.B) return false;
     x.before = x.at;
-    ++x.b;
     x.of = (uint32_t)__builtin_amdgcn_readfirstlane(
         (int)attend_units<UNIT>(a, x.b, attend_last<ROWS>(a, x.first)));
     attend_part(x);
@@ -731,175 +730,175 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : MT == 2 || DP == 128 ? 2 : 3) 
     if (!attend_share<UNIT, MT * 16>(args, pc)) return;
     ArgsAgain again;
     do {
-    const Kv8Attend& a = again.args();
-    const int lane = again.thread() & (WAVE - 1);
-    const int tid = again.thread();
-    const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
-    const int g = lane >> 4, col = lane & 15;
-    const int h = pc.h, first = pc.first;
-    const int rows = min(a.s.N * a.group - first, MT * 16);
-    const AttendRow row = attend_row(a, pc.b);
+        const Kv8Attend& a = again.args();
+        const int lane = again.thread() & (WAVE - 1);
+        const int tid = again.thread();
+        const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
+        const int g = lane >> 4, col = lane & 15;
+        const int h = pc.h, first = pc.first;
+        const int rows = min(a.s.N * a.group - first, MT * 16);
+        const AttendRow row = attend_row(a, pc.b);
 
-    AttendState<DP, MT> w;
-    unsigned long long rooted = 0;  // nodes that hang below the root
-    if (a.s.parents) rooted = __ballot(tree_node(a.s.parents + (int64_t)pc.b * a.s.N, a.s.N).above != 0);
-    uint32_t k_on = 0;  // the pieces of 64 dimensions that reach into the head's
+        AttendState<DP, MT> w;
+        unsigned long long rooted = 0;  // nodes that hang below the root
+        if (a.s.parents) rooted = __ballot(tree_node(a.s.parents + (int64_t)pc.b * a.s.N, a.s.N).above != 0);
+        uint32_t k_on = 0;  // the pieces of 64 dimensions that reach into the head's
 #pragma unroll
-    for (int c = 0; c < DP / 64; ++c) k_on |= (c * 64 + g * 16 < a.g.dim ? 1u : 0u) << c;
+        for (int c = 0; c < DP / 64; ++c) k_on |= (c * 64 + g * 16 < a.g.dim ? 1u : 0u) << c;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int r = first + min(m * 16 + col, rows - 1);
-        const int n = r / a.group;
-        w.l[m] = 0.0f;
-        w.ref[m] = AT_NONE;
-        const bool live = n < row.count && (!a.s.parents || (rooted >> (n & 63) & 1));
-        if (wave == 0 && g == 0) s_live[m * 16 + col] = live;
-        const uint16_t* q = a.q.data + pc.b * a.q.row + n * a.q.token +
-                            (h * a.group + r - n * a.group) * a.q.head + g * 16;
+        for (int m = 0; m < MT; ++m) {
+            const int r = first + min(m * 16 + col, rows - 1);
+            const int n = r / a.group;
+            w.l[m] = 0.0f;
+            w.ref[m] = AT_NONE;
+            const bool live = n < row.count && (!a.s.parents || (rooted >> (n & 63) & 1));
+            if (wave == 0 && g == 0) s_live[m * 16 + col] = live;
+            const uint16_t* q = a.q.data + pc.b * a.q.row + n * a.q.token +
+                                (h * a.group + r - n * a.group) * a.q.head + g * 16;
 #pragma unroll
-        for (int st = 0; st < DP / 32; ++st) {
-            w.q[m][st] = u32x4{0, 0, 0, 0};
-            if (k_on >> (st / 2) & 1)
-                w.q[m][st] = *reinterpret_cast<const u32x4*>(q + st / 2 * 64 + st % 2 * 8);
+            for (int st = 0; st < DP / 32; ++st) {
+                w.q[m][st] = u32x4{0, 0, 0, 0};
+                if (k_on >> (st / 2) & 1)
+                    w.q[m][st] = *reinterpret_cast<const u32x4*>(q + st / 2 * 64 + st % 2 * 8);
+            }
+#pragma unroll
+            for (int d = 0; d < DT; ++d) w.o[m][d] = f32x4{0, 0, 0, 0};
         }
-#pragma unroll
-        for (int d = 0; d < DT; ++d) w.o[m][d] = f32x4{0, 0, 0, 0};
-    }
 
-    // the slots of this piece, and of this wave of it, in steps
-    const int see = attend_see(a, row, (first + rows - 1) / a.group);
-    int full = min(row.base, row.end);  // slots before it all rows see
-    if (!a.s.parents && row.count) full = (int)min((int64_t)row.end, (int64_t)row.base + first / a.group + 1);
-    const int steps = (int)(((int64_t)see + AT_STEP - 1) / AT_STEP);
-    const int s0 = (int)min((int64_t)pc.from * WAVES, (int64_t)steps);
-    const int s1 = (int)min((int64_t)pc.to * WAVES, (int64_t)steps);
-    const int per = (s1 - s0 + WAVES - 1) / WAVES;
-    const int from = min(s0 + wave * per, s1), to = min(from + per, s1);
-    const int plain = max(min(to, full / AT_STEP), from);  // steps before it need no mask
-    if (from < to) {
-        AttendCursor at;
-        at.table = (const_i32)(a.s.t.tables + (int64_t)pc.b * a.s.t.stride);
-        at.tiles = a.g.page_size / 16;
-        at.block = from * 2 / at.tiles;
-        at.inner = from * 2 - at.block * at.tiles;
-        at.left = (row.end + 15) / 16 - from * 2;
-        uint32_t k_at[DP / 64], v_at[4];
+        // the slots of this piece, and of this wave of it, in steps
+        const int see = attend_see(a, row, (first + rows - 1) / a.group);
+        int full = min(row.base, row.end);  // slots before it all rows see
+        if (!a.s.parents && row.count) full = (int)min((int64_t)row.end, (int64_t)row.base + first / a.group + 1);
+        const int steps = (int)(((int64_t)see + AT_STEP - 1) / AT_STEP);
+        const int s0 = (int)min((int64_t)pc.from * WAVES, (int64_t)steps);
+        const int s1 = (int)min((int64_t)pc.to * WAVES, (int64_t)steps);
+        const int per = (s1 - s0 + WAVES - 1) / WAVES;
+        const int from = min(s0 + wave * per, s1), to = min(from + per, s1);
+        const int plain = max(min(to, full / AT_STEP), from);  // steps before it need no mask
+        if (from < to) {
+            AttendCursor at;
+            at.table = (const_i32)(a.s.t.tables + (int64_t)pc.b * a.s.t.stride);
+            at.tiles = a.g.page_size / 16;
+            at.block = from * 2 / at.tiles;
+            at.inner = from * 2 - at.block * at.tiles;
+            at.left = (row.end + 15) / 16 - from * 2;
+            uint32_t k_at[DP / 64], v_at[4];
 #pragma unroll
-        for (int c = 0; c < DP / 64; ++c)
-            k_at[c] = (uint32_t)col * (uint32_t)a.g.slot + (k_on >> c & 1 ? c * 64 + g * 16 : 0);
+            for (int c = 0; c < DP / 64; ++c)
+                k_at[c] = (uint32_t)col * (uint32_t)a.g.slot + (k_on >> c & 1 ? c * 64 + g * 16 : 0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            v_at[j] = (uint32_t)(g * 4 + j) * (uint32_t)a.g.slot + (col * DT < a.g.dim ? col * DT : 0);
-        AttendKeys<DP> k;
-        AttendValues<DP> v;
-        f32x4 e[2][MT];
-        u32x4 p[1][MT];
-        const uint32_t none[MT] = {};
-        attend_look(at);
-        AttendPlace place = attend_next(a, at, h);
-        load_keys<DP>(a, place, k_at, k);
-        // keys of the next step are on their way while this one's weights and values are
-        // worked on, values while its scores are (a step's values loaded a step ahead as well,
-        // into registers of their own: 1 to 3 % slower)
-        for (int s = from; s < plain; ++s) {
-            load_values<DP>(a, place, v_at, v);
-            if (!(k.ok[0] && k.ok[1])) put_out<DP>(k, v);
-            attend_scores<DP, MT, F16>(k, w, e);
-            const uint32_t ks[2] = {k.s[0], k.s[1]};
-            const bool ok[2] = {k.ok[0], k.ok[1]};
-            place = attend_next(a, at, h);  // behind the last step: page 0
+            for (int j = 0; j < 4; ++j)
+                v_at[j] = (uint32_t)(g * 4 + j) * (uint32_t)a.g.slot + (col * DT < a.g.dim ? col * DT : 0);
+            AttendKeys<DP> k;
+            AttendValues<DP> v;
+            f32x4 e[2][MT];
+            u32x4 p[MT];
+            const uint32_t none[MT] = {};
+            attend_look(at);
+            AttendPlace place = attend_next(a, at, h);
             load_keys<DP>(a, place, k_at, k);
-            attend_weights<DP, MT, 2>(scales_of(a, ks, v.s, ok), e, w, p);
-            attend_values<DP, MT, false>(v, p[0], none, w);
-        }
-        unsigned long long above = 0;
-        if (a.s.parents && plain < to)
-            above = tree_node(a.s.parents + (int64_t)pc.b * a.s.N, a.s.N).above;
-        // steps with slots that some row does not see
-#pragma clang loop unroll(disable)
-        for (int s = plain; s < to; ++s) {
-            if (s > plain) {
-                place = attend_next(a, at, h);
+            // keys of the next step are on their way while this one's weights and values are
+            // worked on, values while its scores are (a step's values loaded a step ahead as well,
+            // into registers of their own: 1 to 3 % slower)
+            for (int s = from; s < plain; ++s) {
+                load_values<DP>(a, place, v_at, v);
+                if (!(k.ok[0] && k.ok[1])) put_out<DP>(k, v);
+                attend_scores<DP, MT, F16>(k, w, e);
+                const uint32_t ks[2] = {k.s[0], k.s[1]};
+                const bool ok[2] = {k.ok[0], k.ok[1]};
+                place = attend_next(a, at, h);  // behind the last step: page 0
                 load_keys<DP>(a, place, k_at, k);
+                attend_weights<DP, MT>(scales_of(a, ks, v.s, ok), e, w, p);
+                attend_values<DP, MT, false>(v, p, none, w);
             }
-            load_values<DP>(a, place, v_at, v);
-            if (!(k.ok[0] && k.ok[1])) put_out<DP>(k, v);
-            attend_scores<DP, MT, F16>(k, w, e);
-            const int rel = s * AT_STEP - row.base + g * 4, end = row.end - row.base;
-            uint32_t vis[MT];
-            attend_mask<MT>(a, above, first, rows, rel, end, e, vis);
-            // values behind the last token are not numbers to be multiplied by 0
-            const uint32_t there = ((1u << min(max(end - rel, 0), 4)) - 1) |
-                                   ((1u << min(max(end - rel - 16, 0), 4)) - 1) << 4;
+            unsigned long long above = 0;
+            if (a.s.parents && plain < to)
+                above = tree_node(a.s.parents + (int64_t)pc.b * a.s.N, a.s.N).above;
+            // steps with slots that some row does not see
+#pragma clang loop unroll(disable)
+            for (int s = plain; s < to; ++s) {
+                if (s > plain) {
+                    place = attend_next(a, at, h);
+                    load_keys<DP>(a, place, k_at, k);
+                }
+                load_values<DP>(a, place, v_at, v);
+                if (!(k.ok[0] && k.ok[1])) put_out<DP>(k, v);
+                attend_scores<DP, MT, F16>(k, w, e);
+                const int rel = s * AT_STEP - row.base + g * 4, end = row.end - row.base;
+                uint32_t vis[MT];
+                attend_mask<MT>(a, above, first, rows, rel, end, e, vis);
+                // values behind the last token are not numbers to be multiplied by 0
+                const uint32_t there = ((1u << min(max(end - rel, 0), 4)) - 1) |
+                                       ((1u << min(max(end - rel - 16, 0), 4)) - 1) << 4;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < 8; ++j) {
 #pragma unroll
-                for (int c = 0; c < DP / 64; ++c)
-                    set_word<DP>(v.v[j], c, keep_if(there, j, word_of<DP>(v.v[j], c), 0u));
+                    for (int c = 0; c < DP / 64; ++c)
+                        set_word<DP>(v.v[j], c, keep_if(there, j, word_of<DP>(v.v[j], c), 0u));
+                }
+                attend_weights<DP, MT>(scales_of(a, k.s, v.s, k.ok), e, w, p);
+                attend_values<DP, MT, true>(v, p, vis, w);
             }
-            attend_weights<DP, MT, 2>(scales_of(a, k.s, v.s, k.ok), e, w, p);
-            attend_values<DP, MT, true>(v, p[0], vis, w);
         }
-    }
 
-    // the waves' sums to one reference
+        // the waves' sums to one reference
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        w.l[m] += xor_lane_f<16>(w.l[m]);
-        w.l[m] += xor_lane_f<32>(w.l[m]);
-        if (g == 0) {
-            s_ref[wave][m * 16 + col] = w.ref[m];
-            s_l[wave][m * 16 + col] = w.l[m];
-        }
-    }
-    // a thread adds pairs of entries of a row, neighbours' pairs side by side
-    constexpr int PER_ROW = WAVES * 4;
-    const int r16 = tid / PER_ROW, part = tid % PER_ROW;
-    float* slot = a.part + (int64_t)attend_left(a, pc, pc.p, pc.c == 0) * SLOT;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        __syncthreads();
-        float ref = s_ref[0][m * 16 + col];
-#pragma unroll
-        for (int v = 1; v < WAVES; ++v) ref = fmaxf(ref, s_ref[v][m * 16 + col]);
-        const float f = __builtin_amdgcn_exp2f(w.ref[m] - ref);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int d = 0; d < DT; d += 4) {
-                const f32x4 v = {w.o[m][d][i] * f, w.o[m][d + 1][i] * f, w.o[m][d + 2][i] * f,
-                                 w.o[m][d + 3][i] * f};
-                *reinterpret_cast<f32x4*>(&s_o[wave][col][(g * 4 + i) * DT + d]) = v;
+        for (int m = 0; m < MT; ++m) {
+            w.l[m] += xor_lane_f<16>(w.l[m]);
+            w.l[m] += xor_lane_f<32>(w.l[m]);
+            if (g == 0) {
+                s_ref[wave][m * 16 + col] = w.ref[m];
+                s_l[wave][m * 16 + col] = w.l[m];
             }
-        __syncthreads();
-        const int rr = m * 16 + r16;
-        if (rr >= rows) continue;
-        ref = s_ref[0][rr];
-#pragma unroll
-        for (int v = 1; v < WAVES; ++v) ref = fmaxf(ref, s_ref[v][rr]);
-        float l = 0.0f;
-#pragma unroll
-        for (int v = 0; v < WAVES; ++v)
-            l = __builtin_fmaf(s_l[v][rr], __builtin_amdgcn_exp2f(s_ref[v][rr] - ref), l);
-        const bool live = s_live[rr] != 0;
-        const AttendOut out = attend_out(a, pc.b, h, first + rr);
-        const float to = attend_factor(l, live);
-        if (part == 0) {
-            if (pc.n > 1) put(slot + rr * 2, ref, l);
-            else if (a.lse) a.lse[out.lse] = attend_lse(ref, l, live);
         }
+        // a thread adds pairs of entries of a row, neighbours' pairs side by side
+        constexpr int PER_ROW = WAVES * 4;
+        const int r16 = tid / PER_ROW, part = tid % PER_ROW;
+        float* slot = a.part + (int64_t)attend_left(a, pc, pc.p, pc.c == 0) * SLOT;
 #pragma unroll
-        for (int k = 0; k < DP / 2 / PER_ROW; ++k) {
-            const int e = (k * PER_ROW + part) * 2;
-            f32x2 o = {0.0f, 0.0f};
+        for (int m = 0; m < MT; ++m) {
+            __syncthreads();
+            float ref = s_ref[0][m * 16 + col];
 #pragma unroll
-            for (int v = 0; v < WAVES; ++v) o += *reinterpret_cast<const f32x2*>(&s_o[v][r16][e]);
-            if (pc.n > 1) put(slot + 2 * MT * 16 + rr * DP + e, o[0], o[1]);
-            else if (e < a.g.dim) put_pair<F16>(out.to + e, o[0], o[1], to, live);
+            for (int v = 1; v < WAVES; ++v) ref = fmaxf(ref, s_ref[v][m * 16 + col]);
+            const float f = __builtin_amdgcn_exp2f(w.ref[m] - ref);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int d = 0; d < DT; d += 4) {
+                    const f32x4 v = {w.o[m][d][i] * f, w.o[m][d + 1][i] * f, w.o[m][d + 2][i] * f,
+                                     w.o[m][d + 3][i] * f};
+                    *reinterpret_cast<f32x4*>(&s_o[wave][col][(g * 4 + i) * DT + d]) = v;
+                }
+            __syncthreads();
+            const int rr = m * 16 + r16;
+            if (rr >= rows) continue;
+            ref = s_ref[0][rr];
+#pragma unroll
+            for (int v = 1; v < WAVES; ++v) ref = fmaxf(ref, s_ref[v][rr]);
+            float l = 0.0f;
+#pragma unroll
+            for (int v = 0; v < WAVES; ++v)
+                l = __builtin_fmaf(s_l[v][rr], __builtin_amdgcn_exp2f(s_ref[v][rr] - ref), l);
+            const bool live = s_live[rr] != 0;
+            const AttendOut out = attend_out(a, pc.b, h, first + rr);
+            const float to = attend_factor(l, live);
+            if (part == 0) {
+                if (pc.n > 1) put(slot + rr * 2, ref, l);
+                else if (a.lse) a.lse[out.lse] = attend_lse(ref, l, live);
+            }
+#pragma unroll
+            for (int k = 0; k < DP / 2 / PER_ROW; ++k) {
+                const int e = (k * PER_ROW + part) * 2;
+                f32x2 o = {0.0f, 0.0f};
+#pragma unroll
+                for (int v = 0; v < WAVES; ++v) o += *reinterpret_cast<const f32x2*>(&s_o[v][r16][e]);
+                if (pc.n > 1) put(slot + 2 * MT * 16 + rr * DP + e, o[0], o[1]);
+                else if (e < a.g.dim) put_pair<F16>(out.to + e, o[0], o[1], to, live);
+            }
         }
-    }
-    if (pc.n > 1) add_pieces<DP, MT * 16, F16>(a, pc, rows, &s_o[0][0][0], s_live);
-    __syncthreads();  // LDS is read
+        if (pc.n > 1) add_pieces<DP, MT * 16, F16>(a, pc, rows, &s_o[0][0][0], s_live);
+        __syncthreads();  // LDS is read
     } while (attend_on<UNIT, MT * 16>(args, pc));
 }
 
@@ -1009,18 +1008,18 @@ __device__ __forceinline__ void leave_raw(const Kv8Attend& a, AttendRaw<DP>& x, 
     }
 }
 
-// NT tiles of 16 slots of the tile in LDS: all four, or two that need a mask, the half-th. rel
-// and end as attend_mask has them, for the wave's rows from `first` on.
-template <int DP, int MT, bool F16, int NT, bool MASK>
+// The half-th 32 slots of the tile in LDS. rel and end as attend_mask has them, for the wave's
+// rows from `first` on.
+template <int DP, int MT, bool F16, bool MASK>
 __device__ __forceinline__ void attend_tile(const Kv8Attend& a, const AttendTile<DP>& t, int half, int rel,
                                             int end, unsigned long long above, int first, int rows,
                                             AttendState<DP, MT>& w) {
     const int lane = threadIdx.x & (WAVE - 1);
-    f32x4 e[NT][MT];
-    u32x4 p[NT / 2][MT];
-    AttendScales<NT> x;
+    f32x4 e[2][MT];
+    u32x4 p[MT];
+    AttendScales x;
 #pragma unroll
-    for (int k = 0; k < NT; ++k) {
+    for (int k = 0; k < 2; ++k) {
         const f32x4 v = t.x[half * 2 + k];
         x.fk[k] = v[0];
         x.xv[k] = v[1];
@@ -1036,26 +1035,23 @@ __device__ __forceinline__ void attend_tile(const Kv8Attend& a, const AttendTile
     }
     uint32_t vis[MT] = {};
     if constexpr (MASK) attend_mask<MT>(a, above, first, rows, rel, end, e, vis);
-    attend_weights<DP, MT, NT>(x, e, w, p);
+    attend_weights<DP, MT>(x, e, w, p);
 #pragma unroll
-    for (int k = 0; k < NT / 2; ++k) {
+    for (int d = 0; d < DP / 16; ++d) {
+        u32x4 v = t.v[half][d][lane];
+        if constexpr (MASK) {
+            f32x4* o[MT];
 #pragma unroll
-        for (int d = 0; d < DP / 16; ++d) {
-            u32x4 v = t.v[half + k][d][lane];
-            if constexpr (MASK) {
-                f32x4* o[MT];
-#pragma unroll
-                for (int m = 0; m < MT; ++m) o[m] = &w.o[m][d];
-                v = take_nans<MT>(v, vis, o);
-            }
-#pragma unroll
-            for (int m = 0; m < MT; ++m) w.o[m][d] = mfma<true>(v, p[k][m], w.o[m][d]);
+            for (int m = 0; m < MT; ++m) o[m] = &w.o[m][d];
+            v = take_nans<MT>(v, vis, o);
         }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) w.o[m][d] = mfma<true>(v, p[m], w.o[m][d]);
     }
 }
 
 template <int DP, int MT, bool F16>
-__global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attend_rows(Kv8Attend args) {
+__global__ __launch_bounds__(256, 2) void k_attend_rows(Kv8Attend args) {
     constexpr int WAVES = 4;
     constexpr int DT = DP / 16;
     constexpr int ROWS = WAVES * MT * 16;
@@ -1070,196 +1066,198 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attend_rows(Kv8Atten
     if (!attend_share<AT_TILE, ROWS>(args, pc)) return;
     ArgsAgain again;
     do {
-    const Kv8Attend& a = again.args();
-    const int lane = again.thread() & (WAVE - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(again.thread() / WAVE);
-    const int g = lane >> 4, col = lane & 15;
-    const int h = pc.h, first = pc.first;
-    const int rows = min(a.s.N * a.group - first, ROWS);
-    const AttendRow row = attend_row(a, pc.b);
+        const Kv8Attend& a = again.args();
+        const int lane = again.thread() & (WAVE - 1);
+        const int wave = __builtin_amdgcn_readfirstlane(again.thread() / WAVE);
+        const int g = lane >> 4, col = lane & 15;
+        const int h = pc.h, first = pc.first;
+        const int rows = min(a.s.N * a.group - first, ROWS);
+        const AttendRow row = attend_row(a, pc.b);
 
-    const int mine = first + wave * MT * 16;                       // rows of this wave
-    const int count = min(max(rows - wave * MT * 16, 0), MT * 16);
-    unsigned long long above = 0, rooted = 0;
-    if (a.s.parents) {
-        above = tree_node(a.s.parents + (int64_t)pc.b * a.s.N, a.s.N).above;
-        rooted = __ballot(above != 0);
-    }
-    AttendState<DP, MT> w;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int r = mine + min(m * 16 + col, max(count, 1) - 1);
-        const int rc = min(r, first + rows - 1);
-        const int n = rc / a.group;
-        w.l[m] = 0.0f;
-        w.ref[m] = AT_NONE;
-        if (g == 0)
-            s_live[wave * MT * 16 + m * 16 + col] = n < row.count && (!a.s.parents || (rooted >> (n & 63) & 1));
-        const uint16_t* q = a.q.data + pc.b * a.q.row + n * a.q.token +
-                            (h * a.group + rc - n * a.group) * a.q.head + g * 16;
-#pragma unroll
-        for (int st = 0; st < DP / 32; ++st) {
-            w.q[m][st] = u32x4{0, 0, 0, 0};
-            if (st / 2 * 64 + g * 16 < a.g.dim)
-                w.q[m][st] = *reinterpret_cast<const u32x4*>(q + st / 2 * 64 + st % 2 * 8);
+        const int mine = first + wave * MT * 16;                       // rows of this wave
+        const int count = min(max(rows - wave * MT * 16, 0), MT * 16);
+        unsigned long long above = 0, rooted = 0;
+        if (a.s.parents) {
+            above = tree_node(a.s.parents + (int64_t)pc.b * a.s.N, a.s.N).above;
+            rooted = __ballot(above != 0);
         }
+        AttendState<DP, MT> w;
 #pragma unroll
-        for (int d = 0; d < DT; ++d) w.o[m][d] = f32x4{0, 0, 0, 0};
-    }
-
-    // tiles of this piece, and what this wave's rows see of them
-    const int see = count ? attend_see(a, row, (mine + count - 1) / a.group) : 0;
-    int full = min(row.base, row.end);
-    if (!a.s.parents && row.count) full = (int)min((int64_t)row.end, (int64_t)row.base + first / a.group + 1);
-    const int t0 = pc.from;
-    const int t1 = min(pc.to, (int)(((int64_t)attend_see(a, row, (first + rows - 1) / a.group) + AT_TILE - 1) / AT_TILE));
-    const int t2 = max(min(full / AT_TILE, t1), t0);  // tiles before it need no mask
-    if (t0 < t1) {
-        AttendWalk at;
-        at.table = (const_i32)(a.s.t.tables + (int64_t)pc.b * a.s.t.stride);
-        at.tiles = a.g.page_size / 16;
-        at.over = 4 / at.tiles;
-        at.ahead = 4 - at.over * at.tiles;
-        at.block = (t0 * 4 + wave) / at.tiles;
-        at.inner = t0 * 4 + wave - at.block * at.tiles;
-        at.left = row.end - (t0 * AT_TILE + wave * 16);
-        uint32_t k_at[DP / 64], v_at[4];
+        for (int m = 0; m < MT; ++m) {
+            const int r = mine + min(m * 16 + col, max(count, 1) - 1);
+            const int rc = min(r, first + rows - 1);
+            const int n = rc / a.group;
+            w.l[m] = 0.0f;
+            w.ref[m] = AT_NONE;
+            if (g == 0)
+                s_live[wave * MT * 16 + m * 16 + col] = n < row.count && (!a.s.parents || (rooted >> (n & 63) & 1));
+            const uint16_t* q = a.q.data + pc.b * a.q.row + n * a.q.token +
+                                (h * a.group + rc - n * a.group) * a.q.head + g * 16;
 #pragma unroll
-        for (int c = 0; c < DP / 64; ++c)
-            k_at[c] = (uint32_t)col * (uint32_t)a.g.slot + (c * 64 + g * 16 < a.g.dim ? c * 64 + g * 16 : 0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            v_at[j] = (uint32_t)(g * 4 + j) * (uint32_t)a.g.slot + (col * DT < a.g.dim ? col * DT : 0);
-        AttendRaw<DP> raw;
-        load_raw<DP>(a, at, h, k_at, v_at, raw);
-        leave_raw<DP, F16>(a, raw, wave, sh.t[0]);
-        load_raw<DP>(a, at, h, k_at, v_at, raw);
-        auto next = [&](int i) {
-            __syncthreads();
-            if (i + 1 < t1) {
-                leave_raw<DP, F16>(a, raw, wave, sh.t[(i - t0 + 1) & 1]);
-                load_raw<DP>(a, at, h, k_at, v_at, raw);
+            for (int st = 0; st < DP / 32; ++st) {
+                w.q[m][st] = u32x4{0, 0, 0, 0};
+                if (st / 2 * 64 + g * 16 < a.g.dim)
+                    w.q[m][st] = *reinterpret_cast<const u32x4*>(q + st / 2 * 64 + st % 2 * 8);
             }
-        };
-        // tiles that all rows see
-        for (int i = t0; i < t2; ++i) {
-            next(i);
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-                attend_tile<DP, MT, F16, 2, false>(a, sh.t[(i - t0) & 1], k, 0, 0, 0, mine, count, w);
+            for (int d = 0; d < DT; ++d) w.o[m][d] = f32x4{0, 0, 0, 0};
         }
-        // those that some row does not see, of the step's own tokens or behind the last one: in a
-        // loop of their own, or what they need is kept, in scratch memory, through the other
-#pragma clang loop unroll(disable)
-        for (int i = t2; i < t1; ++i) {
-            next(i);
-            const int s0 = i * AT_TILE;
-#pragma clang loop unroll(disable)
-            for (int k = 0; k < 2 && s0 + k * AT_STEP < see; ++k)
-                attend_tile<DP, MT, F16, 2, true>(a, sh.t[(i - t0) & 1], k, s0 + k * AT_STEP - row.base + g * 4,
-                                                  row.end - row.base, above, mine, count, w);
-        }
-    }
 
-    float* slot = a.part + (int64_t)attend_left(a, pc, pc.p, pc.c == 0) * SLOT;
-    if (pc.n > 1) __syncthreads();  // the tiles are read; what pieces leave goes through LDS, in whole lines
+        // tiles of this piece, and what this wave's rows see of them
+        const int see = count ? attend_see(a, row, (mine + count - 1) / a.group) : 0;
+        int full = min(row.base, row.end);
+        if (!a.s.parents && row.count) full = (int)min((int64_t)row.end, (int64_t)row.base + first / a.group + 1);
+        const int t0 = pc.from;
+        const int t1 = min(pc.to, (int)(((int64_t)attend_see(a, row, (first + rows - 1) / a.group) + AT_TILE - 1) / AT_TILE));
+        const int t2 = max(min(full / AT_TILE, t1), t0);  // tiles before it need no mask
+        if (t0 < t1) {
+            AttendWalk at;
+            at.table = (const_i32)(a.s.t.tables + (int64_t)pc.b * a.s.t.stride);
+            at.tiles = a.g.page_size / 16;
+            at.over = 4 / at.tiles;
+            at.ahead = 4 - at.over * at.tiles;
+            at.block = (t0 * 4 + wave) / at.tiles;
+            at.inner = t0 * 4 + wave - at.block * at.tiles;
+            at.left = row.end - (t0 * AT_TILE + wave * 16);
+            uint32_t k_at[DP / 64], v_at[4];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        w.l[m] += xor_lane_f<16>(w.l[m]);
-        w.l[m] += xor_lane_f<32>(w.l[m]);
-        const int r0 = wave * MT * 16 + m * 16, rr = r0 + col;
-        if (pc.n > 1) {
-            if (g == 0 && rr < rows) put(slot + rr * 2, w.ref[m], w.l[m]);
+            for (int c = 0; c < DP / 64; ++c)
+                k_at[c] = (uint32_t)col * (uint32_t)a.g.slot + (c * 64 + g * 16 < a.g.dim ? c * 64 + g * 16 : 0);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int d = 0; d < DT; d += 4)
-                    *reinterpret_cast<f32x4*>(&sh.o[wave][col][(g * 4 + k) * DT + d]) =
-                        f32x4{w.o[m][d][k], w.o[m][d + 1][k], w.o[m][d + 2][k], w.o[m][d + 3][k]};
-            __builtin_amdgcn_wave_barrier();  // a wave's own part: its LDS operations stay in order
-#pragma unroll
-            for (int k = 0; k < DP / 8; ++k) {
-                const int r = (k * WAVE + lane) * 2 / DP, e = (k * WAVE + lane) * 2 % DP;
-                const f32x2 o = *reinterpret_cast<const f32x2*>(&sh.o[wave][r][e]);
-                if (r0 + r < rows) put(slot + 2 * ROWS + (r0 + r) * DP + e, o[0], o[1]);
-            }
-            __builtin_amdgcn_wave_barrier();
-        } else if (rr < rows) {  // a lane has 4 * DT neighbouring entries of a row
-            const bool live = s_live[rr] != 0;
-            const float f = attend_factor(w.l[m], live);
-            const AttendOut out = attend_out(a, pc.b, h, first + rr);
-            if (a.lse && g == 0) a.lse[out.lse] = attend_lse(w.ref[m], w.l[m], live);
-#pragma unroll
-            for (int e = 0; e < 4 * DT; e += 8) {
-                if (g * 4 * DT + e >= a.g.dim) break;
-                u32x4 v;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int x = e + 2 * k;
-                    v[k] = live ? narrow<F16>(w.o[m][x % DT][x / DT] * f, w.o[m][x % DT + 1][x / DT] * f) : 0u;
+            for (int j = 0; j < 4; ++j)
+                v_at[j] = (uint32_t)(g * 4 + j) * (uint32_t)a.g.slot + (col * DT < a.g.dim ? col * DT : 0);
+            AttendRaw<DP> raw;
+            load_raw<DP>(a, at, h, k_at, v_at, raw);
+            leave_raw<DP, F16>(a, raw, wave, sh.t[0]);
+            load_raw<DP>(a, at, h, k_at, v_at, raw);
+            auto next = [&](int i) {
+                __syncthreads();
+                if (i + 1 < t1) {
+                    leave_raw<DP, F16>(a, raw, wave, sh.t[(i - t0 + 1) & 1]);
+                    load_raw<DP>(a, at, h, k_at, v_at, raw);
                 }
-                *reinterpret_cast<u32x4*>(out.to + g * 4 * DT + e) = v;
+            };
+            // tiles that all rows see
+            for (int i = t0; i < t2; ++i) {
+                next(i);
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    attend_tile<DP, MT, F16, false>(a, sh.t[(i - t0) & 1], k, 0, 0, 0, mine, count, w);
+            }
+            // those that some row does not see, of the step's own tokens or behind the last one: in a
+            // loop of their own, or what they need is kept, in scratch memory, through the other
+#pragma clang loop unroll(disable)
+            for (int i = t2; i < t1; ++i) {
+                next(i);
+                const int s0 = i * AT_TILE;
+#pragma clang loop unroll(disable)
+                for (int k = 0; k < 2 && s0 + k * AT_STEP < see; ++k)
+                    attend_tile<DP, MT, F16, true>(a, sh.t[(i - t0) & 1], k, s0 + k * AT_STEP - row.base + g * 4,
+                                                      row.end - row.base, above, mine, count, w);
             }
         }
-    }
-    if (pc.n > 1) add_pieces<DP, ROWS, F16>(a, pc, rows, &sh.o[0][0][0], s_live);
-    __syncthreads();  // LDS is read
+
+        float* slot = a.part + (int64_t)attend_left(a, pc, pc.p, pc.c == 0) * SLOT;
+        if (pc.n > 1) __syncthreads();  // the tiles are read; what pieces leave goes through LDS, in whole lines
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            w.l[m] += xor_lane_f<16>(w.l[m]);
+            w.l[m] += xor_lane_f<32>(w.l[m]);
+            const int r0 = wave * MT * 16 + m * 16, rr = r0 + col;
+            if (pc.n > 1) {
+                if (g == 0 && rr < rows) put(slot + rr * 2, w.ref[m], w.l[m]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int d = 0; d < DT; d += 4)
+                        *reinterpret_cast<f32x4*>(&sh.o[wave][col][(g * 4 + k) * DT + d]) =
+                            f32x4{w.o[m][d][k], w.o[m][d + 1][k], w.o[m][d + 2][k], w.o[m][d + 3][k]};
+                __builtin_amdgcn_wave_barrier();  // a wave's own part: its LDS operations stay in order
+#pragma unroll
+                for (int k = 0; k < DP / 8; ++k) {
+                    const int r = (k * WAVE + lane) * 2 / DP, e = (k * WAVE + lane) * 2 % DP;
+                    const f32x2 o = *reinterpret_cast<const f32x2*>(&sh.o[wave][r][e]);
+                    if (r0 + r < rows) put(slot + 2 * ROWS + (r0 + r) * DP + e, o[0], o[1]);
+                }
+                __builtin_amdgcn_wave_barrier();
+            } else if (rr < rows) {  // a lane has 4 * DT neighbouring entries of a row
+                const bool live = s_live[rr] != 0;
+                const float f = attend_factor(w.l[m], live);
+                const AttendOut out = attend_out(a, pc.b, h, first + rr);
+                if (a.lse && g == 0) a.lse[out.lse] = attend_lse(w.ref[m], w.l[m], live);
+#pragma unroll
+                for (int e = 0; e < 4 * DT; e += 8) {
+                    if (g * 4 * DT + e >= a.g.dim) break;
+                    u32x4 v;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int x = e + 2 * k;
+                        v[k] = live ? narrow<F16>(w.o[m][x % DT][x / DT] * f, w.o[m][x % DT + 1][x / DT] * f) : 0u;
+                    }
+                    *reinterpret_cast<u32x4*>(out.to + g * 4 * DT + e) = v;
+                }
+            }
+        }
+        if (pc.n > 1) add_pieces<DP, ROWS, F16>(a, pc, rows, &sh.o[0][0][0], s_live);
+        __syncthreads();  // LDS is read
     } while (attend_on<AT_TILE, ROWS>(args, pc));
 }
 
-// Into how many shares the slots of a head and block of rows are cut.
+// Into how many shares the slots of a head and block of rows are cut: as many as there are CUs
+// (few rows: a workgroup a CU; twice as many took 60 -> 73 us for one request of 131072 slots and
+// 115 -> 130 for 64 uneven ones of 4000, since more pages are read at a time) or twice that (many
+// rows: two a CU; 32 trees of 64 rows over 2000 slots 81 -> 68 us).
 template <int ROWS>
-static int64_t attend_grid(Kv8Attend& a, int dp, int target) {
+static int64_t attend_grid(Kv8Attend& a, int dp, int workgroups) {
     a.blocks = (int)(((int64_t)a.s.N * a.group + ROWS - 1) / ROWS);
     const int64_t lines = (int64_t)a.g.heads * a.blocks;
     const int64_t most = KV8_PART_FLOATS / (2 * attend_slot(dp, ROWS));
-    if (target > most) target = (int)most;
-    a.shares = (int)(target / lines);
-    // whole requests where there are many, or where the card is full of blocks of rows
-    if (lines * a.s.B >= 4 * target || a.s.B * ((int64_t)a.g.max_blocks * a.g.page_size / 64 + 1) > INT_MAX)
+    if (workgroups > most) workgroups = (int)most;
+    a.shares = (int)(workgroups / lines);
+    // whole requests where there are many, or where lines alone fill the card
+    if (lines * a.s.B >= 4 * workgroups || a.s.B * ((int64_t)a.g.max_blocks * a.g.page_size / 64 + 1) > INT_MAX)
         a.shares = 0;
     return lines * (a.shares ? a.shares : a.s.B);
 }
 
 template <int DP, int MT, bool F16>
-static hipError_t launch_attend(Kv8Attend a, hipStream_t st) {
-    static const int target = getenv("AT_TARGET") ? atoi(getenv("AT_TARGET")) : 256;
-    static const int least = getenv("AT_LEAST") ? atoi(getenv("AT_LEAST")) : 1;
-    a.least = least;
-    const int64_t grid = attend_grid<MT * 16>(a, DP, target);
+static hipError_t launch_few(Kv8Attend a, hipStream_t st) {
+    const int64_t grid = attend_grid<MT * 16>(a, DP, AT_CUS);
     if (grid > INT_MAX) return hipErrorInvalidValue;
     hipLaunchKernelGGL((k_attend<DP, MT, F16>), dim3((unsigned)grid), dim3(256), 0, st, a);
     return hipGetLastError();
 }
 
 template <int DP, int MT, bool F16>
-static hipError_t launch_rows(Kv8Attend a, hipStream_t st) {
-    static const int target = getenv("AT_TARGET2") ? atoi(getenv("AT_TARGET2")) : 512;
-    static const int least = getenv("AT_LEAST2") ? atoi(getenv("AT_LEAST2")) : 1;
-    a.least = least;
-    const int64_t grid = attend_grid<MT * 64>(a, DP, target);
+static hipError_t launch_many(Kv8Attend a, hipStream_t st) {
+    const int64_t grid = attend_grid<MT * 64>(a, DP, 2 * AT_CUS);
     if (grid > INT_MAX) return hipErrorInvalidValue;
     hipLaunchKernelGGL((k_attend_rows<DP, MT, F16>), dim3((unsigned)grid), dim3(256), 0, st, a);
     return hipGetLastError();
 }
 
+// Up to 32 rows a wave takes them all, and heads above 128 always go that way: 32 requests of 8
+// nodes and 4 query heads a head over 2000 slots take 50 us so and 57 where four waves share
+// keys and values (16 nodes: 73 and 62); in heads of 256 16 nodes take 118 and 208, a prompt's
+// 2048 tokens over 6144 slots 410 and 562. Above 64 rows a wave takes 32 of them; so it does
+// not where workgroups of 128 rows leave CUs idle.
 template <int DP, bool F16>
-static hipError_t launch_attend_by_rows(const Kv8Attend& a, hipStream_t st) {
+static hipError_t launch_attend_rows(const Kv8Attend& a, hipStream_t st) {
     const int64_t rows = (int64_t)a.s.N * a.group;
-    static const int sh = getenv("AT_SHARED") ? atoi(getenv("AT_SHARED")) : 32;
-    if (rows > sh) {
-        if (rows <= 64 || DP == 256) return launch_rows<DP, 1, F16>(a, st);
-        return launch_rows<DP, DP == 256 ? 1 : 2, F16>(a, st);
+    if (rows <= 16) return launch_few<DP, 1, F16>(a, st);
+    if (rows <= 32 || DP > 128) return launch_few<DP, 2, F16>(a, st);
+    if constexpr (DP <= 128) {
+        if (rows <= 64 || (rows + 127) / 128 * a.g.heads * a.s.B < AT_CUS) return launch_many<DP, 1, F16>(a, st);
+        return launch_many<DP, 2, F16>(a, st);
     }
-    if (rows <= 16) return launch_attend<DP, 1, F16>(a, st);
-    return launch_attend<DP, 2, F16>(a, st);
+    return hipErrorInvalidValue;
 }
 
 template <bool F16>
 static hipError_t launch_attend_dim(const Kv8Attend& a, hipStream_t st) {
-    if (a.g.dim <= 64) return launch_attend_by_rows<64, F16>(a, st);
-    if (a.g.dim <= 128) return launch_attend_by_rows<128, F16>(a, st);
-    return launch_attend_by_rows<256, F16>(a, st);
+    if (a.g.dim <= 64) return launch_attend_rows<64, F16>(a, st);
+    if (a.g.dim <= 128) return launch_attend_rows<128, F16>(a, st);
+    return launch_attend_rows<256, F16>(a, st);
 }
 
 hipError_t launch_kv8_attend(const Kv8Attend& a, ss_dtype dt, hipStream_t st) {

@@ -442,9 +442,9 @@ struct Kv8Read {
     int B, N;
 };
 
-// Attention: a workgroup takes a piece of one row's slots, one head of the cache and
-// 16 * tiles rows (query heads of tokens). What splits leave for the last of a row lies
-// in `part`.
+// Attention: a workgroup takes a share of the requests' slots, for one head of the cache and a
+// block of rows (query heads of tokens). What it sums up of requests that others go on with
+// lies in `part`.
 struct Kv8Attend {
     Kv8Geo g;
     Kv8Step s;
@@ -456,7 +456,6 @@ struct Kv8Attend {
     int blocks;       // blocks of rows of one request and head
     int shares;       // that the slots of a head and block of rows over all requests are cut
                       //   into; 0: none is cut
-    int least;        // units of a share, at least
     float scale_log2; // scale * log2(e)
     float* part;
     int32_t* arrived;
