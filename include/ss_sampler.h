@@ -666,8 +666,8 @@ ss_status ss_rotate(int32_t device, const ss_rotary* rotary, ss_dtype dtype, int
 /* ss_cache_write -- write a step's keys and values into planes k_plane and v_plane.
  *   keys, values  [B, N, heads, dim] of dtype (SS_BF16 or SS_F16), heads and dim those of
  *                 the cache.
- *   rotary        NULL, or the rotation of the keys (and queries) before they are written:
- *                 its dim and the halves of its pairs multiples of 16 and 8.
+ *   rotary        NULL, or the rotation of the keys (and queries) before they are written;
+ *                 its dim a multiple of 16.
  *   positions     [B, N] int32 positions for the rotation, or NULL: base_b + i, in a tree
  *                 base_b + the node's depth.
  *   queries       NULL, or [B, N, q_heads, dim] turned along into out_queries (which may
@@ -715,8 +715,8 @@ ss_status ss_cache_read(ss_cache* c, const ss_block_tables* t, const int32_t* st
  * Errors of the calls on a scaled cache, before any launch: as of the other ss_cache
  * calls, and SS_ERR_INVALID_ARG for a handle without scales, planes out of range or the
  * same twice, another dtype, sizes out of range or a rotary without turns;
- * SS_ERR_UNSUPPORTED for data or strides that are not aligned and a rotary whose sizes
- * are not multiples as said. */
+ * SS_ERR_UNSUPPORTED for data or strides that are not aligned and a rotary whose dim is no
+ * multiple of 16. */
 ss_status ss_cache_attend(ss_cache* c, const ss_block_tables* t, const ss_cache_step* step,
                           int32_t k_plane, int32_t v_plane, ss_dtype dtype,
                           const ss_heads* queries, const ss_heads* out, int32_t q_heads,

@@ -1,0 +1,110 @@
+"""Host-side argument checks, without a GPU, of rotary positions, 8-bit pages and
+attention over them."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+from speculative_decoding_verification_pipeline_amd import sampler as SM
+from speculative_decoding_verification_pipeline_amd.cache import PageCache
+
+BAD, NOT_SERVED = SM.SS_ERR_INVALID_ARG, SM.SS_ERR_UNSUPPORTED
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(SM.LIB_PATH):
+        from speculative_decoding_verification_pipeline_amd import build
+        build.build()
+    return SM.load_library()
+
+
+def test_packed_structures_have_the_c_layout():
+    assert len(SM._pack_tables(0, 0, 0, 0, 0)) == ctypes.sizeof(SM.CBlockTables) == 40
+    t = SM.CBlockTables.from_buffer_copy(SM._pack_tables(64, 7, 3, 128, 256))
+    assert (t.tables, t.stride, t.rows, t.ref, t.len) == (64, 7, 3, 128, 256)
+    assert len(SM._pack_heads(0, 0, 0, 0)) == 32 and len(SM._pack_rotary(0, 0, 0, 1.0)) == 24
+    assert len(SM._pack_step(0, 0, 0, 0, 0, 0)) == 40
+
+
+def test_calls_reject_null_handles(lib):
+    t, step = SM._pack_tables(64, 8, 1, 64, 64), SM._pack_step(1, 1, 0, 0, 0, 0)
+    h = SM._pack_heads(64, 64, 64, 64)
+    assert lib.ss_cache_write(None, t, step, 0, 1, 1, h, h, None, None, None, None, 0, None) == BAD
+    assert lib.ss_cache_read(None, t, None, None, 1, 1, 0, 1, 1, h, h, None) == BAD
+    assert lib.ss_cache_attend(None, t, step, 0, 1, 1, h, h, 1, 1.0, None, None) == BAD
+    assert lib.ss_cache_write(None, t, None, 0, 1, 1, h, h, None, None, None, None, 0, None) == BAD
+    assert lib.ss_cache_attend(None, t, None, 0, 1, 1, h, h, 1, 1.0, None, None) == BAD
+
+
+@pytest.mark.parametrize("change", [
+    dict(rotary=None), dict(rotary=SM._pack_rotary(0, 8, 0, 1.0)), dict(rotary=SM._pack_rotary(68, 8, 0, 1.0)),
+    dict(rotary=SM._pack_rotary(64, 0, 0, 1.0)), dict(rotary=SM._pack_rotary(64, 7, 0, 1.0)),
+    dict(rotary=SM._pack_rotary(64, 18, 0, 1.0)), dict(dtype=SM.SS_F32), dict(B=-1), dict(N=-1),
+    dict(B=1 << 16, N=1 << 16), dict(dim=0), dict(dim=65537), dict(q_heads=0), dict(q_heads=-1),
+    dict(q_heads=65537), dict(k_heads=65536), dict(positions=None), dict(positions=66), dict(q=None),
+    dict(oq=None), dict(q=SM._pack_heads(0, 1, 1, 1)), dict(q=SM._pack_heads(65, 1, 1, 1)),
+    dict(k_heads=1), dict(k_heads=1, k=SM._pack_heads(64, 1, 1, 1)),
+])
+def test_rotate_rejects_before_touching_hip(lib, change):
+    h = SM._pack_heads(64, 16, 16, 16)
+    a = dict(rotary=SM._pack_rotary(64, 16, 0, 1.0), dtype=SM.SS_BF16, B=1, N=1, dim=16, positions=64, q=h,
+             oq=h, q_heads=1, k=None, ok=None, k_heads=0)
+    a.update(change)
+    assert lib.ss_rotate(0, a["rotary"], a["dtype"], a["B"], a["N"], a["dim"], a["positions"], a["q"], a["oq"],
+                         a["q_heads"], a["k"], a["ok"], a["k_heads"], None) == BAD
+
+
+def test_rotate_of_nothing(lib):
+    assert lib.ss_rotate(0, SM._pack_rotary(64, 16, 0, 1.0), SM.SS_F16, 0, 5, 16, None, None, None, 1, None,
+                         None, 0, None) == SM.SS_OK
+
+
+GOOD = dict(num_planes=2, num_pages=8, page_size=32, heads=2, piece_bytes=64, page_stride=4096,
+            slot_stride=128, head_stride=64, max_batch=3, max_blocks=5, device=0)
+LAYOUT = dict(block=16, page_stride=4, block_stride=2, head_stride=1)
+
+
+@pytest.mark.parametrize("change,layout,status", [
+    ({}, dict(block=8), BAD), ({}, dict(block=0), BAD), ({}, dict(block=64), BAD), ({}, dict(block=17), BAD),
+    ({}, dict(block=128), BAD), ({}, dict(page_stride=3), BAD), ({}, dict(block_stride=1), BAD),
+    ({}, dict(head_stride=0), BAD), ({}, dict(head_stride=-1), BAD), ({"num_pages": 0}, {}, BAD),
+    ({"page_size": 24, "page_stride": 3072 + 1024}, dict(block=16), BAD),
+    ({"piece_bytes": 24, "head_stride": 64}, {}, NOT_SERVED),
+    ({"piece_bytes": 272, "head_stride": 272, "slot_stride": 544, "page_stride": 17408}, {}, NOT_SERVED),
+    ({"slot_stride": 136, "page_stride": 4352}, {}, NOT_SERVED),
+    ({"page_stride": 4104}, {}, NOT_SERVED),
+    ({"slot_stride": 1 << 30, "page_stride": 64 * 2}, {}, NOT_SERVED),
+    ({"slot_stride": 128, "head_stride": 1 << 32}, {}, NOT_SERVED),
+])
+def test_create_scaled_rejects_before_touching_hip(lib, change, layout, status):
+    cfg = SM.CacheConfig(**{**GOOD, **change})
+    lay = SM.CacheScales(**{**LAYOUT, **layout})
+    planes, scales = (ctypes.c_void_p * 2)(1 << 20, 1 << 21), (ctypes.c_void_p * 2)(1 << 22, 1 << 23)
+    h = ctypes.c_void_p()
+    assert lib.ss_cache_create_scaled(ctypes.byref(cfg), planes, scales, ctypes.byref(lay),
+                                      ctypes.byref(h)) == status
+    assert not h.value
+
+
+def test_create_scaled_rejects_pointers(lib):
+    cfg, lay = SM.CacheConfig(**GOOD), SM.CacheScales(**LAYOUT)
+    h = ctypes.c_void_p()
+
+    def make(planes, scales, layout=ctypes.byref(lay)):
+        return lib.ss_cache_create_scaled(ctypes.byref(cfg), (ctypes.c_void_p * 2)(*planes),
+                                          None if scales is None else (ctypes.c_void_p * 2)(*scales), layout,
+                                          ctypes.byref(h))
+    good = (1 << 20, 1 << 21)
+    assert make(good, None) == BAD and make(good, (64, 128), None) == BAD
+    assert make(good, (64, None)) == BAD and make(good, (64, 64)) == BAD
+    assert make((None, 64), (64, 128)) == BAD and make((1 << 20, 1 << 20), (64, 128)) == BAD
+    assert make((1 << 20, (1 << 21) + 8), (64, 128)) == NOT_SERVED  # a plane that 16 bytes do not divide
+    assert not h.value
+
+
+def test_scaled_cache_takes_device_tensors_only(lib):
+    with pytest.raises(ValueError):
+        PageCache(torch.zeros(2, 2, 16, 1, 16, dtype=torch.uint8), 2, 2,
+                  scales=torch.zeros(2, 2, 1, 1, dtype=torch.uint8))
