@@ -434,8 +434,8 @@ __device__ __forceinline__ void attend_values(const AttendValues<DP>& x, const u
 // see, in units of UNIT, are one line, and a.shares workgroups take equal shares of it: the end of
 // one request's slots, whole requests, the start of the next one's. So all are done at the same
 // time, however uneven the contexts, and as many requests are cut as there are shares (64 requests
-// of 2000 to 6000 slots: 115 us, a workgroup a request 135). With a.shares = 0 there are requests
-// enough, and each is a workgroup's.
+// of 4000 slots on average: 115 us, each request cut into workgroups of its own 147). With
+// a.shares = 0 there are requests enough, and each is a workgroup's.
 //
 // Neighbouring workgroups, which run on different XCDs, take different heads of one share: they
 // read the same pages at about the same time, and with eight heads an XCD's cache holds the
@@ -721,7 +721,7 @@ struct ArgsAgain {
 // values go to registers straight from the pages: they are read once, and a step's 8 KB a wave,
 // half of them on their way at any time, are what a CU needs at one wave a SIMD.
 // What bounds it: HBM. 64 single tokens over uneven contexts of 4000 slots on average, 8 heads of
-// 128: 113 us, 4.7 TB/s; even ones 102 us, 5.2 TB/s; one token over 131072 slots 61 us, 4.4 TB/s
+// 128: 113 to 115 us, 4.6 TB/s; even ones 102 us, 5.2 TB/s; one token over 131072 slots 61 us, 4.4 TB/s
 // with its start and the addition of 32 pieces. Where requests are few and short it is a chain of
 // loads: 9.4 us for four of 900 slots.
 template <int DP, int MT, bool F16>
@@ -915,12 +915,12 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : MT == 2 || DP == 128 ? 2 : 3) 
 // registers hold them, 16 bytes a lane, so that neither its writes nor the reads meet in a
 // bank. Two tiles take turns: one is read while the next is left, with a barrier a tile; the
 // one after that is on its way from memory meanwhile.
-// What bounds it: of a tile a wave has 64 matrix instructions (1024 cycles) and about 250 vector
-// ones, a third of them the softmax's (1400); two waves a SIMD take 2.2 us for it, one alone 2.0,
-// waiting for LDS and for its own results. 2048 tokens behind 6144 slots, 32 heads of 128: 284 us,
-// 845 TFLOP/s; 32 trees of 16 nodes over 2000 slots: 59 us, 2.4 TB/s. Scores of the next half tile
-// formed between this one's weights, with a second barrier, took 299 us; a wave of higher priority
-// while it multiplies 291.
+// What bounds it: instructions of both kinds on one SIMD. Of a tile a wave of 32 rows has 64 matrix
+// instructions and 209 other vector ones (counted), and two waves a SIMD take 2.6 us for it.
+// 2048 tokens behind 6144 slots, 32 heads of 128: 284 to 291 us, 826 to 848 TFLOP/s; 32 trees of
+// 16 nodes over 2000 slots: 58 to 68 us by their lengths. Scores of the next half tile formed
+// between this one's weights, with a second barrier, took 299 us; a wave of higher priority while
+// it multiplies 291.
 
 constexpr int AT_TILE = 64;
 
@@ -1121,7 +1121,8 @@ __global__ __launch_bounds__(256, 2) void k_attend_rows(Kv8Attend args) {
         int full = min(row.base, row.end);
         if (!a.s.parents && row.count) full = (int)min((int64_t)row.end, (int64_t)row.base + first / a.group + 1);
         const int t0 = pc.from;
-        const int t1 = min(pc.to, (int)(((int64_t)attend_see(a, row, (first + rows - 1) / a.group) + AT_TILE - 1) / AT_TILE));
+        const int most = attend_see(a, row, (first + rows - 1) / a.group);
+        const int t1 = min(pc.to, (int)(((int64_t)most + AT_TILE - 1) / AT_TILE));
         const int t2 = max(min(full / AT_TILE, t1), t0);  // tiles before it need no mask
         if (t0 < t1) {
             AttendWalk at;

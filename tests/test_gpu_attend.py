@@ -111,6 +111,29 @@ def test_long_rows_are_cut(B, N, len_):
         assert torch.equal(a, w.cache.attend(w.bt, 0, q))
 
 
+@pytest.mark.parametrize("B,N,heads,group,tree", [
+    (300, 1, 4, 2, False),    # few rows, 16 of them a workgroup
+    (257, 5, 4, 4, False),    # few rows, 32
+    (300, 9, 7, 4, True),    # many rows, a block of 64 each
+    (1, 140, 260, 1, False),  # more blocks of rows than shares
+])
+def test_whole_requests(B, N, heads, group, tree):
+    """Requests enough that each is a workgroup's, uneven ones, empty ones among them."""
+    ps = 16
+    M = -(-(40 + N) // ps)
+    w = World(seed=B + N, P=B * M + 2, ps=ps, heads=heads, dim=16, rows=B, M=M)
+    lens = [int(x) for x in w.rng.integers(0, 41, B)]
+    if B > 1:
+        lens[0] = lens[B - 1] = 0
+    w.hold(lens, extra=N)
+    log(f"attend whole requests: B={B} N={N} heads={heads}")
+    q = w.heads(B, N, heads * group, 16, "bf16")
+    step = {"parents": w.tree(B, N)} if tree else {}
+    if B > 1:
+        step["counts"] = [N if b % 7 else 0 for b in range(B)]
+    check(w, q, "bf16", "whole", **step)
+
+
 def test_peaks_and_rising_scores():
     """A score that towers over the others, first, in the middle and last, and scores that
     rise slot by slot: the running reference moves."""
