@@ -70,7 +70,7 @@ LAYOUT = dict(block=16, page_stride=4, block_stride=2, head_stride=1)
     ({}, dict(block=8), BAD), ({}, dict(block=0), BAD), ({}, dict(block=64), BAD), ({}, dict(block=17), BAD),
     ({}, dict(block=128), BAD), ({}, dict(page_stride=3), BAD), ({}, dict(block_stride=1), BAD),
     ({}, dict(head_stride=0), BAD), ({}, dict(head_stride=-1), BAD), ({"num_pages": 0}, {}, BAD),
-    ({"page_size": 24, "page_stride": 3072 + 1024}, dict(block=16), BAD),
+    ({"page_size": 24, "page_stride": 4096}, dict(block=16), BAD),
     ({"piece_bytes": 24, "head_stride": 64}, {}, NOT_SERVED),
     ({"piece_bytes": 272, "head_stride": 272, "slot_stride": 544, "page_stride": 17408}, {}, NOT_SERVED),
     ({"slot_stride": 136, "page_stride": 4352}, {}, NOT_SERVED),
