@@ -42,8 +42,9 @@ def frequencies(dim, base=10000.0, scaling=None, factor=1.0, original=None, fast
     def pair(turns):  # the index, not rounded, of the pair that turns so often
         return dim * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))
 
+    # the ramp may end behind the last pair: of a long original length all turn more than `slow` times
     lo = max(math.floor(pair(fast)), 0)
-    hi = min(math.ceil(pair(slow)), dim // 2 - 1)
+    hi = min(math.ceil(pair(slow)), dim - 1)
     out = []
     for i, x in enumerate(f):
         ramp = min(max((i - lo) / max(hi - lo, 0.001), 0.0), 1.0)
