@@ -667,7 +667,8 @@ ss_status ss_rotate(int32_t device, const ss_rotary* rotary, ss_dtype dtype, int
  *   keys, values  [B, N, heads, dim] of dtype (SS_BF16 or SS_F16), heads and dim those of
  *                 the cache.
  *   rotary        NULL, or the rotation of the keys (and queries) before they are written;
- *                 its dim a multiple of 16.
+ *                 its dim a multiple of 16, or one that divides the cache's dim (half a
+ *                 head of 80; read and written in smaller pieces by halves).
  *   positions     [B, N] int32 positions for the rotation, or NULL: base_b + i, in a tree
  *                 base_b + the node's depth.
  *   queries       NULL, or [B, N, q_heads, dim] turned along into out_queries (which may
@@ -715,8 +716,8 @@ ss_status ss_cache_read(ss_cache* c, const ss_block_tables* t, const int32_t* st
  * Errors of the calls on a scaled cache, before any launch: as of the other ss_cache
  * calls, and SS_ERR_INVALID_ARG for a handle without scales, planes out of range or the
  * same twice, another dtype, sizes out of range or a rotary without turns;
- * SS_ERR_UNSUPPORTED for data or strides that are not aligned and a rotary whose dim is no
- * multiple of 16. */
+ * SS_ERR_UNSUPPORTED for data or strides that are not aligned and a rotary whose dim is
+ * neither a multiple of 16 nor divides the cache's. */
 ss_status ss_cache_attend(ss_cache* c, const ss_block_tables* t, const ss_cache_step* step,
                           int32_t k_plane, int32_t v_plane, ss_dtype dtype,
                           const ss_heads* queries, const ss_heads* out, int32_t q_heads,

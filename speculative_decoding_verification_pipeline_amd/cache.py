@@ -278,12 +278,12 @@ class PageCache:
         slot lens[b] + i, the first counts[b] of them (None: all N). reserved: what
         reserve returned; rows with 0 there write nothing.
 
-        rotary (a Rotary whose dim is a multiple of 16): the keys are turned by their
-        positions first: positions [B, N] int32, else lens + i, with parents [B, N]
-        (a draft tree as tree_verify takes it) lens + the node's depth. queries
-        [B, N, q_heads, dim] are turned along, into out_queries, which is returned
-        (None: a new array; queries itself: in place); rows of tokens that there are
-        not become 0."""
+        rotary (a Rotary whose dim is a multiple of 16 or divides the head's): the keys
+        are turned by their positions first: positions [B, N] int32, else lens + i, with
+        parents [B, N] (a draft tree as tree_verify takes it) lens + the node's depth.
+        queries [B, N, q_heads, dim] are turned along, into out_queries, which is
+        returned (None: a new array; queries itself: in place); rows of tokens that
+        there are not become 0."""
         k_plane, v_plane = self._layer(layer)
         code = self._dtype(keys, "keys")
         shape = (*keys.shape[:2], self.heads, self.dim)

@@ -567,7 +567,8 @@ ss_status ss_cache_write(ss_cache* c, const ss_block_tables* t, const ss_cache_s
         st = check_heads(h, true);
         if (st != SS_OK) return st;
     }
-    if (rotary && rotary->dim % 16) return SS_ERR_UNSUPPORTED;
+    // a rotated part is a multiple of 16, or divides the head (a half, a quarter of it)
+    if (rotary && rotary->dim % 16 && c->cfg.piece_bytes % rotary->dim) return SS_ERR_UNSUPPORTED;
     ss::Kv8Write a;
     std::memset(&a, 0, sizeof(a));
     a.g = geo_of(c);

@@ -22,6 +22,7 @@ namespace ss {
 constexpr int KV_NT = 256;
 constexpr int KV_UNIT = 16;         // entries of a head that a thread takes at once
 constexpr int KV_UNITS = 4;         // units of a thread that stay in registers
+constexpr int KV_PART_UNITS = 5;    // where a head of 256 has 17
 constexpr int KV_SIN_BYTES = 32768; // sines and cosines held at once
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -65,11 +66,88 @@ __device__ __forceinline__ void unit_at(const Rotary& r, bool turned, int u, int
     }
 }
 
-// Turns a unit's 16 values by its 8 pairs' cosines and sines.
+// A unit of a head whose rotated part 16 does not divide: two runs of entries, some of them
+// no full 8, and the first `pairs` of lo's and hi's are pairs (of neighbours: the first
+// 2 * pairs entries). By halves the pairs' units come first, the last of them short, then
+// the entries behind them, which start where the rotated part ends.
+struct PartUnit {
+    int lo, hi, n_lo, n_hi, pairs;
+};
+
+__host__ __device__ __forceinline__ int part_units(int dim, int rot, bool interleaved) {
+    return interleaved ? dim / KV_UNIT : (rot / 2 + 7) / 8 + (dim - rot + KV_UNIT - 1) / KV_UNIT;
+}
+
+__device__ __forceinline__ PartUnit part_unit(const Rotary& r, int dim, int u) {
+    const int half = r.dim / 2, turned = (half + 7) / 8;
+    if (r.interleaved) return {u * KV_UNIT, u * KV_UNIT + 8, 8, 8, min(max(half - u * 8, 0), 8)};
+    if (u < turned) {
+        const int n = min(half - u * 8, 8);
+        return {u * 8, half + u * 8, n, n, n};
+    }
+    const int lo = r.dim + (u - turned) * KV_UNIT, hi = min(lo + 8, dim);
+    return {lo, hi, hi - lo, min(dim - hi, 8), 0};
+}
+
+// A run of n <= 8 values, four at a time where `fours` says that all runs start and end at
+// multiples of four, else one by one; those behind n are 0.
+template <bool F16>
+__device__ __forceinline__ void load_run(const uint16_t* from, int n, bool fours, float* x) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+        u32x2 w = {0, 0};
+        if (fours) {
+            if (i < n) w = *reinterpret_cast<const u32x2*>(from + i);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (i + k < n) w[k / 2] |= (uint32_t)from[i + k] << (k % 2 * 16);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const f32x2 v = from16<F16>(w[k]);
+            x[i + 2 * k] = v[0];
+            x[i + 2 * k + 1] = v[1];
+        }
+    }
+}
+
+template <bool F16>
+__device__ __forceinline__ void store_run(uint16_t* to, int n, bool fours, const float* x) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+        const u32x2 w = {to16<F16>(x[i], x[i + 1]), to16<F16>(x[i + 2], x[i + 3])};
+        if (fours) {
+            if (i < n) *reinterpret_cast<u32x2*>(to + i) = w;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (i + k < n) to[i + k] = (uint16_t)(w[k / 2] >> (k % 2 * 16));
+        }
+    }
+}
+
+// The same of bytes, by words of four.
+__device__ __forceinline__ void store_run8(char* to, int n, bool fours, uint32_t w0, uint32_t w1) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+        const uint32_t w = i ? w1 : w0;
+        if (fours) {
+            if (i < n) *reinterpret_cast<uint32_t*>(to + i) = w;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (i + k < n) to[i + k] = (char)(w >> (k * 8));
+        }
+    }
+}
+
+// Turns a unit's 16 values by its 8 pairs' cosines and sines, or the first `pairs` of them.
 template <class T>
-__device__ __forceinline__ void turn_unit(bool interleaved, const T* c, const T* s, T x[16]) {
+__device__ __forceinline__ void turn_unit(bool interleaved, const T* c, const T* s, T x[16], int pairs = 8) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+        if (i >= pairs) break;
         const int p = interleaved ? 2 * i : i, q = interleaved ? 2 * i + 1 : i + 8;
         const T u = x[p], v = x[q];
         x[p] = fma(u, c[i], -(v * s[i]));
@@ -230,6 +308,7 @@ __device__ __forceinline__ uint32_t to8(const float* x, float f) {
 }
 
 struct WritePlan {
+    int units;        // of a turned head
     int blocks;       // of a row's slots that a step can touch
     int heads;        // of the cache that a workgroup takes
     int parts;        // workgroups for the heads of a block
@@ -242,8 +321,15 @@ struct WritePlan {
 // largest, then the scale, and writes. Two uneven prompts of 3000 tokens on average, 32 query
 // heads and 8 of the cache: 36 to 40 us (HBM); one token 6 us, 48 trees of 16 nodes 11.6, chains
 // of loads, the tree's depths and binary64 sines.
-template <bool F16>
+// PART: 16 does not divide the rotated part. Of a rotation by halves the runs of a unit then
+// start where no 16 bytes do, and are read and written 8 (keys in 8 bits 4) at a time where
+// pairs come in fours, else entry by entry; still a unit's thread reads what it writes, so
+// queries may be turned where they lie. Two prompts of 3000 tokens on average, 32 query heads
+// and 8 of the cache of 80, written and their ends read: 38 us turned whole, 43 turned by halves
+// in 40 entries (38 in neighbours), 86 in 20, entry by entry.
+template <bool F16, bool PART>
 __global__ __launch_bounds__(KV_NT) void k_kv8_write(Kv8Write a, WritePlan p) {
+    constexpr int UNITS = PART ? KV_PART_UNITS : KV_UNITS;
     __shared__ __align__(16) char s_mem[KV_SIN_BYTES];
     __shared__ uint32_t s_amax[64];
     __shared__ int s_depth[WAVE];
@@ -263,9 +349,10 @@ __global__ __launch_bounds__(KV_NT) void k_kv8_write(Kv8Write a, WritePlan p) {
         if (a.positions) return (double)a.positions[(int64_t)b * a.s.N + i];
         return (double)(row.base + (a.s.parents ? s_depth[i] : i));
     };
-    const int per_head = a.g.dim / KV_UNIT;
+    const bool in_runs = PART && !a.r.interleaved, fours = half % 4 == 0;
 
     if (queries) {
+        const int per_head = p.units;
         float* turns = reinterpret_cast<float*>(s_mem);
         const int i0 = ((int)blockIdx.x - 2 * kv) * p.q_tokens;
         const int n = min(p.q_tokens, a.s.N - i0);
@@ -282,16 +369,36 @@ __global__ __launch_bounds__(KV_NT) void k_kv8_write(Kv8Write a, WritePlan p) {
         for (int i = tid; i < n * per_token; i += KV_NT) {
             const int t = i / per_token, j = i - t * per_token;
             const int h = j / per_head, u = j - h * per_head;
-            const bool turned = u * KV_UNIT < a.r.dim;
-            int lo, hi;
-            unit_at(a.r, turned, u, lo, hi);
             const uint16_t* from = a.q.data + b * a.q.row + (i0 + t) * a.q.token + h * a.q.head;
             uint16_t* to = a.q_out.data + b * a.q_out.row + (i0 + t) * a.q_out.token + h * a.q_out.head;
+            int pairs = u * KV_UNIT < a.r.dim ? 8 : 0;
+            if constexpr (PART) {
+                const PartUnit at = part_unit(a.r, a.g.dim, u);
+                pairs = at.pairs;
+                if (in_runs) {
+                    float x[16] = {}, c[8], s[8];
+                    if (t < live) {
+                        load_run<F16>(from + at.lo, at.n_lo, fours, x);
+                        load_run<F16>(from + at.hi, at.n_hi, fours, x + 8);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            c[k] = k < pairs ? turns[t * a.r.dim + u * 8 + k] : 0.0f;
+                            s[k] = k < pairs ? turns[t * a.r.dim + half + u * 8 + k] : 0.0f;
+                        }
+                        turn_unit<float>(false, c, s, x, pairs);
+                    }
+                    store_run<F16>(to + at.lo, at.n_lo, fours, x);
+                    store_run<F16>(to + at.hi, at.n_hi, fours, x + 8);
+                    continue;
+                }
+            }
+            int lo, hi;
+            unit_at(a.r, pairs != 0, u, lo, hi);
             u32x4 r0 = {0, 0, 0, 0}, r1 = {0, 0, 0, 0};
             if (t < live) {
                 r0 = *reinterpret_cast<const u32x4*>(from + lo);
                 r1 = *reinterpret_cast<const u32x4*>(from + hi);
-                if (turned) {
+                if (pairs) {
                     float x[16], c[8], s[8];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -303,10 +410,11 @@ __global__ __launch_bounds__(KV_NT) void k_kv8_write(Kv8Write a, WritePlan p) {
                     }
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        c[k] = turns[t * a.r.dim + u * 8 + k];
-                        s[k] = turns[t * a.r.dim + half + u * 8 + k];
+                        const bool on = !PART || k < pairs;
+                        c[k] = on ? turns[t * a.r.dim + u * 8 + k] : 0.0f;
+                        s[k] = on ? turns[t * a.r.dim + half + u * 8 + k] : 0.0f;
                     }
-                    turn_unit<float>(a.r.interleaved, c, s, x);
+                    turn_unit<float>(a.r.interleaved, c, s, x, PART ? pairs : 8);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         r0[k] = to16<F16>(x[2 * k], x[2 * k + 1]);
@@ -339,34 +447,45 @@ __global__ __launch_bounds__(KV_NT) void k_kv8_write(Kv8Write a, WritePlan p) {
     uint8_t* scales = plane.scales + page * a.g.sc_page + slot0 / a.g.block * a.g.sc_block;
     if (tid < heads) s_amax[tid] = 0;
 
+    const bool turns = keys && a.r.turns;
+    const bool runs = in_runs && keys;  // PART: there is a rotation
+    const int per_head = turns ? p.units : a.g.dim / KV_UNIT;
     const int per_slot = heads * per_head;
     const int tokens = hi_t - lo_t;
     const int total = tokens * per_slot;
     const int i0 = (int)(j0 + lo_t - row.base);  // the step's token in slot lo_t
-    const bool turns = keys && a.r.turns;
-    u32x4 w[KV_UNITS][2];
-    int tok[KV_UNITS], hd[KV_UNITS], un[KV_UNITS];
+    u32x4 w[UNITS][2];
+    float x[UNITS][16];
+    int tok[UNITS], hd[UNITS], un[UNITS];
 #pragma unroll
-    for (int k = 0; k < KV_UNITS; ++k) {
+    for (int k = 0; k < UNITS; ++k) {
         const int i = tid + k * KV_NT;
         tok[k] = i / per_slot;
         const int j = i - tok[k] * per_slot;
         hd[k] = j / per_head;
         un[k] = j - hd[k] * per_head;
         if (i < total) {
-            int lo, hi;
-            unit_at(a.r, turns && un[k] * KV_UNIT < a.r.dim, un[k], lo, hi);
             const uint16_t* from = src.data + b * src.row + (i0 + tok[k]) * src.token +
                                    (h0 + hd[k]) * src.head;
+            if constexpr (PART) {
+                if (runs) {
+                    const PartUnit at = part_unit(a.r, a.g.dim, un[k]);
+                    load_run<F16>(from + at.lo, at.n_lo, fours, x[k]);
+                    load_run<F16>(from + at.hi, at.n_hi, fours, x[k] + 8);
+                    continue;
+                }
+            }
+            int lo, hi;
+            unit_at(a.r, turns && un[k] * KV_UNIT < a.r.dim, un[k], lo, hi);
             w[k][0] = *reinterpret_cast<const u32x4*>(from + lo);
             w[k][1] = *reinterpret_cast<const u32x4*>(from + hi);
         } else {
             tok[k] = INT_MAX;
         }
     }
-    float x[KV_UNITS][16];
 #pragma unroll
-    for (int k = 0; k < KV_UNITS; ++k)
+    for (int k = 0; k < UNITS; ++k) {
+        if (PART && runs) continue;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             const f32x2 v0 = from16<F16>(w[k][0][c]), v1 = from16<F16>(w[k][1][c]);
@@ -375,6 +494,7 @@ __global__ __launch_bounds__(KV_NT) void k_kv8_write(Kv8Write a, WritePlan p) {
             x[k][8 + 2 * c] = v1[0];
             x[k][9 + 2 * c] = v1[1];
         }
+    }
     if (turns) {
         double* s_turn = reinterpret_cast<double*>(s_mem);
         const int most = KV_SIN_BYTES / 8 / a.r.dim;  // tokens whose sines are held at once
@@ -390,11 +510,14 @@ __global__ __launch_bounds__(KV_NT) void k_kv8_write(Kv8Write a, WritePlan p) {
             }
             __syncthreads();
 #pragma unroll
-            for (int k = 0; k < KV_UNITS; ++k) {
-                if (tok[k] < t0 || tok[k] >= t0 + n || un[k] * KV_UNIT >= a.r.dim) continue;
+            for (int k = 0; k < UNITS; ++k) {
+                int pairs = un[k] * KV_UNIT < a.r.dim ? 8 : 0;
+                if constexpr (PART) pairs = part_unit(a.r, a.g.dim, un[k]).pairs;
+                if (tok[k] < t0 || tok[k] >= t0 + n || !pairs) continue;
                 const double* at = s_turn + (tok[k] - t0) * a.r.dim + un[k] * 8;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
+                    if (PART && i >= pairs) break;
                     const double c = at[i], s = at[half + i];
                     const int p0 = i, q0 = i + 8, p1 = 2 * i, q1 = 2 * i + 1;
                     if (a.r.interleaved) {
@@ -412,7 +535,7 @@ __global__ __launch_bounds__(KV_NT) void k_kv8_write(Kv8Write a, WritePlan p) {
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < KV_UNITS; ++k) {
+    for (int k = 0; k < UNITS; ++k) {
         if (tok[k] == INT_MAX) continue;
         uint32_t most = 0;
 #pragma unroll
@@ -425,21 +548,31 @@ __global__ __launch_bounds__(KV_NT) void k_kv8_write(Kv8Write a, WritePlan p) {
     __syncthreads();
     // slots that the block holds before the step's: the scale may grow, never shrink
 #pragma unroll
-    for (int k = 0; k < KV_UNITS; ++k) {
+    for (int k = 0; k < UNITS; ++k) {
         if (tok[k] == INT_MAX) continue;
         int e = scale_of(s_amax[hd[k]]);
         if (lo_t > 0) e = max(e, (int)scales[(h0 + hd[k]) * a.g.sc_head] - 127);
         e = min(max(e, KV8_XMIN), KV8_XMAX);
         const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+        char* at = to + (lo_t + tok[k]) * a.g.slot + (h0 + hd[k]) * a.g.head;
+        const u32x2 v0 = {to8(x[k], f), to8(x[k] + 4, f)}, v1 = {to8(x[k] + 8, f), to8(x[k] + 12, f)};
+        if constexpr (PART) {
+            if (runs) {
+                const PartUnit u = part_unit(a.r, a.g.dim, un[k]);
+                store_run8(at + u.lo, u.n_lo, fours, v0[0], v0[1]);
+                store_run8(at + u.hi, u.n_hi, fours, v1[0], v1[1]);
+                continue;
+            }
+        }
         int lo, hi;
         unit_at(a.r, turns && un[k] * KV_UNIT < a.r.dim, un[k], lo, hi);
-        char* at = to + (lo_t + tok[k]) * a.g.slot + (h0 + hd[k]) * a.g.head;
-        *reinterpret_cast<u32x2*>(at + lo) = u32x2{to8(x[k], f), to8(x[k] + 4, f)};
-        *reinterpret_cast<u32x2*>(at + hi) = u32x2{to8(x[k] + 8, f), to8(x[k] + 12, f)};
+        *reinterpret_cast<u32x2*>(at + lo) = v0;
+        *reinterpret_cast<u32x2*>(at + hi) = v1;
     }
-    for (int i = tid; i < lo_t * per_slot; i += KV_NT) {
-        const int t = i / per_slot, j = i - t * per_slot;
-        const int h = j / per_head, u = j - h * per_head;
+    const int held_head = a.g.dim / KV_UNIT, held_slot = heads * held_head;
+    for (int i = tid; i < lo_t * held_slot; i += KV_NT) {
+        const int t = i / held_slot, j = i - t * held_slot;
+        const int h = j / held_head, u = j - h * held_head;
         const int was = (int)scales[(h0 + h) * a.g.sc_head] - 127;
         const int e = scale_of(s_amax[h]);
         if (e <= was) continue;
@@ -525,10 +658,13 @@ hipError_t launch_rotate(const RotateArgs& a, ss_dtype dt, hipStream_t st) {
 }
 
 hipError_t launch_kv8_write(const Kv8Write& a, ss_dtype dt, hipStream_t st) {
-    const int per_head = a.g.dim / KV_UNIT;
+    const bool part = a.r.turns && a.r.dim % KV_UNIT;
+    const int per_head = part ? part_units(a.g.dim, a.r.dim, a.r.interleaved) : a.g.dim / KV_UNIT;
     WritePlan p;
+    p.units = per_head;
     p.blocks = (int)(((int64_t)a.g.block + a.s.N - 2) / a.g.block) + 1;
-    p.heads = KV_UNITS * KV_NT / (a.g.block * per_head);  // at least 1: block <= 64, dim <= 256
+    // at least 1: block <= 64, dim <= 256, so 16 units a head, 17 where a part's last one is short
+    p.heads = (part ? KV_PART_UNITS : KV_UNITS) * KV_NT / (a.g.block * per_head);
     if (p.heads > a.g.heads) p.heads = a.g.heads;
     if (p.heads > 64) p.heads = 64;
     p.parts = (a.g.heads + p.heads - 1) / p.heads;
@@ -542,8 +678,10 @@ hipError_t launch_kv8_write(const Kv8Write& a, ss_dtype dt, hipStream_t st) {
     const int64_t grid = 2ll * p.blocks * p.parts + p.q_chunks;
     if (grid > INT_MAX) return hipErrorInvalidValue;
     const dim3 g((unsigned)grid, a.s.B);
-    if (dt == SS_F16) hipLaunchKernelGGL(k_kv8_write<true>, g, dim3(KV_NT), 0, st, a, p);
-    else hipLaunchKernelGGL(k_kv8_write<false>, g, dim3(KV_NT), 0, st, a, p);
+    if (dt == SS_F16 && part) hipLaunchKernelGGL((k_kv8_write<true, true>), g, dim3(KV_NT), 0, st, a, p);
+    else if (part) hipLaunchKernelGGL((k_kv8_write<false, true>), g, dim3(KV_NT), 0, st, a, p);
+    else if (dt == SS_F16) hipLaunchKernelGGL((k_kv8_write<true, false>), g, dim3(KV_NT), 0, st, a, p);
+    else hipLaunchKernelGGL((k_kv8_write<false, false>), g, dim3(KV_NT), 0, st, a, p);
     return hipGetLastError();
 }
 
