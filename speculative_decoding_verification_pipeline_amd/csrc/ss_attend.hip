@@ -213,6 +213,21 @@ __device__ __forceinline__ void put_out(AttendKeys<DP>& k, AttendValues<DP>& v) 
     }
 }
 
+// Scores of tiles on no page are 0, whatever the queries hold: zeros times what is not finite
+// are NaN. Without a branch: behind one the compiler has read a product's accumulator in the
+// next instruction, where it must wait for seven.
+template <int MT>
+__device__ __forceinline__ void put_out_scores(const bool (&ok)[2], f32x4 (&s)[2][MT]) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const uint32_t keep = ok[t] ? ~0u : 0u;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[t][m][i] = as<float>(as<uint32_t>((float)s[t][m][i]) & keep);
+    }
+}
+
 // What a wave holds of its rows.
 template <int DP, int MT>
 struct AttendState {
@@ -252,17 +267,20 @@ __device__ __forceinline__ uint32_t keep_if(uint32_t bits, int bit, uint32_t w, 
 }
 
 // Puts out the scores of a step's slots that a row does not see. rel: this lane's first slot
-// behind the committed ones; vis: those seen, bit 4 t + i slot i of tile t.
+// behind the committed ones; ok: tiles on a page; vis: those seen, bit 4 t + i slot i of tile t.
 template <int MT>
 __device__ __forceinline__ void attend_mask(const Kv8Attend& a, unsigned long long above, int first, int rows,
-                                            int rel, int end, f32x4 (&s)[2][MT], uint32_t (&vis)[MT]) {
+                                            int rel, int end, const bool (&ok)[2], f32x4 (&s)[2][MT],
+                                            uint32_t (&vis)[MT]) {
     const int col = threadIdx.x & 15;
+    const uint32_t on = (ok[0] ? 0xfu : 0u) | (ok[1] ? 0xf0u : 0u);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
         const int n = (first + min(m * 16 + col, rows - 1)) / a.group;
         const unsigned long long up = (unsigned long long)(uint32_t)__shfl((int)(above >> 32), n & 63) << 32 |
                                       (uint32_t)__shfl((int)above, n & 63);
-        vis[m] = attend_sees(a.s.parents, up, n, rel, end) | attend_sees(a.s.parents, up, n, rel + 16, end) << 4;
+        vis[m] = (attend_sees(a.s.parents, up, n, rel, end) |
+                  attend_sees(a.s.parents, up, n, rel + 16, end) << 4) & on;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -811,6 +829,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : MT == 2 || DP == 128 ? 2 : 3) 
                 load_values<DP>(a, place, v_at, v);
                 if (!(k.ok[0] && k.ok[1])) put_out<DP>(k, v);
                 attend_scores<DP, MT, F16>(k, w, e);
+                put_out_scores<MT>(k.ok, e);
                 const uint32_t ks[2] = {k.s[0], k.s[1]};
                 const bool ok[2] = {k.ok[0], k.ok[1]};
                 place = attend_next(a, at, h);  // behind the last step: page 0
@@ -833,7 +852,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : MT == 2 || DP == 128 ? 2 : 3) 
                 attend_scores<DP, MT, F16>(k, w, e);
                 const int rel = s * AT_STEP - row.base + g * 4, end = row.end - row.base;
                 uint32_t vis[MT];
-                attend_mask<MT>(a, above, first, rows, rel, end, e, vis);
+                attend_mask<MT>(a, above, first, rows, rel, end, k.ok, e, vis);
                 // values behind the last token are not numbers to be multiplied by 0
                 const uint32_t there = ((1u << min(max(end - rel, 0), 4)) - 1) |
                                        ((1u << min(max(end - rel - 16, 0), 4)) - 1) << 4;
@@ -1047,7 +1066,11 @@ __device__ __forceinline__ void attend_tile(const Kv8Attend& a, const AttendTile
         }
     }
     uint32_t vis[MT] = {};
-    if constexpr (MASK) attend_mask<MT>(a, above, first, rows, rel, end, e, vis);
+    // the same in all lanes
+    const bool ok[2] = {__builtin_amdgcn_readfirstlane(as<int>(x.xv[0])) != as<int>(-INFINITY),
+                        __builtin_amdgcn_readfirstlane(as<int>(x.xv[1])) != as<int>(-INFINITY)};
+    if constexpr (MASK) attend_mask<MT>(a, above, first, rows, rel, end, ok, e, vis);
+    else put_out_scores<MT>(ok, e);
     attend_weights<DP, MT>(x, e, w, p);
 #pragma unroll
     for (int d = 0; d < DP / 16; ++d) {
