@@ -346,9 +346,9 @@ class PageCache:
         lens[b] + i (None: tables.lens) and sees the slots before lens[b] and, of the
         step's, its own and those before it; with parents [B, N] (a draft tree as
         tree_verify takes it) its own and those of the nodes above it. counts and
-        reserved as for write. scale: None is 1 / sqrt(dim). Returns out, like queries
-        (None: a new array); a token that sees nothing gets 0. lse: None, or a
-        contiguous [B, N, q_heads] float32 array for the logarithms of the sums of
+        reserved as for write. scale: 2^-60 .. 2^60, None is 1 / sqrt(dim). Returns out,
+        like queries (None: a new array); a token that sees nothing gets 0. lse: None, or
+        a contiguous [B, N, q_heads] float32 array for the logarithms of the sums of
         exponentials."""
         k_plane, v_plane = self._layer(layer)
         code = self._dtype(queries, "queries")

@@ -2,7 +2,6 @@
 // Nothing here allocates or synchronises after create.
 #include <hip/hip_runtime.h>
 
-#include <cfloat>
 #include <cstdint>
 #include <cstring>
 #include <initializer_list>
@@ -629,7 +628,9 @@ ss_status ss_cache_attend(ss_cache* c, const ss_block_tables* t, const ss_cache_
     if (st != SS_OK) return st;
     st = check_step(step);
     if (st != SS_OK) return st;
-    if (q_heads < 1 || q_heads > 65536 || q_heads % c->cfg.heads || !(scale > 0.0f && scale <= FLT_MAX) ||
+    // times a block's scale, 2^-60 to 2^60, neither 0 nor an infinity, which masked or zero scores
+    // would turn into a NaN
+    if (q_heads < 1 || q_heads > 65536 || q_heads % c->cfg.heads || !(scale >= 0x1p-60f && scale <= 0x1p60f) ||
         !aligned4(out_lse) || (int64_t)step->N * (q_heads / c->cfg.heads) > INT32_MAX - 64)
         return SS_ERR_INVALID_ARG;
     if (step->B == 0) return SS_OK;
