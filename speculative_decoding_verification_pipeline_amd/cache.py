@@ -292,6 +292,8 @@ class PageCache:
         v = _heads(values, "values", shape, keys.dtype, self.device)
         at = None
         if positions is not None:
+            if rotary is None:
+                raise ValueError("positions are for a rotary: give one")
             at = _check_block(positions, "positions", shape[:2], torch.int32, self.device)
         r = q = o = None
         q_heads = 0
@@ -305,6 +307,8 @@ class PageCache:
             if q_heads < 1 or queries.shape != (*shape[:2], q_heads, self.dim):
                 raise ValueError("queries must be [B, N, q_heads, dim]")
             out_queries, o = _out_heads(out_queries, "out_queries", queries.shape, queries, keys.dtype, stream)
+        elif out_queries is not None:
+            raise ValueError("out_queries needs queries")
         st = self.lib.ss_cache_write(self.handle, ct, step, k_plane, v_plane, code, k, v, r, at, q, o,
                                      q_heads, _stream_on(stream, self.device))
         if st != SS_OK:
