@@ -1118,6 +1118,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_rows(Kv8Attend args) {
             rooted = __ballot(above != 0);
         }
         AttendState<DP, MT> w;
+        uint32_t lives = 0;  // of a lane's rows; in LDS for other lanes, which a barrier must divide
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             const int r = mine + min(m * 16 + col, max(count, 1) - 1);
@@ -1125,8 +1126,9 @@ __global__ __launch_bounds__(256, 2) void k_attend_rows(Kv8Attend args) {
             const int n = rc / a.group;
             w.l[m] = 0.0f;
             w.ref[m] = AT_NONE;
-            if (g == 0)
-                s_live[wave * MT * 16 + m * 16 + col] = n < row.count && (!a.s.parents || (rooted >> (n & 63) & 1));
+            const bool live = n < row.count && (!a.s.parents || (rooted >> (n & 63) & 1));
+            if (g == 0) s_live[wave * MT * 16 + m * 16 + col] = live;
+            lives |= (live ? 1u : 0u) << m;
             const uint16_t* q = a.q.data + pc.b * a.q.row + n * a.q.token +
                                 (h * a.group + rc - n * a.group) * a.q.head + g * 16;
 #pragma unroll
@@ -1218,7 +1220,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_rows(Kv8Attend args) {
                 }
                 __builtin_amdgcn_wave_barrier();
             } else if (rr < rows) {  // a lane has 4 * DT neighbouring entries of a row
-                const bool live = s_live[rr] != 0;
+                const bool live = lives >> m & 1;
                 const float f = attend_factor(w.l[m], live);
                 const AttendOut out = attend_out(a, pc.b, h, first + rr);
                 if (a.lse && g == 0) a.lse[out.lse] = attend_lse(w.ref[m], w.l[m], live);
