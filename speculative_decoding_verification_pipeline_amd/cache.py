@@ -326,9 +326,12 @@ class PageCache:
         if code is None:
             raise ValueError("dtype must be bfloat16 or float16")
         words = self._table_words(tables)
-        B = words[2] if start is None and counts is None else \
-            (start if start is not None else counts).shape[0]
-        if B > words[2] or not 1 <= N <= self.max_blocks * self.page_size:
+        B = words[2]
+        if start is not None:
+            B, _ = self._count(start, "start", B)
+        elif counts is not None:
+            B, _ = self._count(counts, "counts", B)
+        if not 1 <= N <= self.max_blocks * self.page_size:
             raise ValueError(f"at most {words[2]} rows of 1 .. {self.max_blocks * self.page_size} "
                              f"slots are read")
         first = _check_array(start, "start", B, self.device)

@@ -103,8 +103,8 @@ class Rotary:
         k = ok = None
         k_heads = 0
         if keys is not None:
-            k_heads = keys.shape[-2]
-            if keys.shape != (*lead, k_heads, dim):
+            k_heads = keys.shape[-2] if getattr(keys, "ndim", 0) == len(shape) else -1
+            if k_heads < 0 or keys.shape != (*lead, k_heads, dim):
                 raise ValueError("keys must match queries but for the number of heads")
             k = _heads(keys, "keys", None, dtype, dev)
             out_keys, ok = _out_heads(out_keys, "out_keys", keys.shape, keys, dtype, stream)
