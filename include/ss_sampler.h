@@ -597,7 +597,9 @@ ss_status ss_cache_copy_pages(ss_cache* src_cache, const int32_t* src, ss_cache*
  * q 2^(s - 127). Its pages are those of ss_cache_*, which carry the scales along:
  * reserve and copy_pages copy them with the slots, and commit, where an accepted
  * node moves to a block of another scale, gives the block the largest of the scales
- * that its kept slots had and rounds them to it. */
+ * that its kept slots had and rounds them to it. While a block holds slots its scale only
+ * grows: after a rejected draft of large values the committed slots of its block stay
+ * rounded to the scale that the draft needed, which may change those below 2^-6 under it. */
 
 /* The scales: planes of num_pages pages of page_size / block blocks of heads bytes. */
 typedef struct {
@@ -611,7 +613,8 @@ typedef struct {
  * size (a multiple of 16 up to 256), page_size a multiple of 16, and planes and strides
  * aligned to 16 bytes (SS_ERR_UNSUPPORTED otherwise). scales: HOST array of num_planes
  * device pointers, read during the call; no two arrays may share bytes. Scale bytes lie
- * in 67 .. 187 (2^-60 .. 2^60), as ss_cache_write leaves them. */
+ * in 67 .. 187 (2^-60 .. 2^60), as ss_cache_write leaves them. The workspace takes 36 MiB
+ * more than ss_cache_create's, for what the pieces of ss_cache_attend leave. */
 ss_status ss_cache_create_scaled(const ss_cache_config* cfg, void* const* planes,
                                  uint8_t* const* scales, const ss_cache_scales* layout,
                                  ss_cache** out);
@@ -707,9 +710,13 @@ ss_status ss_cache_read(ss_cache* c, const ss_block_tables* t, const int32_t* st
  * Token i of request b sees the slots before base_b and, of the step's, its own and those
  * before it; in a tree its own and those of the nodes above it. Slots on no page are not
  * seen. A token that sees nothing (behind n_b, below no root, of a row without tokens or
- * pages), or scores of -inf alone, gets 0. Whatever slots hold that a token does not see, NaN among it, does not reach it.
+ * pages), or scores of -inf alone, gets 0. Whatever slots hold that a token does not see,
+ * NaN among it, does not reach it.
  * Products are exact, sums and the softmax's statistics binary32; weights are rounded to
  * float16 under a running power of two before they meet the values, the result once more.
+ * Weights are held with their values' scales: a slot counts in the sum as long as its
+ * exponential times its value's scale is at least 2^-126 of the largest such product, so
+ * that none of weight is lost where the scales that a token sees lie within 2^100.
  * Results do not depend on the order in which workgroups run. One kernel; it counts in
  * the handle's workspace.
  *

@@ -931,13 +931,16 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : MT == 2 || DP == 128 ? 2 : 3) 
 // ---------------------------------------------------------------------------
 // Many rows: the waves of a workgroup take rows of their own, 16 * MT each, and share keys and
 // values. Of a tile of 64 slots every wave widens 16 and leaves them in LDS as the operands'
-// registers hold them, 16 bytes a lane, so that neither its writes nor the reads meet in a
-// bank. Two tiles take turns: one is read while the next is left, with a barrier a tile; the
-// one after that is on its way from memory meanwhile.
-// What bounds it: instructions of both kinds on one SIMD. Of a tile a wave of 32 rows has 64 matrix
-// instructions and 209 other vector ones (counted), and two waves a SIMD take 2.6 us for it.
-// 2048 tokens behind 6144 slots, 32 heads of 128: 284 to 291 us, 826 to 848 TFLOP/s; 32 trees of
-// 16 nodes over 2000 slots: 58 to 68 us by their lengths. Scores of the next half tile formed
+// registers hold them: keys 16 bytes a lane, so that neither its writes nor the reads meet in a
+// bank; values, of which a wave has half of an operand, 8 bytes at a stride of 16, whose writes
+// do (4 % of a CU's cycles). Two tiles take turns: one is read while the next is left, with a
+// barrier a tile; the one after that is on its way from memory meanwhile.
+// What bounds it: no unit alone. Of a tile a wave of 32 rows has 64 matrix instructions and 248
+// other vector ones (counted), and two waves a SIMD take 2.5 us for it. Vector instructions take
+// 52 % of a SIMD's cycles, products 39 %, reading operands from LDS about as long as they, by
+// their bytes; a wave waits for 28 % of its cycles. 2048 tokens behind 6144 slots, 32 heads of
+// 128: 283 to 291 us, 826 to 850 TFLOP/s; 32 trees of 16 nodes over 2000 slots: 58 to 68 us by
+// their lengths, with 25 MB of pieces left and read again beside 130 MB of pages. Scores of the next half tile formed
 // between this one's weights, with a second barrier, took 299 us; a wave of higher priority while
 // it multiplies 291.
 
@@ -1245,7 +1248,10 @@ __global__ __launch_bounds__(256, 2) void k_attend_rows(Kv8Attend args) {
 // Into how many shares the slots of a head and block of rows are cut: as many as there are CUs
 // (few rows: a workgroup a CU; twice as many took 60 -> 73 us for one request of 131072 slots and
 // 115 -> 130 for 64 uneven ones of 4000, since more pages are read at a time) or twice that (many
-// rows: two a CU; 32 trees of 64 rows over 2000 slots 81 -> 68 us).
+// rows: two a CU; 32 trees of 64 rows over 2000 slots 81 -> 68 us), as far as what they leave has
+// room: of blocks of 128 rows in heads of 128 283, so that several prompts, which are cut, run one
+// workgroup a CU (8 of 512 tokens behind 512: 146 us, 354 TFLOP/s; 64 trees of 64 nodes and 8
+// query heads a head: 633).
 template <int ROWS>
 static int64_t attend_grid(Kv8Attend& a, int dp, int workgroups) {
     a.blocks = (int)(((int64_t)a.s.N * a.group + ROWS - 1) / ROWS);
@@ -1278,7 +1284,7 @@ static hipError_t launch_many(Kv8Attend a, hipStream_t st) {
 // Up to 32 rows a wave takes them all, and heads above 128 always go that way: 32 requests of 8
 // nodes and 4 query heads a head over 2000 slots take 50 us so and 57 where four waves share
 // keys and values (16 nodes: 73 and 62); in heads of 256 16 nodes take 118 and 208, a prompt's
-// 2048 tokens over 6144 slots 410 and 562. Above 64 rows a wave takes 32 of them; so it does
+// 2048 tokens over 6144 slots, 16 query heads, 410 and 562. Above 64 rows a wave takes 32 of them; so it does
 // not where workgroups of 128 rows leave CUs idle.
 template <int DP, bool F16>
 static hipError_t launch_attend_rows(const Kv8Attend& a, hipStream_t st) {
