@@ -703,7 +703,8 @@ ss_status ss_cache_read(ss_cache* c, const ss_block_tables* t, const int32_t* st
 
 /* ss_cache_attend -- attention of a step's tokens over the cache.
  *   queries, out  [B, N, q_heads, dim] of dtype (SS_BF16 or SS_F16); q_heads a multiple of
- *                 the cache's heads: queries h read head h / (q_heads / heads).
+ *                 the cache's heads: queries h read head h / (q_heads / heads). Rows of a
+ *                 head, N * q_heads / heads, at most 2^31 - 129.
  *   scale         2^-60 .. 2^60: what dot products are multiplied by.
  *   out_lse       NULL, or [B, N, q_heads] float32: the logarithm of the sum of
  *                 exponentials, -inf where a token sees nothing.

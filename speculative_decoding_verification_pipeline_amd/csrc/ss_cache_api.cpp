@@ -628,11 +628,12 @@ ss_status ss_cache_attend(ss_cache* c, const ss_block_tables* t, const ss_cache_
     if (st != SS_OK) return st;
     st = check_step(step);
     if (st != SS_OK) return st;
+    if (q_heads < 1 || q_heads > 65536 || q_heads % c->cfg.heads || !aligned4(out_lse)) return SS_ERR_INVALID_ARG;
+    // rows and a block of 128 of them behind the last are counted in 32 bits
+    if ((int64_t)step->N * (q_heads / c->cfg.heads) > INT32_MAX - 128) return SS_ERR_INVALID_ARG;
     // times a block's scale, 2^-60 to 2^60, neither 0 nor an infinity, which masked or zero scores
     // would turn into a NaN
-    if (q_heads < 1 || q_heads > 65536 || q_heads % c->cfg.heads || !(scale >= 0x1p-60f && scale <= 0x1p60f) ||
-        !aligned4(out_lse) || (int64_t)step->N * (q_heads / c->cfg.heads) > INT32_MAX - 64)
-        return SS_ERR_INVALID_ARG;
+    if (!(scale >= 0x1p-60f && scale <= 0x1p60f)) return SS_ERR_INVALID_ARG;
     if (step->B == 0) return SS_OK;
     for (const ss_heads* h : {queries, out}) {
         st = check_heads(h, true);
